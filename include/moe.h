@@ -807,6 +807,112 @@ moe_status_t moe_ep_sum_partials(const moe_config_t *cfg, int32_t n_parts,
                                  moe_stream_t stream);
 
 /* ----------------------------------------------------------------------
+ * The norms before and after a block, with the branch's gate and the
+ * residual's scale.  A transformer block wraps the MoE layer as
+ *     h   = N(x; w_pre)            y = moe_layer(h)
+ *     out = res_scale * x + gate * N(y; w_post)
+ * with the root-mean-square norm
+ *     N(v; w)[t, c] = v[t, c] * rstd_t * (w_offset + w[c]),
+ *     rstd_t = 1 / sqrt(mean_c v[t, c]^2 + eps).
+ * Sums are float32; `out`, `y` and the norms are rounded to cfg->dtype once,
+ * where they are stored, and a norm of a stored tensor reads the rounded
+ * values.  From cfg these calls read T, H, dtype (and k for the combine).
+ *   row tensors    [T, H] dtype, 16-byte aligned
+ *   w_*            [H] float32 (4-byte aligned; faster 16-byte aligned)
+ *   gate           MOE_GATE_NONE: NULL (1 everywhere); MOE_GATE_TOKEN [T]
+ *                  float32; MOE_GATE_CHANNEL [H] float32; MOE_GATE_FULL
+ *                  [T, H] dtype
+ *   rstd_*         [T] float32, what the backward calls read
+ * A row of zeros has rstd 1/sqrt(eps); a NaN or infinity stays in its row
+ * (and in the column gradients).  A row is held on chip: H * bytes <= 65536,
+ * else MOE_ERR_UNSUPPORTED.  eps must be > 0.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_TOKEN = 1,
+  MOE_GATE_CHANNEL = 2,
+  MOE_GATE_FULL = 3
+} moe_gate_t;
+
+typedef struct {
+  float eps;         /* > 0                                               */
+  float w_offset;    /* added to every norm weight (0, or 1 for 1 + w)    */
+  float res_scale;   /* scale of the residual x                           */
+  int32_t gate_kind; /* moe_gate_t                                        */
+} moe_block_norm_t;
+
+/* moe_norm -- the norm before the block: h = N(x; w).
+ *   h    out [T, H]; may be x
+ *   rstd out [T] float32, or NULL */
+moe_status_t moe_norm(const moe_config_t *cfg, const moe_block_norm_t *opt,
+                      const void *x, const float *w, void *h, float *rstd,
+                      moe_stream_t stream);
+
+/* moe_norm_backward -- its gradient:
+ *   dx = dres + d/dx <dh, N(x; w)>,   dw[c] = sum_t dh[t, c] x[t, c] rstd_t.
+ *   dres       in  [T, H] or NULL: the gradient that reaches x by another
+ *                  way (the residual)
+ *   dx         out [T, H]; may be dh or dres
+ *   dw         out [H] float32, overwritten, or added to with accumulate
+ *   workspace  moe_workspace_bytes(cfg, MOE_WS_BLOCK_BACKWARD) bytes
+ * Column sums are added in a fixed order (no atomics). */
+moe_status_t moe_norm_backward(const moe_config_t *cfg,
+                               const moe_block_norm_t *opt, const void *x,
+                               const float *w, const float *rstd,
+                               const void *dh, const void *dres, void *dx,
+                               float *dw, int32_t accumulate,
+                               void *workspace, size_t workspace_bytes,
+                               moe_stream_t stream);
+
+/* moe_block_out -- the end of the block, and the norm that follows it:
+ *   out = res_scale * x + gate * N(y; w_post),   h_next = N(out; w_next).
+ *   w_post   in  [H] or NULL: no norm (the branch is y itself)
+ *   w_next   in  [H] or NULL: no following norm, h_next unused
+ *   out      out [T, H]; may be x or y
+ *   h_next   out [T, H]; may be x or y, not out
+ *   rstd_y, rstd_out  out [T] float32, or NULL */
+moe_status_t moe_block_out(const moe_config_t *cfg,
+                           const moe_block_norm_t *opt, const void *x,
+                           const void *y, const float *w_post,
+                           const void *gate, const float *w_next, void *out,
+                           void *h_next, float *rstd_y, float *rstd_out,
+                           moe_stream_t stream);
+
+/* moe_combine_block_out -- moe_block_out of the layer's combine, without
+ * writing and reading y in between: y[t] = sum_j topk_w[t, j] *
+ * y_sorted[row_of[t, j]] (moe_combine), rounded to dtype.
+ *   y        out [T, H] or NULL: the combined rows, which the backward needs
+ *            (moe_combine's bits) */
+moe_status_t moe_combine_block_out(
+    const moe_config_t *cfg, const moe_block_norm_t *opt,
+    const void *y_sorted, const int32_t *row_of, const float *topk_w,
+    const void *x, const float *w_post, const void *gate,
+    const float *w_next, void *y, void *out, void *h_next, float *rstd_y,
+    float *rstd_out, moe_stream_t stream);
+
+/* moe_block_out_backward -- the gradients of moe_block_out:
+ *   dO = dout + d/dout <dh_next, N(out; w_next)>,
+ *   dx = res_scale * dO,   dgate = dO * N(y; w_post) summed to the gate's
+ *   shape,   dy = d/dy <dO * gate, N(y; w_post)>, and the norms' weights.
+ *   y, out     in  what the forward read and stored; out, rstd_out only with
+ *                  dh_next; rstd_y only with w_post
+ *   dout, dh_next  in  [T, H]; either may be NULL (zero), not both
+ *   dx         out [T, H]; may be dout or dh_next
+ *   dy         out [T, H]; may be y
+ *   dw_post, dw_next  out [H] float32 (needed with w_post, w_next): all zero
+ *                  without dh_next for dw_next
+ *   dgate      out the gate's shape and type (needed with a gate)
+ *   accumulate nonzero adds into dw_post, dw_next and a [H] dgate
+ *   workspace  moe_workspace_bytes(cfg, MOE_WS_BLOCK_BACKWARD) bytes */
+moe_status_t moe_block_out_backward(
+    const moe_config_t *cfg, const moe_block_norm_t *opt, const void *y,
+    const float *w_post, const void *gate, const float *rstd_y,
+    const void *out, const float *w_next, const float *rstd_out,
+    const void *dout, const void *dh_next, void *dx, void *dy,
+    float *dw_post, void *dgate, float *dw_next, int32_t accumulate,
+    void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------
  * Host-side queries (no GPU work).
  * ---------------------------------------------------------------------- */
 typedef enum {
@@ -814,7 +920,8 @@ typedef enum {
   MOE_WS_CHUNKED = 1,       /* moe_layer_dropless_chunked               */
   MOE_WS_LAYER = 2,         /* moe_layer                                */
   MOE_WS_GMM_BACKWARD = 3,  /* moe_gmm_swiglu_backward                  */
-  MOE_WS_LAYER_BACKWARD = 4 /* moe_layer_backward                       */
+  MOE_WS_LAYER_BACKWARD = 4, /* moe_layer_backward                      */
+  MOE_WS_BLOCK_BACKWARD = 5 /* moe_norm_backward, moe_block_out_backward */
 } moe_ws_kind_t;
 
 /* Workspace bytes an entry point needs for cfg (0 for an invalid cfg). */

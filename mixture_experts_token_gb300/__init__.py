@@ -26,6 +26,8 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_MODE_FALLBACK_LAYER, MOE_MODE_CAPPED, MOE_MODE_DROPLESS = 0, 1, 2
 MOE_WS_PERMUTE, MOE_WS_CHUNKED, MOE_WS_LAYER = 0, 1, 2
 MOE_WS_GMM_BACKWARD, MOE_WS_LAYER_BACKWARD = 3, 4
+MOE_WS_BLOCK_BACKWARD = 5
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL = range(4)
 
 
 class MoeConfig(ctypes.Structure):
@@ -59,6 +61,12 @@ class MoeRowSegment(ctypes.Structure):
     _fields_ = [("group_offsets", c_void_p), ("first_row", c_int32)]
 
 
+class MoeBlockNorm(ctypes.Structure):
+    """moe_block_norm_t."""
+    _fields_ = [("eps", c_float), ("w_offset", c_float),
+                ("res_scale", c_float), ("gate_kind", c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -85,6 +93,7 @@ def lib():
 def _declare(h):
     P = c_void_p
     cfg = ctypes.POINTER(MoeConfig)
+    opt = ctypes.POINTER(MoeBlockNorm)
     sig = {
         "moe_router_logits": [cfg, P, P, P, P, P, P],
         "moe_ep_check": [cfg, P, P, P, P, P],
@@ -142,6 +151,14 @@ def _declare(h):
         "moe_layer_backward": [cfg, P, P, P, P, P, P, P, P, P, P, P, c_int,
                                ctypes.POINTER(MoeLayerInfo), P, P, c_size_t,
                                P],
+        "moe_norm": [cfg, opt, P, P, P, P, P],
+        "moe_norm_backward": [cfg, opt, P, P, P, P, P, P, P, c_int32, P,
+                              c_size_t, P],
+        "moe_block_out": [cfg, opt, P, P, P, P, P, P, P, P, P, P],
+        "moe_combine_block_out": [cfg, opt, P, P, P, P, P, P, P, P, P, P, P,
+                                  P, P],
+        "moe_block_out_backward": [cfg, opt, P, P, P, P, P, P, P, P, P, P, P,
+                                   P, P, P, c_int32, P, c_size_t, P],
     }
     for name, args in sig.items():
         fn = getattr(h, name)
@@ -220,6 +237,12 @@ def make_config(T, H, E, k, F, S, factor=2.0, n_chunks=0, dtype="bf16",
     return MoeConfig(T, H, E, k, F, S, float(factor), n_chunks,
                      MOE_F32 if dtype in ("f32", "float32") else MOE_BF16,
                      1 if renorm else 0, redundant_slots)
+
+
+def make_block_norm(eps=1e-6, w_offset=0.0, res_scale=1.0,
+                    gate=MOE_GATE_NONE) -> MoeBlockNorm:
+    return MoeBlockNorm(float(eps), float(w_offset), float(res_scale),
+                        int(gate))
 
 
 # --------------------------------------------------------- entry points ---
@@ -607,6 +630,54 @@ def moe_layer_backward(cfg, x, logits, w_gate, w_up, w_down, dy, dx,
         _stream(stream)), "moe_layer_backward")
     return {"overflow": info.overflow, "n_chunks": info.n_chunks,
             "capacity": info.capacity}
+
+
+# ------------------------------------------------------ block norms ------
+def moe_norm(cfg, opt, x, w, h, rstd=None, stream=None):
+    """h = N(x; w), the norm before the block; rstd [T] for the backward."""
+    _check(lib().moe_norm(
+        ctypes.byref(cfg), ctypes.byref(opt), _ptr(x), _ptr(w), _ptr(h),
+        _ptr(rstd), _stream(stream)), "moe_norm")
+
+
+def moe_norm_backward(cfg, opt, x, w, rstd, dh, dres, dx, dw, accumulate,
+                      workspace, stream=None):
+    _check(lib().moe_norm_backward(
+        ctypes.byref(cfg), ctypes.byref(opt), _ptr(x), _ptr(w), _ptr(rstd),
+        _ptr(dh), _ptr(dres), _ptr(dx), _ptr(dw), int(accumulate),
+        _ptr(workspace), _nbytes(workspace), _stream(stream)),
+        "moe_norm_backward")
+
+
+def moe_block_out(cfg, opt, x, y, w_post, gate, w_next, out, h_next=None,
+                  rstd_y=None, rstd_out=None, stream=None):
+    """out = res_scale*x + gate*N(y; w_post) and h_next = N(out; w_next)."""
+    _check(lib().moe_block_out(
+        ctypes.byref(cfg), ctypes.byref(opt), _ptr(x), _ptr(y),
+        _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(out), _ptr(h_next),
+        _ptr(rstd_y), _ptr(rstd_out), _stream(stream)), "moe_block_out")
+
+
+def moe_combine_block_out(cfg, opt, y_sorted, row_of, topk_w, x, w_post,
+                          gate, w_next, y, out, h_next=None, rstd_y=None,
+                          rstd_out=None, stream=None):
+    """moe_block_out of moe_combine's rows; y (or None) receives them."""
+    _check(lib().moe_combine_block_out(
+        ctypes.byref(cfg), ctypes.byref(opt), _ptr(y_sorted), _ptr(row_of),
+        _ptr(topk_w), _ptr(x), _ptr(w_post), _ptr(gate), _ptr(w_next),
+        _ptr(y), _ptr(out), _ptr(h_next), _ptr(rstd_y), _ptr(rstd_out),
+        _stream(stream)), "moe_combine_block_out")
+
+
+def moe_block_out_backward(cfg, opt, y, w_post, gate, rstd_y, out, w_next,
+                           rstd_out, dout, dh_next, dx, dy, dw_post, dgate,
+                           dw_next, accumulate, workspace, stream=None):
+    _check(lib().moe_block_out_backward(
+        ctypes.byref(cfg), ctypes.byref(opt), _ptr(y), _ptr(w_post),
+        _ptr(gate), _ptr(rstd_y), _ptr(out), _ptr(w_next), _ptr(rstd_out),
+        _ptr(dout), _ptr(dh_next), _ptr(dx), _ptr(dy), _ptr(dw_post),
+        _ptr(dgate), _ptr(dw_next), int(accumulate), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)), "moe_block_out_backward")
 
 
 class MoeLayerGraph:

@@ -435,6 +435,8 @@ size_t moe_workspace_bytes(const moe_config_t* cfg, moe_ws_kind_t which) {
       return gmm_backward_bytes(*cfg);
     case MOE_WS_LAYER_BACKWARD:
       return layer_backward_bytes(*cfg);
+    case MOE_WS_BLOCK_BACKWARD:
+      return block_backward_bytes(*cfg);
   }
   return 0;
 }

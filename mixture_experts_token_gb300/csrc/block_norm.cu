@@ -1,0 +1,319 @@
+// The norms before and after a block, with the branch's gate and the
+// residual's scale, forward.
+//
+//   N(v; w)[t, c] = v[t, c] * rstd_t * (w_offset + w[c]),
+//   rstd_t = 1 / sqrt(mean_c v[t, c]^2 + eps)
+//   out = res_scale * x + gate * N(y; w_post),   h_next = N(out; w_next)
+//
+// One kernel serves the norm alone (moe_norm), the branch's end
+// (moe_block_out) and the branch's end with the weighted combine in front
+// (moe_combine_block_out).  A row is read once and kept, packed, in
+// registers over both reductions, so the traffic is each input once and each
+// output once; no product is large enough to matter and HBM bounds all of
+// it.  `y` and `out` are rounded to the layer's type where they are stored
+// and the norm that follows reads the rounded value: a backward pass that
+// starts from the stored tensors then differentiates what was computed.
+// Sums of squares are float32.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "block_norm.cuh"
+
+namespace moe {
+namespace {
+
+using namespace block;
+
+enum Mode { kNormOnly = 0, kOut = 1, kCombineOut = 2 };
+
+// NV 16-byte words of the row per thread; WARP: a warp per row and several
+// rows per CTA, else one row per CTA.
+template <typename T, int NV, bool WARP, int MAXT, int MODE>
+__global__ void __launch_bounds__(MAXT)
+    block_fwd_kernel(const FwdArgs a) {
+  using V = Vec<T>;
+  __shared__ float red[2][32];
+  __shared__ int rows[kMaxTopK];
+  __shared__ float wts[kMaxTopK];
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int step = WARP ? 32 : blockDim.x;
+  const int t = WARP ? blockIdx.x * kRowWarps + (threadIdx.x >> 5)
+                     : blockIdx.x;
+  if (WARP && t >= a.T) return;
+  const long long base = static_cast<long long>(t) * a.n16;
+  int4 x[NV], y[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int c = tid + u * step;
+    x[u] = y[u] = make_int4(0, 0, 0, 0);
+    if (c < a.n16) {
+      x[u] = load_stream(a.x + base + c);
+      if (MODE == kOut) y[u] = load_stream(a.y + base + c);
+    }
+  }
+  if (MODE == kCombineOut) {
+    const long long r0 = static_cast<long long>(t) * a.k;
+    if (!WARP) {
+      if (tid < a.k) {
+        rows[tid] = a.row_of[r0 + tid];
+        wts[tid] = a.topk_w[r0 + tid];
+      }
+      __syncthreads();
+    }
+    float acc[NV][V::N];
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) acc[u][i] = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {
+      const int r = WARP ? a.row_of[r0 + j] : rows[j];
+      const float w = WARP ? a.topk_w[r0 + j] : wts[j];
+      if (r < 0) continue;
+      const int4* src = a.y_sorted + static_cast<long long>(r) * a.n16;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int c = tid + u * step;
+        if (c < a.n16) {
+          float f[V::N];
+          V::load(load_stream(src + c), f);
+#pragma unroll
+          for (int i = 0; i < V::N; ++i) acc[u][i] = fmaf(w, f[i], acc[u][i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int c = tid + u * step;
+      y[u] = V::store(acc[u]);
+      if (c < a.n16 && a.y_out) store_stream(a.y_out + base + c, y[u]);
+    }
+  }
+  if (MODE != kNormOnly) {
+    float r = 1.0f;
+    if (a.w_post) {
+      float s = 0.0f;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        float f[V::N];
+        V::load(y[u], f);
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) s = fmaf(f[i], f[i], s);
+      }
+      s = row_sum<WARP>(s, red[0]);
+      r = 1.0f / sqrtf(s * a.inv_h + a.eps);
+      if (tid == 0 && a.rstd_y) a.rstd_y[t] = r;
+    }
+    const float gt = a.gate_kind == MOE_GATE_TOKEN
+                         ? static_cast<const float*>(a.gate)[t]
+                         : 1.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int c = tid + u * step;
+      if (c >= a.n16) continue;
+      float fx[V::N], fy[V::N], w[V::N];
+      V::load(x[u], fx);
+      V::load(y[u], fy);
+      if (a.w_post) {
+        load_weight<V::N>(a.w_post, c, a.vec_w, w);
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) fy[i] *= r * (a.w_offset + w[i]);
+      }
+      if (a.gate_kind == MOE_GATE_CHANNEL) {
+        load_weight<V::N>(static_cast<const float*>(a.gate), c, a.vec_w, w);
+      } else if (a.gate_kind == MOE_GATE_FULL) {
+        V::load(load_stream(static_cast<const int4*>(a.gate) + base + c), w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) w[i] = gt;
+      }
+#pragma unroll
+      for (int i = 0; i < V::N; ++i)
+        fx[i] = fmaf(w[i], fy[i], a.res_scale * fx[i]);
+      x[u] = V::store(fx);
+      store_stream(a.out + base + c, x[u]);
+    }
+  }
+  if (a.w_next == nullptr) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    float f[V::N];
+    V::load(x[u], f);
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) s = fmaf(f[i], f[i], s);
+  }
+  s = row_sum<WARP>(s, red[1]);
+  const float r = 1.0f / sqrtf(s * a.inv_h + a.eps);
+  if (tid == 0 && a.rstd_out) a.rstd_out[t] = r;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int c = tid + u * step;
+    if (c >= a.n16) continue;
+    float f[V::N], w[V::N];
+    V::load(x[u], f);
+    load_weight<V::N>(a.w_next, c, a.vec_w, w);
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) f[i] *= r * (a.w_offset + w[i]);
+    store_stream(a.h + base + c, V::store(f));
+  }
+}
+
+template <typename T, int NV, bool WARP, int MAXT>
+cudaError_t launch_mode(const FwdArgs& a, int mode, int threads,
+                        cudaStream_t s) {
+  const unsigned grid =
+      WARP ? (a.T + kRowWarps - 1) / kRowWarps : static_cast<unsigned>(a.T);
+  if (mode == kNormOnly)
+    block_fwd_kernel<T, NV, WARP, MAXT, kNormOnly><<<grid, threads, 0, s>>>(a);
+  else if (mode == kOut)
+    block_fwd_kernel<T, NV, WARP, MAXT, kOut><<<grid, threads, 0, s>>>(a);
+  else
+    block_fwd_kernel<T, NV, WARP, MAXT, kCombineOut><<<grid, threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_typed(const FwdArgs& a, int mode, cudaStream_t s) {
+  constexpr int W = kRowWarps * 32;
+  if (a.n16 <= 32) return launch_mode<T, 1, true, W>(a, mode, W, s);
+  if (a.n16 <= 64) return launch_mode<T, 2, true, W>(a, mode, W, s);
+  if (a.n16 <= 128) return launch_mode<T, 4, true, W>(a, mode, W, s);
+  const auto threads = [&](int nv) {
+    return ((a.n16 + nv - 1) / nv + 31) / 32 * 32;
+  };
+  if (a.n16 <= 512)
+    return launch_mode<T, 1, false, 512>(a, mode, threads(1), s);
+  if (a.n16 <= 1024)
+    return launch_mode<T, 2, false, 512>(a, mode, threads(2), s);
+  if (a.n16 <= 2048)
+    return launch_mode<T, 4, false, 512>(a, mode, threads(4), s);
+  return launch_mode<T, 4, false, 1024>(a, mode, threads(4), s);
+}
+
+}  // namespace
+
+cudaError_t launch_block_fwd(const moe_config_t& c, const block::FwdArgs& a,
+                             int mode, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  if (c.dtype == MOE_F32) return launch_typed<float>(a, mode, s);
+  return launch_typed<__nv_bfloat16>(a, mode, s);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+namespace {
+
+// T rows of x, and the float arrays of the columns.
+moe_status_t check_common(const moe_config_t* cfg,
+                          const moe_block_norm_t* opt) {
+  const moe_status_t st = moe_validate_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!block::options_ok(opt)) return MOE_ERR_INVALID_ARG;
+  if (block::row_words(*cfg) > block::kMaxRowWords)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+block::FwdArgs common_args(const moe_config_t& c, const moe_block_norm_t& o) {
+  block::FwdArgs a = {};
+  a.T = c.T;
+  a.n16 = block::row_words(c);
+  a.k = c.k;
+  a.inv_h = 1.0f / static_cast<float>(c.H);
+  a.eps = o.eps;
+  a.w_offset = o.w_offset;
+  a.res_scale = o.res_scale;
+  a.gate_kind = o.gate_kind;
+  return a;
+}
+
+moe_status_t block_out(const moe_config_t* cfg, const moe_block_norm_t* opt,
+                       block::FwdArgs a, int mode, const void* x,
+                       const float* w_post, const void* gate,
+                       const float* w_next, void* out, void* h_next,
+                       float* rstd_y, float* rstd_out, cudaStream_t s) {
+  if (!ok_ptr(x, true) || !ok_ptr(out, true) ||
+      !block::opt_ptr(w_post, false) || !block::opt_ptr(w_next, false) ||
+      !block::gate_ok(*opt, gate) || !block::opt_ptr(rstd_y, false) ||
+      !block::opt_ptr(rstd_out, false) ||
+      (w_next != nullptr && !ok_ptr(h_next, true)))
+    return MOE_ERR_INVALID_ARG;
+  a.x = static_cast<const int4*>(x);
+  a.w_post = w_post;
+  a.w_next = w_next;
+  a.gate = gate;
+  a.out = static_cast<int4*>(out);
+  a.h = static_cast<int4*>(h_next);
+  a.rstd_y = rstd_y;
+  a.rstd_out = rstd_out;
+  a.vec_w = block::columns_aligned(*opt, w_post, w_next, gate);
+  return launch_block_fwd(*cfg, a, mode, s) == cudaSuccess ? MOE_OK
+                                                           : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_norm(const moe_config_t* cfg, const moe_block_norm_t* opt,
+                      const void* x, const float* w, void* h, float* rstd,
+                      moe_stream_t stream) {
+  const moe_status_t st = check_common(cfg, opt);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!ok_ptr(x, true) || !ok_ptr(w, false) || !ok_ptr(h, true) ||
+      !block::opt_ptr(rstd, false))
+    return MOE_ERR_INVALID_ARG;
+  block::FwdArgs a = common_args(*cfg, *opt);
+  a.x = static_cast<const int4*>(x);
+  a.w_next = w;
+  a.h = static_cast<int4*>(h);
+  a.rstd_out = rstd;
+  a.vec_w = aligned16(w);
+  return launch_block_fwd(*cfg, a, kNormOnly, stream) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_block_out(const moe_config_t* cfg,
+                           const moe_block_norm_t* opt, const void* x,
+                           const void* y, const float* w_post,
+                           const void* gate, const float* w_next, void* out,
+                           void* h_next, float* rstd_y, float* rstd_out,
+                           moe_stream_t stream) {
+  const moe_status_t st = check_common(cfg, opt);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!ok_ptr(y, true)) return MOE_ERR_INVALID_ARG;
+  block::FwdArgs a = common_args(*cfg, *opt);
+  a.y = static_cast<const int4*>(y);
+  return block_out(cfg, opt, a, kOut, x, w_post, gate, w_next, out, h_next,
+                   rstd_y, rstd_out, stream);
+}
+
+moe_status_t moe_combine_block_out(
+    const moe_config_t* cfg, const moe_block_norm_t* opt,
+    const void* y_sorted, const int32_t* row_of, const float* topk_w,
+    const void* x, const float* w_post, const void* gate,
+    const float* w_next, void* y, void* out, void* h_next, float* rstd_y,
+    float* rstd_out, moe_stream_t stream) {
+  const moe_status_t st = check_common(cfg, opt);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!ok_ptr(y_sorted, true) || !ok_ptr(row_of, false) ||
+      !ok_ptr(topk_w, false) || !block::opt_ptr(y, true))
+    return MOE_ERR_INVALID_ARG;
+  block::FwdArgs a = common_args(*cfg, *opt);
+  a.y_sorted = static_cast<const int4*>(y_sorted);
+  a.row_of = row_of;
+  a.topk_w = topk_w;
+  a.y_out = static_cast<int4*>(y);
+  return block_out(cfg, opt, a, kCombineOut, x, w_post, gate, w_next, out,
+                   h_next, rstd_y, rstd_out, stream);
+}
+
+}  // extern "C"

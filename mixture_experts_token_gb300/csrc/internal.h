@@ -341,6 +341,8 @@ cudaError_t launch_regroup(const moe_config_t& c, int G,
                            cudaStream_t s, const float* w_row = nullptr);
 size_t gmm_backward_bytes(const moe_config_t& c);
 size_t layer_backward_bytes(const moe_config_t& c);
+// Column partials of the block norms' backward (block_norm_backward.cu).
+size_t block_backward_bytes(const moe_config_t& c);
 
 // Tests of the GEMM's bounded waits: stop the TMA producer after `fills`
 // stage fills (-1: normal operation).

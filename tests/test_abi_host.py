@@ -228,3 +228,57 @@ def test_backward_arguments_are_rejected_before_any_launch(m):
     assert lib.moe_layer_backward(ctypes.byref(c), p, p, p, p, p, p, p, p, p,
                                   p, p, 0, ctypes.byref(info), None, None, 0,
                                   None) == m.MOE_ERR_WORKSPACE
+
+
+def test_block_norm_arguments_are_rejected_before_any_launch(m):
+    lib, p = m.lib(), ctypes.c_void_p(0x1000)
+    off = ctypes.c_void_p(0x1008)
+    c, o = cfg_of(m), m.make_block_norm()
+    C, O = ctypes.byref(c), ctypes.byref(o)
+    bad, un = m.MOE_ERR_INVALID_ARG, m.MOE_ERR_UNSUPPORTED
+    # options
+    for kw in (dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")),
+               dict(eps=float("inf")), dict(gate=4), dict(gate=-1)):
+        w = m.make_block_norm(**kw)
+        assert lib.moe_norm(C, ctypes.byref(w), p, p, p, p, None) == bad, kw
+    assert lib.moe_norm(C, None, p, p, p, p, None) == bad
+    assert lib.moe_norm(None, O, p, p, p, p, None) == bad
+    # rows wider than a CTA holds
+    wide = cfg_of(m, H=32776)
+    assert lib.moe_norm(ctypes.byref(wide), O, p, p, p, p, None) == un
+    # missing and misaligned pointers
+    assert lib.moe_norm(C, O, None, p, p, p, None) == bad
+    assert lib.moe_norm(C, O, off, p, p, p, None) == bad
+    assert lib.moe_norm(C, O, p, None, p, p, None) == bad
+    assert lib.moe_norm(C, O, p, ctypes.c_void_p(0x1002), p, p, None) == bad
+    fwd = lambda *a: lib.moe_block_out(C, *a, None)  # noqa: E731
+    assert fwd(O, p, None, p, None, p, p, p, p, p) == bad      # y
+    assert fwd(O, p, p, p, p, p, p, p, p, p) == bad            # gate unasked
+    assert fwd(O, p, p, p, None, p, p, None, p, p) == bad      # h_next
+    for kind in (1, 2, 3):                                     # gate missing
+        w = ctypes.byref(m.make_block_norm(gate=kind))
+        assert fwd(w, p, p, p, None, p, p, p, p, p) == bad
+    full = ctypes.byref(m.make_block_norm(gate=m.MOE_GATE_FULL))
+    assert fwd(full, p, p, p, off, p, p, p, p, p) == bad
+    assert lib.moe_combine_block_out(C, O, p, None, p, p, p, None, p, p, p,
+                                     p, p, p, None) == bad
+    assert lib.moe_combine_block_out(C, O, p, p, p, p, p, None, p, off, p,
+                                     p, p, p, None) == bad
+    # backward: workspace, then pointers
+    n = m.moe_workspace_bytes(c, m.MOE_WS_BLOCK_BACKWARD)
+    assert n >= 16 * 2 * c.H * 4
+    ws = m.MOE_ERR_WORKSPACE
+    nb = lambda *a: lib.moe_norm_backward(C, O, *a, None)  # noqa: E731
+    assert nb(p, p, p, p, None, p, p, 0, None, n) == ws
+    assert nb(p, p, p, p, None, p, p, 0, p, n - 1) == ws
+    assert nb(p, p, p, p, None, p, None, 0, p, n) == bad       # dw
+    assert nb(p, p, None, p, None, p, p, 0, p, n) == bad       # rstd
+    bw = lambda o_, *a: lib.moe_block_out_backward(  # noqa: E731
+        C, o_, *a, 0, p, n, None)
+    none = (p, p, None, p, p, p, p)
+    assert bw(O, *none, None, None, p, p, p, None, p) == bad   # no gradient
+    assert bw(O, *none, p, p, p, p, None, None, p) == bad      # dw_post
+    assert bw(O, *none, p, p, p, p, p, None, None) == bad      # dw_next
+    assert bw(full, p, p, p, p, p, p, p, p, p, p, p, p, None, p) == bad
+    chan = ctypes.byref(m.make_block_norm(gate=m.MOE_GATE_CHANNEL))
+    assert bw(chan, p, p, p, p, p, p, p, p, p, p, p, p, None, p) == bad
