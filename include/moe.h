@@ -913,6 +913,80 @@ moe_status_t moe_block_out_backward(
     void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ----------------------------------------------------------------------
+ * Expert weights in 4 bits with group scales, for serving: a decode step
+ * reads every weight of the experts it routes to once, so its time is the
+ * weights' bytes.  A matrix [K, N] holds, for groups of group_size rows of K
+ * (the last may be shorter),
+ *     w[k, n] = (code[k, n] - zero[k / group_size, n]) *
+ *               scale[k / group_size, n]
+ * with codes 0..15, bf16 scales, and zero = 8 without zero points.  The
+ * weights are constants: there is no gradient of them.
+ *   w       [n, K, N] dtype          n matrices (one for each expert)
+ *   codes   [n, K/2, N] uint8        row 2i in the low four bits, 2i+1 high
+ *   scales  [n, G, N] bf16           G = ceil(K / group_size)
+ *   zeros   [n, G, N] uint8, 0..15   NULL without zero points
+ *   packed  moe_w4_bytes() bytes, 16-byte aligned: what the products read
+ * K must be even; K, N <= 2^20.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t group_size;  /* 32, 64 or 128 rows share a scale                */
+  int32_t zero_points; /* 0: codes are centred on 8; 1: zeros given       */
+} moe_w4_t;
+
+/* Bytes of n packed [K, N] matrices (0 for an invalid argument). */
+size_t moe_w4_bytes(const moe_w4_t *opt, int32_t n, int32_t K, int32_t N);
+
+/* moe_w4_quantize -- codes, scales and zeros of weights: the scale is the
+ * range of a group (with zero in it) over 15 steps, or its largest magnitude
+ * over 7 without zero points, rounded to bf16; codes are nearest (ties to
+ * even) under the rounded scale.  A group of zeros gets scale 0.  Weights
+ * must be finite. */
+moe_status_t moe_w4_quantize(const moe_w4_t *opt, int32_t n, int32_t K,
+                             int32_t N, moe_dtype_t dtype, const void *w,
+                             uint8_t *codes, void *scales, uint8_t *zeros,
+                             moe_stream_t stream);
+
+/* moe_w4_pack -- lays codes, scales and zeros out for the products, once
+ * when a model is loaded. */
+moe_status_t moe_w4_pack(const moe_w4_t *opt, int32_t n, int32_t K, int32_t N,
+                         const uint8_t *codes, const void *scales,
+                         const uint8_t *zeros, void *packed,
+                         moe_stream_t stream);
+
+/* moe_w4_dequantize -- w from packed (for a long prompt, say, whose experts
+ * have rows enough for moe_layer's tensor-core products).  Each value is
+ * computed in float32 and rounded to dtype once. */
+moe_status_t moe_w4_dequantize(const moe_w4_t *opt, int32_t n, int32_t K,
+                               int32_t N, const void *packed,
+                               moe_dtype_t dtype, void *w,
+                               moe_stream_t stream);
+
+/* moe_gmm_gate_up_w4, moe_gmm_down_w4, moe_gmm_swiglu_w4 -- moe_gmm_gate_up,
+ * moe_gmm_down and moe_gmm_swiglu with packed 4-bit weights: w_gate and w_up
+ * are E matrices [H, F], w_down E matrices [F, H].  Made for few rows in a
+ * group, one upward; any number is computed.  Any H and F that a cfg allows
+ * (F >= 1).  Sums are float32; h and y_sorted are rounded to dtype.  A group
+ * whose expert index is outside [0, E) is skipped and sets
+ * MOE_DEV_BAD_INDEX. */
+moe_status_t moe_gmm_gate_up_w4(const moe_config_t *cfg, const moe_w4_t *opt,
+                                int32_t n_groups, const int32_t *group_expert,
+                                const void *x_sorted,
+                                const int32_t *group_offsets,
+                                const void *w_gate, const void *w_up, void *h,
+                                int32_t *status_word, moe_stream_t stream);
+moe_status_t moe_gmm_down_w4(const moe_config_t *cfg, const moe_w4_t *opt,
+                             int32_t n_groups, const int32_t *group_expert,
+                             const void *h, const int32_t *group_offsets,
+                             const void *w_down, void *y_sorted,
+                             int32_t *status_word, moe_stream_t stream);
+moe_status_t moe_gmm_swiglu_w4(const moe_config_t *cfg, const moe_w4_t *opt,
+                               const void *x_sorted,
+                               const int32_t *group_offsets,
+                               const void *w_gate, const void *w_up,
+                               const void *w_down, void *h, void *y_sorted,
+                               int32_t *status_word, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------
  * Host-side queries (no GPU work).
  * ---------------------------------------------------------------------- */
 typedef enum {

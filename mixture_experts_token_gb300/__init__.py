@@ -67,6 +67,11 @@ class MoeBlockNorm(ctypes.Structure):
                 ("res_scale", c_float), ("gate_kind", c_int32)]
 
 
+class MoeW4(ctypes.Structure):
+    """moe_w4_t."""
+    _fields_ = [("group_size", c_int32), ("zero_points", c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -94,6 +99,8 @@ def _declare(h):
     P = c_void_p
     cfg = ctypes.POINTER(MoeConfig)
     opt = ctypes.POINTER(MoeBlockNorm)
+    w4 = ctypes.POINTER(MoeW4)
+    i32 = c_int32
     sig = {
         "moe_router_logits": [cfg, P, P, P, P, P, P],
         "moe_ep_check": [cfg, P, P, P, P, P],
@@ -159,6 +166,12 @@ def _declare(h):
                                   P, P],
         "moe_block_out_backward": [cfg, opt, P, P, P, P, P, P, P, P, P, P, P,
                                    P, P, P, c_int32, P, c_size_t, P],
+        "moe_w4_quantize": [w4, i32, i32, i32, c_int, P, P, P, P, P],
+        "moe_w4_pack": [w4, i32, i32, i32, P, P, P, P, P],
+        "moe_w4_dequantize": [w4, i32, i32, i32, P, c_int, P, P],
+        "moe_gmm_gate_up_w4": [cfg, w4, i32, P, P, P, P, P, P, P, P],
+        "moe_gmm_down_w4": [cfg, w4, i32, P, P, P, P, P, P, P],
+        "moe_gmm_swiglu_w4": [cfg, w4, P, P, P, P, P, P, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(h, name)
@@ -183,6 +196,8 @@ def _declare(h):
     h.moe_layer_graph_destroy.restype = None
     h.moe_workspace_bytes.argtypes = [cfg, c_int]
     h.moe_workspace_bytes.restype = c_size_t
+    h.moe_w4_bytes.argtypes = [w4, i32, i32, i32]
+    h.moe_w4_bytes.restype = c_size_t
     h.moe_validate_config.argtypes = [cfg]
     h.moe_validate_config.restype = c_int
     h.moe_row_dot_parts.argtypes = [cfg]
@@ -243,6 +258,10 @@ def make_block_norm(eps=1e-6, w_offset=0.0, res_scale=1.0,
                     gate=MOE_GATE_NONE) -> MoeBlockNorm:
     return MoeBlockNorm(float(eps), float(w_offset), float(res_scale),
                         int(gate))
+
+
+def make_w4(group_size=128, zero_points=False) -> MoeW4:
+    return MoeW4(int(group_size), int(zero_points))
 
 
 # --------------------------------------------------------- entry points ---
@@ -680,6 +699,64 @@ def moe_block_out_backward(cfg, opt, y, w_post, gate, rstd_y, out, w_next,
         _nbytes(workspace), _stream(stream)), "moe_block_out_backward")
 
 
+# ---------------------------------------------------- 4-bit weights ------
+def moe_w4_bytes(w4, n, K, N) -> int:
+    return int(lib().moe_w4_bytes(ctypes.byref(w4), n, K, N))
+
+
+def _float_type(t):
+    import torch
+    kinds = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    return kinds.get(t.dtype, -1)
+
+
+def moe_w4_quantize(w4, n, K, N, w, codes, scales, zeros=None, stream=None):
+    """Codes, bf16 scales and (with zero points) zeros of w [n, K, N]."""
+    _check(lib().moe_w4_quantize(
+        ctypes.byref(w4), n, K, N, _float_type(w), _ptr(w), _ptr(codes),
+        _ptr(scales), _ptr(zeros), _stream(stream)), "moe_w4_quantize")
+
+
+def moe_w4_pack(w4, n, K, N, codes, scales, zeros, packed, stream=None):
+    """Lays 4-bit weights out for the products, into alloc_w4()'s buffer."""
+    _check(lib().moe_w4_pack(
+        ctypes.byref(w4), n, K, N, _ptr(codes), _ptr(scales), _ptr(zeros),
+        _ptr(packed), _stream(stream)), "moe_w4_pack")
+
+
+def moe_w4_dequantize(w4, n, K, N, packed, w, stream=None):
+    _check(lib().moe_w4_dequantize(
+        ctypes.byref(w4), n, K, N, _ptr(packed), _float_type(w), _ptr(w),
+        _stream(stream)), "moe_w4_dequantize")
+
+
+def moe_gmm_gate_up_w4(cfg, w4, x_sorted, group_offsets, w_gate, w_up, h,
+                       status_word=None, stream=None, n_groups=0,
+                       group_expert=None):
+    _check(lib().moe_gmm_gate_up_w4(
+        ctypes.byref(cfg), ctypes.byref(w4), n_groups, _ptr(group_expert),
+        _ptr(x_sorted), _ptr(group_offsets), _ptr(w_gate), _ptr(w_up),
+        _ptr(h), _ptr(status_word), _stream(stream)), "moe_gmm_gate_up_w4")
+
+
+def moe_gmm_down_w4(cfg, w4, h, group_offsets, w_down, y_sorted,
+                    status_word=None, stream=None, n_groups=0,
+                    group_expert=None):
+    _check(lib().moe_gmm_down_w4(
+        ctypes.byref(cfg), ctypes.byref(w4), n_groups, _ptr(group_expert),
+        _ptr(h), _ptr(group_offsets), _ptr(w_down), _ptr(y_sorted),
+        _ptr(status_word), _stream(stream)), "moe_gmm_down_w4")
+
+
+def moe_gmm_swiglu_w4(cfg, w4, x_sorted, group_offsets, w_gate, w_up, w_down,
+                      h, y_sorted, status_word=None, stream=None):
+    _check(lib().moe_gmm_swiglu_w4(
+        ctypes.byref(cfg), ctypes.byref(w4), _ptr(x_sorted),
+        _ptr(group_offsets), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(h),
+        _ptr(y_sorted), _ptr(status_word), _stream(stream)),
+        "moe_gmm_swiglu_w4")
+
+
 class MoeLayerGraph:
     """moe_layer_graph_t: the fallback=layer layer as one CUDA graph, bound
     to the tensors given here (they must outlive the graph)."""
@@ -769,3 +846,12 @@ def layer_workspace(cfg, which=MOE_WS_LAYER, device="cuda"):
     import torch
     n = moe_workspace_bytes(cfg, which)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def alloc_w4(w4, n, K, N, device="cuda"):
+    """A buffer for n packed 4-bit [K, N] matrices."""
+    import torch
+    b = moe_w4_bytes(w4, n, K, N)
+    if b == 0 and n != 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_w4_bytes")
+    return torch.empty(b, dtype=torch.uint8, device=device)

@@ -382,6 +382,18 @@ bool gmm_shape_ok(const moe_config_t& c) {
   return c.dtype == MOE_F32 || gmm_tc_supported(c);
 }
 
+// n_groups = 0 with a null map: the experts' own groups.
+bool groups_of(const moe_config_t& c, int32_t n, const int32_t* map,
+               Groups* g) {
+  if (n == 0 && map == nullptr) {
+    *g = identity_groups(c);
+    return true;
+  }
+  if (n < 1 || n > kMaxExperts || !ok_ptr(map, false)) return false;
+  *g = {n, map};
+  return true;
+}
+
 bool weights_ok(const void* wg, const void* wu, const void* wd) {
   return ok_ptr(wg, true) && ok_ptr(wu, true) && ok_ptr(wd, true);
 }
@@ -545,20 +557,6 @@ moe_status_t moe_gmm_swiglu(const moe_config_t* cfg, const void* x_sorted,
                                 group_offsets, w_gate, w_up, w_down, h,
                                 y_sorted, status_word, stream));
 }
-
-namespace {
-// n_groups = 0 with a null map: the experts' own groups.
-bool groups_of(const moe_config_t& c, int32_t n, const int32_t* map,
-               Groups* g) {
-  if (n == 0 && map == nullptr) {
-    *g = identity_groups(c);
-    return true;
-  }
-  if (n < 1 || n > kMaxExperts || !ok_ptr(map, false)) return false;
-  *g = {n, map};
-  return true;
-}
-}  // namespace
 
 moe_status_t moe_gmm_gate_up(const moe_config_t* cfg, int32_t n_groups,
                              const int32_t* group_expert,

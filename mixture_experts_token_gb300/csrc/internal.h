@@ -211,6 +211,8 @@ cudaError_t chunked_passes(const moe_config_t& c, const void* x,
 moe_status_t validate(const moe_config_t* c);
 bool ok_ptr(const void* p, bool need16);
 bool gmm_shape_ok(const moe_config_t& c);
+bool groups_of(const moe_config_t& c, int32_t n, const int32_t* map,
+               Groups* g);
 bool weights_ok(const void* wg, const void* wu, const void* wd);
 
 // ---------------------------------------------------------- backward ---

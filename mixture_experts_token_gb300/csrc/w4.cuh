@@ -1,0 +1,69 @@
+// Layout of 4-bit weight matrices (internal).  A matrix [K, N] of one expert
+// is stored as ceil(N / 16) records of 16 columns, one after another:
+//
+//   codes   ceil(K / 64) tiles of 64 x 16 codes, 512 bytes each
+//   scales  [8][Gs] pairs of bf16: (column c, column c + 8) of group g at
+//           [c][g]
+//   zeros   the same with pairs of bytes (only with zero points)
+//
+// where Gs counts groups over K rounded up to 256.  A tile is one 16-byte
+// load per lane of a warp and each of the lane's four words is the weight
+// operand of one m16n8k16 matrix instruction: with c = lane / 4 and
+// t = lane % 4, word s of the lane holds rows k..k+3 with
+//   k = 32 * (s / 2) + 8 * t + 4 * (s % 2)
+// of columns c and c + 8.  Its nibbles, low to high, are
+//   (c,k) (c+8,k) (c,k+2) (c+8,k+2) (c,k+1) (c+8,k+1) (c,k+3) (c+8,k+3),
+// so that masking two nibbles 16 bits apart yields a packed operand pair,
+// and a lane's eight consecutive k of a 32-row half are one 16-byte word of
+// the activations.  A half never mixes groups (groups are 32, 64 or 128
+// rows).  Codes of rows and columns past the matrix are the zero point, so
+// they weigh nothing.
+#pragma once
+
+#include "internal.h"
+
+namespace moe {
+namespace w4 {
+
+constexpr int kTileK = 64;
+constexpr int kTileN = 16;
+constexpr int kTileBytes = kTileK * kTileN / 2;
+constexpr int kStepK = 256;  // rows a warp takes per step: 4 tiles
+
+struct Layout {
+  int K, N, group;
+  bool zeros;
+  __host__ __device__ int tiles_k() const {
+    return (K + kTileK - 1) / kTileK;
+  }
+  __host__ __device__ int tiles_n() const {
+    return (N + kTileN - 1) / kTileN;
+  }
+  __host__ __device__ int groups() const { return (K + group - 1) / group; }
+  __host__ __device__ int stored_groups() const {  // Gs
+    return (K + kStepK - 1) / kStepK * (kStepK / group);
+  }
+  __host__ __device__ long long scales_at() const {
+    return static_cast<long long>(tiles_k()) * kTileBytes;
+  }
+  __host__ __device__ long long zeros_at() const {
+    return scales_at() + 32ll * stored_groups();
+  }
+  __host__ __device__ long long record() const {
+    return zeros_at() + (zeros ? 16ll * stored_groups() : 0);
+  }
+  __host__ __device__ long long matrix() const { return record() * tiles_n(); }
+};
+
+inline bool options_ok(const moe_w4_t* o) {
+  return o != nullptr &&
+         (o->group_size == 32 || o->group_size == 64 ||
+          o->group_size == 128) &&
+         (o->zero_points == 0 || o->zero_points == 1);
+}
+inline Layout layout(const moe_w4_t& o, int K, int N) {
+  return {K, N, o.group_size, o.zero_points != 0};
+}
+
+}  // namespace w4
+}  // namespace moe

@@ -1,0 +1,254 @@
+// 4-bit weights with group scales: quantising, laying out for the products
+// (w4.cuh has the layout) and expanding again.  Work of loading a model, not
+// of a step: each kernel reads its input once and writes its output once
+// (the quantiser reads a group twice, the second time from the caches).
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <limits>
+
+#include "w4.cuh"
+
+namespace moe {
+namespace {
+
+using namespace w4;
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+__device__ __forceinline__ void from_float(float v, float* p) { *p = v; }
+__device__ __forceinline__ void from_float(float v, __nv_bfloat16* p) {
+  *p = __float2bfloat16(v);
+}
+
+// A thread per (matrix, group, column): its group's scale (and zero), then
+// its codes.  The scale is rounded to bf16 first and the codes are nearest
+// to the weights under the rounded scale.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    quantize_kernel(const T* __restrict__ w, int n_mats, Layout l,
+                    uint8_t* __restrict__ codes,
+                    __nv_bfloat16* __restrict__ scales,
+                    uint8_t* __restrict__ zeros) {
+  const int G = l.groups();
+  const long long total = static_cast<long long>(n_mats) * G * l.N;
+  for (long long i = blockIdx.x * static_cast<long long>(kThreads) +
+                     threadIdx.x;
+       i < total; i += static_cast<long long>(gridDim.x) * kThreads) {
+    const int n = static_cast<int>(i % l.N);
+    const long long mg = i / l.N;
+    const int g = static_cast<int>(mg % G);
+    const long long m = mg / G;
+    const int k0 = g * l.group, k1 = min(l.K, k0 + l.group);
+    const T* src = w + m * l.K * l.N + n;
+    float lo = 0.0f, hi = 0.0f;  // the range always holds zero
+    for (int k = k0; k < k1; ++k) {
+      const float v = to_float(src[static_cast<long long>(k) * l.N]);
+      lo = fminf(lo, v);
+      hi = fmaxf(hi, v);
+    }
+    const float span = l.zeros ? (hi - lo) / 15.0f : fmaxf(-lo, hi) / 7.0f;
+    const __nv_bfloat16 sb = __float2bfloat16(span);
+    const float s = __bfloat162float(sb);
+    const float z =
+        !l.zeros ? 8.0f
+        : s > 0.0f ? fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f)
+                   : 0.0f;
+    scales[i] = sb;
+    if (l.zeros) zeros[i] = static_cast<uint8_t>(z);
+    uint8_t* dst = codes + m * (l.K / 2) * l.N + n;
+    for (int k = k0; k < k1; k += 2) {
+      int q[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float v = to_float(src[static_cast<long long>(k + j) * l.N]);
+        const float c = s > 0.0f ? rintf(v / s) + z : z;
+        q[j] = static_cast<int>(fminf(fmaxf(c, 0.0f), 15.0f));
+      }
+      dst[static_cast<long long>(k / 2) * l.N] =
+          static_cast<uint8_t>(q[0] | (q[1] << 4));
+    }
+  }
+}
+
+// Row and column of nibble i of word s of lane `lane` within a tile.
+__device__ __forceinline__ int nibble_k(int lane, int s, int i) {
+  return 32 * (s >> 1) + 8 * (lane & 3) + 4 * (s & 1) + ((i >> 2) & 1) +
+         (i & 2);
+}
+__device__ __forceinline__ int nibble_n(int lane, int i) {
+  return (lane >> 2) + 8 * (i & 1);
+}
+
+// One CTA per (column record, matrix).  grid.y strides over matrices.
+__global__ void __launch_bounds__(kThreads)
+    pack_kernel(const uint8_t* __restrict__ codes,
+                const __nv_bfloat16* __restrict__ scales,
+                const uint8_t* __restrict__ zeros, int n_mats, Layout l,
+                char* __restrict__ packed) {
+  const int n0 = blockIdx.x * kTileN, G = l.groups(), Gs = l.stored_groups();
+  for (long long m = blockIdx.y; m < n_mats; m += gridDim.y) {
+    const uint8_t* c = codes + m * (l.K / 2) * l.N;
+    const __nv_bfloat16* sc = scales + m * G * l.N;
+    const uint8_t* zp = l.zeros ? zeros + m * G * l.N : nullptr;
+    char* rec = packed + m * l.matrix() + blockIdx.x * l.record();
+    const int words = l.tiles_k() * 128;
+    for (int i = threadIdx.x; i < words; i += kThreads) {
+      const int tile = i >> 7, lane = (i >> 2) & 31, s = i & 3;
+      uint32_t v = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = tile * kTileK + nibble_k(lane, s, j);
+        const int n = n0 + nibble_n(lane, j);
+        uint32_t q = 8;
+        if (n < l.N) {
+          if (k < l.K) {
+            const uint32_t b = c[static_cast<long long>(k / 2) * l.N + n];
+            q = k & 1 ? b >> 4 : b & 15;
+          } else if (l.zeros) {
+            // the stored zero of k's group: 0 past the last group
+            const int g = k / l.group;
+            q = g < G ? zp[static_cast<long long>(g) * l.N + n] & 15 : 0;
+          }
+        } else if (l.zeros) {
+          q = 0;
+        }
+        v |= q << (4 * j);
+      }
+      reinterpret_cast<uint32_t*>(rec)[i] = v;
+    }
+    __nv_bfloat16* so =
+        reinterpret_cast<__nv_bfloat16*>(rec + l.scales_at());
+    uint8_t* zo = reinterpret_cast<uint8_t*>(rec + l.zeros_at());
+    for (int i = threadIdx.x; i < 16 * Gs; i += kThreads) {
+      const int col = i / (2 * Gs), g = i / 2 % Gs;
+      const int n = n0 + col + 8 * (i & 1);
+      const bool in = n < l.N && g < G;
+      const long long at = static_cast<long long>(g) * l.N + n;
+      so[i] = in ? sc[at] : __float2bfloat16(0.0f);
+      if (l.zeros) zo[i] = in ? zp[at] & 15 : 0;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    dequantize_kernel(const char* __restrict__ packed, int n_mats, Layout l,
+                      T* __restrict__ w) {
+  const int n0 = blockIdx.x * kTileN, Gs = l.stored_groups();
+  for (long long m = blockIdx.y; m < n_mats; m += gridDim.y) {
+    const char* rec = packed + m * l.matrix() + blockIdx.x * l.record();
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(rec);
+    const __nv_bfloat16* sc =
+        reinterpret_cast<const __nv_bfloat16*>(rec + l.scales_at());
+    const uint8_t* zp =
+        reinterpret_cast<const uint8_t*>(rec + l.zeros_at());
+    T* dst = w + m * l.K * l.N;
+    for (int i = threadIdx.x; i < l.K * kTileN; i += kThreads) {
+      const int k = i / kTileN, col = i % kTileN, n = n0 + col;
+      if (n >= l.N) continue;
+      const int r = k % kTileK;
+      const int lane = (col & 7) * 4 + ((r >> 3) & 3);
+      const int s = 2 * (r >> 5) + ((r >> 2) & 1);
+      const int j = (col >> 3) + (r & 2) + 4 * (r & 1);
+      const uint32_t q =
+          words[(k / kTileK) * 128 + lane * 4 + s] >> (4 * j) & 15;
+      const int at = ((col & 7) * Gs + k / l.group) * 2 + (col >> 3);
+      const int z = l.zeros ? zp[at] : 8;
+      from_float(static_cast<float>(static_cast<int>(q) - z) *
+                     __bfloat162float(sc[at]),
+                 dst + static_cast<long long>(k) * l.N + n);
+    }
+  }
+}
+
+bool shape_ok(int n, int K, int N) {
+  return n >= 0 && K >= 2 && K % 2 == 0 && N >= 1 && K <= (1 << 20) &&
+         N <= (1 << 20);
+}
+dim3 record_grid(const Layout& l, int n) {
+  return dim3(l.tiles_n(), n < 4096 ? n : 4096);
+}
+moe_status_t launched() {
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::w4;
+
+extern "C" {
+
+size_t moe_w4_bytes(const moe_w4_t* opt, int32_t n, int32_t K, int32_t N) {
+  if (!w4::options_ok(opt) || !shape_ok(n, K, N)) return 0;
+  return static_cast<size_t>(layout(*opt, K, N).matrix()) * n;
+}
+
+moe_status_t moe_w4_quantize(const moe_w4_t* opt, int32_t n, int32_t K,
+                             int32_t N, moe_dtype_t dtype, const void* w,
+                             uint8_t* codes, void* scales, uint8_t* zeros,
+                             moe_stream_t stream) {
+  if (!w4::options_ok(opt) || !shape_ok(n, K, N) ||
+      (dtype != MOE_F32 && dtype != MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!ok_ptr(w, true) || codes == nullptr || !ok_ptr(scales, false) ||
+      (zeros != nullptr) != (opt->zero_points != 0))
+    return MOE_ERR_INVALID_ARG;
+  const Layout l = layout(*opt, K, N);
+  const long long total = static_cast<long long>(n) * l.groups() * N;
+  const unsigned grid = static_cast<unsigned>(
+      std::min<long long>((total + kThreads - 1) / kThreads, 1 << 20));
+  __nv_bfloat16* sc = static_cast<__nv_bfloat16*>(scales);
+  if (dtype == MOE_F32)
+    quantize_kernel<<<grid, kThreads, 0, stream>>>(
+        static_cast<const float*>(w), n, l, codes, sc, zeros);
+  else
+    quantize_kernel<<<grid, kThreads, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(w), n, l, codes, sc, zeros);
+  return launched();
+}
+
+moe_status_t moe_w4_pack(const moe_w4_t* opt, int32_t n, int32_t K, int32_t N,
+                         const uint8_t* codes, const void* scales,
+                         const uint8_t* zeros, void* packed,
+                         moe_stream_t stream) {
+  if (!w4::options_ok(opt) || !shape_ok(n, K, N)) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (codes == nullptr || !ok_ptr(scales, false) || !ok_ptr(packed, true) ||
+      (zeros != nullptr) != (opt->zero_points != 0))
+    return MOE_ERR_INVALID_ARG;
+  const Layout l = layout(*opt, K, N);
+  pack_kernel<<<record_grid(l, n), kThreads, 0, stream>>>(
+      codes, static_cast<const __nv_bfloat16*>(scales), zeros, n, l,
+      static_cast<char*>(packed));
+  return launched();
+}
+
+moe_status_t moe_w4_dequantize(const moe_w4_t* opt, int32_t n, int32_t K,
+                               int32_t N, const void* packed,
+                               moe_dtype_t dtype, void* w,
+                               moe_stream_t stream) {
+  if (!w4::options_ok(opt) || !shape_ok(n, K, N) ||
+      (dtype != MOE_F32 && dtype != MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!ok_ptr(packed, true) || !ok_ptr(w, true)) return MOE_ERR_INVALID_ARG;
+  const Layout l = layout(*opt, K, N);
+  const char* p = static_cast<const char*>(packed);
+  if (dtype == MOE_F32)
+    dequantize_kernel<<<record_grid(l, n), kThreads, 0, stream>>>(
+        p, n, l, static_cast<float*>(w));
+  else
+    dequantize_kernel<<<record_grid(l, n), kThreads, 0, stream>>>(
+        p, n, l, static_cast<__nv_bfloat16*>(w));
+  return launched();
+}
+
+}  // extern "C"

@@ -282,3 +282,60 @@ def test_block_norm_arguments_are_rejected_before_any_launch(m):
     assert bw(full, p, p, p, p, p, p, p, p, p, p, p, p, None, p) == bad
     chan = ctypes.byref(m.make_block_norm(gate=m.MOE_GATE_CHANNEL))
     assert bw(chan, p, p, p, p, p, p, p, p, p, p, p, p, None, p) == bad
+
+
+def test_w4_sizes_and_arguments(m):
+    lib, p = m.lib(), ctypes.c_void_p(0x1000)
+    off = ctypes.c_void_p(0x1008)
+    bad = m.MOE_ERR_INVALID_ARG
+    # 16-column records: 64-row code tiles, scales for rows in steps of 256
+    w = m.make_w4(128)
+    assert m.moe_w4_bytes(w, 3, 256, 32) == 3 * 2 * (4 * 512 + 2 * 32)
+    assert m.moe_w4_bytes(m.make_w4(32, True), 1, 66, 17) == \
+        2 * (2 * 512 + 8 * 48)
+    assert m.moe_w4_bytes(w, 0, 64, 16) == 0
+    for args in ((-1, 64, 16), (1, 65, 16), (1, 0, 16), (1, 64, 0),
+                 (1, 1 << 21, 16), (1, 64, 1 << 21)):
+        assert m.moe_w4_bytes(w, *args) == 0, args
+    for g in (0, 16, 48, 256):
+        o = ctypes.byref(m.make_w4(g))
+        assert m.moe_w4_bytes(m.make_w4(g), 1, 64, 16) == 0
+        assert lib.moe_w4_pack(o, 1, 64, 16, p, p, None, p, None) == bad
+    z = m.make_w4(64)
+    z.zero_points = 2
+    assert m.moe_w4_bytes(z, 1, 64, 16) == 0
+    W, Z = ctypes.byref(w), ctypes.byref(m.make_w4(64, True))
+    pack = lambda o, *a: lib.moe_w4_pack(o, 1, 64, 16, *a, None)  # noqa: E731
+    assert pack(W, None, p, None, p) == bad
+    assert pack(W, p, None, None, p) == bad
+    assert pack(W, p, p, p, p) == bad          # zeros nobody asked for
+    assert pack(Z, p, p, None, p) == bad       # zeros missing
+    assert pack(W, p, p, None, off) == bad
+    q = lambda o, d, *a: lib.moe_w4_quantize(  # noqa: E731
+        o, 1, 64, 16, d, *a, None)
+    assert q(W, 2, p, p, p, None) == bad
+    assert q(W, m.MOE_F32, off, p, p, None) == bad
+    assert q(Z, m.MOE_BF16, p, p, p, None) == bad
+    assert lib.moe_w4_dequantize(W, 1, 64, 16, off, 0, p, None) == bad
+    assert lib.moe_w4_dequantize(W, 1, 64, 16, p, 5, p, None) == bad
+    # the products
+    c = cfg_of(m)
+    C = ctypes.byref(c)
+    gu = lambda o, n, e, *a: lib.moe_gmm_gate_up_w4(  # noqa: E731
+        C, o, n, e, *a, None, None)
+    assert gu(None, 0, None, p, p, p, p, p) == bad
+    assert gu(ctypes.byref(m.make_w4(48)), 0, None, p, p, p, p, p) == bad
+    assert gu(W, 3, None, p, p, p, p, p) == bad      # groups without a map
+    assert gu(W, 1025, p, p, p, p, p, p) == bad
+    for i in range(5):
+        a = [p] * 5
+        a[i] = None
+        assert gu(W, 0, None, *a) == bad, i
+    assert gu(W, 0, None, off, p, p, p, p) == bad
+    assert lib.moe_gmm_down_w4(C, W, 0, None, p, p, off, p, None,
+                               None) == bad
+    assert lib.moe_gmm_swiglu_w4(C, W, p, p, p, p, p, None, p, None,
+                                 None) == bad
+    c0 = cfg_of(m, F=0)
+    assert lib.moe_gmm_swiglu_w4(ctypes.byref(c0), W, p, p, p, p, p, p, p,
+                                 None, None) == bad
