@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         v |= q << (4 * j);
       }
-      reinterpret_cast<uint32_t*>(rec)[i] = v;
+      reinterpret_cast<uint32_t*>(rec)[i] = __funnelshift_l(v, v, 3);
     }
     __nv_bfloat16* so =
         reinterpret_cast<__nv_bfloat16*>(rec + l.scales_at());
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
       const bool in = n < l.N && g < G;
       const long long at = static_cast<long long>(g) * l.N + n;
       so[i] = in ? sc[at] : __float2bfloat16(0.0f);
-      if (l.zeros) zo[i] = in ? zp[at] & 15 : 0;
+      if (l.zeros) zo[i] = in ? (zp[at] & 15) << 3 : 0;
     }
   }
 }
@@ -155,10 +155,10 @@ __global__ void __launch_bounds__(kThreads)
       const int lane = (col & 7) * 4 + ((r >> 3) & 3);
       const int s = 2 * (r >> 5) + ((r >> 2) & 1);
       const int j = (col >> 3) + (r & 2) + 4 * (r & 1);
-      const uint32_t q =
-          words[(k / kTileK) * 128 + lane * 4 + s] >> (4 * j) & 15;
+      const uint32_t v = words[(k / kTileK) * 128 + lane * 4 + s];
+      const uint32_t q = __funnelshift_r(v, v, 3 + 4 * j) & 15;
       const int at = ((col & 7) * Gs + k / l.group) * 2 + (col >> 3);
-      const int z = l.zeros ? zp[at] : 8;
+      const int z = l.zeros ? zp[at] >> 3 : 8;
       from_float(static_cast<float>(static_cast<int>(q) - z) *
                      __bfloat162float(sc[at]),
                  dst + static_cast<long long>(k) * l.N + n);
