@@ -52,7 +52,7 @@ cudaError_t launch_gmm_w4_f32(bool dual, const GmmArgs& a, int tokens,
                               cudaStream_t s);
 
 constexpr int kTiles = kStepK / kTileK;  // tiles of a step
-constexpr int kXSlots = 3;               // steps of x (and scales) in flight
+constexpr int kXSlots = 3;               // steps of x (and scales) held
 constexpr int kRing = 2 * kTiles;        // tiles of codes in flight
 
 struct GmmArgs {
@@ -129,11 +129,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4],
 }
 
 // The operand registers of one word of codes: 8 * (16 + code) as bf16
-// pairs, exactly.
-__device__ __forceinline__ void expand(uint32_t w, uint32_t (&a)[4]) {
+// pairs, exactly.  `one` holds two bf16 128, from shared memory: a known
+// constant would be moved into a register again for every use.
+__device__ __forceinline__ void expand(uint32_t w, uint32_t one,
+                                       uint32_t (&a)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    a[i] = (__funnelshift_r(w, w, 4 * i) & 0x00780078u) | 0x43004300u;
+    a[i] = (__funnelshift_r(w, w, 4 * i) & 0x00780078u) | one;
 }
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -200,7 +202,8 @@ struct Kernel {
   static constexpr int kStepBytes = kStepK * sizeof(T);
   static constexpr int kPitch = kStepBytes + Rows<T>::kPad;
   static constexpr int E = kStepK / G;  // groups of a step
-  static constexpr int kScaleRec = 8 * E * (Z ? 6 : 4);
+  static constexpr int kScaleRec = 8 * E * (Z ? 6 : 4);  // of a step
+  static constexpr int kChunk = kTiles * kTileBytes + kScaleRec;
   static constexpr int kTilePair = 2 * kTileBytes;
   // columns of an item
   static constexpr int kCols = DUAL ? NW * kTileN : 2 * NW * kTileN;
@@ -229,21 +232,34 @@ struct Kernel {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nw = warp % NW, kw = warp / NW;
     const int c = lane >> 2, t = lane & 3;
-    const int tiles_k = l.tiles_k(), n_steps = (l.K + kStepK - 1) / kStepK;
+    const int tiles_k = l.tiles_k(), n_steps = l.steps();
     const uint32_t sb = smem_u32(base);
     int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
-    const int n_active = find_active(a, active);
+    __shared__ uint32_t constant;
+    if (threadIdx.x == 0) constant = 0x43004300u;
+    const int n_active = find_active(a, active);  // a barrier within
+    const uint32_t one = lds4(smem_u32(&constant));
     const int blocks = (l.N + kCols - 1) / kCols;
     const int n_items = n_active * blocks;
 
-    // --- the copying side, two steps ahead
+    // --- the copying side, two steps ahead: this lane's place in the
+    // warp's records of the cursor's step, and in the rows of x
     Cursor in = {};
-    const char *p0 = nullptr, *p1 = nullptr;  // this lane's codes of the cursor's step
-    const char *s0 = nullptr, *s1 = nullptr;  // the step's scales or zeros that the lane copies
-    // lanes t < 2 copy scales, t = 2 zeros; where a step's scales fit one
-    // copy, t = 1 has none
-    const int lane_scale =
-        t < 2 ? c * 4 * E + 16 * t : static_cast<int>(32 * E) + c * 2 * E;
+    const char *p0 = nullptr, *p1 = nullptr, *xp = nullptr;
+    int left = 0;  // tiles of the cursor's step and after, 0 past the end
+    const long long row_bytes = static_cast<long long>(l.K) * sizeof(T);
+    // a lane copies the words x_lane, x_lane + 32, ... of row x_first, ...
+    constexpr int kWords = kStepBytes / 16;
+    const int x_first = kShareX ? warp : 0;
+    constexpr int kRowStride = kShareX ? kWarps : 1;
+    const uint32_t x_dst = sb + m.x +
+                           (kShareX ? 0 : warp * a.x_rows * kPitch) +
+                           x_first * kPitch + lane * 16;
+    const auto rewind = [&] {  // to the first step, rows from in.row on
+      in.step = kw;
+      left = tiles_k - kw * kTiles;
+      xp = a.x + (in.row + x_first) * row_bytes + kw * kStepBytes + lane * 16;
+    };
     const auto enter = [&] {  // the item's group and records
       const int g = active[in.item / blocks], nb = in.item % blocks;
       const int ex = a.map ? a.map[g] : g;
@@ -254,99 +270,76 @@ struct Kernel {
       const int rec = DUAL ? nb * NW + nw : 2 * (nb * NW + nw);
       const int last = l.tiles_n() - 1;
       const long long mat = ex * l.matrix(), len = l.record();
-      p0 = a.w0 + mat + min(rec, last) * len;
-      p1 = DUAL ? a.w1 + mat + min(rec, last) * len
-                : a.w0 + mat + min(rec + 1, last) * len;
+      const int at = kw * kChunk + lane * 16;
+      p0 = a.w0 + mat + min(rec, last) * len + at;
+      p1 = DUAL ? a.w1 + mat + min(rec, last) * len + at
+                : a.w0 + mat + min(rec + 1, last) * len + at;
+      rewind();
     };
-    const auto start = [&] {  // from the records' starts to the first step
-      const long long at =
-          t < 2 ? l.scales_at() + c * 4ll * l.stored_groups() +
-                      kw * 4 * E + 16 * t
-                : l.zeros_at() + c * 2ll * l.stored_groups() + kw * 2 * E;
-      s0 = p0 + at;
-      s1 = p1 + at;
-      p0 += kw * kTiles * kTileBytes + lane * 16;
-      p1 += kw * kTiles * kTileBytes + lane * 16;
-      in.step = kw;
-    };
-    int left = 0;  // tiles of the cursor's step, 0 past the last item
     const auto advance = [&] {
       in.step += KW;
-      p0 += KW * kTiles * kTileBytes;
-      p1 += KW * kTiles * kTileBytes;
-      s0 += KW * (t < 2 ? 4 : 2) * E;
-      s1 += KW * (t < 2 ? 4 : 2) * E;
-      left = tiles_k - in.step * kTiles;
+      left -= KW * kTiles;
+      p0 += KW * kChunk;
+      p1 += KW * kChunk;
+      xp += KW * kStepBytes;
       if (left > 0) return;
       in.row += a.x_rows;
       if (in.row < in.r1) {  // the group's next rows: the same weights
-        const int back = (in.step - kw) / KW;
-        p0 -= static_cast<long long>(back) * KW * kTiles * kTileBytes;
-        p1 -= static_cast<long long>(back) * KW * kTiles * kTileBytes;
-        s0 -= back * KW * (t < 2 ? 4 : 2) * E;
-        s1 -= back * KW * (t < 2 ? 4 : 2) * E;
-        in.step = kw;
+        const long long back =
+            static_cast<long long>((in.step - kw) / KW) * (KW * kChunk);
+        p0 -= back;
+        p1 -= back;
+        rewind();
       } else {
         in.item += gridDim.x;
-        if (in.item >= n_items) return;
-        enter();
-        start();
+        if (in.item < n_items) enter();
       }
-      left = tiles_k - in.step * kTiles;
     };
-    const uint32_t codes =
-        sb + warp * (kRing * kTilePair) + lane * 16;
+    const uint32_t codes = sb + warp * (kRing * kTilePair) + lane * 16;
     const uint32_t sc0 = sb + m.scales + warp * 2 * kScaleRec;
-    const auto copy_tile = [&](int slot, int tile) {
+    // Tile `tile` of the cursor's step into slot `half` (of two); with tile
+    // 0 the rows of x and the scales, into slot xs (of three).
+    const auto copy_tile = [&](int half, int xs, int tile) {
       if (tile < left) {
-        const uint32_t dst = codes + ((slot & 1) * kTiles + tile) * kTilePair;
+        const uint32_t dst = codes + (half * kTiles + tile) * kTilePair;
         copy16(dst, p0 + tile * kTileBytes);
         copy16(dst + kTileBytes, p1 + tile * kTileBytes);
         if (tile == 0) {
-          const int xs = slot % kXSlots;
-          copy_x(a, in, sb + m.x + xs * m.x_slot, warp, lane);
-          const uint32_t d =
-              sc0 + xs * kWarps * 2 * kScaleRec + lane_scale;
-          if (t < (E == 8 ? 2 : 1)) {
-            if (E >= 4) {
-              copy16(d, s0);
-              copy16(d + kScaleRec, s1);
-            } else {
-              copy8(d, s0);
-              copy8(d + kScaleRec, s1);
-            }
-          } else if (Z && t == 2) {
-            if (E == 8) {
-              copy16(d, s0);
-              copy16(d + kScaleRec, s1);
-            } else if (E == 4) {
-              copy8(d, s0);
-              copy8(d + kScaleRec, s1);
-            } else {
-              copy4(d, s0);
-              copy4(d + kScaleRec, s1);
-            }
+          if (lane * 16 < kScaleRec) {
+            const int at = min(left, kTiles) * kTileBytes;
+            const uint32_t d =
+                sc0 + xs * kWarps * 2 * kScaleRec + lane * 16;
+            copy16(d, p0 + at);
+            copy16(d + kScaleRec, p1 + at);
           }
+          const int rows = min(a.x_rows, in.r1 - in.row) - x_first;
+          const long long rest =  // of the rows from this lane's place on
+              row_bytes - static_cast<long long>(in.step) * kStepBytes -
+              lane * 16;
+          const uint32_t d = x_dst + xs * m.x_slot;
+#pragma unroll
+          for (int r = 0; r < kRows; r += kRowStride)
+            if (r < rows)
+#pragma unroll
+              for (int w = 0; w < kWords; w += 32)
+                copy16_or_zero(d + r * kPitch + w * 16,
+                               xp + r * row_bytes + w * 16, w * 16 < rest);
         }
       }
       copies_commit();
     };
 
     in.item = blockIdx.x;
-    if (in.item < n_items && kw < n_steps) {
-      enter();
-      start();
-      left = tiles_k - in.step * kTiles;
-    }
+    if (in.item < n_items && kw < n_steps) enter();
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int tile = 0; tile < kTiles; ++tile) copy_tile(s, tile);
+      for (int tile = 0; tile < kTiles; ++tile) copy_tile(s, s, tile);
       if (left > 0) advance();
     }
 
     // --- the computing side
-    int slot = 0;
+    int half = 0, xs = 0;  // the slots of the step
     uint32_t x_row[NT];  // this lane's row of each eight
 #pragma unroll
     for (int b = 0; b < NT; ++b)
@@ -368,11 +361,14 @@ struct Kernel {
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][b][i] = 0.0f;
 #pragma unroll 1
-        for (int step = kw; step < n_steps; step += KW, ++slot) {
-          const int xs = slot % kXSlots, tiles = tiles_k - step * kTiles;
+        for (int step = kw; step < n_steps; step += KW) {
+          const int tiles = tiles_k - step * kTiles;
           const uint32_t x0 = xs * m.x_slot;
-          const uint32_t sc = sc0 + xs * kWarps * 2 * kScaleRec;
-          const uint32_t w = codes + (slot & 1) * kTiles * kTilePair;
+          const uint32_t sc =
+              sc0 + xs * kWarps * 2 * kScaleRec + c * 4 * E;
+          const uint32_t w = codes + half * kTiles * kTilePair;
+          const int next = xs == 0 ? kXSlots - 1 : xs - 1;  // two on
+          Scales scale;
 #pragma unroll
           for (int tile = 0; tile < kTiles; ++tile) {
             copies_wait<kRing - 1>();
@@ -383,12 +379,14 @@ struct Kernel {
                 __syncwarp();
             }
             if (tile < tiles)
-              multiply(acc, rows, w + tile * kTilePair, x_row, x0, sc, tile,
-                       c);
+              multiply(one, acc, rows, w + tile * kTilePair, x_row, x0,
+                       sc, tile, c, scale);
             // the slot's next tile: this lane has read what it overwrites
-            copy_tile(slot + 2, tile);
+            copy_tile(half, next, tile);
           }
           if (left > 0) advance();
+          half ^= 1;
+          xs = xs == kXSlots - 1 ? 0 : xs + 1;
         }
         finish(a, m, acc, row, (item % blocks) * kCols, rows, base, warp, nw,
                c, t);
@@ -396,6 +394,12 @@ struct Kernel {
     }
     copies_wait<0>();
   }
+
+  // Scales and zero operands of the group at hand, of both records.
+  struct Scales {
+    float s[2][2];
+    uint32_t z[2][2];
+  };
 
   // The groups that have rows and an expert, in order; their number.
   __device__ static int find_active(const GmmArgs& a, int32_t* active) {
@@ -428,51 +432,36 @@ struct Kernel {
     return total;
   }
 
-  __device__ static __forceinline__ void copy_x(const GmmArgs& a,
-                                                const Cursor& q, uint32_t dst,
-                                                int warp, int lane) {
-    constexpr int kWords = kStepBytes / 16;  // of a row
-    const int rows = min(a.x_rows, q.r1 - q.row);
-    const int first = kShareX ? threadIdx.x : lane;
-    constexpr int kStride = kShareX ? kThreads : 32;
-    if (!kShareX) dst += warp * a.x_rows * kPitch;
-    const long long pitch = static_cast<long long>(a.l.K) * sizeof(T);
-    for (int i = first; i < rows * kWords; i += kStride) {
-      const int r = i / kWords, w = i % kWords;
-      const long long at = static_cast<long long>(q.step) * kStepBytes +
-                           w * 16;
-      const bool in = at < pitch;
-      copy16_or_zero(dst + r * kPitch + w * 16,
-                     a.x + (q.row + r) * pitch + (in ? at : 0), in);
-    }
-  }
-
   // One tile of both records times the rows of x.
   __device__ static __forceinline__ void multiply(
-      float (&acc)[2][NT][4], int rows, uint32_t codes,
-      const uint32_t (&x_row)[NT], uint32_t x0, uint32_t sc, int tile,
-      int c) {
+      uint32_t one, float (&acc)[2][NT][4], int rows, uint32_t codes,
+      const uint32_t (&x_row)[NT], uint32_t x0, uint32_t sc, int tile, int c,
+      Scales& scale) {
     constexpr int GH = G == 32 ? 1 : 2;  // halves that share a scale
     const uint4 w[2] = {lds16(codes), lds16(codes + kTileBytes)};
 #pragma unroll
     for (int h = 0; h < 2; h += GH) {
       const int g = (tile * kTileK + 32 * h) / G;
       uint32_t op[2][2 * GH][4], zero[2][4];
-      float s[2][2];
+      float (&s)[2][2] = scale.s;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint32_t at = sc + r * kScaleRec;
-        const uint32_t pair = lds4(at + (c * E + g) * 4);
-        s[r][0] = __uint_as_float(pair << 16);
-        s[r][1] = __uint_as_float(pair & 0xffff0000u);
-        // -8 * (16 + zero); the stored byte is 8 * zero
-        uint32_t z = 0x4040;
-        if (Z) z = lds2(at + 32 * E + (c * E + g) * 2);
-        zero[r][0] = zero[r][2] = __byte_perm(z, 0xc3, 0x4040);
-        zero[r][1] = zero[r][3] = __byte_perm(z, 0xc3, 0x4141);
+        if ((tile * kTileK + 32 * h) % G == 0) {  // else the tile before's
+          const uint32_t at = sc + r * kScaleRec;
+          const uint32_t pair = lds4(at + g * 4);
+          s[r][0] = __uint_as_float(pair << 16);
+          s[r][1] = __uint_as_float(pair & 0xffff0000u);
+          // -8 * (16 + zero); the stored byte is 8 * zero
+          uint32_t z = 0x4040;
+          if (Z) z = lds2(at + 32 * E + g * 2 - c * 2 * E);
+          scale.z[r][0] = __byte_perm(z, 0xc3, 0x4040);
+          scale.z[r][1] = __byte_perm(z, 0xc3, 0x4141);
+        }
+        zero[r][0] = zero[r][2] = scale.z[r][0];
+        zero[r][1] = zero[r][3] = scale.z[r][1];
         const uint32_t words[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
 #pragma unroll
-        for (int i = 0; i < 2 * GH; ++i) expand(words[2 * h + i], op[r][i]);
+        for (int i = 0; i < 2 * GH; ++i) expand(words[2 * h + i], one, op[r][i]);
       }
 #pragma unroll
       for (int b = 0; b < NT; ++b) {

@@ -1,12 +1,13 @@
 // Layout of 4-bit weight matrices (internal).  A matrix [K, N] of one expert
 // is stored as ceil(N / 16) records of 16 columns, one after another:
 //
-//   codes   ceil(K / 64) tiles of 64 x 16 codes, 512 bytes each
-//   scales  [8][Gs] pairs of bf16: (column c, column c + 8) of group g at
-//           [c][g]
-//   zeros   the same with pairs of bytes, 8 * zero (only with zero points)
+//   for each step of 256 rows of K (the last may have fewer tiles):
+//     codes   tiles of 64 x 16 codes, 512 bytes each
+//     scales  [8][256 / group] pairs of bf16: (column c, column c + 8) of the
+//             step's group g at [c][g]
+//     zeros   the same with pairs of bytes, 8 * zero (only with zero points)
 //
-// where Gs counts groups over K rounded up to 256.  A tile is one 16-byte
+// so that a product copies one contiguous piece a step.  A tile is one 16-byte
 // load per lane of a warp and each of the lane's four words is the weight
 // operand of one m16n8k16 matrix instruction: with c = lane / 4 and
 // t = lane % 4, word s of the lane holds rows k..k+3 with
@@ -28,7 +29,7 @@ namespace w4 {
 constexpr int kTileK = 64;
 constexpr int kTileN = 16;
 constexpr int kTileBytes = kTileK * kTileN / 2;
-constexpr int kStepK = 256;  // rows a warp takes per step: 4 tiles
+constexpr int kStepK = 256;  // rows of a step: four tiles
 
 struct Layout {
   int K, N, group;
@@ -40,17 +41,22 @@ struct Layout {
     return (N + kTileN - 1) / kTileN;
   }
   __host__ __device__ int groups() const { return (K + group - 1) / group; }
-  __host__ __device__ int stored_groups() const {  // Gs
-    return (K + kStepK - 1) / kStepK * (kStepK / group);
+  __host__ __device__ int steps() const { return (K + kStepK - 1) / kStepK; }
+  __host__ __device__ int scale_bytes() const {  // scales and zeros of a step
+    return 8 * (kStepK / group) * (zeros ? 6 : 4);
   }
-  __host__ __device__ long long scales_at() const {
-    return static_cast<long long>(tiles_k()) * kTileBytes;
+  // Bytes from a record's start to a step, and to its scales.
+  __host__ __device__ long long step_at(int s) const {
+    return static_cast<long long>(s) *
+           (kStepK / kTileK * kTileBytes + scale_bytes());
   }
-  __host__ __device__ long long zeros_at() const {
-    return scales_at() + 32ll * stored_groups();
+  __host__ __device__ long long scales_at(int s) const {
+    const int left = tiles_k() - s * (kStepK / kTileK);
+    return step_at(s) +
+           (left < kStepK / kTileK ? left : kStepK / kTileK) * kTileBytes;
   }
   __host__ __device__ long long record() const {
-    return zeros_at() + (zeros ? 16ll * stored_groups() : 0);
+    return scales_at(steps() - 1) + scale_bytes();
   }
   __host__ __device__ long long matrix() const { return record() * tiles_n(); }
 };

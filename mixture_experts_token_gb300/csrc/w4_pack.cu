@@ -83,6 +83,11 @@ __device__ __forceinline__ int nibble_k(int lane, int s, int i) {
 __device__ __forceinline__ int nibble_n(int lane, int i) {
   return (lane >> 2) + 8 * (i & 1);
 }
+// Bytes from a record's start to a tile of codes.
+__device__ __forceinline__ long long code_at(const Layout& l, int tile) {
+  constexpr int kPer = kStepK / kTileK;
+  return l.step_at(tile / kPer) + tile % kPer * kTileBytes;
+}
 
 // One CTA per (column record, matrix).  grid.y strides over matrices.
 __global__ void __launch_bounds__(kThreads)
@@ -90,7 +95,8 @@ __global__ void __launch_bounds__(kThreads)
                 const __nv_bfloat16* __restrict__ scales,
                 const uint8_t* __restrict__ zeros, int n_mats, Layout l,
                 char* __restrict__ packed) {
-  const int n0 = blockIdx.x * kTileN, G = l.groups(), Gs = l.stored_groups();
+  const int n0 = blockIdx.x * kTileN, G = l.groups();
+  const int E = kStepK / l.group;  // groups of a step
   for (long long m = blockIdx.y; m < n_mats; m += gridDim.y) {
     const uint8_t* c = codes + m * (l.K / 2) * l.N;
     const __nv_bfloat16* sc = scales + m * G * l.N;
@@ -119,18 +125,19 @@ __global__ void __launch_bounds__(kThreads)
         }
         v |= q << (4 * j);
       }
-      reinterpret_cast<uint32_t*>(rec)[i] = __funnelshift_l(v, v, 3);
+      *reinterpret_cast<uint32_t*>(rec + code_at(l, tile) + (i & 127) * 4) =
+          __funnelshift_l(v, v, 3);
     }
-    __nv_bfloat16* so =
-        reinterpret_cast<__nv_bfloat16*>(rec + l.scales_at());
-    uint8_t* zo = reinterpret_cast<uint8_t*>(rec + l.zeros_at());
-    for (int i = threadIdx.x; i < 16 * Gs; i += kThreads) {
-      const int col = i / (2 * Gs), g = i / 2 % Gs;
-      const int n = n0 + col + 8 * (i & 1);
+    for (int i = threadIdx.x; i < l.steps() * 16 * E; i += kThreads) {
+      const int step = i / (16 * E), j = i % (16 * E);
+      const int n = n0 + j / (2 * E) + 8 * (j & 1);
+      const int g = step * E + j / 2 % E;
       const bool in = n < l.N && g < G;
       const long long at = static_cast<long long>(g) * l.N + n;
-      so[i] = in ? sc[at] : __float2bfloat16(0.0f);
-      if (l.zeros) zo[i] = in ? (zp[at] & 15) << 3 : 0;
+      char* so = rec + l.scales_at(step);
+      reinterpret_cast<__nv_bfloat16*>(so)[j] =
+          in ? sc[at] : __float2bfloat16(0.0f);
+      if (l.zeros) so[32 * E + j] = in ? (zp[at] & 15) << 3 : 0;
     }
   }
 }
@@ -139,14 +146,9 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const char* __restrict__ packed, int n_mats, Layout l,
                       T* __restrict__ w) {
-  const int n0 = blockIdx.x * kTileN, Gs = l.stored_groups();
+  const int n0 = blockIdx.x * kTileN, E = kStepK / l.group;
   for (long long m = blockIdx.y; m < n_mats; m += gridDim.y) {
     const char* rec = packed + m * l.matrix() + blockIdx.x * l.record();
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(rec);
-    const __nv_bfloat16* sc =
-        reinterpret_cast<const __nv_bfloat16*>(rec + l.scales_at());
-    const uint8_t* zp =
-        reinterpret_cast<const uint8_t*>(rec + l.zeros_at());
     T* dst = w + m * l.K * l.N;
     for (int i = threadIdx.x; i < l.K * kTileN; i += kThreads) {
       const int k = i / kTileN, col = i % kTileN, n = n0 + col;
@@ -155,12 +157,15 @@ __global__ void __launch_bounds__(kThreads)
       const int lane = (col & 7) * 4 + ((r >> 3) & 3);
       const int s = 2 * (r >> 5) + ((r >> 2) & 1);
       const int j = (col >> 3) + (r & 2) + 4 * (r & 1);
-      const uint32_t v = words[(k / kTileK) * 128 + lane * 4 + s];
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(
+          rec + code_at(l, k / kTileK) + lane * 16 + s * 4);
       const uint32_t q = __funnelshift_r(v, v, 3 + 4 * j) & 15;
-      const int at = ((col & 7) * Gs + k / l.group) * 2 + (col >> 3);
-      const int z = l.zeros ? zp[at] >> 3 : 8;
+      const char* so = rec + l.scales_at(k / kStepK);
+      const int at = ((col & 7) * E + k % kStepK / l.group) * 2 + (col >> 3);
+      const int z = l.zeros ? so[32 * E + at] >> 3 : 8;
       from_float(static_cast<float>(static_cast<int>(q) - z) *
-                     __bfloat162float(sc[at]),
+                     __bfloat162float(
+                         reinterpret_cast<const __nv_bfloat16*>(so)[at]),
                  dst + static_cast<long long>(k) * l.N + n);
     }
   }
