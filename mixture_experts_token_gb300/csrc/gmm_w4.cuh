@@ -11,14 +11,10 @@
 //   m16n8k16 takes 16 columns of weights as its 16-row operand and up to 8
 //   rows of x as its 8 columns, so a batch of one token wastes no more than
 //   idle lanes.
-// * Issue slots come next: 1 KB of codes (one tile of both records) has 172
-//   at full bandwidth.  A code masked into bits 3..6 of a bf16 128 is
-//   8 * (16 + code), one rotation and one logic operation for two of them,
-//   and nothing is subtracted from it: the sums start from those of the
-//   constant operand -8 * (16 + zero), four more matrix instructions.  That
-//   sum is at most 31/7.5 times as large as the one it stands for, so
-//   float32 loses about two bits of its 24.  The scale multiplies the
-//   partial sum of each 32 or 64 rows of W, the 1/8 the final one.
+// * Next comes the arithmetic of expanding codes: logic and shifts run at 16
+//   lanes a clock, so a tile of 64 rows of both records costs a scheduler 80
+//   clocks of masks and byte shifts (see expand()), beside 72 of matrix
+//   instructions and 32 bf16 multiply-adds, against 172 at full bandwidth.
 // * Weights go from HBM to a ring in shared memory by asynchronous 16-byte
 //   copies, two steps of 256 rows ahead.  A lane reads back exactly what it
 //   copied itself, so that ring needs no barrier.  CTAs are persistent, one
@@ -52,8 +48,10 @@ cudaError_t launch_gmm_w4_f32(bool dual, const GmmArgs& a, int tokens,
                               cudaStream_t s);
 
 constexpr int kTiles = kStepK / kTileK;  // tiles of a step
+constexpr int kUnit = 2;                 // tiles copied and waited for at once
+constexpr int kUnits = kTiles / kUnit;
 constexpr int kXSlots = 3;               // steps of x (and scales) held
-constexpr int kRing = 2 * kTiles;        // tiles of codes in flight
+constexpr int kRing = 2 * kTiles;        // tiles of codes held: two steps
 
 struct GmmArgs {
   const char* x;
@@ -128,14 +126,29 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4],
         "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// The operand registers of one word of codes: 8 * (16 + code) as bf16
-// pairs, exactly.  `one` holds two bf16 128, from shared memory: a known
-// constant would be moved into a register again for every use.
-__device__ __forceinline__ void expand(uint32_t w, uint32_t one,
+// a * b + c on bf16 pairs.
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// Powers of two as bf16 pairs.
+constexpr uint32_t kPow127 = 0x7f007f00u, kPow123 = 0x7d007d00u;
+
+// The operand registers of one word of codes: (code - zero) / 64 as bf16
+// pairs, exactly.  The low eight bits of a bf16 whose other bits are zero
+// are a whole number times 2^-133 (a subnormal, or the first binade, which
+// continues them), so a masked code needs no shift within its byte, and the
+// multiplication that scales it subtracts the zero as well: z holds -zero/64
+// of columns c and c + 8.
+__device__ __forceinline__ void expand(uint32_t w, const uint32_t (&z)[2],
                                        uint32_t (&a)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    a[i] = (__funnelshift_r(w, w, 4 * i) & 0x00780078u) | one;
+  const uint32_t v = w >> 8;
+  a[0] = fma2(w & 0x000f000fu, kPow127, z[0]);
+  a[1] = fma2(w & 0x00f000f0u, kPow123, z[1]);
+  a[2] = fma2(v & 0x000f000fu, kPow127, z[0]);
+  a[3] = fma2(v & 0x00f000f0u, kPow123, z[1]);
 }
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -205,6 +218,8 @@ struct Kernel {
   static constexpr int kScaleRec = 8 * E * (Z ? 6 : 4);  // of a step
   static constexpr int kChunk = kTiles * kTileBytes + kScaleRec;
   static constexpr int kTilePair = 2 * kTileBytes;
+  // CTAs an SM has registers for
+  static constexpr int kPerSm = kWarps > 8 ? 1 : 2;
   // columns of an item
   static constexpr int kCols = DUAL ? NW * kTileN : 2 * NW * kTileN;
   static_assert(!kShareX || KW == 1, "x is shared by warps of the same k");
@@ -229,16 +244,14 @@ struct Kernel {
     extern __shared__ __align__(128) char base[];
     const Layout l = a.l;
     const Smem m = smem(a.x_rows, a.n_groups);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int nw = warp % NW, kw = warp / NW;
     const int c = lane >> 2, t = lane & 3;
     const int tiles_k = l.tiles_k(), n_steps = l.steps();
     const uint32_t sb = smem_u32(base);
     int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
-    __shared__ uint32_t constant;
-    if (threadIdx.x == 0) constant = 0x43004300u;
     const int n_active = find_active(a, active);  // a barrier within
-    const uint32_t one = lds4(smem_u32(&constant));
     const int blocks = (l.N + kCols - 1) / kCols;
     const int n_items = n_active * blocks;
 
@@ -248,17 +261,19 @@ struct Kernel {
     const char *p0 = nullptr, *p1 = nullptr, *xp = nullptr;
     int left = 0;  // tiles of the cursor's step and after, 0 past the end
     const long long row_bytes = static_cast<long long>(l.K) * sizeof(T);
-    // a lane copies the words x_lane, x_lane + 32, ... of row x_first, ...
+    // rows side by side in a warp's copy, and the lane's word of its row
     constexpr int kWords = kStepBytes / 16;
-    const int x_first = kShareX ? warp : 0;
-    constexpr int kRowStride = kShareX ? kWarps : 1;
+    constexpr int kSide = kWords < 32 ? 32 / kWords : 1;
+    const int x_first = (kShareX ? warp * kSide : 0) + lane * kSide / 32;
+    constexpr int kRowStride = (kShareX ? kWarps : 1) * kSide;
+    const int x_word = lane % (32 / kSide) * 16;
     const uint32_t x_dst = sb + m.x +
                            (kShareX ? 0 : warp * a.x_rows * kPitch) +
-                           x_first * kPitch + lane * 16;
+                           x_first * kPitch + x_word;
     const auto rewind = [&] {  // to the first step, rows from in.row on
       in.step = kw;
       left = tiles_k - kw * kTiles;
-      xp = a.x + (in.row + x_first) * row_bytes + kw * kStepBytes + lane * 16;
+      xp = a.x + (in.row + x_first) * row_bytes + kw * kStepBytes + x_word;
     };
     const auto enter = [&] {  // the item's group and records
       const int g = active[in.item / blocks], nb = in.item % blocks;
@@ -297,34 +312,39 @@ struct Kernel {
     };
     const uint32_t codes = sb + warp * (kRing * kTilePair) + lane * 16;
     const uint32_t sc0 = sb + m.scales + warp * 2 * kScaleRec;
-    // Tile `tile` of the cursor's step into slot `half` (of two); with tile
+    // Tiles first.. of the cursor's step into slot `half` (of two); with tile
     // 0 the rows of x and the scales, into slot xs (of three).
-    const auto copy_tile = [&](int half, int xs, int tile) {
-      if (tile < left) {
-        const uint32_t dst = codes + (half * kTiles + tile) * kTilePair;
-        copy16(dst, p0 + tile * kTileBytes);
-        copy16(dst + kTileBytes, p1 + tile * kTileBytes);
-        if (tile == 0) {
-          if (lane * 16 < kScaleRec) {
-            const int at = min(left, kTiles) * kTileBytes;
-            const uint32_t d =
-                sc0 + xs * kWarps * 2 * kScaleRec + lane * 16;
-            copy16(d, p0 + at);
-            copy16(d + kScaleRec, p1 + at);
-          }
-          const int rows = min(a.x_rows, in.r1 - in.row) - x_first;
-          const long long rest =  // of the rows from this lane's place on
-              row_bytes - static_cast<long long>(in.step) * kStepBytes -
-              lane * 16;
-          const uint32_t d = x_dst + xs * m.x_slot;
+    const auto copy_unit = [&](int half, int xs, int first) {
+      const uint32_t dst = codes + (half * kTiles + first) * kTilePair;
+      const auto copy_tile = [&](int i) {
+        copy16(dst + i * kTilePair, p0 + (first + i) * kTileBytes);
+        copy16(dst + i * kTilePair + kTileBytes,
+               p1 + (first + i) * kTileBytes);
+      };
+      if (left >= first + kUnit) {
 #pragma unroll
-          for (int r = 0; r < kRows; r += kRowStride)
-            if (r < rows)
-#pragma unroll
-              for (int w = 0; w < kWords; w += 32)
-                copy16_or_zero(d + r * kPitch + w * 16,
-                               xp + r * row_bytes + w * 16, w * 16 < rest);
+        for (int i = 0; i < kUnit; ++i) copy_tile(i);
+      } else if (left > first) {
+        copy_tile(0);
+      }
+      if (first == 0 && left > 0) {
+        if (lane * 16 < kScaleRec) {
+          const int at = min(left, kTiles) * kTileBytes;
+          const uint32_t d = sc0 + xs * kWarps * 2 * kScaleRec + lane * 16;
+          copy16(d, p0 + at);
+          copy16(d + kScaleRec, p1 + at);
         }
+        const int rows = min(a.x_rows, in.r1 - in.row) - x_first;
+        const long long rest =  // of the rows from this lane's place on
+            row_bytes - static_cast<long long>(in.step) * kStepBytes - x_word;
+        const uint32_t d = x_dst + xs * m.x_slot;
+#pragma unroll
+        for (int r = 0; r < kRows; r += kRowStride)
+          if (r < rows)
+#pragma unroll
+            for (int w = 0; w < kWords; w += 32)
+              copy16_or_zero(d + r * kPitch + w * 16,
+                             xp + r * row_bytes + w * 16, w * 16 < rest);
       }
       copies_commit();
     };
@@ -334,7 +354,7 @@ struct Kernel {
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int tile = 0; tile < kTiles; ++tile) copy_tile(s, s, tile);
+      for (int u = 0; u < kUnits; ++u) copy_unit(s, s, u * kUnit);
       if (left > 0) advance();
     }
 
@@ -368,21 +388,23 @@ struct Kernel {
               sc0 + xs * kWarps * 2 * kScaleRec + c * 4 * E;
           const uint32_t w = codes + half * kTiles * kTilePair;
           const int next = xs == 0 ? kXSlots - 1 : xs - 1;  // two on
-          Scales scale;
 #pragma unroll
-          for (int tile = 0; tile < kTiles; ++tile) {
-            copies_wait<kRing - 1>();
-            if (tile == 0) {
+          for (int u = 0; u < kUnits; ++u) {
+            copies_wait<2 * kUnits - 1>();
+            if (u == 0) {
               if (kShareX)
                 __syncthreads();
               else
                 __syncwarp();
             }
-            if (tile < tiles)
-              multiply(one, acc, rows, w + tile * kTilePair, x_row, x0,
-                       sc, tile, c, scale);
-            // the slot's next tile: this lane has read what it overwrites
-            copy_tile(half, next, tile);
+            if (tiles >= (u + 1) * kUnit)
+              multiply<kUnit>(acc, rows, w + u * kUnit * kTilePair,
+                              x_row, x0, sc, u * kUnit, c);
+            else if (tiles > u * kUnit)
+              multiply<1>(acc, rows, w + u * kUnit * kTilePair, x_row,
+                          x0, sc, u * kUnit, c);
+            // the slot's next tiles: this lane has read what they overwrite
+            copy_unit(half, next, u * kUnit);
           }
           if (left > 0) advance();
           half ^= 1;
@@ -394,12 +416,6 @@ struct Kernel {
     }
     copies_wait<0>();
   }
-
-  // Scales and zero operands of the group at hand, of both records.
-  struct Scales {
-    float s[2][2];
-    uint32_t z[2][2];
-  };
 
   // The groups that have rows and an expert, in order; their number.
   __device__ static int find_active(const GmmArgs& a, int32_t* active) {
@@ -432,75 +448,78 @@ struct Kernel {
     return total;
   }
 
-  // One tile of both records times the rows of x.
+  // TILES tiles of both records, from tile `first` of the step on, times the
+  // rows of x.
+  template <int TILES>
   __device__ static __forceinline__ void multiply(
-      uint32_t one, float (&acc)[2][NT][4], int rows, uint32_t codes,
-      const uint32_t (&x_row)[NT], uint32_t x0, uint32_t sc, int tile, int c,
-      Scales& scale) {
-    constexpr int GH = G == 32 ? 1 : 2;  // halves that share a scale
-    const uint4 w[2] = {lds16(codes), lds16(codes + kTileBytes)};
+      float (&acc)[2][NT][4], int rows, uint32_t codes,
+      const uint32_t (&x_row)[NT], uint32_t x0, uint32_t sc, int first,
+      int c) {
+    uint32_t w[TILES][2][4];
 #pragma unroll
-    for (int h = 0; h < 2; h += GH) {
-      const int g = (tile * kTileK + 32 * h) / G;
-      uint32_t op[2][2 * GH][4], zero[2][4];
-      float (&s)[2][2] = scale.s;
+    for (int i = 0; i < TILES; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        if ((tile * kTileK + 32 * h) % G == 0) {  // else the tile before's
-          const uint32_t at = sc + r * kScaleRec;
-          const uint32_t pair = lds4(at + g * 4);
+        const uint4 q = lds16(codes + i * kTilePair + r * kTileBytes);
+        w[i][r][0] = q.x, w[i][r][1] = q.y, w[i][r][2] = q.z;
+        w[i][r][3] = q.w;
+      }
+    float part[2][NT][4], s[2][2];
+    uint32_t zero[2][2];
+    constexpr int kHalves = 2 * TILES;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const int k = first * kTileK + 32 * h;
+      if (h == 0 || k % G == 0) {  // a group begins
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t pair = lds4(sc + r * kScaleRec + k / G * 4);
           s[r][0] = __uint_as_float(pair << 16);
           s[r][1] = __uint_as_float(pair & 0xffff0000u);
-          // -8 * (16 + zero); the stored byte is 8 * zero
-          uint32_t z = 0x4040;
-          if (Z) z = lds2(at + 32 * E + g * 2 - c * 2 * E);
-          scale.z[r][0] = __byte_perm(z, 0xc3, 0x4040);
-          scale.z[r][1] = __byte_perm(z, 0xc3, 0x4141);
+          zero[r][0] = zero[r][1] = 0xbe00be00u;  // -8/64
+          if (Z) {
+            const uint32_t z =
+                lds2(sc + r * kScaleRec + (32 - 2 * c) * E + k / G * 2);
+            zero[r][0] = fma2(__byte_perm(z, 0, 0x4040), kPow127 | 0x80008000u, 0);
+            zero[r][1] = fma2(__byte_perm(z, 0, 0x4141), kPow127 | 0x80008000u, 0);
+          }
         }
-        zero[r][0] = zero[r][2] = scale.z[r][0];
-        zero[r][1] = zero[r][3] = scale.z[r][1];
-        const uint32_t words[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
 #pragma unroll
-        for (int i = 0; i < 2 * GH; ++i) expand(words[2 * h + i], one, op[r][i]);
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[0][b][i] = part[1][b][i] = 0.0f;
       }
+      uint32_t op[2][2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          expand(w[h / 2][r][h % 2 * 2 + i], zero[r], op[r][i]);
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
         if (NT > 1 && 8 * b >= rows) break;
-        float part[2][4] = {};
-        Rows<T> v[GH];
-        uint32_t o[Rows<T>::P][GH][4];
+        Rows<T> v;
+        v.load(x_row[b] + x0 + first * kTileK * static_cast<int>(sizeof(T)) +
+               h * 4 * Rows<T>::kLaneBytes);
 #pragma unroll
-        for (int i = 0; i < GH; ++i) {
-          v[i].load(x_row[b] + x0 + tile * kTileK * sizeof(T) +
-                    (h + i) * 4 * Rows<T>::kLaneBytes);
+        for (int p = 0; p < Rows<T>::P; ++p) {
+          uint32_t o[4];
+          v.part(p, o);
 #pragma unroll
-          for (int p = 0; p < Rows<T>::P; ++p) v[i].part(p, o[p][i]);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              mma(part[r][b], op[r][i], o[2 * i], o[2 * i + 1], part[r][b]);
         }
-        // without zero points both records start from the same sums
+        if (h == kHalves - 1 || (k + 32) % G == 0) {  // a group ends
 #pragma unroll
-        for (int r = 0; r < (Z ? 2 : 1); ++r)
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int i = 0; i < GH; ++i)
-#pragma unroll
-            for (int p = 0; p < Rows<T>::P; ++p) {
-              mma(part[r], zero[r], o[p][i][0], o[p][i][1], part[r]);
-              mma(part[r], zero[r], o[p][i][2], o[p][i][3], part[r]);
-            }
-#pragma unroll
-        for (int r = 1; r >= 0; --r)
-#pragma unroll
-          for (int i = 0; i < GH; ++i)
-#pragma unroll
-            for (int p = 0; p < Rows<T>::P; ++p) {
-              mma(part[r], op[r][2 * i], o[p][i][0], o[p][i][1],
-                  part[!Z && r == 1 && i == 0 && p == 0 ? 0 : r]);
-              mma(part[r], op[r][2 * i + 1], o[p][i][2], o[p][i][3], part[r]);
-            }
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[r][b][i] = fmaf(s[r][i >> 1], part[r][i], acc[r][b][i]);
+            for (int i = 0; i < 4; ++i)
+              acc[r][b][i] =
+                  fmaf(s[r][i >> 1], part[r][b][i],
+                       acc[r][b][i]);
+        }
       }
     }
   }
@@ -527,7 +546,7 @@ struct Kernel {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int n = n0 + (2 * nw + h) * kTileN + col;
-              if (n < a.l.N) put(o + n, 0.125f * acc[h][b][i]);
+              if (n < a.l.N) put(o + n, 64.0f * acc[h][b][i]);
             }
           }
         }
@@ -559,21 +578,22 @@ struct Kernel {
         if (DUAL) u += p[kRec];
       }
       put(out + static_cast<long long>(row + r) * a.l.N + n,
-          DUAL ? swiglu(v, u) : 0.125f * v);
+          DUAL ? swiglu(v, u) : 64.0f * v);
     }
     __syncthreads();
   }
 
-  // of sums that are 8 times the products
+  // of sums that are 1/64 of the products
   __device__ static __forceinline__ float swiglu(float g, float u) {
-    g *= 0.125f;
-    u *= 0.125f;
+    g *= 64.0f;
+    u *= 64.0f;
     return g / (1.0f + expf(-g)) * u;
   }
 };
 
 template <typename T, bool DUAL, int NW, int KW, int NT, int G, bool Z>
-__global__ void __launch_bounds__(NW* KW * 32, NW* KW <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(
+    NW* KW * 32, Kernel<T, DUAL, NW, KW, NT, G, Z>::kPerSm)
     gmm_w4_kernel(const GmmArgs a) {
   Kernel<T, DUAL, NW, KW, NT, G, Z>::run(a);
 }
@@ -608,8 +628,7 @@ cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const int per_sm =
-      Ker::kThreads <= 256 && 2 * (bytes + 1024) <= d.smem ? 2 : 1;
+  const int per_sm = std::min(Ker::kPerSm, d.smem / (bytes + 1024));
   const long long items =
       static_cast<long long>((a.l.N + Ker::kCols - 1) / Ker::kCols) *
       std::min(a.n_groups, a.rows);
@@ -629,7 +648,9 @@ cudaError_t launch_shape(const GmmArgs& a, int tokens, cudaStream_t s) {
       groups * ((a.l.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
   if (tokens <= 8 && items < 4ll * d.sms)
     return launch_one<T, DUAL, 1, 8, 1, G, Z>(a, tokens, d, s);
-  if (sizeof(T) == 4 || a.rows <= 8 * groups)
+  if (a.rows <= 4 * groups)
+    return launch_one<T, DUAL, 8, 1, 1, G, Z>(a, tokens, d, s);
+  if (sizeof(T) == 4 || a.rows <= 12 * groups)
     return launch_one<T, DUAL, 8, 1, 2, G, Z>(a, tokens, d, s);
   if constexpr (sizeof(T) == 2)
     return launch_one<T, DUAL, 16, 1, 4, G, Z>(a, tokens, d, s);

@@ -5,7 +5,7 @@
 //     codes   tiles of 64 x 16 codes, 512 bytes each
 //     scales  [8][256 / group] pairs of bf16: (column c, column c + 8) of the
 //             step's group g at [c][g]
-//     zeros   the same with pairs of bytes, 8 * zero (only with zero points)
+//     zeros   the same with pairs of bytes (only with zero points)
 //
 // so that a product copies one contiguous piece a step.  A tile is one 16-byte
 // load per lane of a warp and each of the lane's four words is the weight
@@ -14,8 +14,7 @@
 //   k = 32 * (s / 2) + 8 * t + 4 * (s % 2)
 // of columns c and c + 8.  Its nibbles, low to high, are
 //   (c,k) (c+8,k) (c,k+2) (c+8,k+2) (c,k+1) (c+8,k+1) (c,k+3) (c+8,k+3),
-// the word rotated left by three bits, so that masking two nibbles 16 bits
-// apart, in bits 3..6 of each half, yields a packed operand pair, and a lane's eight consecutive k of a 32-row half are one 16-byte word of
+// so that masking two nibbles 16 bits apart yields a packed operand pair, and a lane's eight consecutive k of a 32-row half are one 16-byte word of
 // the activations.  A half never mixes groups (groups are 32, 64 or 128
 // rows).  Codes of rows and columns past the matrix are the zero point, so
 // they weigh nothing.

@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         v |= q << (4 * j);
       }
-      *reinterpret_cast<uint32_t*>(rec + code_at(l, tile) + (i & 127) * 4) =
-          __funnelshift_l(v, v, 3);
+      *reinterpret_cast<uint32_t*>(rec + code_at(l, tile) + (i & 127) * 4) = v;
     }
     for (int i = threadIdx.x; i < l.steps() * 16 * E; i += kThreads) {
       const int step = i / (16 * E), j = i % (16 * E);
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kThreads)
       char* so = rec + l.scales_at(step);
       reinterpret_cast<__nv_bfloat16*>(so)[j] =
           in ? sc[at] : __float2bfloat16(0.0f);
-      if (l.zeros) so[32 * E + j] = in ? (zp[at] & 15) << 3 : 0;
+      if (l.zeros) so[32 * E + j] = in ? zp[at] & 15 : 0;
     }
   }
 }
@@ -159,10 +158,10 @@ __global__ void __launch_bounds__(kThreads)
       const int j = (col >> 3) + (r & 2) + 4 * (r & 1);
       const uint32_t v = *reinterpret_cast<const uint32_t*>(
           rec + code_at(l, k / kTileK) + lane * 16 + s * 4);
-      const uint32_t q = __funnelshift_r(v, v, 3 + 4 * j) & 15;
+      const uint32_t q = v >> (4 * j) & 15;
       const char* so = rec + l.scales_at(k / kStepK);
       const int at = ((col & 7) * E + k % kStepK / l.group) * 2 + (col >> 3);
-      const int z = l.zeros ? so[32 * E + at] >> 3 : 8;
+      const int z = l.zeros ? so[32 * E + at] : 8;
       from_float(static_cast<float>(static_cast<int>(q) - z) *
                      __bfloat162float(
                          reinterpret_cast<const __nv_bfloat16*>(so)[at]),
