@@ -218,11 +218,12 @@ def _declare(h):
 
 # ------------------------------------------------------------ marshalling --
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return c_void_p(t)
-    return c_void_p(t.data_ptr())
+    """The device address of a tensor (or of an int or None, itself): what a
+    c_void_p argument takes.  Plain ints convert faster than c_void_p
+    objects, and a step of one token is mostly such conversions."""
+    if t is None or isinstance(t, int):
+        return t
+    return t.data_ptr()
 
 
 def _nbytes(t):
@@ -231,15 +232,33 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
-def _stream(stream):
-    if stream is None:
-        import torch
-        if torch.cuda.is_available():
-            return c_void_p(torch.cuda.current_stream().cuda_stream)
+_raw_stream = None
+
+
+def _find_raw_stream():
+    """A function for the current stream's handle, once a GPU is there."""
+    import torch
+    if not torch.cuda.is_available():
         return None
+    torch.cuda.current_stream()  # brings the runtime up
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch._C._cuda_getDevice
+    return lambda: raw(device())
+
+
+def _stream(stream):
+    global _raw_stream
+    if stream is None:
+        if _raw_stream is None:
+            _raw_stream = _find_raw_stream()
+            if _raw_stream is None:
+                return None
+        return _raw_stream()
     if isinstance(stream, int):
-        return c_void_p(stream)
-    return c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check(status, where):
