@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(MAXT)
         for (int i = 0; i < V::N; ++i) s = fmaf(f[i], f[i], s);
       }
       s = row_sum<WARP>(s, red[0]);
-      r = 1.0f / sqrtf(s * a.inv_h + a.eps);
+      r = rsqrtf(s * a.inv_h + a.eps);
       if (tid == 0 && a.rstd_y) a.rstd_y[t] = r;
     }
     const float gt = a.gate_kind == MOE_GATE_TOKEN
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(MAXT)
     for (int i = 0; i < V::N; ++i) s = fmaf(f[i], f[i], s);
   }
   s = row_sum<WARP>(s, red[1]);
-  const float r = 1.0f / sqrtf(s * a.inv_h + a.eps);
+  const float r = rsqrtf(s * a.inv_h + a.eps);
   if (tid == 0 && a.rstd_out) a.rstd_out[t] = r;
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
@@ -174,6 +174,264 @@ cudaError_t launch_mode(const FwdArgs& a, int mode, int threads,
   return cudaGetLastError();
 }
 
+// ---- rows streamed through shared memory -------------------------------
+// For rows of one CTA.  A persistent CTA walks its rows with the column
+// weights in registers (read once) and the rows' words in a queue in shared
+// memory that runs kQueue words ahead, across rows: a row's reductions leave
+// memory no pause.  A thread holds word tid of the row (and tid + blockDim.x
+// with NV = 2).  A row is, in queue order, y (or its k expert rows), x, and
+// a full gate.
+constexpr int kQueue = 8;
+constexpr int kTable = 16;  // rows whose routing is held, kQueue ahead
+
+template <typename T, int NV, int MAXT, int MODE, bool FULL>
+__global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
+  using V = Vec<T>;
+  constexpr int N = V::N;
+  extern __shared__ __align__(16) char queue[];
+  __shared__ float red[2][32];
+  __shared__ int2 table[MODE == kCombineOut ? kTable * kMaxTopK : 1];
+  const int tid = threadIdx.x, step = blockDim.x;
+  const long long row_step = static_cast<long long>(gridDim.x) * a.n16;
+  const uint32_t word_bytes = step * NV * 16;
+  const uint32_t first = shared_address(queue) + tid * 16;
+  const uint32_t last = first + (kQueue - 1) * word_bytes;
+  const bool in = NV == 1 ? tid < a.n16 : true;  // NV = 2 tests each word
+  const auto held = [&](int u) {
+    return NV == 1 ? in : tid + u * step < a.n16;
+  };
+
+  // routing of the i-th row of this CTA: (row, weight) of slot tid
+  const auto load_route = [&](int i) {
+    const long long t = blockIdx.x + static_cast<long long>(i) * gridDim.x;
+    return tid < a.k && t < a.T
+               ? make_int2(a.row_of[t * a.k + tid],
+                           __float_as_int(a.topk_w[t * a.k + tid]))
+               : make_int2(-1, 0);
+  };
+  const auto keep_route = [&](int i, int2 v) {
+    if (tid < a.k) table[i % kTable * kMaxTopK + tid] = v;
+  };
+  int2 routed = make_int2(-1, 0);  // of row i + kTable - 2, loaded a row ago
+  if (MODE == kCombineOut) {
+    for (int i = 0; i < kTable - 2; ++i) keep_route(i, load_route(i));
+    routed = load_route(kTable - 2);
+    __syncthreads();
+  }
+  const bool token = MODE != kNormOnly && !FULL &&
+                     a.gate_kind == MOE_GATE_TOKEN;
+  const float* gates = static_cast<const float*>(a.gate);
+  float gate = token ? gates[blockIdx.x] : 0.0f;  // of the row, loaded ahead
+
+  // --- the queue's end: the next word to copy
+  const long long at0 = static_cast<long long>(blockIdx.x) * a.n16 + tid;
+  const int4* xp = a.x + at0;
+  const int4* yp = MODE == kOut ? a.y + at0 : nullptr;
+  const int4* gp = FULL ? static_cast<const int4*>(a.gate) + at0 : nullptr;
+  int copy_row = blockIdx.x, copy_word = 0, copy_at = 0;  // copy_at: in table
+  uint32_t dst = first;
+  constexpr int kTail = 1 + (FULL ? 1 : 0);  // words after y
+  const int ys = MODE == kNormOnly ? 0 : MODE == kOut ? 1 : a.k;
+  const auto copy = [&] {
+    if (copy_row < a.T) {
+      const int4* src;
+      if (MODE != kNormOnly && copy_word < ys) {
+        if (MODE == kOut) {
+          src = yp;
+        } else {
+          const int r = table[copy_at + copy_word].x;
+          src = r < 0 ? nullptr
+                      : a.y_sorted + static_cast<long long>(r) * a.n16 + tid;
+        }
+      } else {
+        src = !FULL || copy_word == ys ? xp : gp;
+      }
+      if (MODE != kCombineOut || src != nullptr)
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+          if (held(u)) copy16(dst + u * step * 16, src + u * step);
+      if (++copy_word == ys + kTail) {
+        copy_word = 0;
+        copy_row += gridDim.x;
+        xp += row_step;
+        if (MODE == kOut) yp += row_step;
+        if (FULL) gp += row_step;
+        if (MODE == kCombineOut)
+          copy_at = (copy_at + kMaxTopK) % (kTable * kMaxTopK);
+      }
+    }
+    copies_commit();
+    dst = dst == last ? first : dst + word_bytes;
+  };
+  // --- its front: the next word to read, whose place is copied into again
+  uint32_t src = first;
+  const auto next = [&](int4 (&v)[NV]) {
+    copies_wait<kQueue - 1>();
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      v[u] = held(u) ? read16(src + u * step * 16) : make_int4(0, 0, 0, 0);
+    src = src == last ? first : src + word_bytes;
+    copy();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kQueue; ++i) copy();
+
+  float wp[NV][N], wn[NV][N], wg[NV][N];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int c = tid + u * step;
+    if (MODE != kNormOnly) {
+      columns_or<N>(a.w_post, c, c < a.n16, a.vec_w, 1.0f, wp[u]);
+      columns_or<N>(a.gate_kind == MOE_GATE_CHANNEL
+                        ? static_cast<const float*>(a.gate)
+                        : nullptr,
+                    c, c < a.n16, a.vec_w, 1.0f, wg[u]);
+    }
+    columns_or<N>(a.w_next, c, c < a.n16, a.vec_w, 0.0f, wn[u]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (MODE != kNormOnly && a.w_post) wp[u][i] += a.w_offset;
+      wn[u][i] += a.w_offset;
+    }
+  }
+
+  int sums = 0;  // row sums so far: they alternate between two buffers
+  const auto inverse_rms = [&](const float (&f)[NV][N]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s = fmaf(f[u][i], f[u][i], s);
+    return rsqrtf(row_sum<false>(s, red[sums++ & 1]) * a.inv_h + a.eps);
+  };
+  long long base = at0;
+  int at = 0;  // the row's place in the table
+#pragma unroll 1
+  for (int t = blockIdx.x, i = 0; t < a.T; t += gridDim.x, ++i) {
+    float f[NV][N];  // the row that is stored, and the next norm reads
+    int4 q[NV];
+    if (MODE == kNormOnly) {
+      next(q);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) V::load(q[u], f[u]);
+    } else {
+      float y[NV][N];
+      if (MODE == kOut) {
+        next(q);
+      } else {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+          for (int n = 0; n < N; ++n) y[u][n] = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < a.k; ++j) {
+          const int2 rw = table[at + j];
+          next(q);
+          if (rw.x < 0) continue;
+#pragma unroll
+          for (int u = 0; u < NV; ++u) {
+            float e[N];
+            V::load(q[u], e);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+              y[u][n] = fmaf(__int_as_float(rw.y), e[n], y[u][n]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          q[u] = V::store(y[u]);
+          if (held(u) && a.y_out)
+            store_stream(a.y_out + base + u * step, q[u]);
+        }
+        at = (at + kMaxTopK) % (kTable * kMaxTopK);
+      }
+#pragma unroll
+      for (int u = 0; u < NV; ++u) V::load(q[u], y[u]);
+      float r = 1.0f;
+      if (a.w_post) {
+        r = inverse_rms(y);
+        if (tid == 0 && a.rstd_y) a.rstd_y[t] = r;
+      }
+      if (token) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+          for (int n = 0; n < N; ++n) wg[u][n] = gate;
+        const long long ahead = static_cast<long long>(t) + gridDim.x;
+        if (ahead < a.T) gate = gates[ahead];
+      }
+      next(q);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) V::load(q[u], f[u]);
+      if (FULL) {
+        next(q);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) V::load(q[u], wg[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          f[u][n] = fmaf(wg[u][n], y[u][n] * (r * wp[u][n]),
+                         a.res_scale * f[u][n]);
+        const int4 o = V::store(f[u]);
+        if (held(u)) store_stream(a.out + base + u * step, o);
+        V::load(o, f[u]);
+      }
+    }
+    // the routing that the queue will need; the row sums' barriers lie
+    // between a table row's last reader, its writer and its next reader
+    if (MODE == kCombineOut) {
+      keep_route(i + kTable - 2, routed);
+      routed = load_route(i + kTable - 1);
+    }
+    if (a.w_next) {
+      const float r = inverse_rms(f);
+      if (tid == 0 && a.rstd_out) a.rstd_out[t] = r;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) f[u][n] *= r * wn[u][n];
+        if (held(u)) store_stream(a.h + base + u * step, V::store(f[u]));
+      }
+    } else if (MODE == kCombineOut && !a.w_post) {
+      __syncthreads();
+    }
+    base += row_step;
+  }
+  copies_wait<0>();
+}
+
+template <typename T, int NV, int MAXT, int MODE, bool FULL>
+cudaError_t launch_stream(const FwdArgs& a, cudaStream_t s) {
+  Device d;
+  cudaError_t e = device(&d);
+  if (e != cudaSuccess) return e;
+  const int threads = ((a.n16 + NV - 1) / NV + 31) / 32 * 32;
+  const int bytes = kQueue * threads * NV * 16;
+  auto* kernel = block_fwd_stream<T, NV, MAXT, MODE, FULL>;
+  int per_sm = 0;
+  if ((e = cudaFuncSetAttribute(kernel,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes)) != cudaSuccess ||
+      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+           &per_sm, kernel, threads, bytes)) != cudaSuccess)
+    return e;
+  kernel<<<std::min(a.T, std::max(per_sm, 1) * d.sms), threads, bytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int NV, int MAXT>
+cudaError_t launch_stream_mode(const FwdArgs& a, int mode, cudaStream_t s) {
+  if (mode == kNormOnly)
+    return launch_stream<T, NV, MAXT, kNormOnly, false>(a, s);
+  if (a.gate_kind == MOE_GATE_FULL)
+    return mode == kOut ? launch_stream<T, NV, MAXT, kOut, true>(a, s)
+                        : launch_stream<T, NV, MAXT, kCombineOut, true>(a, s);
+  return mode == kOut ? launch_stream<T, NV, MAXT, kOut, false>(a, s)
+                      : launch_stream<T, NV, MAXT, kCombineOut, false>(a, s);
+}
+
 template <typename T>
 cudaError_t launch_typed(const FwdArgs& a, int mode, cudaStream_t s) {
   constexpr int W = kRowWarps * 32;
@@ -183,10 +441,9 @@ cudaError_t launch_typed(const FwdArgs& a, int mode, cudaStream_t s) {
   const auto threads = [&](int nv) {
     return ((a.n16 + nv - 1) / nv + 31) / 32 * 32;
   };
-  if (a.n16 <= 512)
-    return launch_mode<T, 1, false, 512>(a, mode, threads(1), s);
-  if (a.n16 <= 1024)
-    return launch_mode<T, 2, false, 512>(a, mode, threads(2), s);
+  if (a.n16 <= 512) return launch_stream_mode<T, 1, 512>(a, mode, s);
+  if (a.n16 <= 896) return launch_stream_mode<T, 1, 896>(a, mode, s);
+  if (a.n16 <= 1280) return launch_stream_mode<T, 2, 640>(a, mode, s);
   if (a.n16 <= 2048)
     return launch_mode<T, 4, false, 512>(a, mode, threads(4), s);
   return launch_mode<T, 4, false, 1024>(a, mode, threads(4), s);

@@ -75,6 +75,32 @@ __device__ __forceinline__ void store_stream(int4* p, const int4& v) {
   __stcs(p, v);
 }
 
+// 16 bytes from global to shared memory, asynchronously; a lane reads back
+// only what it copied itself, so waiting for its own copies is enough.
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ int4 read16(uint32_t a) {
+  int4 v;
+  asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 // N float column values that belong to the row's word c.
 template <int N>
 __device__ __forceinline__ void load_weight(const float* p, int c, bool vec,
@@ -112,7 +138,35 @@ __device__ __forceinline__ float row_sum(float s, float* red) {
   return s;
 }
 
+// The N column values of word c, or `other` where there are none.
+template <int N>
+__device__ __forceinline__ void columns_or(const float* p, int c, bool in,
+                                           bool vec, float other, float* w) {
+  if (p != nullptr && in) {
+    load_weight<N>(p, c, vec, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = other;
+  }
+}
+
 // ------------------------------------------------------------- host ------
+struct Device {
+  int sms = 0, smem_sm = 0, smem_cta = 0;
+};
+inline cudaError_t device(Device* d) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(
+        &d->smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&d->smem_cta,
+                               cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  return e;
+}
 inline int row_words(const moe_config_t& c) {
   return static_cast<int>(static_cast<int64_t>(c.H) * elem_bytes(c.dtype) /
                           16);

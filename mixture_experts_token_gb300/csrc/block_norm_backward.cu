@@ -225,6 +225,223 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
   }
 }
 
+// ---- rows streamed through shared memory -------------------------------
+// For rows of one CTA whose words fit twice into shared memory: the CTA's
+// next row is on its way while it reduces the current one.  A thread holds
+// word tid of the row (and tid + blockDim.x with NV = 2), copies it to
+// shared memory itself and reads it back where it is needed, so only the
+// column weights, the column sums and dO stay in registers.
+template <typename T, int NV, int MAXT, bool POST, bool FULL>
+__global__ void __launch_bounds__(MAXT)
+    block_bwd_stream(const BwdArgs a, int slots) {
+  using V = Vec<T>;
+  constexpr int N = V::N;
+  extern __shared__ __align__(16) char queue[];
+  __shared__ float red[2][32];
+  const int tid = threadIdx.x, step = blockDim.x;
+  const bool next = a.dh != nullptr;
+  const bool post = POST && a.w_post != nullptr;
+  const bool token = POST && !FULL && a.gate_kind == MOE_GATE_TOKEN;
+  const bool in = tid < a.n16;
+  const auto held = [&](int u) {
+    return NV == 1 ? in : tid + u * step < a.n16;
+  };
+  const long long row_step = static_cast<long long>(gridDim.x) * a.n16;
+  const long long at0 = static_cast<long long>(blockIdx.x) * a.n16 + tid;
+  // a row's words in shared memory, in this order; absent ones have no room
+  const uint32_t word_bytes = step * NV * 16;
+  const uint32_t at_dh = word_bytes, at_go = next ? 2 * word_bytes : 0;
+  const uint32_t at_y = at_go + (a.dout ? word_bytes : 0);
+  const uint32_t at_g = at_y + word_bytes;
+  const uint32_t row_bytes = at_y + (POST ? word_bytes : 0) +
+                             (FULL ? word_bytes : 0);
+  const uint32_t first = shared_address(queue) + tid * 16;
+  const uint32_t last = first + (slots - 1) * row_bytes;
+
+  long long copy_at = at0;
+  int copy_row = blockIdx.x;
+  uint32_t dst = first;
+  const auto copy = [&] {  // a row
+    if (copy_row < a.T) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (held(u)) {
+          const long long at = copy_at + u * step;
+          const uint32_t d = dst + u * step * 16;
+          if (next) {
+            copy16(d, a.v + at);
+            copy16(d + at_dh, a.dh + at);
+          }
+          if (a.dout) copy16(d + at_go, a.dout + at);
+          if (POST) copy16(d + at_y, a.y + at);
+          if (FULL) copy16(d + at_g, static_cast<const int4*>(a.gate) + at);
+        }
+      copy_row += gridDim.x;
+      copy_at += row_step;
+    }
+    copies_commit();
+    dst = dst == last ? first : dst + row_bytes;
+  };
+  // per-row numbers of the next row, loaded a row ahead
+  const float* gates = static_cast<const float*>(a.gate);
+  float rv = 0.0f, ry = 1.0f, gt = 1.0f;
+  const auto load_row = [&](long long t) {
+    if (t >= a.T) return;
+    if (next) rv = a.rstd_v[t];
+    if (post) ry = a.rstd_y[t];
+    if (token) gt = gates[t];
+  };
+  load_row(blockIdx.x);
+#pragma unroll 1
+  for (int i = 0; i < slots; ++i) copy();
+
+  float wn[NV][N], wp[NV][N], wg[NV][N];
+  float sum_post[NV][N], sum_next[NV][N];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int c = tid + u * step;
+    columns_or<N>(next ? a.w_next : nullptr, c, c < a.n16, a.vec_w, 0.0f,
+                  wn[u]);
+    if (POST) {
+      columns_or<N>(a.w_post, c, c < a.n16, a.vec_w, 1.0f, wp[u]);
+      columns_or<N>(a.gate_kind == MOE_GATE_CHANNEL ? gates : nullptr, c,
+                    c < a.n16, a.vec_w, 1.0f, wg[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      wn[u][i] += a.w_offset;
+      if (post) wp[u][i] += a.w_offset;
+      sum_post[u][i] = sum_next[u][i] = 0.0f;
+    }
+  }
+  const auto load = [&](uint32_t p, int u, float (&f)[N]) {
+    V::load(held(u) ? read16(p + u * step * 16) : make_int4(0, 0, 0, 0), f);
+  };
+  uint32_t src = first;
+  long long base = at0;
+  int sums = 0;  // row sums so far: they alternate between two buffers
+#pragma unroll 1
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (slots == 2)
+      copies_wait<1>();
+    else
+      copies_wait<2>();
+    const float r_v = rv, r_y = ry, g_t = gt;
+    load_row(static_cast<long long>(t) + gridDim.x);
+    float d[NV][N];
+    if (next) {
+      // dO = dout + rstd (dh w' - vh mean(dh w' vh))
+      float s = 0.0f;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        float v[N];
+        load(src, u, v);
+        load(src + at_dh, u, d[u]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float vh = v[i] * r_v;
+          sum_next[u][i] = fmaf(d[u][i], vh, sum_next[u][i]);
+          d[u][i] *= wn[u][i];
+          s = fmaf(d[u][i], vh, s);
+        }
+      }
+      s = row_sum<false>(s, red[sums++ & 1]) * a.inv_h * r_v * r_v;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        float v[N];
+        load(src, u, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          d[u][i] = fmaf(r_v, d[u][i], -(v[i] * s));
+      }
+    }
+    if (a.dout) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        float g[N];
+        load(src + at_go, u, g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[u][i] = next ? d[u][i] + g[i] : g[i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = a.res_scale * d[u][i];
+      if (held(u)) store_stream(a.dx + base + u * step, V::store(f));
+    }
+    if (POST) {
+      // The branch.  A per-token gate multiplies whole rows, so it stays
+      // out of the row sum, which is then that gate's gradient; a
+      // per-channel gate multiplies its column sum once, at the end.
+      float s = 0.0f;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        float y[N], g[N];
+        load(src + at_y, u, y);
+        if (FULL) {
+          float dg[N];
+          load(src + at_g, u, g);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            y[i] *= r_y;
+            dg[i] = d[u][i] * y[i] * wp[u][i];
+            d[u][i] *= g[i];
+            sum_post[u][i] = fmaf(d[u][i], y[i], sum_post[u][i]);
+            d[u][i] *= wp[u][i];
+            s = fmaf(d[u][i], y[i], s);
+          }
+          if (held(u))
+            store_stream(static_cast<int4*>(a.dgate) + base + u * step,
+                         V::store(dg));
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            y[i] *= r_y;
+            sum_post[u][i] = fmaf(g_t * d[u][i], y[i], sum_post[u][i]);
+            d[u][i] *= wg[u][i] * wp[u][i];
+            s = fmaf(d[u][i], y[i], s);
+          }
+        }
+      }
+      if (post || token) {
+        s = row_sum<false>(s, red[sums++ & 1]);
+        if (token && tid == 0) static_cast<float*>(a.dgate)[t] = s;
+        s = post ? s * a.inv_h * r_y : 0.0f;
+      }
+      const float scale = g_t * r_y;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        float y[N];
+        load(src + at_y, u, y);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          d[u][i] = scale * (d[u][i] - (post ? y[i] * s : 0.0f));
+        if (held(u)) store_stream(a.dy + base + u * step, V::store(d[u]));
+      }
+    }
+    copy();  // into the slot that this thread has read
+    src = src == last ? first : src + row_bytes;
+    base += row_step;
+  }
+  copies_wait<0>();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    float* out = a.parts +
+                 (static_cast<long long>(blockIdx.x) * 2 + q) * a.n16 * N;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const float(&f)[N] = q == 0 ? sum_post[u] : sum_next[u];
+      if (held(u))
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+          *reinterpret_cast<float4*>(out + (tid + u * step) * N + i) =
+              make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    }
+  }
+}
+
 struct ColArgs {
   const float *parts, *w_post, *gate;  // gate: per channel, or null
   float *dw_post, *dgate, *dw_next;
@@ -285,9 +502,48 @@ cudaError_t launch_post(const BwdArgs& a, bool post, int grid, int threads,
   return cudaGetLastError();
 }
 
+// The streamed form with as many CTAs as fit, at most `parts`; returns their
+// number in *grid, or 0 where two rows do not fit.
+template <typename T, int NV, int MAXT, bool POST, bool FULL>
+cudaError_t launch_stream(const BwdArgs& a, int parts, int* grid,
+                          cudaStream_t s) {
+  Device d;
+  cudaError_t e = device(&d);
+  if (e != cudaSuccess) return e;
+  const int threads = ((a.n16 + NV - 1) / NV + 31) / 32 * 32;
+  const int words = (a.dh ? 2 : 0) + (a.dout ? 1 : 0) + POST + FULL;
+  const int row = words * threads * NV * 16;
+  auto* kernel = block_bwd_stream<T, NV, MAXT, POST, FULL>;
+  const int slots = 3 * row <= d.smem_cta / 2 ? 3 : 2;
+  int per_sm = 0;
+  *grid = 0;
+  if (slots * row + 1024 > d.smem_cta) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kernel,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                slots * row)) != cudaSuccess ||
+      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+           &per_sm, kernel, threads, slots * row)) != cudaSuccess)
+    return e;
+  *grid = std::min(parts, std::max(per_sm, 1) * d.sms);
+  kernel<<<*grid, threads, slots * row, s>>>(a, slots);
+  return cudaGetLastError();
+}
+
+template <typename T, int NV, int MAXT>
+cudaError_t launch_stream_post(const BwdArgs& a, bool post, int parts,
+                               int* grid, cudaStream_t s) {
+  if (!post)
+    return launch_stream<T, NV, MAXT, false, false>(a, parts, grid, s);
+  if (a.gate_kind == MOE_GATE_FULL)
+    return launch_stream<T, NV, MAXT, true, true>(a, parts, grid, s);
+  return launch_stream<T, NV, MAXT, true, false>(a, parts, grid, s);
+}
+
+// At most `parts` CTAs; *grid receives how many partials there are.
 template <typename T>
-cudaError_t launch_rows(const BwdArgs& a, bool post, int grid,
+cudaError_t launch_rows(const BwdArgs& a, bool post, int parts, int* grid_out,
                         cudaStream_t s) {
+  const int grid = *grid_out = parts;
   constexpr int W = kRowWarps * 32;
   if (a.n16 <= 32) return launch_post<T, 1, true, W>(a, post, grid, W, s);
   if (a.n16 <= 64) return launch_post<T, 2, true, W>(a, post, grid, W, s);
@@ -295,10 +551,18 @@ cudaError_t launch_rows(const BwdArgs& a, bool post, int grid,
   const auto threads = [&](int nv) {
     return ((a.n16 + nv - 1) / nv + 31) / 32 * 32;
   };
+  cudaError_t e = cudaSuccess;
+  int streamed = 0;
   if (a.n16 <= 512)
-    return launch_post<T, 1, false, 512>(a, post, grid, threads(1), s);
-  if (a.n16 <= 1024)
-    return launch_post<T, 2, false, 512>(a, post, grid, threads(2), s);
+    e = launch_stream_post<T, 1, 512>(a, post, parts, &streamed, s);
+  else if (a.n16 <= 896)
+    e = launch_stream_post<T, 1, 896>(a, post, parts, &streamed, s);
+  else if (a.n16 <= 1280)
+    e = launch_stream_post<T, 2, 640>(a, post, parts, &streamed, s);
+  if (e != cudaSuccess || streamed > 0) {
+    *grid_out = streamed;
+    return e;
+  }
   if (a.n16 <= 2048)
     return launch_post<T, 4, false, 512>(a, post, grid, threads(4), s);
   return launch_post<T, 4, false, 1024>(a, post, grid, threads(4), s);
@@ -310,15 +574,15 @@ moe_status_t run(const moe_config_t& c, BwdArgs a, ColArgs ca, bool post,
   a.n16 = row_words(c);
   a.inv_h = 1.0f / static_cast<float>(c.H);
   Carve cv(workspace);
-  const int grid = parts_of(c);
-  a.parts = cv.take<float>(static_cast<size_t>(grid) * 2 * c.H);
+  const int parts = parts_of(c);
+  a.parts = cv.take<float>(static_cast<size_t>(parts) * 2 * c.H);
   ca.parts = a.parts;
   ca.H = c.H;
-  ca.n_parts = grid;
   ca.w_offset = a.w_offset;
-  cudaError_t e = c.dtype == MOE_F32
-                      ? launch_rows<float>(a, post, grid, s)
-                      : launch_rows<__nv_bfloat16>(a, post, grid, s);
+  const cudaError_t e =
+      c.dtype == MOE_F32
+          ? launch_rows<float>(a, post, parts, &ca.n_parts, s)
+          : launch_rows<__nv_bfloat16>(a, post, parts, &ca.n_parts, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   const dim3 cols((c.H + kColThreads - 1) / kColThreads, 2);
   block_bwd_columns<<<cols, dim3(kColThreads, kColRows), 0, s>>>(ca);
