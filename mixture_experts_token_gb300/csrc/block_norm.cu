@@ -409,15 +409,13 @@ cudaError_t launch_stream(const FwdArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int threads = ((a.n16 + NV - 1) / NV + 31) / 32 * 32;
   const int bytes = kQueue * threads * NV * 16;
-  auto* kernel = block_fwd_stream<T, NV, MAXT, MODE, FULL>;
+  constexpr auto kernel = block_fwd_stream<T, NV, MAXT, MODE, FULL>;
   int per_sm = 0;
-  if ((e = cudaFuncSetAttribute(kernel,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                bytes)) != cudaSuccess ||
-      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-           &per_sm, kernel, threads, bytes)) != cudaSuccess)
+  if ((e = launch::allow_shared<kernel>(d)) != cudaSuccess ||
+      (e = launch::ctas_per_sm<kernel>(d, threads, bytes, &per_sm)) !=
+          cudaSuccess)
     return e;
-  kernel<<<std::min(a.T, std::max(per_sm, 1) * d.sms), threads, bytes, s>>>(a);
+  kernel<<<std::min(a.T, per_sm * d.sms), threads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "launch.cuh"
 
 namespace moe {
 namespace block {
@@ -101,6 +102,11 @@ __device__ __forceinline__ int4 read16(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void zero16(uint32_t a) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0)
+               : "memory");
+}
+
 // N float column values that belong to the row's word c.
 template <int N>
 __device__ __forceinline__ void load_weight(const float* p, int c, bool vec,
@@ -150,23 +156,25 @@ __device__ __forceinline__ void columns_or(const float* p, int c, bool in,
   }
 }
 
-// ------------------------------------------------------------- host ------
-struct Device {
-  int sms = 0, smem_sm = 0, smem_cta = 0;
-};
-inline cudaError_t device(Device* d) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(
-        &d->smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&d->smem_cta,
-                               cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  return e;
+// The same over the `threads` (a multiple of 32) consecutive threads of
+// group `group` of the CTA; `red` has a place for each warp of the CTA.
+__device__ __forceinline__ float group_sum(float s, float* red, int group,
+                                           int threads) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (threads == 32) return s;
+  const int lane = threadIdx.x & 31, warps = threads >> 5;
+  if (lane == 0) red[threadIdx.x >> 5] = s;
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+  s = lane < warps ? red[group * warps + lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
+
+// ------------------------------------------------------------- host ------
+using launch::Device;
+using launch::device;
 inline int row_words(const moe_config_t& c) {
   return static_cast<int>(static_cast<int64_t>(c.H) * elem_bytes(c.dtype) /
                           16);

@@ -38,25 +38,21 @@ struct BwdArgs {
   bool vec_w;
 };
 
+// Rows wider than the streamed form holds: one row per CTA, in registers.
 // POST: the branch's end is part of it; else only the norm of v.
-template <typename T, int NV, bool WARP, int MAXT, bool POST>
+template <typename T, int NV, int MAXT, bool POST>
 __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
   using V = Vec<T>;
   constexpr int N = V::N;
   __shared__ float red[2][32];
-  __shared__ float cols[WARP ? 32 * NV * N : 1];
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int step = WARP ? 32 : blockDim.x;
-  const int first = WARP ? blockIdx.x * kRowWarps + (threadIdx.x >> 5)
-                         : blockIdx.x;
-  const int rows = WARP ? gridDim.x * kRowWarps : gridDim.x;
+  const int tid = threadIdx.x, step = blockDim.x;
   float sum_post[NV][N], sum_next[NV][N];
 #pragma unroll
   for (int u = 0; u < NV; ++u)
 #pragma unroll
     for (int i = 0; i < N; ++i) sum_post[u][i] = sum_next[u][i] = 0.0f;
 
-  for (int t = first; t < a.T; t += rows) {
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const long long base = static_cast<long long>(t) * a.n16;
     int4 v[NV], dh[NV], go[NV], y[NV];
     float d[NV][N];
@@ -97,7 +93,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
           s = fmaf(d[u][i], vh, s);
         }
       }
-      s = row_sum<WARP>(s, red[0]) * a.inv_h;
+      s = row_sum<false>(s, red[0]) * a.inv_h;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         float fv[N], g[N];
@@ -169,7 +165,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
       }
     }
     if (post || token) {
-      s = row_sum<WARP>(s, red[1]);
+      s = row_sum<false>(s, red[1]);
       if (token && tid == 0) static_cast<float*>(a.dgate)[t] = s;
       s = post ? s * a.inv_h : 0.0f;
     }
@@ -186,157 +182,149 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
     }
   }
 
-  // One partial per CTA: this thread's columns, or, where every warp holds
-  // whole rows, the warps' columns added in warp order.
-  const int H = a.n16 * N;
+  // one partial per CTA
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    float* out = a.parts + (static_cast<long long>(blockIdx.x) * 2 + q) * H;
-    if (WARP) {
-      for (int w = 0; w < kRowWarps; ++w) {
-        if (static_cast<int>(threadIdx.x >> 5) == w) {
+    float* out =
+        a.parts + (static_cast<long long>(blockIdx.x) * 2 + q) * a.n16 * N;
 #pragma unroll
-          for (int u = 0; u < NV; ++u)
+    for (int u = 0; u < NV; ++u) {
+      const int c = tid + u * step;
+      if (c >= a.n16) continue;
+      const float(&f)[N] = q == 0 ? sum_post[u] : sum_next[u];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int at = (tid + u * step) * N + i;
-              const float add = q == 0 ? sum_post[u][i] : sum_next[u][i];
-              cols[at] = w == 0 ? add : cols[at] + add;
-            }
-        }
-        __syncthreads();
-      }
-      for (int c = threadIdx.x; c < H; c += blockDim.x) out[c] = cols[c];
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        const int c = tid + u * step;
-        if (c >= a.n16) continue;
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-          *reinterpret_cast<float4*>(out + c * N + i) =
-              q == 0 ? make_float4(sum_post[u][i], sum_post[u][i + 1],
-                                   sum_post[u][i + 2], sum_post[u][i + 3])
-                     : make_float4(sum_next[u][i], sum_next[u][i + 1],
-                                   sum_next[u][i + 2], sum_next[u][i + 3]);
-      }
+      for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<float4*>(out + c * N + i) =
+            make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
     }
   }
 }
 
 // ---- rows streamed through shared memory -------------------------------
-// For rows of one CTA whose words fit twice into shared memory: the CTA's
-// next row is on its way while it reduces the current one.  A thread holds
-// word tid of the row (and tid + blockDim.x with NV = 2), copies it to
-// shared memory itself and reads it back where it is needed, so only the
-// column weights, the column sums and dO stay in registers.
-template <typename T, int NV, int MAXT, bool POST, bool FULL>
+// S rows ahead.  A row belongs to a group of `threads` threads, of which a
+// CTA has one or more: thread tid of a group holds word tid of the row (and
+// tid + threads with NV = 2), copies it to shared memory itself and reads it
+// back where it is needed, so only the column weights, the column sums and
+// dO stay in registers.  A word is copied anew, for the row S on, as soon as
+// it has been read for the last time.
+template <typename T, int NV, int MAXT, bool POST, int GATE, int S>
 __global__ void __launch_bounds__(MAXT)
-    block_bwd_stream(const BwdArgs a, int slots) {
+    block_bwd_stream(const BwdArgs a, int threads) {
   using V = Vec<T>;
   constexpr int N = V::N;
+  constexpr bool FULL = GATE == MOE_GATE_FULL;
+  constexpr bool TOKEN = GATE == MOE_GATE_TOKEN;
+  constexpr int W = 3 + POST + FULL;  // groups of copies of a row
   extern __shared__ __align__(16) char queue[];
   __shared__ float red[2][32];
-  const int tid = threadIdx.x, step = blockDim.x;
+  const int group = threadIdx.x / threads, tid = threadIdx.x % threads;
+  const int groups = blockDim.x / threads;
+  const int t0 = blockIdx.x * groups + group, t_step = gridDim.x * groups;
   const bool next = a.dh != nullptr;
   const bool post = POST && a.w_post != nullptr;
-  const bool token = POST && !FULL && a.gate_kind == MOE_GATE_TOKEN;
   const bool in = tid < a.n16;
   const auto held = [&](int u) {
-    return NV == 1 ? in : tid + u * step < a.n16;
+    return NV == 1 ? in : tid + u * threads < a.n16;
   };
-  const long long row_step = static_cast<long long>(gridDim.x) * a.n16;
-  const long long at0 = static_cast<long long>(blockIdx.x) * a.n16 + tid;
+  const long long row_step = static_cast<long long>(t_step) * a.n16;
+  long long base = static_cast<long long>(t0) * a.n16 + tid;
   // a row's words in shared memory, in this order; absent ones have no room
-  const uint32_t word_bytes = step * NV * 16;
-  const uint32_t at_dh = word_bytes, at_go = next ? 2 * word_bytes : 0;
-  const uint32_t at_y = at_go + (a.dout ? word_bytes : 0);
-  const uint32_t at_g = at_y + word_bytes;
-  const uint32_t row_bytes = at_y + (POST ? word_bytes : 0) +
-                             (FULL ? word_bytes : 0);
-  const uint32_t first = shared_address(queue) + tid * 16;
-  const uint32_t last = first + (slots - 1) * row_bytes;
-
-  long long copy_at = at0;
-  int copy_row = blockIdx.x;
-  uint32_t dst = first;
-  const auto copy = [&] {  // a row
-    if (copy_row < a.T) {
+  const uint32_t word = threads * NV * 16;
+  const uint32_t at_v = word, at_go = next ? 2 * word : 0;
+  const uint32_t at_y = at_go + (a.dout ? word : 0);
+  const uint32_t at_g = at_y + word;
+  const uint32_t row_bytes =
+      at_y + (POST ? word : 0) + (FULL ? word : 0);
+  const uint32_t first =
+      shared_address(queue) + group * S * row_bytes + tid * 16;
+  const uint32_t last = first + (S - 1) * row_bytes;
+  const int4* gate = static_cast<const int4*>(a.gate);
+  const auto copy = [&](const int4* p, long long at, uint32_t dst) {
 #pragma unroll
-      for (int u = 0; u < NV; ++u)
-        if (held(u)) {
-          const long long at = copy_at + u * step;
-          const uint32_t d = dst + u * step * 16;
-          if (next) {
-            copy16(d, a.v + at);
-            copy16(d + at_dh, a.dh + at);
-          }
-          if (a.dout) copy16(d + at_go, a.dout + at);
-          if (POST) copy16(d + at_y, a.y + at);
-          if (FULL) copy16(d + at_g, static_cast<const int4*>(a.gate) + at);
-        }
-      copy_row += gridDim.x;
-      copy_at += row_step;
-    }
-    copies_commit();
-    dst = dst == last ? first : dst + row_bytes;
+    for (int u = 0; u < NV; ++u)
+      if (held(u)) copy16(dst + u * threads * 16, p + at + u * threads);
   };
-  // per-row numbers of the next row, loaded a row ahead
+  // places past the row's end stay zero
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    if (!held(u))
+      for (uint32_t p = 0; p < S * row_bytes; p += word)
+        zero16(first + p + u * threads * 16);
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const bool on = t0 + static_cast<long long>(i) * t_step < a.T;
+    const long long at = base + i * row_step;
+    const uint32_t dst = first + i * row_bytes;
+    if (on && next) copy(a.dh, at, dst);
+    copies_commit();
+    if (on && next) copy(a.v, at, dst + at_v);
+    copies_commit();
+    if (on && a.dout) copy(a.dout, at, dst + at_go);
+    copies_commit();
+    if (POST) {
+      if (on) copy(a.y, at, dst + at_y);
+      copies_commit();
+    }
+    if (FULL) {
+      if (on) copy(gate, at, dst + at_g);
+      copies_commit();
+    }
+  }
+  // per-row numbers, loaded a row ahead
   const float* gates = static_cast<const float*>(a.gate);
   float rv = 0.0f, ry = 1.0f, gt = 1.0f;
   const auto load_row = [&](long long t) {
     if (t >= a.T) return;
     if (next) rv = a.rstd_v[t];
     if (post) ry = a.rstd_y[t];
-    if (token) gt = gates[t];
+    if (TOKEN) gt = gates[t];
   };
-  load_row(blockIdx.x);
-#pragma unroll 1
-  for (int i = 0; i < slots; ++i) copy();
+  load_row(t0);
 
-  float wn[NV][N], wp[NV][N], wg[NV][N];
+  // w' of the next norm, and of the post norm (times a channel's gate)
+  float wn[NV][N], wp[NV][N];
   float sum_post[NV][N], sum_next[NV][N];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
-    const int c = tid + u * step;
+    const int c = tid + u * threads;
     columns_or<N>(next ? a.w_next : nullptr, c, c < a.n16, a.vec_w, 0.0f,
                   wn[u]);
     if (POST) {
       columns_or<N>(a.w_post, c, c < a.n16, a.vec_w, 1.0f, wp[u]);
-      columns_or<N>(a.gate_kind == MOE_GATE_CHANNEL ? gates : nullptr, c,
-                    c < a.n16, a.vec_w, 1.0f, wg[u]);
+      float g[N];
+      columns_or<N>(GATE == MOE_GATE_CHANNEL ? gates : nullptr, c, c < a.n16,
+                    a.vec_w, 1.0f, g);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        wp[u][i] = g[i] * (post ? wp[u][i] + a.w_offset : 1.0f);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       wn[u][i] += a.w_offset;
-      if (post) wp[u][i] += a.w_offset;
       sum_post[u][i] = sum_next[u][i] = 0.0f;
     }
   }
   const auto load = [&](uint32_t p, int u, float (&f)[N]) {
-    V::load(held(u) ? read16(p + u * step * 16) : make_int4(0, 0, 0, 0), f);
+    V::load(read16(p + u * threads * 16), f);
   };
   uint32_t src = first;
-  long long base = at0;
   int sums = 0;  // row sums so far: they alternate between two buffers
 #pragma unroll 1
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    if (slots == 2)
-      copies_wait<1>();
-    else
-      copies_wait<2>();
+  for (int t = t0; t < a.T; t += t_step) {
     const float r_v = rv, r_y = ry, g_t = gt;
-    load_row(static_cast<long long>(t) + gridDim.x);
+    load_row(static_cast<long long>(t) + t_step);
+    const bool more = static_cast<long long>(t) + S * t_step < a.T;
+    const long long ahead = base + S * row_step;
     float d[NV][N];
+    copies_wait<S * W - 2>();  // dh and v
     if (next) {
       // dO = dout + rstd (dh w' - vh mean(dh w' vh))
       float s = 0.0f;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         float v[N];
-        load(src, u, v);
-        load(src + at_dh, u, d[u]);
+        load(src + at_v, u, v);
+        load(src, u, d[u]);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float vh = v[i] * r_v;
@@ -345,16 +333,24 @@ __global__ void __launch_bounds__(MAXT)
           s = fmaf(d[u][i], vh, s);
         }
       }
-      s = row_sum<false>(s, red[sums++ & 1]) * a.inv_h * r_v * r_v;
+      if (more) copy(a.dh, ahead, src);
+      copies_commit();
+      s = group_sum(s, red[sums++ & 1], group, threads) * a.inv_h * r_v * r_v;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         float v[N];
-        load(src, u, v);
+        load(src + at_v, u, v);
 #pragma unroll
         for (int i = 0; i < N; ++i)
           d[u][i] = fmaf(r_v, d[u][i], -(v[i] * s));
       }
+      if (more) copy(a.v, ahead, src + at_v);
+      copies_commit();
+    } else {
+      copies_commit();
+      copies_commit();
     }
+    copies_wait<S * W - 1>();  // dout
     if (a.dout) {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
@@ -363,18 +359,21 @@ __global__ void __launch_bounds__(MAXT)
 #pragma unroll
         for (int i = 0; i < N; ++i) d[u][i] = next ? d[u][i] + g[i] : g[i];
       }
+      if (more) copy(a.dout, ahead, src + at_go);
     }
+    copies_commit();
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float f[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) f[i] = a.res_scale * d[u][i];
-      if (held(u)) store_stream(a.dx + base + u * step, V::store(f));
+      if (held(u)) store_stream(a.dx + base + u * threads, V::store(f));
     }
     if (POST) {
       // The branch.  A per-token gate multiplies whole rows, so it stays
       // out of the row sum, which is then that gate's gradient; a
       // per-channel gate multiplies its column sum once, at the end.
+      copies_wait<S * W - (FULL ? 2 : 1)>();  // y (and the gate)
       float s = 0.0f;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
@@ -393,21 +392,22 @@ __global__ void __launch_bounds__(MAXT)
             s = fmaf(d[u][i], y[i], s);
           }
           if (held(u))
-            store_stream(static_cast<int4*>(a.dgate) + base + u * step,
+            store_stream(static_cast<int4*>(a.dgate) + base + u * threads,
                          V::store(dg));
         } else {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             y[i] *= r_y;
-            sum_post[u][i] = fmaf(g_t * d[u][i], y[i], sum_post[u][i]);
-            d[u][i] *= wg[u][i] * wp[u][i];
+            sum_post[u][i] = fmaf(TOKEN ? g_t * d[u][i] : d[u][i], y[i],
+                                  sum_post[u][i]);
+            d[u][i] *= wp[u][i];
             s = fmaf(d[u][i], y[i], s);
           }
         }
       }
-      if (post || token) {
-        s = row_sum<false>(s, red[sums++ & 1]);
-        if (token && tid == 0) static_cast<float*>(a.dgate)[t] = s;
+      if (post || TOKEN) {
+        s = group_sum(s, red[sums++ & 1], group, threads);
+        if (TOKEN && tid == 0) static_cast<float*>(a.dgate)[t] = s;
         s = post ? s * a.inv_h * r_y : 0.0f;
       }
       const float scale = g_t * r_y;
@@ -418,26 +418,47 @@ __global__ void __launch_bounds__(MAXT)
 #pragma unroll
         for (int i = 0; i < N; ++i)
           d[u][i] = scale * (d[u][i] - (post ? y[i] * s : 0.0f));
-        if (held(u)) store_stream(a.dy + base + u * step, V::store(d[u]));
+        if (held(u)) store_stream(a.dy + base + u * threads, V::store(d[u]));
+      }
+      if (more) copy(a.y, ahead, src + at_y);
+      copies_commit();
+      if (FULL) {
+        if (more) copy(gate, ahead, src + at_g);
+        copies_commit();
       }
     }
-    copy();  // into the slot that this thread has read
     src = src == last ? first : src + row_bytes;
     base += row_step;
   }
   copies_wait<0>();
+
+  launch::let_next_start();
+  // One partial per CTA: this thread's columns, or the groups' added in
+  // group order.
+  float* cols = reinterpret_cast<float*>(queue);
+  const int H = a.n16 * N;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    float* out = a.parts +
-                 (static_cast<long long>(blockIdx.x) * 2 + q) * a.n16 * N;
+    float* out = a.parts + (static_cast<long long>(blockIdx.x) * 2 + q) * H;
+    for (int g = 0; g < groups; ++g) {
+      if (groups > 1) __syncthreads();
+      if (g != group) continue;
+      float* to = g == groups - 1 ? out : cols;
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const float(&f)[N] = q == 0 ? sum_post[u] : sum_next[u];
-      if (held(u))
+      for (int u = 0; u < NV; ++u) {
+        const float(&f)[N] = q == 0 ? sum_post[u] : sum_next[u];
+        const int c = (tid + u * threads) * N;
+        if (!held(u)) continue;
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-          *reinterpret_cast<float4*>(out + (tid + u * step) * N + i) =
-              make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        for (int i = 0; i < N; i += 4) {
+          float4 v = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+          if (g > 0) {
+            const float4 w = *reinterpret_cast<const float4*>(cols + c + i);
+            v = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
+          }
+          *reinterpret_cast<float4*>(to + c + i) = v;
+        }
+      }
     }
   }
 }
@@ -451,7 +472,7 @@ struct ColArgs {
 };
 
 constexpr int kColThreads = 32;  // columns of a CTA
-constexpr int kColRows = 8;      // partials added side by side
+constexpr int kColRows = 16;     // partials added side by side
 
 // Adds the CTAs' partials: blockIdx.y 0 the branch's column sums, 1 the next
 // norm's.
@@ -460,10 +481,11 @@ __global__ void __launch_bounds__(kColThreads* kColRows)
   __shared__ float part[kColRows][kColThreads];
   const int c = blockIdx.x * kColThreads + threadIdx.x;
   const int q = blockIdx.y;
+  launch::wait_for_previous();
   float s = 0.0f;
   if (c < a.H) {
     const float* p = a.parts + static_cast<long long>(q) * a.H + c;
-#pragma unroll 4
+#pragma unroll 10
     for (int i = threadIdx.y; i < a.n_parts; i += kColRows)
       s += p[static_cast<long long>(i) * 2 * a.H];
   }
@@ -488,84 +510,86 @@ __global__ void __launch_bounds__(kColThreads* kColRows)
 constexpr int kMaxParts = 304;
 
 int parts_of(const moe_config_t& c) {
-  const int n = row_words(c) <= 128 ? (c.T + kRowWarps - 1) / kRowWarps : c.T;
-  return std::max(1, std::min(n, kMaxParts));
-}
-
-template <typename T, int NV, bool WARP, int MAXT>
-cudaError_t launch_post(const BwdArgs& a, bool post, int grid, int threads,
-                        cudaStream_t s) {
-  if (post)
-    block_bwd_kernel<T, NV, WARP, MAXT, true><<<grid, threads, 0, s>>>(a);
-  else
-    block_bwd_kernel<T, NV, WARP, MAXT, false><<<grid, threads, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-// The streamed form with as many CTAs as fit, at most `parts`; returns their
-// number in *grid, or 0 where two rows do not fit.
-template <typename T, int NV, int MAXT, bool POST, bool FULL>
-cudaError_t launch_stream(const BwdArgs& a, int parts, int* grid,
-                          cudaStream_t s) {
-  Device d;
-  cudaError_t e = device(&d);
-  if (e != cudaSuccess) return e;
-  const int threads = ((a.n16 + NV - 1) / NV + 31) / 32 * 32;
-  const int words = (a.dh ? 2 : 0) + (a.dout ? 1 : 0) + POST + FULL;
-  const int row = words * threads * NV * 16;
-  auto* kernel = block_bwd_stream<T, NV, MAXT, POST, FULL>;
-  const int slots = 3 * row <= d.smem_cta / 2 ? 3 : 2;
-  int per_sm = 0;
-  *grid = 0;
-  if (slots * row + 1024 > d.smem_cta) return cudaSuccess;
-  if ((e = cudaFuncSetAttribute(kernel,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                slots * row)) != cudaSuccess ||
-      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-           &per_sm, kernel, threads, slots * row)) != cudaSuccess)
-    return e;
-  *grid = std::min(parts, std::max(per_sm, 1) * d.sms);
-  kernel<<<*grid, threads, slots * row, s>>>(a, slots);
-  return cudaGetLastError();
+  return std::max(1, std::min(c.T, kMaxParts));
 }
 
 template <typename T, int NV, int MAXT>
+cudaError_t launch_post(const BwdArgs& a, bool post, int grid, int threads,
+                        cudaStream_t s) {
+  if (post)
+    block_bwd_kernel<T, NV, MAXT, true><<<grid, threads, 0, s>>>(a);
+  else
+    block_bwd_kernel<T, NV, MAXT, false><<<grid, threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// CTAs of the streamed form: `groups` groups of `threads` threads, as many
+// CTAs as fit and at most `parts`; returns their number in *grid, or 0 where
+// the rows do not fit.
+template <typename T, int NV, int MAXT, bool POST, int GATE, int S>
+cudaError_t launch_stream(const BwdArgs& a, int parts, int threads,
+                          int groups, const Device& d, int* grid,
+                          cudaStream_t s) {
+  const int words = (a.dh ? 2 : 0) + (a.dout ? 1 : 0) + POST +
+                    (GATE == MOE_GATE_FULL);
+  const int bytes = groups * S * words * threads * NV * 16;
+  *grid = 0;
+  if (bytes + 1024 > d.smem_cta) return cudaSuccess;
+  constexpr auto kernel = block_bwd_stream<T, NV, MAXT, POST, GATE, S>;
+  int per_sm = 0;
+  cudaError_t e = launch::allow_shared<kernel>(d);
+  if (e == cudaSuccess)
+    e = launch::ctas_per_sm<kernel>(d, threads * groups, bytes, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int rows = (a.T + groups - 1) / groups;
+  *grid = std::max(1, std::min({parts, rows, per_sm * d.sms}));
+  kernel<<<*grid, threads * groups, bytes, s>>>(a, threads);
+  return cudaGetLastError();
+}
+
+template <typename T, int NV, int MAXT, int S>
 cudaError_t launch_stream_post(const BwdArgs& a, bool post, int parts,
                                int* grid, cudaStream_t s) {
+  Device d;
+  const cudaError_t e = device(&d);
+  if (e != cudaSuccess) return e;
+  const int threads = ((a.n16 + NV - 1) / NV + 31) / 32 * 32;
+  // groups that make a CTA of about 512 threads (a barrier for each)
+  const int groups = std::max(1, std::min(8, 512 / threads));
   if (!post)
-    return launch_stream<T, NV, MAXT, false, false>(a, parts, grid, s);
-  if (a.gate_kind == MOE_GATE_FULL)
-    return launch_stream<T, NV, MAXT, true, true>(a, parts, grid, s);
-  return launch_stream<T, NV, MAXT, true, false>(a, parts, grid, s);
+    return launch_stream<T, NV, MAXT, false, MOE_GATE_NONE, S>(
+        a, parts, threads, groups, d, grid, s);
+#define MOE_GATE_CASE(GATE)                                                 \
+  if (a.gate_kind == GATE)                                                  \
+  return launch_stream<T, NV, MAXT, true, GATE, S>(a, parts, threads,       \
+                                                   groups, d, grid, s)
+  MOE_GATE_CASE(MOE_GATE_NONE);
+  MOE_GATE_CASE(MOE_GATE_TOKEN);
+  MOE_GATE_CASE(MOE_GATE_CHANNEL);
+  MOE_GATE_CASE(MOE_GATE_FULL);
+#undef MOE_GATE_CASE
+  return cudaErrorInvalidValue;
 }
 
 // At most `parts` CTAs; *grid receives how many partials there are.
 template <typename T>
-cudaError_t launch_rows(const BwdArgs& a, bool post, int parts, int* grid_out,
+cudaError_t launch_rows(const BwdArgs& a, bool post, int parts, int* grid,
                         cudaStream_t s) {
-  const int grid = *grid_out = parts;
-  constexpr int W = kRowWarps * 32;
-  if (a.n16 <= 32) return launch_post<T, 1, true, W>(a, post, grid, W, s);
-  if (a.n16 <= 64) return launch_post<T, 2, true, W>(a, post, grid, W, s);
-  if (a.n16 <= 128) return launch_post<T, 4, true, W>(a, post, grid, W, s);
-  const auto threads = [&](int nv) {
-    return ((a.n16 + nv - 1) / nv + 31) / 32 * 32;
-  };
   cudaError_t e = cudaSuccess;
-  int streamed = 0;
+  *grid = 0;
   if (a.n16 <= 512)
-    e = launch_stream_post<T, 1, 512>(a, post, parts, &streamed, s);
-  else if (a.n16 <= 896)
-    e = launch_stream_post<T, 1, 896>(a, post, parts, &streamed, s);
-  else if (a.n16 <= 1280)
-    e = launch_stream_post<T, 2, 640>(a, post, parts, &streamed, s);
-  if (e != cudaSuccess || streamed > 0) {
-    *grid_out = streamed;
-    return e;
-  }
+    e = launch_stream_post<T, 1, 512, 3>(a, post, parts, grid, s);
+  else if (a.n16 <= 1024)
+    e = launch_stream_post<T, 2, 512, 3>(a, post, parts, grid, s);
+  if (e != cudaSuccess || *grid > 0) return e;
+  if (a.n16 <= 1280)
+    e = launch_stream_post<T, 2, 640, 2>(a, post, parts, grid, s);
+  if (e != cudaSuccess || *grid > 0) return e;
+  *grid = parts;
+  const int threads = (a.n16 + 127) / 128 * 32;
   if (a.n16 <= 2048)
-    return launch_post<T, 4, false, 512>(a, post, grid, threads(4), s);
-  return launch_post<T, 4, false, 1024>(a, post, grid, threads(4), s);
+    return launch_post<T, 4, 512>(a, post, parts, threads, s);
+  return launch_post<T, 4, 1024>(a, post, parts, threads, s);
 }
 
 moe_status_t run(const moe_config_t& c, BwdArgs a, ColArgs ca, bool post,
@@ -585,8 +609,11 @@ moe_status_t run(const moe_config_t& c, BwdArgs a, ColArgs ca, bool post,
           : launch_rows<__nv_bfloat16>(a, post, parts, &ca.n_parts, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   const dim3 cols((c.H + kColThreads - 1) / kColThreads, 2);
-  block_bwd_columns<<<cols, dim3(kColThreads, kColRows), 0, s>>>(ca);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch::overlapping(block_bwd_columns, cols,
+                             dim3(kColThreads, kColRows), 0, s,
+                             ca) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 moe_status_t check(const moe_config_t* cfg, const moe_block_norm_t* opt,

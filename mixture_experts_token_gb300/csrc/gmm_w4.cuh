@@ -35,10 +35,13 @@
 
 #include <algorithm>
 
+#include "launch.cuh"
 #include "w4.cuh"
 
 namespace moe {
 namespace w4 {
+
+using launch::Device;
 
 // Products of one row type (gmm_w4_bf16.cu, gmm_w4_f32.cu): dual is gate_up.
 struct GmmArgs;
@@ -598,20 +601,6 @@ __global__ void __launch_bounds__(
   Kernel<T, DUAL, NW, KW, NT, G, Z>::run(a);
 }
 
-struct Device {
-  int sms = 0, smem = 0;
-};
-inline cudaError_t device(Device* d) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(
-        &d->smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-  return e;
-}
-
 template <typename T, bool DUAL, int NW, int KW, int NT, int G, bool Z>
 cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
                        cudaStream_t s) {
@@ -620,15 +609,14 @@ cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
   // eight warps' k fill shared memory at half the rows
   a.x_rows = std::max(1, std::min(Ker::kRows, tokens));
   int bytes = Ker::smem(a.x_rows, a.n_groups).total;
-  while (bytes + 1024 > d.smem && a.x_rows > 1) {
+  while (bytes + 1024 > d.smem_sm && a.x_rows > 1) {
     a.x_rows /= 2;
     bytes = Ker::smem(a.x_rows, a.n_groups).total;
   }
-  auto* kernel = gmm_w4_kernel<T, DUAL, NW, KW, NT, G, Z>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr auto kernel = gmm_w4_kernel<T, DUAL, NW, KW, NT, G, Z>;
+  const cudaError_t e = launch::allow_shared<kernel>(d);
   if (e != cudaSuccess) return e;
-  const int per_sm = std::min(Ker::kPerSm, d.smem / (bytes + 1024));
+  const int per_sm = std::min(Ker::kPerSm, d.smem_sm / (bytes + 1024));
   const long long items =
       static_cast<long long>((a.l.N + Ker::kCols - 1) / Ker::kCols) *
       std::min(a.n_groups, a.rows);
@@ -641,7 +629,7 @@ cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
 template <typename T, bool DUAL, int G, bool Z>
 cudaError_t launch_shape(const GmmArgs& a, int tokens, cudaStream_t s) {
   Device d;
-  const cudaError_t e = device(&d);
+  const cudaError_t e = launch::device(&d);
   if (e != cudaSuccess) return e;
   const long long groups = std::min(a.n_groups, a.rows);
   const long long items =
