@@ -179,10 +179,18 @@ cudaError_t launch_mode(const FwdArgs& a, int mode, int threads,
 // weights in registers (read once) and the rows' words in a queue in shared
 // memory that runs kQueue words ahead, across rows: a row's reductions leave
 // memory no pause.  A thread holds word tid of the row (and tid + blockDim.x
-// with NV = 2).  A row is, in queue order, y (or its k expert rows), x, and
+// with NV = 2, which halves the instructions of the reductions where a row
+// has over 512 words: 7168 bf16 columns and one expert 113 -> 81 us).  A row is, in queue order, y (or its k expert rows), x, and
 // a full gate.
 constexpr int kQueue = 8;
-constexpr int kTable = 16;  // rows whose routing is held, kQueue ahead
+// Where the words of the coming rows are, for the combine: a ring of rows
+// whose entries are a word's address and its weight.
+struct Entry {
+  const int4* src;  // null: nothing to copy
+  float weight;
+};
+constexpr int kEntries = 144;  // four rows of 32 experts, x and a gate
+constexpr int kMaxAhead = 12;  // rows that the ring runs ahead
 
 template <typename T, int NV, int MAXT, int MODE, bool FULL>
 __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
   constexpr int N = V::N;
   extern __shared__ __align__(16) char queue[];
   __shared__ float red[2][32];
-  __shared__ int2 table[MODE == kCombineOut ? kTable * kMaxTopK : 1];
+  __shared__ Entry table[MODE == kCombineOut ? kEntries : 1];
   const int tid = threadIdx.x, step = blockDim.x;
   const long long row_step = static_cast<long long>(gridDim.x) * a.n16;
   const uint32_t word_bytes = step * NV * 16;
@@ -201,21 +209,34 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
     return NV == 1 ? in : tid + u * step < a.n16;
   };
 
-  // routing of the i-th row of this CTA: (row, weight) of slot tid
-  const auto load_route = [&](int i) {
+  constexpr int kTail = 1 + (FULL ? 1 : 0);  // words after y
+  const int ys = MODE == kNormOnly ? 0 : MODE == kOut ? 1 : a.k;
+  const int words = ys + kTail;
+  const int held_rows = min(kMaxAhead + 1, kEntries / words);
+  const int ahead = held_rows - 1;
+  // entry tid of the i-th row of this CTA
+  const auto load_entry = [&](int i) {
     const long long t = blockIdx.x + static_cast<long long>(i) * gridDim.x;
-    return tid < a.k && t < a.T
-               ? make_int2(a.row_of[t * a.k + tid],
-                           __float_as_int(a.topk_w[t * a.k + tid]))
-               : make_int2(-1, 0);
+    Entry e = {nullptr, 0.0f};
+    if (tid < words && t < a.T) {
+      if (tid < ys) {
+        const int r = a.row_of[t * a.k + tid];
+        e.weight = a.topk_w[t * a.k + tid];
+        if (r >= 0) e.src = a.y_sorted + static_cast<long long>(r) * a.n16;
+      } else {
+        e.src = (tid == ys ? a.x : static_cast<const int4*>(a.gate)) +
+                t * a.n16;
+      }
+    }
+    return e;
   };
-  const auto keep_route = [&](int i, int2 v) {
-    if (tid < a.k) table[i % kTable * kMaxTopK + tid] = v;
+  const auto keep_entry = [&](int i, const Entry& e) {
+    if (tid < words) table[i % held_rows * words + tid] = e;
   };
-  int2 routed = make_int2(-1, 0);  // of row i + kTable - 2, loaded a row ago
+  Entry entry = {nullptr, 0.0f};  // of row i + ahead, loaded a row ago
   if (MODE == kCombineOut) {
-    for (int i = 0; i < kTable - 2; ++i) keep_route(i, load_route(i));
-    routed = load_route(kTable - 2);
+    for (int i = 0; i < ahead; ++i) keep_entry(i, load_entry(i));
+    entry = load_entry(ahead);
     __syncthreads();
   }
   const bool token = MODE != kNormOnly && !FULL &&
@@ -228,36 +249,28 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
   const int4* xp = a.x + at0;
   const int4* yp = MODE == kOut ? a.y + at0 : nullptr;
   const int4* gp = FULL ? static_cast<const int4*>(a.gate) + at0 : nullptr;
-  int copy_row = blockIdx.x, copy_word = 0, copy_at = 0;  // copy_at: in table
+  int copy_row = blockIdx.x, copy_word = 0;  // or the entry in the table
   uint32_t dst = first;
-  constexpr int kTail = 1 + (FULL ? 1 : 0);  // words after y
-  const int ys = MODE == kNormOnly ? 0 : MODE == kOut ? 1 : a.k;
-  const auto copy = [&] {
-    if (copy_row < a.T) {
-      const int4* src;
-      if (MODE != kNormOnly && copy_word < ys) {
-        if (MODE == kOut) {
-          src = yp;
-        } else {
-          const int r = table[copy_at + copy_word].x;
-          src = r < 0 ? nullptr
-                      : a.y_sorted + static_cast<long long>(r) * a.n16 + tid;
-        }
-      } else {
-        src = !FULL || copy_word == ys ? xp : gp;
-      }
-      if (MODE != kCombineOut || src != nullptr)
+  const auto copy_from = [&](const int4* src) {
 #pragma unroll
-        for (int u = 0; u < NV; ++u)
-          if (held(u)) copy16(dst + u * step * 16, src + u * step);
+    for (int u = 0; u < NV; ++u)
+      if (held(u)) copy16(dst + u * step * 16, src + u * step);
+  };
+  const auto copy = [&] {
+    if (MODE == kCombineOut) {
+      const int4* src = table[copy_word].src;
+      if (src != nullptr) copy_from(src + tid);
+      if (++copy_word == held_rows * words) copy_word = 0;
+    } else if (copy_row < a.T) {
+      copy_from(MODE == kOut && copy_word == 0 ? yp
+                : !FULL || copy_word == ys     ? xp
+                                               : gp);
       if (++copy_word == ys + kTail) {
         copy_word = 0;
         copy_row += gridDim.x;
         xp += row_step;
         if (MODE == kOut) yp += row_step;
         if (FULL) gp += row_step;
-        if (MODE == kCombineOut)
-          copy_at = (copy_at + kMaxTopK) % (kTable * kMaxTopK);
       }
     }
     copies_commit();
@@ -276,21 +289,22 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
 #pragma unroll 1
   for (int i = 0; i < kQueue; ++i) copy();
 
-  float wp[NV][N], wn[NV][N], wg[NV][N];
+  // w' of the post norm (times a channel's gate) and of the next norm
+  float wp[NV][N], wn[NV][N];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int c = tid + u * step;
+    float wg[N];
     if (MODE != kNormOnly) {
       columns_or<N>(a.w_post, c, c < a.n16, a.vec_w, 1.0f, wp[u]);
-      columns_or<N>(a.gate_kind == MOE_GATE_CHANNEL
-                        ? static_cast<const float*>(a.gate)
-                        : nullptr,
-                    c, c < a.n16, a.vec_w, 1.0f, wg[u]);
+      columns_or<N>(a.gate_kind == MOE_GATE_CHANNEL ? gates : nullptr, c,
+                    c < a.n16, a.vec_w, 1.0f, wg);
     }
     columns_or<N>(a.w_next, c, c < a.n16, a.vec_w, 0.0f, wn[u]);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (MODE != kNormOnly && a.w_post) wp[u][i] += a.w_offset;
+      if (MODE != kNormOnly)
+        wp[u][i] = wg[i] * (a.w_post ? wp[u][i] + a.w_offset : 1.0f);
       wn[u][i] += a.w_offset;
     }
   }
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
     return rsqrtf(row_sum<false>(s, red[sums++ & 1]) * a.inv_h + a.eps);
   };
   long long base = at0;
-  int at = 0;  // the row's place in the table
+  int at = 0;  // the row's first entry in the table
 #pragma unroll 1
   for (int t = blockIdx.x, i = 0; t < a.T; t += gridDim.x, ++i) {
     float f[NV][N];  // the row that is stored, and the next norm reads
@@ -325,16 +339,16 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
           for (int n = 0; n < N; ++n) y[u][n] = 0.0f;
 #pragma unroll 1
         for (int j = 0; j < a.k; ++j) {
-          const int2 rw = table[at + j];
+          const Entry e_j = table[at + j];
           next(q);
-          if (rw.x < 0) continue;
+          if (e_j.src == nullptr) continue;
 #pragma unroll
           for (int u = 0; u < NV; ++u) {
             float e[N];
             V::load(q[u], e);
 #pragma unroll
             for (int n = 0; n < N; ++n)
-              y[u][n] = fmaf(__int_as_float(rw.y), e[n], y[u][n]);
+              y[u][n] = fmaf(e_j.weight, e[n], y[u][n]);
           }
         }
 #pragma unroll
@@ -343,7 +357,6 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
           if (held(u) && a.y_out)
             store_stream(a.y_out + base + u * step, q[u]);
         }
-        at = (at + kMaxTopK) % (kTable * kMaxTopK);
       }
 #pragma unroll
       for (int u = 0; u < NV; ++u) V::load(q[u], y[u]);
@@ -353,12 +366,9 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
         if (tid == 0 && a.rstd_y) a.rstd_y[t] = r;
       }
       if (token) {
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-#pragma unroll
-          for (int n = 0; n < N; ++n) wg[u][n] = gate;
-        const long long ahead = static_cast<long long>(t) + gridDim.x;
-        if (ahead < a.T) gate = gates[ahead];
+        r *= gate;
+        const long long later = static_cast<long long>(t) + gridDim.x;
+        if (later < a.T) gate = gates[later];
       }
       next(q);
 #pragma unroll
@@ -366,14 +376,18 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
       if (FULL) {
         next(q);
 #pragma unroll
-        for (int u = 0; u < NV; ++u) V::load(q[u], wg[u]);
+        for (int u = 0; u < NV; ++u) {
+          float g[N];
+          V::load(q[u], g);
+#pragma unroll
+          for (int n = 0; n < N; ++n) y[u][n] *= g[n];
+        }
       }
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          f[u][n] = fmaf(wg[u][n], y[u][n] * (r * wp[u][n]),
-                         a.res_scale * f[u][n]);
+          f[u][n] = fmaf(y[u][n], r * wp[u][n], a.res_scale * f[u][n]);
         const int4 o = V::store(f[u]);
         if (held(u)) store_stream(a.out + base + u * step, o);
         V::load(o, f[u]);
@@ -382,8 +396,9 @@ __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
     // the routing that the queue will need; the row sums' barriers lie
     // between a table row's last reader, its writer and its next reader
     if (MODE == kCombineOut) {
-      keep_route(i + kTable - 2, routed);
-      routed = load_route(i + kTable - 1);
+      keep_entry(i + ahead, entry);
+      entry = load_entry(i + ahead + 1);
+      at = at + words == held_rows * words ? 0 : at + words;
     }
     if (a.w_next) {
       const float r = inverse_rms(f);
@@ -440,7 +455,7 @@ cudaError_t launch_typed(const FwdArgs& a, int mode, cudaStream_t s) {
     return ((a.n16 + nv - 1) / nv + 31) / 32 * 32;
   };
   if (a.n16 <= 512) return launch_stream_mode<T, 1, 512>(a, mode, s);
-  if (a.n16 <= 896) return launch_stream_mode<T, 1, 896>(a, mode, s);
+  if (a.n16 <= 1024) return launch_stream_mode<T, 2, 512>(a, mode, s);
   if (a.n16 <= 1280) return launch_stream_mode<T, 2, 640>(a, mode, s);
   if (a.n16 <= 2048)
     return launch_mode<T, 4, false, 512>(a, mode, threads(4), s);

@@ -472,7 +472,7 @@ struct ColArgs {
 };
 
 constexpr int kColThreads = 32;  // columns of a CTA
-constexpr int kColRows = 16;     // partials added side by side
+constexpr int kColRows = 32;     // partials added side by side
 
 // Adds the CTAs' partials: blockIdx.y 0 the branch's column sums, 1 the next
 // norm's.

@@ -40,8 +40,9 @@ moe_status_t gate_up(const moe_config_t& c, const moe_w4_t& o,
 
 moe_status_t down(const moe_config_t& c, const moe_w4_t& o, const Groups& g,
                   const void* h, const int32_t* offsets, const void* wd,
-                  void* y, int32_t* status, cudaStream_t s) {
+                  void* y, int32_t* status, bool early, cudaStream_t s) {
   GmmArgs a = args_of(c, o, g, offsets, c.F, c.H, status);
+  a.early = early;
   a.x = static_cast<const char*>(h);
   a.w0 = static_cast<const char*>(wd);
   a.out = y;
@@ -93,7 +94,7 @@ moe_status_t moe_gmm_down_w4(const moe_config_t* cfg, const moe_w4_t* opt,
       !ok_ptr(w_down, true) || !ok_ptr(y_sorted, true))
     return MOE_ERR_INVALID_ARG;
   return down(*cfg, *opt, g, h, group_offsets, w_down, y_sorted, status_word,
-              stream);
+              false, stream);
 }
 
 moe_status_t moe_gmm_swiglu_w4(const moe_config_t* cfg, const moe_w4_t* opt,
@@ -112,8 +113,10 @@ moe_status_t moe_gmm_swiglu_w4(const moe_config_t* cfg, const moe_w4_t* opt,
   const moe_status_t up = gate_up(*cfg, *opt, g, x_sorted, group_offsets,
                                   w_gate, w_up, h, status_word, stream);
   if (up != MOE_OK) return up;
+  // Only gate_up's h is still to come when this one starts early: its
+  // weights and offsets were final before gate_up started.
   return down(*cfg, *opt, g, h, group_offsets, w_down, y_sorted, status_word,
-              stream);
+              true, stream);
 }
 
 }  // extern "C"

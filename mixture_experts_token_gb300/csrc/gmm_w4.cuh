@@ -65,6 +65,7 @@ struct GmmArgs {
   Layout l;
   int n_experts, n_groups, rows;
   int x_rows;  // rows of x that a slot holds: those of one pass
+  bool early;  // may start before the kernel that writes x has ended
 };
 
 // ---------------------------------------------------------------- PTX ----
@@ -254,6 +255,7 @@ struct Kernel {
     const int tiles_k = l.tiles_k(), n_steps = l.steps();
     const uint32_t sb = smem_u32(base);
     int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
+    launch::let_next_start();
     const int n_active = find_active(a, active);  // a barrier within
     const int blocks = (l.N + kCols - 1) / kCols;
     const int n_items = n_active * blocks;
@@ -315,9 +317,8 @@ struct Kernel {
     };
     const uint32_t codes = sb + warp * (kRing * kTilePair) + lane * 16;
     const uint32_t sc0 = sb + m.scales + warp * 2 * kScaleRec;
-    // Tiles first.. of the cursor's step into slot `half` (of two); with tile
-    // 0 the rows of x and the scales, into slot xs (of three).
-    const auto copy_unit = [&](int half, int xs, int first) {
+    // Tiles first.. of the cursor's step into slot `half` (of two).
+    const auto copy_codes = [&](int half, int first) {
       const uint32_t dst = codes + (half * kTiles + first) * kTilePair;
       const auto copy_tile = [&](int i) {
         copy16(dst + i * kTilePair, p0 + (first + i) * kTileBytes);
@@ -330,36 +331,61 @@ struct Kernel {
       } else if (left > first) {
         copy_tile(0);
       }
-      if (first == 0 && left > 0) {
-        if (lane * 16 < kScaleRec) {
-          const int at = min(left, kTiles) * kTileBytes;
-          const uint32_t d = sc0 + xs * kWarps * 2 * kScaleRec + lane * 16;
-          copy16(d, p0 + at);
-          copy16(d + kScaleRec, p1 + at);
-        }
-        const int rows = min(a.x_rows, in.r1 - in.row) - x_first;
-        const long long rest =  // of the rows from this lane's place on
-            row_bytes - static_cast<long long>(in.step) * kStepBytes - x_word;
-        const uint32_t d = x_dst + xs * m.x_slot;
+    };
+    // The step's scales and rows of x into slot xs (of three).
+    const auto copy_scales = [&](int xs) {
+      if (left > 0 && lane * 16 < kScaleRec) {
+        const int at = min(left, kTiles) * kTileBytes;
+        const uint32_t d = sc0 + xs * kWarps * 2 * kScaleRec + lane * 16;
+        copy16(d, p0 + at);
+        copy16(d + kScaleRec, p1 + at);
+      }
+    };
+    const auto copy_rows = [&](int xs) {
+      if (left <= 0) return;
+      const int rows = min(a.x_rows, in.r1 - in.row) - x_first;
+      const long long rest =  // of the rows from this lane's place on
+          row_bytes - static_cast<long long>(in.step) * kStepBytes - x_word;
+      const uint32_t d = x_dst + xs * m.x_slot;
 #pragma unroll
-        for (int r = 0; r < kRows; r += kRowStride)
-          if (r < rows)
+      for (int r = 0; r < kRows; r += kRowStride)
+        if (r < rows)
 #pragma unroll
-            for (int w = 0; w < kWords; w += 32)
-              copy16_or_zero(d + r * kPitch + w * 16,
-                             xp + r * row_bytes + w * 16, w * 16 < rest);
+          for (int w = 0; w < kWords; w += 32)
+            copy16_or_zero(d + r * kPitch + w * 16,
+                           xp + r * row_bytes + w * 16, w * 16 < rest);
+    };
+    const auto copy_unit = [&](int half, int xs, int first) {
+      copy_codes(half, first);
+      if (first == 0) {
+        copy_scales(xs);
+        copy_rows(xs);
       }
       copies_commit();
     };
 
-    in.item = blockIdx.x;
-    if (in.item < n_items && kw < n_steps) enter();
+    // The first two steps: weights first, then, once the kernel before this
+    // one has written them, the rows.
+    const auto begin = [&](bool weights) {
+      in.item = blockIdx.x;
+      left = 0;
+      if (in.item < n_items && kw < n_steps) enter();
 #pragma unroll 1
-    for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 2; ++s) {
+        if (weights) {
+          for (int u = 0; u < kUnits; ++u) copy_codes(s, u * kUnit);
+          copy_scales(s);
+        } else {
+          copy_rows(s);
+        }
+        if (left > 0) advance();
+      }
+    };
+    begin(true);
+    launch::wait_for_previous();
+    begin(false);
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) copy_unit(s, s, u * kUnit);
-      if (left > 0) advance();
-    }
+    for (int u = 0; u < 2 * kUnits; ++u) copies_commit();
 
     // --- the computing side
     int half = 0, xs = 0;  // the slots of the step
@@ -622,6 +648,8 @@ cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
       std::min(a.n_groups, a.rows);
   const unsigned grid = static_cast<unsigned>(
       std::min<long long>(items, static_cast<long long>(per_sm) * d.sms));
+  if (a.early)
+    return launch::overlapping(kernel, grid, Ker::kThreads, bytes, s, a);
   kernel<<<grid, Ker::kThreads, bytes, s>>>(a);
   return cudaGetLastError();
 }
