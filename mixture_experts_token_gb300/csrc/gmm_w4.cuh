@@ -223,7 +223,7 @@ struct Kernel {
   static constexpr int kChunk = kTiles * kTileBytes + kScaleRec;
   static constexpr int kTilePair = 2 * kTileBytes;
   // CTAs an SM has registers for
-  static constexpr int kPerSm = kWarps > 8 ? 1 : 2;
+  static constexpr int kPerSm = kWarps > 8 ? 1 : kWarps == 8 ? 2 : 4;
   // columns of an item
   static constexpr int kCols = DUAL ? NW * kTileN : 2 * NW * kTileN;
   static_assert(!kShareX || KW == 1, "x is shared by warps of the same k");
@@ -347,9 +347,10 @@ struct Kernel {
       const long long rest =  // of the rows from this lane's place on
           row_bytes - static_cast<long long>(in.step) * kStepBytes - x_word;
       const uint32_t d = x_dst + xs * m.x_slot;
-#pragma unroll
-      for (int r = 0; r < kRows; r += kRowStride)
-        if (r < rows)
+      // a warp that copies for itself has one row or few
+#pragma unroll(kShareX ? kRows / kRowStride : 1)
+      for (int r = 0; r < (kShareX ? kRows : rows); r += kRowStride)
+        if (!kShareX || r < rows)
 #pragma unroll
           for (int w = 0; w < kWords; w += 32)
             copy16_or_zero(d + r * kPitch + w * 16,
@@ -663,7 +664,7 @@ cudaError_t launch_shape(const GmmArgs& a, int tokens, cudaStream_t s) {
   const long long items =
       groups * ((a.l.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
   if (tokens <= 8 && items < 4ll * d.sms)
-    return launch_one<T, DUAL, 1, 8, 1, G, Z>(a, tokens, d, s);
+    return launch_one<T, DUAL, 1, 4, 1, G, Z>(a, tokens, d, s);
   if (a.rows <= 4 * groups)
     return launch_one<T, DUAL, 8, 1, 1, G, Z>(a, tokens, d, s);
   if (sizeof(T) == 4 || a.rows <= 12 * groups)
