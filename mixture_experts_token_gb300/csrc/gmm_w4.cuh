@@ -36,6 +36,7 @@
 #include <algorithm>
 
 #include "launch.cuh"
+#include "tc_common.cuh"
 #include "w4.cuh"
 
 namespace moe {
@@ -49,6 +50,8 @@ cudaError_t launch_gmm_w4_bf16(bool dual, const GmmArgs& a, int tokens,
                                cudaStream_t s);
 cudaError_t launch_gmm_w4_f32(bool dual, const GmmArgs& a, int tokens,
                               cudaStream_t s);
+// Groups of many bf16 rows (gmm_w4_tc.cu).
+cudaError_t launch_gmm_w4_tc(bool dual, const GmmArgs& a, cudaStream_t s);
 
 constexpr int kTiles = kStepK / kTileK;  // tiles of a step
 constexpr int kUnit = 2;                 // tiles copied and waited for at once
@@ -69,9 +72,7 @@ struct GmmArgs {
 };
 
 // ---------------------------------------------------------------- PTX ----
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
+using tc::smem_u32;
 // 16 bytes, zeros where `in` is false (then src is not read).
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src,
                                                bool in) {
@@ -160,32 +161,80 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) {
   *p = __float2bfloat16(v);
 }
 
-// The operands of eight k of one row of x: P parts, two instructions each.
+// The groups that have rows and an expert, in order; their number.
+template <int WARPS, typename A>
+__device__ int find_active(const A& a, int32_t* active) {
+  __shared__ int count[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int total = 0;
+  for (int g0 = 0; g0 < a.n_groups; g0 += WARPS * 32) {
+    const int g = g0 + threadIdx.x;
+    bool on = false;
+    if (g < a.n_groups) {
+      on = min(a.rows, a.offsets[g + 1]) > max(0, a.offsets[g]);
+      const int ex = on && a.map ? a.map[g] : g < a.n_experts ? g : -1;
+      if (on && (ex < 0 || ex >= a.n_experts)) {
+        on = false;
+        if (blockIdx.x == 0 && a.status)
+          atomicOr(a.status, MOE_DEV_BAD_INDEX);
+      }
+    }
+    const uint32_t vote = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) count[warp] = __popc(vote);
+    __syncthreads();
+    int before = total;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += count[w];
+      total += count[w];
+    }
+    if (on) active[before + __popc(vote & ((1u << lane) - 1))] = g;
+    __syncthreads();
+  }
+  return total;
+}
+
+// The operands of 32 k of eight rows of x: P parts, two instructions each.
+// lane_at() is where a lane reads, from the start of its row's 32 k; the
+// lane's row is row(lane) of the eight.
 template <typename T>
 struct Rows;
 template <>
 struct Rows<__nv_bfloat16> {
   static constexpr int P = 1;
-  static constexpr int kLaneBytes = 16;
-  static constexpr int kPad = 64;  // rows 64 bytes apart mod 128: no conflict
-  uint4 q;
-  __device__ __forceinline__ void load(uint32_t a) { q = lds16(a); }
+  static constexpr int kPad = 16;  // rows 16 bytes apart mod 128: no conflict
+  static __device__ __forceinline__ int row(int lane) { return lane & 7; }
+  static __device__ __forceinline__ int lane_at(int lane) {
+    return lane / 8 * 16;
+  }
+  uint32_t q[4];
+  __device__ __forceinline__ void load(uint32_t a) {
+    asm volatile(
+        "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+        : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+        : "r"(a)
+        : "memory");
+  }
   __device__ __forceinline__ void part(int, uint32_t (&b)[4]) const {
-    b[0] = q.x, b[1] = q.y, b[2] = q.z, b[3] = q.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = q[i];
   }
 };
 template <>
 struct Rows<float> {
   static constexpr int P = 3;
-  static constexpr int kLaneBytes = 32;
-  static constexpr int kPad = 16;
+  static constexpr int kPad = 32;  // four rows of 32 bytes side by side
+  static __device__ __forceinline__ int row(int lane) { return lane >> 2; }
+  static __device__ __forceinline__ int lane_at(int lane) {
+    return (lane & 3) * 8;
+  }
   float f[8];
   __device__ __forceinline__ void load(uint32_t a) {
-    const uint4 u = lds16(a), v = lds16(a + 16);
-    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
-    f[4] = __uint_as_float(v.x), f[5] = __uint_as_float(v.y);
-    f[6] = __uint_as_float(v.z), f[7] = __uint_as_float(v.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
+                   : "r"(a + 32 * i)
+                   : "memory");
   }
   // Takes the leading 8 bits of what is left, by truncation: no part
   // overflows and the rest is exact.  Nothing is left of an infinity.
@@ -256,7 +305,7 @@ struct Kernel {
     const uint32_t sb = smem_u32(base);
     int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
     launch::let_next_start();
-    const int n_active = find_active(a, active);  // a barrier within
+    const int n_active = find_active<kWarps>(a, active);  // a barrier within
     const int blocks = (l.N + kCols - 1) / kCols;
     const int n_items = n_active * blocks;
 
@@ -394,8 +443,8 @@ struct Kernel {
 #pragma unroll
     for (int b = 0; b < NT; ++b)
       x_row[b] = sb + m.x + (kShareX ? 0 : warp * a.x_rows * kPitch) +
-                 t * Rows<T>::kLaneBytes +
-                 min(8 * b + c, a.x_rows - 1) * kPitch;
+                 Rows<T>::lane_at(lane) +
+                 min(8 * b + Rows<T>::row(lane), a.x_rows - 1) * kPitch;
 #pragma unroll 1
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
       const int g = active[item / blocks];
@@ -445,37 +494,6 @@ struct Kernel {
       }
     }
     copies_wait<0>();
-  }
-
-  // The groups that have rows and an expert, in order; their number.
-  __device__ static int find_active(const GmmArgs& a, int32_t* active) {
-    __shared__ int count[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int total = 0;
-    for (int g0 = 0; g0 < a.n_groups; g0 += kThreads) {
-      const int g = g0 + threadIdx.x;
-      bool on = false;
-      if (g < a.n_groups) {
-        on = min(a.rows, a.offsets[g + 1]) > max(0, a.offsets[g]);
-        const int ex = on && a.map ? a.map[g] : g < a.n_experts ? g : -1;
-        if (on && (ex < 0 || ex >= a.n_experts)) {
-          on = false;
-          if (blockIdx.x == 0 && a.status)
-            atomicOr(a.status, MOE_DEV_BAD_INDEX);
-        }
-      }
-      const uint32_t vote = __ballot_sync(0xffffffffu, on);
-      if (lane == 0) count[warp] = __popc(vote);
-      __syncthreads();
-      int before = total;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += count[w];
-        total += count[w];
-      }
-      if (on) active[before + __popc(vote & ((1u << lane) - 1))] = g;
-      __syncthreads();
-    }
-    return total;
   }
 
   // TILES tiles of both records, from tile `first` of the step on, times the
@@ -530,7 +548,7 @@ struct Kernel {
         if (NT > 1 && 8 * b >= rows) break;
         Rows<T> v;
         v.load(x_row[b] + x0 + first * kTileK * static_cast<int>(sizeof(T)) +
-               h * 4 * Rows<T>::kLaneBytes);
+               h * 32 * static_cast<int>(sizeof(T)));
 #pragma unroll
         for (int p = 0; p < Rows<T>::P; ++p) {
           uint32_t o[4];
@@ -669,9 +687,7 @@ cudaError_t launch_shape(const GmmArgs& a, int tokens, cudaStream_t s) {
     return launch_one<T, DUAL, 8, 1, 1, G, Z>(a, tokens, d, s);
   if (sizeof(T) == 4 || a.rows <= 12 * groups)
     return launch_one<T, DUAL, 8, 1, 2, G, Z>(a, tokens, d, s);
-  if constexpr (sizeof(T) == 2)
-    return launch_one<T, DUAL, 16, 1, 4, G, Z>(a, tokens, d, s);
-  return cudaErrorInvalidValue;
+  return launch_gmm_w4_tc(DUAL, a, s);
 }
 
 // The products of one row type: what gmm_w4_bf16.cu and gmm_w4_f32.cu each

@@ -1,0 +1,605 @@
+// Products of many bf16 rows with 4-bit expert weights on tcgen05.
+//
+// The matrix instructions of gmm_w4.cuh take eight rows at a time, nine
+// clocks each, so past about a dozen rows a group they, and not the weights'
+// bytes, set the time.  Here the weights are the M = 128 operand and up to
+// 48 rows of x the N operand of tcgen05.mma:
+//
+// * Eight warps expand codes to bf16 (exactly code - zero, see expand()) and
+//   store them to tensor memory as the A operand: what shared memory would
+//   have to take and give again, four bytes for each byte of codes, is twice
+//   its bandwidth at the rate HBM delivers codes.  A lane's words are in the
+//   order of the 16x128b store, so nothing is shuffled.
+// * One thread issues the matrix instructions, a group of rows of W at a
+//   time into one of two partial accumulators.
+// * Eight warps, a thread per column of W, add scale * partial in float32
+//   registers while the next group runs, and at the end write the rows.
+// * One thread brings x by TMA (rows past the group are other groups' rows
+//   and columns past K zeros; neither reaches a row that is written).
+//
+// A CTA per SM walks over items: 128 columns of the gate and the up matrix,
+// or 256 of the down matrix, of one group with rows.  Every wait is bounded;
+// one that gives up raises MOE_DEV_TIMEOUT and the CTA drains and returns.
+#include <atomic>
+
+#include "gmm_w4.cuh"
+
+namespace moe {
+namespace tc {
+// The GEMMs' test hook (gmm_tc.cu): stop the producer after this many stage
+// fills (-1: never), so that the next wait runs out.
+extern std::atomic<long long> g_stall_after_fills;
+}  // namespace tc
+
+namespace w4 {
+namespace {
+
+using tc::fence_barrier_init;
+using tc::mbar_arrive;
+using tc::mbar_expect_tx;
+using tc::mbar_init;
+using tc::smem_desc;
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::umma_commit;
+
+constexpr int kNR = 48;            // rows of a pass
+constexpr int kExpandWarps = 8;    // warp w: tile w / 4, lanes 32 (w % 4)..
+constexpr int kAddWarps = 8;       // the same, four further on
+constexpr int kMmaWarp = 16;      // and warp 17 brings x
+constexpr int kTcThreads = 18 * 32;
+constexpr int kAStages = 4;        // 64 rows of W each
+constexpr int kXStages = 8;
+constexpr int kXBytes = kNR * 128;
+constexpr int kCodeTiles = 8;      // tiles of codes in flight, of each warp
+constexpr int kZeroSlots = kCodeTiles + 1;  // steps of zero points held
+constexpr int kTmemA = 256;        // columns: accumulators, then A
+constexpr int kSumPitch = kNR + 1;
+
+struct TcArgs {
+  const int32_t *offsets, *map;
+  const char *w0, *w1;
+  __nv_bfloat16* out;
+  int32_t* status;
+  Layout l;
+  int n_experts, n_groups, rows;
+  long long stall_after_fills;  // tests of the timeout path only (-1: off)
+};
+
+// Shared memory, from a 1024-byte boundary.
+struct TcSmem {
+  int codes, zeros, sums, bars, groups, total;
+};
+__host__ __device__ inline TcSmem tc_smem(const Layout& l, int n_groups) {
+  TcSmem m;
+  m.codes = kXStages * kXBytes;
+  m.zeros = m.codes + kExpandWarps * kCodeTiles * 2 * kTileBytes;
+  m.sums = m.zeros + (l.zeros ? kExpandWarps * kZeroSlots * 2 * 16 *
+                                    (kStepK / l.group)
+                              : 0);
+  m.bars = m.sums + 128 * kSumPitch * 4;
+  m.groups = m.bars + 256;
+  m.total = m.groups + 4 * n_groups;
+  return m;
+}
+
+// D (+)= A B with A in tensor memory.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 16 lanes x 32 columns: four words' operands in order.
+__device__ __forceinline__ void tmem_st_operands(uint32_t at,
+                                                 const uint32_t (&r)[4][4]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(r[0][0]), "r"(r[0][1]), "r"(r[0][2]), "r"(r[0][3]), "r"(r[1][0]),
+      "r"(r[1][1]), "r"(r[1][2]), "r"(r[1][3]), "r"(r[2][0]), "r"(r[2][1]),
+      "r"(r[2][2]), "r"(r[2][3]), "r"(r[3][0]), "r"(r[3][1]), "r"(r[3][2]),
+      "r"(r[3][3])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase,
+                                         volatile int* abort_flag,
+                                         int32_t* status) {
+  const bool ok = tc::mbar_try_wait(bar, phase) ||
+                  tc::mbar_wait(bar, phase, abort_flag, status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+template <bool DUAL, int G, bool Z>
+struct TcKernel {
+  static constexpr int E = kStepK / G;
+  static constexpr int kChunk =
+      kTiles * kTileBytes + 8 * E * (Z ? 6 : 4);  // bytes of a whole step
+  static constexpr int kCols = DUAL ? 128 : 256;  // of an item
+
+  struct Bars {  // shared-memory addresses
+    uint32_t a_full, a_empty, x_full, x_empty, p_full, p_empty, done;
+  };
+  // Where record `i` (0..7) of tile m of an item starts.  One past the last
+  // is the last again: its columns are not written.
+  __device__ static const char* record(const TcArgs& a, int ex, int nb, int m,
+                                       int i) {
+    const int rec = DUAL ? nb * 8 + i : nb * 16 + m * 8 + i;
+    return (DUAL && m == 1 ? a.w1 : a.w0) + ex * a.l.matrix() +
+           min(rec, a.l.tiles_n() - 1) * a.l.record();
+  }
+
+  // Calls f(item's column block, expert, first row, end of rows) for every
+  // pass of this CTA until it returns false.
+  template <typename F>
+  __device__ static void passes(const TcArgs& a, const int32_t* active,
+                                int n_items, int blocks, const F& f) {
+#pragma unroll 1
+    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+      const int g = active[item / blocks];
+      const int ex = a.map ? a.map[g] : g;
+      const int r1 = min(a.rows, a.offsets[g + 1]);
+#pragma unroll 1
+      for (int row = max(0, a.offsets[g]); row < r1; row += kNR)
+        if (!f(item % blocks, ex, row, r1)) return;
+    }
+  }
+
+  __device__ static void run(const TcArgs& a, const CUtensorMap* map) {
+    extern __shared__ __align__(1024) char raw[];
+    char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    __shared__ int abort_word;
+    __shared__ uint32_t tmem_word;
+    volatile int* abort_flag = &abort_word;
+    const TcSmem m = tc_smem(a.l, a.n_groups);
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const uint32_t sb = smem_u32(base);
+    Bars b;
+    b.a_full = sb + m.bars;
+    b.a_empty = b.a_full + 8 * kAStages;
+    b.x_full = b.a_empty + 8 * kAStages;
+    b.x_empty = b.x_full + 8 * kXStages;
+    b.p_full = b.x_empty + 8 * kXStages;
+    b.p_empty = b.p_full + 16;
+    b.done = b.p_empty + 16;
+    if (threadIdx.x == 0) {
+      abort_word = 0;
+      for (int i = 0; i < kAStages; ++i) {
+        mbar_init(b.a_full + 8 * i, kExpandWarps);
+        mbar_init(b.a_empty + 8 * i, 1);
+      }
+      for (int i = 0; i < kXStages; ++i) {
+        mbar_init(b.x_full + 8 * i, 1);
+        mbar_init(b.x_empty + 8 * i, 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(b.p_full + 8 * i, 1);
+        mbar_init(b.p_empty + 8 * i, kAddWarps);
+      }
+      mbar_init(b.done, 1);
+      fence_barrier_init();
+      tc::fence_proxy_async_smem();
+    }
+    if (warp == kMmaWarp) {
+      tc::tmem_alloc(smem_u32(&tmem_word), tc::kTmemCols);
+      tc::tmem_relinquish();
+    }
+    int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
+    const int n_active = find_active<18>(a, active);  // barriers within
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_word;
+    const int blocks = (a.l.N + kCols - 1) / kCols;
+    const int n_items = n_active * blocks;
+    if (warp < kExpandWarps)
+      expand_codes(a, m, sb, b, active, n_items, blocks, tmem, warp, lane,
+                   abort_flag);
+    else if (warp < kExpandWarps + kAddWarps)
+      add_parts(a, reinterpret_cast<float*>(base + m.sums), b, active,
+                n_items, blocks, tmem, warp - kExpandWarps, lane, abort_flag);
+    else if (warp == kMmaWarp)
+      multiply(a, sb, b, active, n_items, blocks, tmem, lane, abort_flag);
+    else
+      copy_rows(a, map, sb, b, active, n_items, blocks, lane, abort_flag);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, tc::kTmemCols);
+  }
+
+  // ---- codes to operands: two records of a tile of 64 rows at a time
+  __device__ static void expand_codes(const TcArgs& a, const TcSmem& m,
+                                      uint32_t sb, const Bars& b,
+                                      const int32_t* active, int n_items,
+                                      int blocks, uint32_t tmem, int warp,
+                                      int lane, volatile int* abort_flag) {
+    const int tiles_k = a.l.tiles_k(), t = warp / 4, q = warp % 4;
+    const int c = lane >> 2;
+    const uint32_t codes =
+        sb + m.codes + warp * (kCodeTiles * 2 * kTileBytes) + lane * 16;
+    const uint32_t zeros = sb + m.zeros + warp * (kZeroSlots * 2 * 16 * E);
+    const uint32_t a_at = tmem + kTmemA + t * 128 +
+                          (static_cast<uint32_t>(32 * q) << 16);
+    // the copying side, kCodeTiles tiles ahead
+    int item = blockIdx.x, row = 0, r1 = 0, tile = 0, zslot = 0;
+    const char *p0 = nullptr, *p1 = nullptr, *s0 = nullptr, *s1 = nullptr;
+    const auto enter = [&] {
+      const int g = active[item / blocks];
+      const int ex = a.map ? a.map[g] : g;
+      row = max(0, a.offsets[g]);
+      r1 = min(a.rows, a.offsets[g + 1]);
+      s0 = record(a, ex, item % blocks, t, 2 * q);
+      s1 = record(a, ex, item % blocks, t, 2 * q + 1);
+      p0 = s0 + lane * 16;
+      p1 = s1 + lane * 16;
+      tile = 0;
+    };
+    if (item < n_items) enter();
+    int in_slot = 0;
+    const auto copy_tile = [&] {
+      if (item < n_items) {
+        const uint32_t dst = codes + in_slot * (2 * kTileBytes);
+        copy16(dst, p0);
+        copy16(dst + kTileBytes, p1);
+        if (tile % kTiles == 0) {
+          if (Z && lane < E) {  // 16 E bytes of zero points
+            const int at =
+                min(tiles_k - tile, kTiles) * kTileBytes + 32 * E;
+            const uint32_t d = zeros + zslot * (2 * 16 * E) + lane * 16;
+            copy16(d, p0 + at);
+            copy16(d + 16 * E, p1 + at);
+          }
+          zslot = zslot == kZeroSlots - 1 ? 0 : zslot + 1;
+        }
+        ++tile;
+        const int skip =
+            kTileBytes + (tile % kTiles == 0 ? kChunk - kTiles * kTileBytes
+                                             : 0);
+        p0 += skip;
+        p1 += skip;
+        if (tile == tiles_k) {
+          row += kNR;
+          if (row < r1) {  // the group's next rows: the same weights
+            p0 = s0 + lane * 16;
+            p1 = s1 + lane * 16;
+            tile = 0;
+          } else {
+            item += gridDim.x;
+            if (item < n_items) enter();
+          }
+        }
+      }
+      copies_commit();
+      in_slot = in_slot == kCodeTiles - 1 ? 0 : in_slot + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kCodeTiles; ++i) copy_tile();
+
+    int slot = 0, zread = 0, as = 0;
+    uint32_t phase = 1;
+    passes(a, active, n_items, blocks, [&](int, int, int, int) {
+      uint32_t z[2][2];
+      z[0][0] = z[0][1] = z[1][0] = z[1][1] = 0xbe00be00u;  // -8/64
+#pragma unroll 1
+      for (int k = 0; k < tiles_k; ++k) {
+        copies_wait<kCodeTiles - 1>();
+        if (Z && k % kTiles == 0) __syncwarp();
+        uint32_t w[2][4], op[2][4][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint4 v =
+              lds16(codes + slot * (2 * kTileBytes) + r * kTileBytes);
+          w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (Z && (h == 0 || G == 32)) {
+              const int g = (k % kTiles * kTileK + 32 * h) / G;
+              const uint32_t v = lds2(zeros + zread * (2 * 16 * E) +
+                                      r * 16 * E + (c * E + g) * 2);
+              constexpr uint32_t kMinus = kPow127 | 0x80008000u;
+              z[r][0] = fma2(__byte_perm(v, 0, 0x4040), kMinus, 0);
+              z[r][1] = fma2(__byte_perm(v, 0, 0x4141), kMinus, 0);
+            }
+            expand(w[r][2 * h], z[r], op[r][2 * h]);
+            expand(w[r][2 * h + 1], z[r], op[r][2 * h + 1]);
+          }
+        }
+        if (k % kTiles == kTiles - 1 || k == tiles_k - 1)
+          zread = zread == kZeroSlots - 1 ? 0 : zread + 1;
+        if (Z) __syncwarp();  // every lane has read what is copied over
+        copy_tile();
+        slot = slot == kCodeTiles - 1 ? 0 : slot + 1;
+        if (!wait_all(b.a_empty + 8 * as, phase, abort_flag, a.status))
+          return false;
+        tc_fence_after();
+        const uint32_t at = a_at + as * 32;
+        tmem_st_operands(at, op[0]);
+        tmem_st_operands(at + (16u << 16), op[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.a_full + 8 * as);
+        if (++as == kAStages) {
+          as = 0;
+          phase ^= 1;
+        }
+      }
+      return true;
+    });
+    copies_wait<0>();
+  }
+
+  // ---- rows of x by TMA: 64 columns of the pass's rows at a time
+  __device__ static void copy_rows(const TcArgs& a, const CUtensorMap* map,
+                                   uint32_t sb, const Bars& b,
+                                   const int32_t* active, int n_items,
+                                   int blocks, int lane,
+                                   volatile int* abort_flag) {
+    if (lane != 0) return;
+    const int tiles_k = a.l.tiles_k();
+    int xs = 0;
+    long long filled = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    passes(a, active, n_items, blocks, [&](int, int, int row, int) {
+#pragma unroll 1
+      for (int k = 0; k < tiles_k; ++k) {
+        ok = (a.stall_after_fills < 0 || filled < a.stall_after_fills) &&
+             tc::mbar_wait(b.x_empty + 8 * xs, phase, abort_flag, a.status);
+        if (!ok) return false;
+        mbar_expect_tx(b.x_full + 8 * xs, kXBytes);
+        tc::tma_load_2d(sb + xs * kXBytes, map, b.x_full + 8 * xs,
+                        k * kTileK, row);
+        ++filled;
+        if (++xs == kXStages) {
+          xs = 0;
+          phase ^= 1;
+        }
+      }
+      return true;
+    });
+    // after a wait that gave up: this thread's own copies
+    if (!ok)
+      for (long long i = 0; i < filled && i < kXStages; ++i) {
+        if (--xs < 0) {
+          xs = kXStages - 1;
+          phase ^= 1;
+        }
+        tc::mbar_wait(b.x_full + 8 * xs, phase ^ 1, nullptr, a.status);
+      }
+  }
+
+  // ---- the matrix instructions: one partial sum for each group of W's rows
+  __device__ static void multiply(const TcArgs& a, uint32_t sb, const Bars& b,
+                                  const int32_t* active, int n_items,
+                                  int blocks, uint32_t tmem, int lane,
+                                  volatile int* abort_flag) {
+    if (lane != 0) return;
+    const int tiles_k = a.l.tiles_k();
+    int as = 0, xs = 0, part = 0;
+    uint32_t a_phase = 0, x_phase = 0, p_phase = 1;
+    passes(a, active, n_items, blocks, [&](int, int, int row, int r1) {
+      const int n = (min(kNR, r1 - row) + 15) / 16 * 16;
+      const uint32_t idesc =
+          tc::make_idesc(128, 16, false) + ((n - 16) >> 3 << 17);
+#pragma unroll 1
+      for (int k = 0; k < tiles_k; ++k) {
+        if (!tc::mbar_wait(b.a_full + 8 * as, a_phase, abort_flag,
+                           a.status) ||
+            !tc::mbar_wait(b.x_full + 8 * xs, x_phase, abort_flag, a.status))
+          return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTileK / 16; ++kk) {
+          const int at = k * kTileK + kk * 16;
+          const bool first = at % G == 0;
+          if (first) {
+            if (!tc::mbar_wait(b.p_empty + 8 * part, p_phase, abort_flag,
+                               a.status))
+              return false;
+            tc_fence_after();
+          }
+          const uint64_t bd = smem_desc(sb + xs * kXBytes + kk * 32, 16, 1024);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            umma_ts(tmem + t * 128 + part * 64,
+                    tmem + kTmemA + t * 128 + as * 32 + kk * 8, bd, idesc,
+                    first ? 0u : 1u);
+          if ((at + 16) % G == 0 ||
+              (k == tiles_k - 1 && kk == kTileK / 16 - 1)) {
+            umma_commit(b.p_full + 8 * part);
+            part ^= 1;
+            if (part == 0) p_phase ^= 1;
+          }
+        }
+        umma_commit(b.a_empty + 8 * as);
+        umma_commit(b.x_empty + 8 * xs);
+        if (++as == kAStages) {
+          as = 0;
+          a_phase ^= 1;
+        }
+        if (++xs == kXStages) {
+          xs = 0;
+          x_phase ^= 1;
+        }
+      }
+      return true;
+    });
+    // drain: every instruction that this thread issued
+    umma_commit(b.done);
+    tc::mbar_wait(b.done, 0, nullptr, a.status);
+  }
+
+  // ---- scale * partial sums, a thread per column of W, and the output
+  __device__ static void add_parts(const TcArgs& a, float* sums,
+                                   const Bars& b, const int32_t* active,
+                                   int n_items, int blocks, uint32_t tmem,
+                                   int warp, int lane,
+                                   volatile int* abort_flag) {
+    const int t = warp / 4, q = warp % 4;
+    const int col = lane & 15, n_in = 32 * q + lane;  // column of the tile
+    const int tiles_k = a.l.tiles_k();
+    const int groups = (tiles_k * kTileK + G - 1) / G;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    int part = 0;
+    uint32_t phase = 0;
+    // After a wait that gave up the loops run on without waiting, so that
+    // the warps meet at their barriers.
+    bool ok = true;
+    passes(a, active, n_items, blocks, [&](int nb, int ex, int row, int r1) {
+      const int rows = min(kNR, r1 - row);
+      const char* rec =
+          record(a, ex, nb, t, 2 * q + (lane >> 4)) + (col & 7) * (4 * E) +
+          (col >> 3) * 2;
+      const auto load_scale = [&](int g) {
+        const int step = g / E;
+        const char* p = rec + step * kChunk +
+                        min(kTiles, tiles_k - step * kTiles) * kTileBytes +
+                        g % E * 4;
+        return __ldg(reinterpret_cast<const unsigned short*>(p));
+      };
+      float acc[kNR];
+#pragma unroll
+      for (int i = 0; i < kNR; ++i) acc[i] = 0.0f;
+      unsigned short next = load_scale(0);
+#pragma unroll 1
+      for (int g = 0; g < groups; ++g) {
+        const float s = __uint_as_float(static_cast<uint32_t>(next) << 16);
+        if (g + 1 < groups) next = load_scale(g + 1);
+        if (ok)
+          ok = wait_all(b.p_full + 8 * part, phase, abort_flag, a.status);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t d = tmem + lanes + t * 128 + part * 64;
+#pragma unroll
+          for (int i = 0; i < kNR; i += 16) {
+            if (i >= rows) break;
+            uint32_t v[16];
+            tmem_ld16(d + i, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[i + j] = fmaf(s, __uint_as_float(v[j]), acc[i + j]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b.p_empty + 8 * part);
+        }
+        part ^= 1;
+        if (part == 0) phase ^= 1;
+      }
+      // the sums are 1/64 of the products
+      if (DUAL) {
+        if (t == 1)
+#pragma unroll
+          for (int i = 0; i < kNR; ++i) sums[n_in * kSumPitch + i] = acc[i];
+        barrier();
+        const int n = nb * 128 + n_in;
+        if (t == 0 && ok && n < a.l.N) {
+#pragma unroll
+          for (int i = 0; i < kNR; ++i) {
+            const float g = 64.0f * acc[i];
+            const float u = 64.0f * sums[n_in * kSumPitch + i];
+            if (i < rows)
+              a.out[static_cast<long long>(row + i) * a.l.N + n] =
+                  __float2bfloat16(g / (1.0f + expf(-g)) * u);
+          }
+        }
+        barrier();
+      } else {
+        const int n = nb * 256 + t * 128 + n_in;
+        if (ok && n < a.l.N) {
+#pragma unroll
+          for (int i = 0; i < kNR; ++i)
+            if (i < rows)
+              a.out[static_cast<long long>(row + i) * a.l.N + n] =
+                  __float2bfloat16(64.0f * acc[i]);
+        }
+      }
+      return true;
+    });
+  }
+
+  __device__ static __forceinline__ void barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kAddWarps * 32) : "memory");
+  }
+};
+
+template <bool DUAL, int G, bool Z>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    gmm_w4_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap map) {
+  TcKernel<DUAL, G, Z>::run(a, &map);
+}
+
+template <bool DUAL, int G, bool Z>
+cudaError_t launch_tc(const TcArgs& a, const CUtensorMap& map,
+                      const Device& d, cudaStream_t s) {
+  constexpr auto kernel = gmm_w4_tc_kernel<DUAL, G, Z>;
+  const cudaError_t e = launch::allow_shared<kernel>(d);
+  if (e != cudaSuccess) return e;
+  const int cols = TcKernel<DUAL, G, Z>::kCols;
+  const long long items = static_cast<long long>((a.l.N + cols - 1) / cols) *
+                          std::min(a.n_groups, a.rows);
+  const unsigned grid =
+      static_cast<unsigned>(std::min<long long>(items, d.sms));
+  kernel<<<grid, kTcThreads, tc_smem(a.l, a.n_groups).total + 1024, s>>>(a,
+                                                                        map);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gmm_w4_tc(bool dual, const GmmArgs& g, cudaStream_t s) {
+  Device d;
+  cudaError_t e = launch::device(&d);
+  if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!tc::make_map(&map, g.x, g.l.K, g.rows, kTileK, kNR))
+    return cudaErrorInvalidValue;
+  const TcArgs a = {g.offsets, g.map,    g.w0,        g.w1,
+                    static_cast<__nv_bfloat16*>(g.out), g.status, g.l,
+                    g.n_experts, g.n_groups, g.rows,
+                    tc::g_stall_after_fills.load()};
+#define MOE_W4_CASE(GROUP)                                                  \
+  if (g.l.group == GROUP) {                                                 \
+    if (dual)                                                               \
+      return g.l.zeros ? launch_tc<true, GROUP, true>(a, map, d, s)         \
+                       : launch_tc<true, GROUP, false>(a, map, d, s);       \
+    return g.l.zeros ? launch_tc<false, GROUP, true>(a, map, d, s)          \
+                     : launch_tc<false, GROUP, false>(a, map, d, s);        \
+  }
+  MOE_W4_CASE(32)
+  MOE_W4_CASE(64)
+  MOE_W4_CASE(128)
+#undef MOE_W4_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace w4
+}  // namespace moe

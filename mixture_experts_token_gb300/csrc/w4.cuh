@@ -8,16 +8,13 @@
 //     zeros   the same with pairs of bytes (only with zero points)
 //
 // so that a product copies one contiguous piece a step.  A tile is one 16-byte
-// load per lane of a warp and each of the lane's four words is the weight
-// operand of one m16n8k16 matrix instruction: with c = lane / 4 and
-// t = lane % 4, word s of the lane holds rows k..k+3 with
-//   k = 32 * (s / 2) + 8 * t + 4 * (s % 2)
-// of columns c and c + 8.  Its nibbles, low to high, are
-//   (c,k) (c+8,k) (c,k+2) (c+8,k+2) (c,k+1) (c+8,k+1) (c,k+3) (c+8,k+3),
-// so that masking two nibbles 16 bits apart yields a packed operand pair, and a lane's eight consecutive k of a 32-row half are one 16-byte word of
-// the activations.  A half never mixes groups (groups are 32, 64 or 128
-// rows).  Codes of rows and columns past the matrix are the zero point, so
-// they weigh nothing.
+// load per lane of a warp.  Word s of the lane is the weight operand of one
+// m16n8k16 matrix instruction, rows 16 s to 16 s + 15 of the tile: with
+// c = lane / 4, t = lane % 4 and k = 16 s + 2 t its nibbles, low to high, are
+//   (c,k) (c+8,k) (c,k+8) (c+8,k+8) (c,k+1) (c+8,k+1) (c,k+9) (c+8,k+9)
+// so that masking two nibbles 16 bits apart yields a packed operand pair.
+// Two words never mix groups of 32 rows.  Codes of rows and columns past the
+// matrix are the zero point, so they weigh nothing.
 #pragma once
 
 #include "internal.h"

@@ -77,8 +77,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // Row and column of nibble i of word s of lane `lane` within a tile.
 __device__ __forceinline__ int nibble_k(int lane, int s, int i) {
-  return 32 * (s >> 1) + 8 * (lane & 3) + 4 * (s & 1) + ((i >> 2) & 1) +
-         (i & 2);
+  return 16 * s + 2 * (lane & 3) + ((i >> 2) & 1) + 4 * (i & 2);
 }
 __device__ __forceinline__ int nibble_n(int lane, int i) {
   return (lane >> 2) + 8 * (i & 1);
@@ -153,9 +152,8 @@ __global__ void __launch_bounds__(kThreads)
       const int k = i / kTileN, col = i % kTileN, n = n0 + col;
       if (n >= l.N) continue;
       const int r = k % kTileK;
-      const int lane = (col & 7) * 4 + ((r >> 3) & 3);
-      const int s = 2 * (r >> 5) + ((r >> 2) & 1);
-      const int j = (col >> 3) + (r & 2) + 4 * (r & 1);
+      const int lane = (col & 7) * 4 + ((r >> 1) & 3), s = r >> 4;
+      const int j = (col >> 3) + 2 * ((r >> 3) & 1) + 4 * (r & 1);
       const uint32_t v = *reinterpret_cast<const uint32_t*>(
           rec + code_at(l, k / kTileK) + lane * 16 + s * 4);
       const uint32_t q = v >> (4 * j) & 15;

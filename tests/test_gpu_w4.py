@@ -177,6 +177,56 @@ def test_swiglu(counts, H, F, dtype, group, zeros):
     check_swiglu(x, off, range(len(counts)), ws, h, y)
 
 
+# groups of many rows: one pass of 48 rows, parts of one, and several; one
+# tile of k, odd numbers of tiles, ends inside a tile; columns that end inside
+# a record, a quarter and a tile
+@pytest.mark.parametrize("counts,H,F", [
+    ([16], 8, 8), ([17, 0, 15], 72, 40), ([48], 64, 136), ([49, 97], 200, 328),
+    ([33, 5], 1000, 264), ([60, 0, 60, 13], 264, 1416), ([250], 2056, 520),
+    ([13, 14, 40, 7, 31], 520, 2056)])
+@pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, True),
+                                         (64, False), (128, True),
+                                         (128, False)])
+def test_swiglu_many_rows(counts, H, F, group, zeros):
+    cfg, w4, x, off, doff, packs, ws = case(counts, H, F, len(counts), "bf16",
+                                            group, zeros, seed=11)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    h, y = run_swiglu(cfg, w4, x, doff, packs, status=status)
+    assert status.item() == 0
+    check_swiglu(x, off, range(len(counts)), ws, h, y)
+
+
+def test_many_rows_next_to_nonfinite_rows():
+    """A pass may read rows of the next group; they stay apart."""
+    cfg, w4, x, off, doff, packs, ws = case([20, 30], 264, 136, 2, "bf16", 64,
+                                            True, seed=12)
+    h0, y0 = run_swiglu(cfg, w4, x, doff, packs)
+    x = x.clone()
+    x[20:] = float("nan")
+    h, y = run_swiglu(cfg, w4, x, doff, packs)
+    assert torch.equal(h[:20], h0[:20]) and torch.equal(y[:20], y0[:20])
+    assert h[20:].isnan().all() and y[20:].isnan().all()
+
+
+def test_stalled_rows_time_out_and_context_survives():
+    """The bounded waits of the many-row products: with the copies of x
+    stopped, the kernel reports MOE_DEV_TIMEOUT and returns, and the next
+    call is right."""
+    cfg, w4, x, off, doff, packs, ws = case([40, 60], 520, 264, 2, "bf16", 64,
+                                            False, seed=13)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        moe.moe_test_stall_gemm_producer(3)
+        run_swiglu(cfg, w4, x, doff, packs, status=status)
+    finally:
+        moe.moe_test_stall_gemm_producer(-1)
+    assert status.item() & moe.MOE_DEV_TIMEOUT
+    status.zero_()
+    h, y = run_swiglu(cfg, w4, x, doff, packs, status=status)
+    assert status.item() == 0
+    check_swiglu(x, off, range(2), ws, h, y)
+
+
 def test_many_experts_one_token():
     """One token of a layer with many experts: few of the groups have a row,
     wherever they lie."""
