@@ -5,7 +5,7 @@
 // bytes, set the time.  Here the weights are the M = 128 operand and up to
 // 48 rows of x the N operand of tcgen05.mma:
 //
-// * Eight warps expand codes to bf16 (exactly code - zero, see expand()) and
+// * Sixteen warps expand codes to bf16 (exactly code - zero, see expand()) and
 //   store them to tensor memory as the A operand: what shared memory would
 //   have to take and give again, four bytes for each byte of codes, is twice
 //   its bandwidth at the rate HBM delivers codes.  A lane's words are in the
@@ -44,15 +44,17 @@ using tc::tc_fence_before;
 using tc::umma_commit;
 
 constexpr int kNR = 48;            // rows of a pass
-constexpr int kExpandWarps = 8;    // warp w: tile w / 4, lanes 32 (w % 4)..
-constexpr int kAddWarps = 8;       // the same, four further on
-constexpr int kMmaWarp = 16;      // and warp 17 brings x
-constexpr int kTcThreads = 18 * 32;
-constexpr int kAStages = 4;        // 64 rows of W each
-constexpr int kXStages = 8;
+// Warps that expand: tile w / 4 % 2, lanes 32 (w % 4).., and every second 64
+// rows of W, from 64 (w / 8) on.
+constexpr int kExpandWarps = 16;
+constexpr int kAddWarps = 8;       // tile w / 4, lanes 32 (w % 4)..
+constexpr int kMmaWarp = kExpandWarps + kAddWarps;  // the next one brings x
+constexpr int kTcWarps = kMmaWarp + 2;
+constexpr int kTcThreads = kTcWarps * 32;
+constexpr int kStages = 4;         // 64 rows of W, and of x, each
 constexpr int kXBytes = kNR * 128;
-constexpr int kCodeTiles = 8;      // tiles of codes in flight, of each warp
-constexpr int kZeroSlots = kCodeTiles + 1;  // steps of zero points held
+constexpr int kCodeTiles = 4;      // tiles of codes in flight, of each warp
+constexpr int kZeroSlots = kCodeTiles;  // zero points, with each tile
 constexpr int kTmemA = 256;        // columns: accumulators, then A
 constexpr int kSumPitch = kNR + 1;
 
@@ -72,7 +74,7 @@ struct TcSmem {
 };
 __host__ __device__ inline TcSmem tc_smem(const Layout& l, int n_groups) {
   TcSmem m;
-  m.codes = kXStages * kXBytes;
+  m.codes = kStages * kXBytes;
   m.zeros = m.codes + kExpandWarps * kCodeTiles * 2 * kTileBytes;
   m.sums = m.zeros + (l.zeros ? kExpandWarps * kZeroSlots * 2 * 16 *
                                     (kStepK / l.group)
@@ -83,16 +85,24 @@ __host__ __device__ inline TcSmem tc_smem(const Layout& l, int n_groups) {
   return m;
 }
 
-// D (+)= A B with A in tensor memory.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b,
-                                        uint32_t idesc, uint32_t accumulate) {
+// D (+)= A B with A in tensor memory; `leader` in one lane of the warp.  The
+// whole warp runs the loop around it: the operands then are uniform, and
+// need not be moved from one lane's registers for every instruction.
+__device__ __forceinline__ void umma_ts(bool leader, uint32_t d, uint32_t a,
+                                        uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(
-          d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::
+          "r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate),
+      "r"(static_cast<uint32_t>(leader))
       : "memory");
+}
+__device__ __forceinline__ void commit(bool leader, uint32_t bar) {
+  if (leader) umma_commit(bar);
 }
 
 // 16 lanes x 32 columns: four words' operands in order.
@@ -110,25 +120,28 @@ __device__ __forceinline__ void tmem_st_operands(uint32_t at,
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, "
-      "%7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, "
+      "%7}, [%8];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
-        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15])
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(at)
       : "memory");
 }
 
+// The first look is inline: a call costs several hundred clocks here.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t phase,
+                                         volatile int* abort_flag,
+                                         int32_t* status) {
+  return tc::mbar_try_wait(bar, phase) ||
+         tc::mbar_wait(bar, phase, abort_flag, status);
+}
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase,
                                          volatile int* abort_flag,
                                          int32_t* status) {
-  const bool ok = tc::mbar_try_wait(bar, phase) ||
-                  tc::mbar_wait(bar, phase, abort_flag, status);
-  return __all_sync(0xffffffffu, ok);
+  return __all_sync(0xffffffffu, wait_one(bar, phase, abort_flag, status));
 }
 
 template <bool DUAL, int G, bool Z>
@@ -139,7 +152,7 @@ struct TcKernel {
   static constexpr int kCols = DUAL ? 128 : 256;  // of an item
 
   struct Bars {  // shared-memory addresses
-    uint32_t a_full, a_empty, x_full, x_empty, p_full, p_empty, done;
+    uint32_t full, empty, p_full, p_empty, done;
   };
   // Where record `i` (0..7) of tile m of an item starts.  One past the last
   // is the last again: its columns are not written.
@@ -177,22 +190,16 @@ struct TcKernel {
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const uint32_t sb = smem_u32(base);
     Bars b;
-    b.a_full = sb + m.bars;
-    b.a_empty = b.a_full + 8 * kAStages;
-    b.x_full = b.a_empty + 8 * kAStages;
-    b.x_empty = b.x_full + 8 * kXStages;
-    b.p_full = b.x_empty + 8 * kXStages;
+    b.full = sb + m.bars;
+    b.empty = b.full + 8 * kStages;
+    b.p_full = b.empty + 8 * kStages;
     b.p_empty = b.p_full + 16;
     b.done = b.p_empty + 16;
     if (threadIdx.x == 0) {
       abort_word = 0;
-      for (int i = 0; i < kAStages; ++i) {
-        mbar_init(b.a_full + 8 * i, kExpandWarps);
-        mbar_init(b.a_empty + 8 * i, 1);
-      }
-      for (int i = 0; i < kXStages; ++i) {
-        mbar_init(b.x_full + 8 * i, 1);
-        mbar_init(b.x_empty + 8 * i, 1);
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(b.full + 8 * i, kExpandWarps / 2 + 1);  // and x
+        mbar_init(b.empty + 8 * i, 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(b.p_full + 8 * i, 1);
@@ -207,7 +214,7 @@ struct TcKernel {
       tc::tmem_relinquish();
     }
     int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
-    const int n_active = find_active<18>(a, active);  // barriers within
+    const int n_active = find_active<kTcWarps>(a, active);  // barriers within
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -237,8 +244,8 @@ struct TcKernel {
                                       const int32_t* active, int n_items,
                                       int blocks, uint32_t tmem, int warp,
                                       int lane, volatile int* abort_flag) {
-    const int tiles_k = a.l.tiles_k(), t = warp / 4, q = warp % 4;
-    const int c = lane >> 2;
+    const int tiles_k = a.l.tiles_k(), t = warp / 4 % 2, q = warp % 4;
+    const int c = lane >> 2, turn = warp / 8;  // of the two sets of warps
     const uint32_t codes =
         sb + m.codes + warp * (kCodeTiles * 2 * kTileBytes) + lane * 16;
     const uint32_t zeros = sb + m.zeros + warp * (kZeroSlots * 2 * 16 * E);
@@ -246,68 +253,75 @@ struct TcKernel {
                           (static_cast<uint32_t>(32 * q) << 16);
     // the copying side, kCodeTiles tiles ahead
     int item = blockIdx.x, row = 0, r1 = 0, tile = 0, zslot = 0;
+    int sent = 0;  // tiles of the passes before: the sets take turns
     const char *p0 = nullptr, *p1 = nullptr, *s0 = nullptr, *s1 = nullptr;
     const auto enter = [&] {
       const int g = active[item / blocks];
       const int ex = a.map ? a.map[g] : g;
       row = max(0, a.offsets[g]);
       r1 = min(a.rows, a.offsets[g + 1]);
-      s0 = record(a, ex, item % blocks, t, 2 * q);
-      s1 = record(a, ex, item % blocks, t, 2 * q + 1);
-      p0 = s0 + lane * 16;
-      p1 = s1 + lane * 16;
-      tile = 0;
+      s0 = record(a, ex, item % blocks, t, 2 * q) + lane * 16;
+      s1 = record(a, ex, item % blocks, t, 2 * q + 1) + lane * 16;
     };
-    if (item < n_items) enter();
+    const auto rewind = [&] {  // to this set's first tile of a pass
+      tile = (sent ^ turn) & 1;
+      p0 = s0 + tile * kTileBytes;
+      p1 = s1 + tile * kTileBytes;
+    };
+    const auto next_pass = [&] {
+      sent += tiles_k;
+      row += kNR;
+      if (row >= r1) {
+        item += gridDim.x;
+        if (item < n_items) enter();
+      }
+      rewind();
+    };
+    if (item < n_items) {
+      enter();
+      rewind();
+      while (tile >= tiles_k && item < n_items) next_pass();
+    }
     int in_slot = 0;
     const auto copy_tile = [&] {
       if (item < n_items) {
         const uint32_t dst = codes + in_slot * (2 * kTileBytes);
         copy16(dst, p0);
         copy16(dst + kTileBytes, p1);
-        if (tile % kTiles == 0) {
-          if (Z && lane < E) {  // 16 E bytes of zero points
-            const int at =
-                min(tiles_k - tile, kTiles) * kTileBytes + 32 * E;
-            const uint32_t d = zeros + zslot * (2 * 16 * E) + lane * 16;
-            copy16(d, p0 + at);
-            copy16(d + 16 * E, p1 + at);
-          }
-          zslot = zslot == kZeroSlots - 1 ? 0 : zslot + 1;
+        if (Z && lane < E) {  // the step's zero points, 16 E bytes
+          const int at = tile % kTiles;  // the pointers are at this tile
+          const int to = (min(tiles_k - tile + at, kTiles) - at) * kTileBytes +
+                         32 * E;
+          const uint32_t d = zeros + zslot * (2 * 16 * E) + lane * 16;
+          copy16(d, p0 + to);
+          copy16(d + 16 * E, p1 + to);
         }
-        ++tile;
-        const int skip =
-            kTileBytes + (tile % kTiles == 0 ? kChunk - kTiles * kTileBytes
-                                             : 0);
+        // two tiles on, past a step's scales where they lie between
+        tile += 2;
+        const int skip = 2 * kTileBytes + (tile % kTiles < 2
+                                               ? kChunk - kTiles * kTileBytes
+                                               : 0);
         p0 += skip;
         p1 += skip;
-        if (tile == tiles_k) {
-          row += kNR;
-          if (row < r1) {  // the group's next rows: the same weights
-            p0 = s0 + lane * 16;
-            p1 = s1 + lane * 16;
-            tile = 0;
-          } else {
-            item += gridDim.x;
-            if (item < n_items) enter();
-          }
-        }
+        while (tile >= tiles_k && item < n_items) next_pass();
       }
       copies_commit();
       in_slot = in_slot == kCodeTiles - 1 ? 0 : in_slot + 1;
+      zslot = in_slot;
     };
 #pragma unroll 1
     for (int i = 0; i < kCodeTiles; ++i) copy_tile();
 
-    int slot = 0, zread = 0, as = 0;
+    int slot = 0, done = 0;  // done: tiles of the passes before
+    int as = turn;
     uint32_t phase = 1;
     passes(a, active, n_items, blocks, [&](int, int, int, int) {
       uint32_t z[2][2];
       z[0][0] = z[0][1] = z[1][0] = z[1][1] = 0xbe00be00u;  // -8/64
 #pragma unroll 1
-      for (int k = 0; k < tiles_k; ++k) {
+      for (int k = (done ^ turn) & 1; k < tiles_k; k += 2) {
         copies_wait<kCodeTiles - 1>();
-        if (Z && k % kTiles == 0) __syncwarp();
+        if (Z) __syncwarp();
         uint32_t w[2][4], op[2][4][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -321,7 +335,7 @@ struct TcKernel {
           for (int r = 0; r < 2; ++r) {
             if (Z && (h == 0 || G == 32)) {
               const int g = (k % kTiles * kTileK + 32 * h) / G;
-              const uint32_t v = lds2(zeros + zread * (2 * 16 * E) +
+              const uint32_t v = lds2(zeros + slot * (2 * 16 * E) +
                                       r * 16 * E + (c * E + g) * 2);
               constexpr uint32_t kMinus = kPow127 | 0x80008000u;
               z[r][0] = fma2(__byte_perm(v, 0, 0x4040), kMinus, 0);
@@ -331,12 +345,10 @@ struct TcKernel {
             expand(w[r][2 * h + 1], z[r], op[r][2 * h + 1]);
           }
         }
-        if (k % kTiles == kTiles - 1 || k == tiles_k - 1)
-          zread = zread == kZeroSlots - 1 ? 0 : zread + 1;
         if (Z) __syncwarp();  // every lane has read what is copied over
         copy_tile();
         slot = slot == kCodeTiles - 1 ? 0 : slot + 1;
-        if (!wait_all(b.a_empty + 8 * as, phase, abort_flag, a.status))
+        if (!wait_all(b.empty + 8 * as, phase, abort_flag, a.status))
           return false;
         tc_fence_after();
         const uint32_t at = a_at + as * 32;
@@ -345,12 +357,14 @@ struct TcKernel {
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b.a_full + 8 * as);
-        if (++as == kAStages) {
-          as = 0;
+        if (lane == 0) mbar_arrive(b.full + 8 * as);
+        as += 2;
+        if (as >= kStages) {
+          as = turn;
           phase ^= 1;
         }
       }
+      done += tiles_k;
       return true;
     });
     copies_wait<0>();
@@ -372,13 +386,13 @@ struct TcKernel {
 #pragma unroll 1
       for (int k = 0; k < tiles_k; ++k) {
         ok = (a.stall_after_fills < 0 || filled < a.stall_after_fills) &&
-             tc::mbar_wait(b.x_empty + 8 * xs, phase, abort_flag, a.status);
+             wait_one(b.empty + 8 * xs, phase, abort_flag, a.status);
         if (!ok) return false;
-        mbar_expect_tx(b.x_full + 8 * xs, kXBytes);
-        tc::tma_load_2d(sb + xs * kXBytes, map, b.x_full + 8 * xs,
+        mbar_expect_tx(b.full + 8 * xs, kXBytes);
+        tc::tma_load_2d(sb + xs * kXBytes, map, b.full + 8 * xs,
                         k * kTileK, row);
         ++filled;
-        if (++xs == kXStages) {
+        if (++xs == kStages) {
           xs = 0;
           phase ^= 1;
         }
@@ -387,12 +401,12 @@ struct TcKernel {
     });
     // after a wait that gave up: this thread's own copies
     if (!ok)
-      for (long long i = 0; i < filled && i < kXStages; ++i) {
+      for (long long i = 0; i < filled && i < kStages; ++i) {
         if (--xs < 0) {
-          xs = kXStages - 1;
+          xs = kStages - 1;
           phase ^= 1;
         }
-        tc::mbar_wait(b.x_full + 8 * xs, phase ^ 1, nullptr, a.status);
+        tc::mbar_wait(b.full + 8 * xs, phase ^ 1, nullptr, a.status);
       }
   }
 
@@ -401,60 +415,54 @@ struct TcKernel {
                                   const int32_t* active, int n_items,
                                   int blocks, uint32_t tmem, int lane,
                                   volatile int* abort_flag) {
-    if (lane != 0) return;
     const int tiles_k = a.l.tiles_k();
-    int as = 0, xs = 0, part = 0;
-    uint32_t a_phase = 0, x_phase = 0, p_phase = 1;
+    const bool leader = lane == 0;
+    int st = 0, part = 0;
+    uint32_t phase = 0, p_phase = 1;
     passes(a, active, n_items, blocks, [&](int, int, int row, int r1) {
       const int n = (min(kNR, r1 - row) + 15) / 16 * 16;
       const uint32_t idesc =
           tc::make_idesc(128, 16, false) + ((n - 16) >> 3 << 17);
 #pragma unroll 1
       for (int k = 0; k < tiles_k; ++k) {
-        if (!tc::mbar_wait(b.a_full + 8 * as, a_phase, abort_flag,
-                           a.status) ||
-            !tc::mbar_wait(b.x_full + 8 * xs, x_phase, abort_flag, a.status))
+        if (!wait_all(b.full + 8 * st, phase, abort_flag, a.status))
           return false;
         tc_fence_after();
+        const uint64_t bd = smem_desc(sb + st * kXBytes, 16, 1024);
+        const uint32_t at = tmem + kTmemA + st * 32;
 #pragma unroll
         for (int kk = 0; kk < kTileK / 16; ++kk) {
-          const int at = k * kTileK + kk * 16;
-          const bool first = at % G == 0;
-          if (first) {
-            if (!tc::mbar_wait(b.p_empty + 8 * part, p_phase, abort_flag,
-                               a.status))
+          const bool first = (k * kTileK + kk * 16) % G == 0;
+          if (kk * 16 % G == 0 && first) {
+            if (!wait_all(b.p_empty + 8 * part, p_phase, abort_flag,
+                          a.status))
               return false;
             tc_fence_after();
           }
-          const uint64_t bd = smem_desc(sb + xs * kXBytes + kk * 32, 16, 1024);
+          // 16 columns of x further on: 32 bytes, 2 in the descriptor
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            umma_ts(tmem + t * 128 + part * 64,
-                    tmem + kTmemA + t * 128 + as * 32 + kk * 8, bd, idesc,
-                    first ? 0u : 1u);
-          if ((at + 16) % G == 0 ||
-              (k == tiles_k - 1 && kk == kTileK / 16 - 1)) {
-            umma_commit(b.p_full + 8 * part);
-            part ^= 1;
-            if (part == 0) p_phase ^= 1;
+            umma_ts(leader, tmem + t * 128 + part * 64, at + t * 128 + kk * 8,
+                    bd + 2 * kk, idesc, first ? 0u : 1u);
+          if ((kk * 16 + 16) % G == 0 || kk == kTileK / 16 - 1) {
+            if ((k * kTileK + kk * 16 + 16) % G == 0 || k == tiles_k - 1) {
+              commit(leader, b.p_full + 8 * part);
+              part ^= 1;
+              if (part == 0) p_phase ^= 1;
+            }
           }
         }
-        umma_commit(b.a_empty + 8 * as);
-        umma_commit(b.x_empty + 8 * xs);
-        if (++as == kAStages) {
-          as = 0;
-          a_phase ^= 1;
-        }
-        if (++xs == kXStages) {
-          xs = 0;
-          x_phase ^= 1;
+        commit(leader, b.empty + 8 * st);
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
         }
       }
       return true;
     });
-    // drain: every instruction that this thread issued
-    umma_commit(b.done);
-    tc::mbar_wait(b.done, 0, nullptr, a.status);
+    // drain: every instruction that this warp issued
+    commit(leader, b.done);
+    if (leader) tc::mbar_wait(b.done, 0, nullptr, a.status);
   }
 
   // ---- scale * partial sums, a thread per column of W, and the output
@@ -499,12 +507,12 @@ struct TcKernel {
           tc_fence_after();
           const uint32_t d = tmem + lanes + t * 128 + part * 64;
 #pragma unroll
-          for (int i = 0; i < kNR; i += 16) {
+          for (int i = 0; i < kNR; i += 8) {
             if (i >= rows) break;
-            uint32_t v[16];
-            tmem_ld16(d + i, v);
+            uint32_t v[8];
+            tmem_ld8(d + i, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < 8; ++j)
               acc[i + j] = fmaf(s, __uint_as_float(v[j]), acc[i + j]);
           }
           tc_fence_before();
