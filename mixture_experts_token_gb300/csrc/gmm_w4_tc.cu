@@ -10,8 +10,8 @@
 //   have to take and give again, four bytes for each byte of codes, is twice
 //   its bandwidth at the rate HBM delivers codes.  A lane's words are in the
 //   order of the 16x128b store, so nothing is shuffled.
-// * One thread issues the matrix instructions, a group of rows of W at a
-//   time into one of two partial accumulators.
+// * Two warps, one for each tile, issue the matrix instructions, a group of
+//   rows of W at a time into one of two partial accumulators.
 // * Eight warps, a thread per column of W, add scale * partial in float32
 //   registers while the next group runs, and at the end write the rows.
 // * One thread brings x by TMA (rows past the group are other groups' rows
@@ -48,8 +48,9 @@ constexpr int kNR = 48;            // rows of a pass
 // rows of W, from 64 (w / 8) on.
 constexpr int kExpandWarps = 16;
 constexpr int kAddWarps = 8;       // tile w / 4, lanes 32 (w % 4)..
-constexpr int kMmaWarp = kExpandWarps + kAddWarps;  // the next one brings x
-constexpr int kTcWarps = kMmaWarp + 2;
+constexpr int kMmaWarp = kExpandWarps + kAddWarps;  // one for each tile
+constexpr int kCopyWarp = kMmaWarp + 2;
+constexpr int kTcWarps = kCopyWarp + 1;
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr int kStages = 4;         // 64 rows of W, and of x, each
 constexpr int kXBytes = kNR * 128;
@@ -151,7 +152,10 @@ struct TcKernel {
       kTiles * kTileBytes + 8 * E * (Z ? 6 : 4);  // bytes of a whole step
   static constexpr int kCols = DUAL ? 128 : 256;  // of an item
 
-  struct Bars {  // shared-memory addresses
+  // Shared-memory addresses.  A stage is full when both tiles' codes and x
+  // are there, and empty when both tiles' instructions have read it; partial
+  // sums have two buffers for each tile.
+  struct Bars {
     uint32_t full, empty, p_full, p_empty, done;
   };
   // Where record `i` (0..7) of tile m of an item starts.  One past the last
@@ -193,19 +197,20 @@ struct TcKernel {
     b.full = sb + m.bars;
     b.empty = b.full + 8 * kStages;
     b.p_full = b.empty + 8 * kStages;
-    b.p_empty = b.p_full + 16;
-    b.done = b.p_empty + 16;
+    b.p_empty = b.p_full + 32;
+    b.done = b.p_empty + 32;
     if (threadIdx.x == 0) {
       abort_word = 0;
       for (int i = 0; i < kStages; ++i) {
         mbar_init(b.full + 8 * i, kExpandWarps / 2 + 1);  // and x
-        mbar_init(b.empty + 8 * i, 1);
+        mbar_init(b.empty + 8 * i, 2);
       }
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         mbar_init(b.p_full + 8 * i, 1);
-        mbar_init(b.p_empty + 8 * i, kAddWarps);
+        mbar_init(b.p_empty + 8 * i, kAddWarps / 2);
       }
       mbar_init(b.done, 1);
+      mbar_init(b.done + 8, 1);
       fence_barrier_init();
       tc::fence_proxy_async_smem();
     }
@@ -227,8 +232,9 @@ struct TcKernel {
     else if (warp < kExpandWarps + kAddWarps)
       add_parts(a, reinterpret_cast<float*>(base + m.sums), b, active,
                 n_items, blocks, tmem, warp - kExpandWarps, lane, abort_flag);
-    else if (warp == kMmaWarp)
-      multiply(a, sb, b, active, n_items, blocks, tmem, lane, abort_flag);
+    else if (warp < kCopyWarp)
+      multiply(a, sb, b, active, n_items, blocks, tmem, warp - kMmaWarp, lane,
+               abort_flag);
     else
       copy_rows(a, map, sb, b, active, n_items, blocks, lane, abort_flag);
     __syncwarp();
@@ -413,9 +419,11 @@ struct TcKernel {
   // ---- the matrix instructions: one partial sum for each group of W's rows
   __device__ static void multiply(const TcArgs& a, uint32_t sb, const Bars& b,
                                   const int32_t* active, int n_items,
-                                  int blocks, uint32_t tmem, int lane,
+                                  int blocks, uint32_t tmem, int t, int lane,
                                   volatile int* abort_flag) {
     const int tiles_k = a.l.tiles_k();
+    const uint32_t p_full = b.p_full + 16 * t, p_empty = b.p_empty + 16 * t;
+    const uint32_t d = tmem + t * 128, a_at = tmem + kTmemA + t * 128;
     const bool leader = lane == 0;
     int st = 0, part = 0;
     uint32_t phase = 0, p_phase = 1;
@@ -429,24 +437,22 @@ struct TcKernel {
           return false;
         tc_fence_after();
         const uint64_t bd = smem_desc(sb + st * kXBytes, 16, 1024);
-        const uint32_t at = tmem + kTmemA + st * 32;
+        const uint32_t at = a_at + st * 32;
 #pragma unroll
         for (int kk = 0; kk < kTileK / 16; ++kk) {
           const bool first = (k * kTileK + kk * 16) % G == 0;
           if (kk * 16 % G == 0 && first) {
-            if (!wait_all(b.p_empty + 8 * part, p_phase, abort_flag,
+            if (!wait_all(p_empty + 8 * part, p_phase, abort_flag,
                           a.status))
               return false;
             tc_fence_after();
           }
           // 16 columns of x further on: 32 bytes, 2 in the descriptor
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            umma_ts(leader, tmem + t * 128 + part * 64, at + t * 128 + kk * 8,
-                    bd + 2 * kk, idesc, first ? 0u : 1u);
+          umma_ts(leader, d + part * 64, at + kk * 8, bd + 2 * kk, idesc,
+                  first ? 0u : 1u);
           if ((kk * 16 + 16) % G == 0 || kk == kTileK / 16 - 1) {
             if ((k * kTileK + kk * 16 + 16) % G == 0 || k == tiles_k - 1) {
-              commit(leader, b.p_full + 8 * part);
+              commit(leader, p_full + 8 * part);
               part ^= 1;
               if (part == 0) p_phase ^= 1;
             }
@@ -461,8 +467,8 @@ struct TcKernel {
       return true;
     });
     // drain: every instruction that this warp issued
-    commit(leader, b.done);
-    if (leader) tc::mbar_wait(b.done, 0, nullptr, a.status);
+    commit(leader, b.done + 8 * t);
+    if (leader) tc::mbar_wait(b.done + 8 * t, 0, nullptr, a.status);
   }
 
   // ---- scale * partial sums, a thread per column of W, and the output
@@ -502,7 +508,8 @@ struct TcKernel {
         const float s = __uint_as_float(static_cast<uint32_t>(next) << 16);
         if (g + 1 < groups) next = load_scale(g + 1);
         if (ok)
-          ok = wait_all(b.p_full + 8 * part, phase, abort_flag, a.status);
+          ok = wait_all(b.p_full + 16 * t + 8 * part, phase, abort_flag,
+                        a.status);
         if (ok) {
           tc_fence_after();
           const uint32_t d = tmem + lanes + t * 128 + part * 64;
@@ -517,7 +524,7 @@ struct TcKernel {
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b.p_empty + 8 * part);
+          if (lane == 0) mbar_arrive(b.p_empty + 16 * t + 8 * part);
         }
         part ^= 1;
         if (part == 0) phase ^= 1;
