@@ -145,6 +145,20 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase,
   return __all_sync(0xffffffffu, wait_one(bar, phase, abort_flag, status));
 }
 
+// A look ahead at a barrier, without waiting: asked before other work, its
+// answer is there after it.
+__device__ __forceinline__ bool ready(uint32_t bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(phase)
+      : "memory");
+  return ok != 0;
+}
+
 template <bool DUAL, int G, bool Z>
 struct TcKernel {
   static constexpr int E = kStepK / G;
@@ -427,26 +441,31 @@ struct TcKernel {
     const bool leader = lane == 0;
     int st = 0, part = 0;
     uint32_t phase = 0, p_phase = 1;
+    bool full = false, p_empty_now = false;  // as seen ahead
     passes(a, active, n_items, blocks, [&](int, int, int row, int r1) {
       const int n = (min(kNR, r1 - row) + 15) / 16 * 16;
       const uint32_t idesc =
           tc::make_idesc(128, 16, false) + ((n - 16) >> 3 << 17);
 #pragma unroll 1
       for (int k = 0; k < tiles_k; ++k) {
-        if (!wait_all(b.full + 8 * st, phase, abort_flag, a.status))
+        if (!__all_sync(0xffffffffu, full) &&
+            !wait_all(b.full + 8 * st, phase, abort_flag, a.status))
           return false;
         tc_fence_after();
+        const int st_next = st == kStages - 1 ? 0 : st + 1;
+        const uint32_t phase_next = st_next == 0 ? phase ^ 1 : phase;
         const uint64_t bd = smem_desc(sb + st * kXBytes, 16, 1024);
         const uint32_t at = a_at + st * 32;
 #pragma unroll
         for (int kk = 0; kk < kTileK / 16; ++kk) {
           const bool first = (k * kTileK + kk * 16) % G == 0;
           if (kk * 16 % G == 0 && first) {
-            if (!wait_all(p_empty + 8 * part, p_phase, abort_flag,
-                          a.status))
+            if (!__all_sync(0xffffffffu, p_empty_now) &&
+                !wait_all(p_empty + 8 * part, p_phase, abort_flag, a.status))
               return false;
             tc_fence_after();
           }
+          if (kk == 0) full = ready(b.full + 8 * st_next, phase_next);
           // 16 columns of x further on: 32 bytes, 2 in the descriptor
           umma_ts(leader, d + part * 64, at + kk * 8, bd + 2 * kk, idesc,
                   first ? 0u : 1u);
@@ -455,14 +474,13 @@ struct TcKernel {
               commit(leader, p_full + 8 * part);
               part ^= 1;
               if (part == 0) p_phase ^= 1;
+              p_empty_now = ready(p_empty + 8 * part, p_phase);
             }
           }
         }
         commit(leader, b.empty + 8 * st);
-        if (++st == kStages) {
-          st = 0;
-          phase ^= 1;
-        }
+        st = st_next;
+        phase = phase_next;
       }
       return true;
     });
