@@ -44,20 +44,23 @@ using tc::tc_fence_before;
 using tc::umma_commit;
 
 constexpr int kNR = 48;            // rows of a pass
-// Warps that expand: tile w / 4 % 2, lanes 32 (w % 4).., and every second 64
-// rows of W, from 64 (w / 8) on.
+// Warps that expand: tile w / 4 % 2, lanes 32 (w % 4).., and the first or the
+// second 64 rows of W of every stage (w / 8).
 constexpr int kExpandWarps = 16;
 constexpr int kAddWarps = 8;       // tile w / 4, lanes 32 (w % 4)..
 constexpr int kMmaWarp = kExpandWarps + kAddWarps;  // one for each tile
 constexpr int kCopyWarp = kMmaWarp + 2;
 constexpr int kTcWarps = kCopyWarp + 1;
 constexpr int kTcThreads = kTcWarps * 32;
-constexpr int kStages = 4;         // 64 rows of W, and of x, each
-constexpr int kXBytes = kNR * 128;
+constexpr int kStageK = 128;       // rows of W in a stage: two tiles
+constexpr int kStages = 2;
+constexpr int kXStages = 4;        // further ahead: x comes from L2 or HBM
+constexpr int kXBytes = kNR * 128;  // 64 columns of x
 constexpr int kCodeTiles = 4;      // tiles of codes in flight, of each warp
 constexpr int kZeroSlots = kCodeTiles;  // zero points, with each tile
 constexpr int kTmemA = 256;        // columns: accumulators, then A
 constexpr int kSumPitch = kNR + 1;
+constexpr unsigned kSleepNs = 100;
 
 struct TcArgs {
   const int32_t *offsets, *map;
@@ -75,32 +78,52 @@ struct TcSmem {
 };
 __host__ __device__ inline TcSmem tc_smem(const Layout& l, int n_groups) {
   TcSmem m;
-  m.codes = kStages * kXBytes;
+  m.codes = kXStages * 2 * kXBytes;
   m.zeros = m.codes + kExpandWarps * kCodeTiles * 2 * kTileBytes;
   m.sums = m.zeros + (l.zeros ? kExpandWarps * kZeroSlots * 2 * 16 *
                                     (kStepK / l.group)
                               : 0);
   m.bars = m.sums + 128 * kSumPitch * 4;
-  m.groups = m.bars + 256;
+  m.groups = m.bars + 512;
   m.total = m.groups + 4 * n_groups;
   return m;
 }
 
-// D (+)= A B with A in tensor memory; `leader` in one lane of the warp.  The
-// whole warp runs the loop around it: the operands then are uniform, and
-// need not be moved from one lane's registers for every instruction.
+// D (+)= A B over N16 * 16 of k, with A in tensor memory (8 columns for each
+// 16 of k) and B in shared memory (32 bytes, 2 in the descriptor); `leader`
+// in one lane of the warp.  The whole warp runs the loop around it: the
+// operands then are uniform, and need not be moved from one lane's registers
+// for every instruction.
+template <int N16>
 __device__ __forceinline__ void umma_ts(bool leader, uint32_t d, uint32_t a,
                                         uint64_t b, uint32_t idesc,
                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::
-          "r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate),
-      "r"(static_cast<uint32_t>(leader))
-      : "memory");
+  if (!leader) return;
+  if (N16 == 4)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t"
+        ".reg .b64 b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %4, %4;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\t"
+        "add.u32 a3, %1, 24;\n\tadd.u64 b1, %2, 2;\n\t"
+        "add.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}\n" ::
+            "r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %4, %4;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, 2;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t}\n" ::
+            "r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 __device__ __forceinline__ void commit(bool leader, uint32_t bar) {
   if (leader) umma_commit(bar);
@@ -132,12 +155,32 @@ __device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
       : "memory");
 }
 
+// Sleeps between looks, so that the many warps that wait leave the issue
+// slots and the shared-memory pipe to those that work.
+static __device__ __noinline__ bool wait_asleep(uint32_t bar, uint32_t phase,
+                                                volatile int* abort_flag,
+                                                int32_t* status) {
+  const uint64_t t0 = tc::globaltimer();
+  uint32_t looks = 0;
+  while (true) {
+    __nanosleep(kSleepNs);
+    if (tc::mbar_try_wait(bar, phase)) return true;
+    if ((++looks & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (tc::globaltimer() - t0 > tc::kWaitLimitNs) {
+        *abort_flag = 1;
+        if (status) atomicOr(status, MOE_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
 // The first look is inline: a call costs several hundred clocks here.
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t phase,
                                          volatile int* abort_flag,
                                          int32_t* status) {
   return tc::mbar_try_wait(bar, phase) ||
-         tc::mbar_wait(bar, phase, abort_flag, status);
+         wait_asleep(bar, phase, abort_flag, status);
 }
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase,
                                          volatile int* abort_flag,
@@ -166,11 +209,11 @@ struct TcKernel {
       kTiles * kTileBytes + 8 * E * (Z ? 6 : 4);  // bytes of a whole step
   static constexpr int kCols = DUAL ? 128 : 256;  // of an item
 
-  // Shared-memory addresses.  A stage is full when both tiles' codes and x
-  // are there, and empty when both tiles' instructions have read it; partial
-  // sums have two buffers for each tile.
+  // Shared-memory addresses.  A stage is full when both tiles' codes are
+  // there, and empty when both tiles' instructions have read it; the same for
+  // x; partial sums have two buffers for each tile.
   struct Bars {
-    uint32_t full, empty, p_full, p_empty, done;
+    uint32_t full, empty, x_full, x_empty, p_full, p_empty, done;
   };
   // Where record `i` (0..7) of tile m of an item starts.  One past the last
   // is the last again: its columns are not written.
@@ -210,14 +253,20 @@ struct TcKernel {
     Bars b;
     b.full = sb + m.bars;
     b.empty = b.full + 8 * kStages;
-    b.p_full = b.empty + 8 * kStages;
+    b.x_full = b.empty + 8 * kStages;
+    b.x_empty = b.x_full + 8 * kXStages;
+    b.p_full = b.x_empty + 8 * kXStages;
     b.p_empty = b.p_full + 32;
     b.done = b.p_empty + 32;
     if (threadIdx.x == 0) {
       abort_word = 0;
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(b.full + 8 * i, kExpandWarps / 2 + 1);  // and x
+        mbar_init(b.full + 8 * i, kExpandWarps);
         mbar_init(b.empty + 8 * i, 2);
+      }
+      for (int i = 0; i < kXStages; ++i) {
+        mbar_init(b.x_full + 8 * i, 1);
+        mbar_init(b.x_empty + 8 * i, 2);
       }
       for (int i = 0; i < 4; ++i) {
         mbar_init(b.p_full + 8 * i, 1);
@@ -265,7 +314,7 @@ struct TcKernel {
                                       int blocks, uint32_t tmem, int warp,
                                       int lane, volatile int* abort_flag) {
     const int tiles_k = a.l.tiles_k(), t = warp / 4 % 2, q = warp % 4;
-    const int c = lane >> 2, turn = warp / 8;  // of the two sets of warps
+    const int c = lane >> 2, turn = warp / 8;  // tile of a stage
     const uint32_t codes =
         sb + m.codes + warp * (kCodeTiles * 2 * kTileBytes) + lane * 16;
     const uint32_t zeros = sb + m.zeros + warp * (kZeroSlots * 2 * 16 * E);
@@ -273,7 +322,6 @@ struct TcKernel {
                           (static_cast<uint32_t>(32 * q) << 16);
     // the copying side, kCodeTiles tiles ahead
     int item = blockIdx.x, row = 0, r1 = 0, tile = 0, zslot = 0;
-    int sent = 0;  // tiles of the passes before: the sets take turns
     const char *p0 = nullptr, *p1 = nullptr, *s0 = nullptr, *s1 = nullptr;
     const auto enter = [&] {
       const int g = active[item / blocks];
@@ -284,12 +332,11 @@ struct TcKernel {
       s1 = record(a, ex, item % blocks, t, 2 * q + 1) + lane * 16;
     };
     const auto rewind = [&] {  // to this set's first tile of a pass
-      tile = (sent ^ turn) & 1;
+      tile = turn;
       p0 = s0 + tile * kTileBytes;
       p1 = s1 + tile * kTileBytes;
     };
     const auto next_pass = [&] {
-      sent += tiles_k;
       row += kNR;
       if (row >= r1) {
         item += gridDim.x;
@@ -332,59 +379,62 @@ struct TcKernel {
 #pragma unroll 1
     for (int i = 0; i < kCodeTiles; ++i) copy_tile();
 
-    int slot = 0, done = 0;  // done: tiles of the passes before
-    int as = turn;
+    int slot = 0, st = 0;
     uint32_t phase = 1;
     passes(a, active, n_items, blocks, [&](int, int, int, int) {
       uint32_t z[2][2];
       z[0][0] = z[0][1] = z[1][0] = z[1][1] = 0xbe00be00u;  // -8/64
 #pragma unroll 1
-      for (int k = (done ^ turn) & 1; k < tiles_k; k += 2) {
-        copies_wait<kCodeTiles - 1>();
-        if (Z) __syncwarp();
-        uint32_t w[2][4], op[2][4][4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint4 v =
-              lds16(codes + slot * (2 * kTileBytes) + r * kTileBytes);
-          w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+      for (int k = turn; k < tiles_k + turn; k += 2) {
+        uint32_t op[2][4][4];
+        const bool here = k < tiles_k;  // else the stage has one tile
+        if (here) {
+          copies_wait<kCodeTiles - 1>();
+          if (Z) __syncwarp();
+          uint32_t w[2][4];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            if (Z && (h == 0 || G == 32)) {
-              const int g = (k % kTiles * kTileK + 32 * h) / G;
-              const uint32_t v = lds2(zeros + slot * (2 * 16 * E) +
-                                      r * 16 * E + (c * E + g) * 2);
-              constexpr uint32_t kMinus = kPow127 | 0x80008000u;
-              z[r][0] = fma2(__byte_perm(v, 0, 0x4040), kMinus, 0);
-              z[r][1] = fma2(__byte_perm(v, 0, 0x4141), kMinus, 0);
-            }
-            expand(w[r][2 * h], z[r], op[r][2 * h]);
-            expand(w[r][2 * h + 1], z[r], op[r][2 * h + 1]);
+            const uint4 v =
+                lds16(codes + slot * (2 * kTileBytes) + r * kTileBytes);
+            w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
           }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if (Z && (h == 0 || G == 32)) {
+                const int g = (k % kTiles * kTileK + 32 * h) / G;
+                const uint32_t v = lds2(zeros + slot * (2 * 16 * E) +
+                                        r * 16 * E + (c * E + g) * 2);
+                constexpr uint32_t kMinus = kPow127 | 0x80008000u;
+                z[r][0] = fma2(__byte_perm(v, 0, 0x4040), kMinus, 0);
+                z[r][1] = fma2(__byte_perm(v, 0, 0x4141), kMinus, 0);
+              }
+              expand(w[r][2 * h], z[r], op[r][2 * h]);
+              expand(w[r][2 * h + 1], z[r], op[r][2 * h + 1]);
+            }
+          }
+          if (Z) __syncwarp();  // every lane has read what is copied over
+          copy_tile();
+          slot = slot == kCodeTiles - 1 ? 0 : slot + 1;
         }
-        if (Z) __syncwarp();  // every lane has read what is copied over
-        copy_tile();
-        slot = slot == kCodeTiles - 1 ? 0 : slot + 1;
-        if (!wait_all(b.empty + 8 * as, phase, abort_flag, a.status))
+        if (!wait_all(b.empty + 8 * st, phase, abort_flag, a.status))
           return false;
-        tc_fence_after();
-        const uint32_t at = a_at + as * 32;
-        tmem_st_operands(at, op[0]);
-        tmem_st_operands(at + (16u << 16), op[1]);
-        tmem_st_wait();
-        tc_fence_before();
+        if (here) {
+          tc_fence_after();
+          const uint32_t at = a_at + st * 64 + turn * 32;
+          tmem_st_operands(at, op[0]);
+          tmem_st_operands(at + (16u << 16), op[1]);
+          tmem_st_wait();
+          tc_fence_before();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(b.full + 8 * as);
-        as += 2;
-        if (as >= kStages) {
-          as = turn;
+        if (lane == 0) mbar_arrive(b.full + 8 * st);
+        if (++st == kStages) {
+          st = 0;
           phase ^= 1;
         }
       }
-      done += tiles_k;
       return true;
     });
     copies_wait<0>();
@@ -404,15 +454,17 @@ struct TcKernel {
     bool ok = true;
     passes(a, active, n_items, blocks, [&](int, int, int row, int) {
 #pragma unroll 1
-      for (int k = 0; k < tiles_k; ++k) {
+      for (int k = 0; k < tiles_k; k += 2) {
         ok = (a.stall_after_fills < 0 || filled < a.stall_after_fills) &&
-             wait_one(b.empty + 8 * xs, phase, abort_flag, a.status);
+             wait_one(b.x_empty + 8 * xs, phase, abort_flag, a.status);
         if (!ok) return false;
-        mbar_expect_tx(b.full + 8 * xs, kXBytes);
-        tc::tma_load_2d(sb + xs * kXBytes, map, b.full + 8 * xs,
-                        k * kTileK, row);
+        const int n = min(2, tiles_k - k);
+        mbar_expect_tx(b.x_full + 8 * xs, n * kXBytes);
+        for (int i = 0; i < n; ++i)
+          tc::tma_load_2d(sb + (2 * xs + i) * kXBytes, map,
+                          b.x_full + 8 * xs, (k + i) * kTileK, row);
         ++filled;
-        if (++xs == kStages) {
+        if (++xs == kXStages) {
           xs = 0;
           phase ^= 1;
         }
@@ -421,12 +473,12 @@ struct TcKernel {
     });
     // after a wait that gave up: this thread's own copies
     if (!ok)
-      for (long long i = 0; i < filled && i < kStages; ++i) {
+      for (long long i = 0; i < filled && i < kXStages; ++i) {
         if (--xs < 0) {
-          xs = kStages - 1;
+          xs = kXStages - 1;
           phase ^= 1;
         }
-        tc::mbar_wait(b.full + 8 * xs, phase ^ 1, nullptr, a.status);
+        tc::mbar_wait(b.x_full + 8 * xs, phase ^ 1, nullptr, a.status);
       }
   }
 
@@ -439,46 +491,57 @@ struct TcKernel {
     const uint32_t p_full = b.p_full + 16 * t, p_empty = b.p_empty + 16 * t;
     const uint32_t d = tmem + t * 128, a_at = tmem + kTmemA + t * 128;
     const bool leader = lane == 0;
-    int st = 0, part = 0;
-    uint32_t phase = 0, p_phase = 1;
-    bool full = false, p_empty_now = false;  // as seen ahead
+    int st = 0, xs = 0, part = 0;
+    uint32_t phase = 0, x_phase = 0, p_phase = 1;
+    bool full = false, x_full = false, empty = false;  // the next ones, as seen ahead
     passes(a, active, n_items, blocks, [&](int, int, int row, int r1) {
       const int n = (min(kNR, r1 - row) + 15) / 16 * 16;
       const uint32_t idesc =
           tc::make_idesc(128, 16, false) + ((n - 16) >> 3 << 17);
 #pragma unroll 1
-      for (int k = 0; k < tiles_k; ++k) {
+      for (int k = 0; k < tiles_k; k += 2) {
         if (!__all_sync(0xffffffffu, full) &&
             !wait_all(b.full + 8 * st, phase, abort_flag, a.status))
+          return false;
+        if (!__all_sync(0xffffffffu, x_full) &&
+            !wait_all(b.x_full + 8 * xs, x_phase, abort_flag, a.status))
           return false;
         tc_fence_after();
         const int st_next = st == kStages - 1 ? 0 : st + 1;
         const uint32_t phase_next = st_next == 0 ? phase ^ 1 : phase;
-        const uint64_t bd = smem_desc(sb + st * kXBytes, 16, 1024);
-        const uint32_t at = a_at + st * 32;
+        const int xs_next = xs == kXStages - 1 ? 0 : xs + 1;
+        const uint32_t x_phase_next = xs_next == 0 ? x_phase ^ 1 : x_phase;
+        const uint64_t bd = smem_desc(sb + xs * 2 * kXBytes, 16, 1024);
+        const uint32_t at = a_at + st * 64;
+        full = ready(b.full + 8 * st_next, phase_next);
+        x_full = ready(b.x_full + 8 * xs_next, x_phase_next);
+        constexpr int kN16 = G == 32 ? 2 : 4;  // instructions in a row
 #pragma unroll
-        for (int kk = 0; kk < kTileK / 16; ++kk) {
-          const bool first = (k * kTileK + kk * 16) % G == 0;
-          if (kk * 16 % G == 0 && first) {
-            if (!__all_sync(0xffffffffu, p_empty_now) &&
+        for (int h = 0; h < kStageK / 16; h += kN16) {
+          if (h >= 4 && k + 1 == tiles_k) break;  // a stage of one tile
+          const bool first = h * 16 % G == 0;
+          if (first) {
+            if (!__all_sync(0xffffffffu, empty) &&
                 !wait_all(p_empty + 8 * part, p_phase, abort_flag, a.status))
               return false;
             tc_fence_after();
           }
-          if (kk == 0) full = ready(b.full + 8 * st_next, phase_next);
-          // 16 columns of x further on: 32 bytes, 2 in the descriptor
-          umma_ts(leader, d + part * 64, at + kk * 8, bd + 2 * kk, idesc,
-                  first ? 0u : 1u);
-          if ((kk * 16 + 16) % G == 0 || kk == kTileK / 16 - 1) {
-            if ((k * kTileK + kk * 16 + 16) % G == 0 || k == tiles_k - 1) {
-              commit(leader, p_full + 8 * part);
-              part ^= 1;
-              if (part == 0) p_phase ^= 1;
-              p_empty_now = ready(p_empty + 8 * part, p_phase);
-            }
+          // the second tile's x is a box further on
+          umma_ts<kN16>(leader, d + part * 64, at + h * 8,
+                        bd + (h / 4 * (kXBytes >> 4) + h % 4 * 2), idesc,
+                        first ? 0u : 1u);
+          if ((h + kN16) * 16 % G == 0 ||
+              (h + kN16 == 4 && k + 1 == tiles_k)) {
+            commit(leader, p_full + 8 * part);
+            part ^= 1;
+            if (part == 0) p_phase ^= 1;
+            empty = ready(p_empty + 8 * part, p_phase);
           }
         }
         commit(leader, b.empty + 8 * st);
+        commit(leader, b.x_empty + 8 * xs);
+        xs = xs_next;
+        x_phase = x_phase_next;
         st = st_next;
         phase = phase_next;
       }
