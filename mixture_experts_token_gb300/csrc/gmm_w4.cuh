@@ -51,7 +51,7 @@ cudaError_t launch_gmm_w4_bf16(bool dual, const GmmArgs& a, int tokens,
 cudaError_t launch_gmm_w4_f32(bool dual, const GmmArgs& a, int tokens,
                               cudaStream_t s);
 // Groups of many bf16 rows (gmm_w4_tc.cu).
-cudaError_t launch_gmm_w4_tc(bool dual, const GmmArgs& a, cudaStream_t s);
+cudaError_t launch_gmm_w4_tc(bool dual, GmmArgs a, cudaStream_t s);
 
 constexpr int kTiles = kStepK / kTileK;  // tiles of a step
 constexpr int kUnit = 2;                 // tiles copied and waited for at once
@@ -67,6 +67,8 @@ struct GmmArgs {
   int32_t* status;
   Layout l;
   int n_experts, n_groups, rows;
+  int chunk;   // rows of a group that one work item takes
+  int chunks;  // at most so many in all
   int x_rows;  // rows of x that a slot holds: those of one pass
   bool early;  // may start before the kernel that writes x has ended
 };
@@ -161,36 +163,51 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) {
   *p = __float2bfloat16(v);
 }
 
-// The groups that have rows and an expert, in order; their number.
+// The chunks of rows of the groups that have rows and an expert, in order:
+// (group, first row); their number.
 template <int WARPS, typename A>
-__device__ int find_active(const A& a, int32_t* active) {
+__device__ int find_chunks(const A& a, int2* chunks) {
   __shared__ int count[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int total = 0;
   for (int g0 = 0; g0 < a.n_groups; g0 += WARPS * 32) {
     const int g = g0 + threadIdx.x;
-    bool on = false;
+    int n = 0, row = 0;
     if (g < a.n_groups) {
-      on = min(a.rows, a.offsets[g + 1]) > max(0, a.offsets[g]);
-      const int ex = on && a.map ? a.map[g] : g < a.n_experts ? g : -1;
-      if (on && (ex < 0 || ex >= a.n_experts)) {
-        on = false;
+      row = max(0, a.offsets[g]);
+      const int rows = min(a.rows, a.offsets[g + 1]) - row;
+      if (rows > 0) n = (rows - 1) / a.chunk + 1;
+      const int ex = n > 0 && a.map ? a.map[g] : g < a.n_experts ? g : -1;
+      if (n > 0 && (ex < 0 || ex >= a.n_experts)) {
+        n = 0;
         if (blockIdx.x == 0 && a.status)
           atomicOr(a.status, MOE_DEV_BAD_INDEX);
       }
     }
-    const uint32_t vote = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) count[warp] = __popc(vote);
+    int upto = n;  // of this warp's groups, this one's included
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int below = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += below;
+    }
+    if (lane == 31) count[warp] = upto;
     __syncthreads();
-    int before = total;
+    int at = total + upto - n;
     for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += count[w];
+      if (w < warp) at += count[w];
       total += count[w];
     }
-    if (on) active[before + __popc(vote & ((1u << lane) - 1))] = g;
+    // offsets that overlap could make more than there is room for
+    for (int i = 0; i < n && at + i < a.chunks; ++i)
+      chunks[at + i] = make_int2(g, row + i * a.chunk);
     __syncthreads();
   }
-  return total;
+  return min(total, a.chunks);
+}
+// The end of the chunk's rows.
+template <typename A>
+__device__ __forceinline__ int chunk_end(const A& a, int2 c) {
+  return min(min(a.rows, a.offsets[c.x + 1]), c.y + a.chunk);
 }
 
 // The operands of 32 k of eight rows of x: P parts, two instructions each.
@@ -282,32 +299,32 @@ struct Kernel {
   struct Smem {
     int x, x_slot, scales, sums, groups, total;
   };
-  __host__ __device__ static Smem smem(int x_rows, int n_groups) {
+  __host__ __device__ static Smem smem(int x_rows, int chunks) {
     Smem m;
     m.x = kWarps * kRing * kTilePair;
     m.x_slot = (kShareX ? 1 : kWarps) * x_rows * kPitch;
     m.scales = m.x + kXSlots * m.x_slot;
     m.sums = m.scales + kXSlots * kWarps * 2 * kScaleRec;
     m.groups = m.sums + (KW > 1 ? kWarps * 2 * kRows * kTileN * 4 : 0);
-    m.total = m.groups + 4 * n_groups + 16;
+    m.total = m.groups + 8 * chunks + 16;
     return m;
   }
 
   __device__ static void run(const GmmArgs& a) {
     extern __shared__ __align__(128) char base[];
     const Layout l = a.l;
-    const Smem m = smem(a.x_rows, a.n_groups);
+    const Smem m = smem(a.x_rows, a.chunks);
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int nw = warp % NW, kw = warp / NW;
     const int c = lane >> 2, t = lane & 3;
     const int tiles_k = l.tiles_k(), n_steps = l.steps();
     const uint32_t sb = smem_u32(base);
-    int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
+    int2* chunks = reinterpret_cast<int2*>(base + m.groups);
     launch::let_next_start();
-    const int n_active = find_active<kWarps>(a, active);  // a barrier within
+    const int n_chunks = find_chunks<kWarps>(a, chunks);  // a barrier within
     const int blocks = (l.N + kCols - 1) / kCols;
-    const int n_items = n_active * blocks;
+    const int n_items = n_chunks * blocks;
 
     // --- the copying side, two steps ahead: this lane's place in the
     // warp's records of the cursor's step, and in the rows of x
@@ -330,10 +347,11 @@ struct Kernel {
       xp = a.x + (in.row + x_first) * row_bytes + kw * kStepBytes + x_word;
     };
     const auto enter = [&] {  // the item's group and records
-      const int g = active[in.item / blocks], nb = in.item % blocks;
-      const int ex = a.map ? a.map[g] : g;
-      in.row = max(0, a.offsets[g]);
-      in.r1 = min(a.rows, a.offsets[g + 1]);
+      const int2 chunk = chunks[in.item / blocks];
+      const int nb = in.item % blocks;
+      const int ex = a.map ? a.map[chunk.x] : chunk.x;
+      in.row = chunk.y;
+      in.r1 = chunk_end(a, chunk);
       // a record past the last one is the last again: its columns are not
       // written
       const int rec = DUAL ? nb * NW + nw : 2 * (nb * NW + nw);
@@ -447,10 +465,10 @@ struct Kernel {
                  min(8 * b + Rows<T>::row(lane), a.x_rows - 1) * kPitch;
 #pragma unroll 1
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-      const int g = active[item / blocks];
-      const int r1 = min(a.rows, a.offsets[g + 1]);
+      const int2 chunk = chunks[item / blocks];
+      const int r1 = chunk_end(a, chunk);
 #pragma unroll 1
-      for (int row = max(0, a.offsets[g]); row < r1; row += a.x_rows) {
+      for (int row = chunk.y; row < r1; row += a.x_rows) {
         const int rows = min(a.x_rows, r1 - row);
         float acc[2][NT][4];
 #pragma unroll
@@ -646,17 +664,29 @@ __global__ void __launch_bounds__(
   Kernel<T, DUAL, NW, KW, NT, G, Z>::run(a);
 }
 
+// Chunks of as few passes of `rows` rows as leave at most kMaxSplits more
+// than there are groups.  CTAs that take chunks of one group at the same time
+// share its weights in L2.
+constexpr int kMaxSplits = 512;
+inline void set_chunk(GmmArgs* a, int rows) {
+  const long long most = static_cast<long long>(rows) * kMaxSplits;
+  a->chunk = rows * static_cast<int>((a->rows + most - 1) / most);
+  a->chunks = std::min(a->n_groups, a->rows) + a->rows / a->chunk;
+}
+
 template <typename T, bool DUAL, int NW, int KW, int NT, int G, bool Z>
 cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
                        cudaStream_t s) {
   using Ker = Kernel<T, DUAL, NW, KW, NT, G, Z>;
-  // routing gives a group at most one row of each token; float32 rows of
-  // eight warps' k fill shared memory at half the rows
+  // routing gives a group at most one row of each token; float32 rows that
+  // every warp copies for itself fill shared memory sooner
   a.x_rows = std::max(1, std::min(Ker::kRows, tokens));
-  int bytes = Ker::smem(a.x_rows, a.n_groups).total;
+  set_chunk(&a, a.x_rows);
+  int bytes = Ker::smem(a.x_rows, a.chunks).total;
   while (bytes + 1024 > d.smem_sm && a.x_rows > 1) {
     a.x_rows /= 2;
-    bytes = Ker::smem(a.x_rows, a.n_groups).total;
+    set_chunk(&a, a.x_rows);
+    bytes = Ker::smem(a.x_rows, a.chunks).total;
   }
   constexpr auto kernel = gmm_w4_kernel<T, DUAL, NW, KW, NT, G, Z>;
   const cudaError_t e = launch::allow_shared<kernel>(d);
@@ -664,7 +694,7 @@ cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
   const int per_sm = std::min(Ker::kPerSm, d.smem_sm / (bytes + 1024));
   const long long items =
       static_cast<long long>((a.l.N + Ker::kCols - 1) / Ker::kCols) *
-      std::min(a.n_groups, a.rows);
+      a.chunks;
   const unsigned grid = static_cast<unsigned>(
       std::min<long long>(items, static_cast<long long>(per_sm) * d.sms));
   if (a.early)
@@ -678,16 +708,28 @@ cudaError_t launch_shape(const GmmArgs& a, int tokens, cudaStream_t s) {
   Device d;
   const cudaError_t e = launch::device(&d);
   if (e != cudaSuccess) return e;
+  // Work items of 128 columns (of both matrices, or 256 of the one), if rows
+  // spread evenly over the groups and a pass takes `rows` of them.
   const long long groups = std::min(a.n_groups, a.rows);
-  const long long items =
-      groups * ((a.l.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
-  if (tokens <= 8 && items < 4ll * d.sms)
+  const long long each = (a.rows + groups - 1) / groups;
+  const auto items = [&](int rows) {
+    return groups * ((a.l.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256)) *
+           ((each + rows - 1) / rows);
+  };
+  // A pass takes 8 rows (NT = 1), 16 (NT = 2) or 48 (tcgen05).  16 rows a
+  // group, 32 groups of 7168 x 2048: 298 us on NT = 2, 324 us on tcgen05; 24
+  // rows: 364 and 331 us.
+  const bool many = sizeof(T) == 2 && a.rows > 20 * groups;
+  // Too few items for the SMs: 16 columns an item, and k over four warps.
+  // One token of 8 experts 46 us against 58 us; 4 tokens 132 us.  33 float32
+  // tokens over 7 experts: see below which is taken.
+  const long long wide = items(many ? 48 : a.rows <= 4 * groups ? 8 : 16);
+  if (wide < (tokens <= 8 ? 4 : 1) * static_cast<long long>(d.sms))
     return launch_one<T, DUAL, 1, 4, 1, G, Z>(a, tokens, d, s);
+  if (many) return launch_gmm_w4_tc(DUAL, a, s);
   if (a.rows <= 4 * groups)
     return launch_one<T, DUAL, 8, 1, 1, G, Z>(a, tokens, d, s);
-  if (sizeof(T) == 4 || a.rows <= 12 * groups)
-    return launch_one<T, DUAL, 8, 1, 2, G, Z>(a, tokens, d, s);
-  return launch_gmm_w4_tc(DUAL, a, s);
+  return launch_one<T, DUAL, 8, 1, 2, G, Z>(a, tokens, d, s);
 }
 
 // The products of one row type: what gmm_w4_bf16.cu and gmm_w4_f32.cu each

@@ -68,7 +68,7 @@ struct TcArgs {
   __nv_bfloat16* out;
   int32_t* status;
   Layout l;
-  int n_experts, n_groups, rows;
+  int n_experts, n_groups, rows, chunk, chunks;
   long long stall_after_fills;  // tests of the timeout path only (-1: off)
 };
 
@@ -76,7 +76,7 @@ struct TcArgs {
 struct TcSmem {
   int codes, zeros, sums, bars, groups, total;
 };
-__host__ __device__ inline TcSmem tc_smem(const Layout& l, int n_groups) {
+__host__ __device__ inline TcSmem tc_smem(const Layout& l, int chunks) {
   TcSmem m;
   m.codes = kXStages * 2 * kXBytes;
   m.zeros = m.codes + kExpandWarps * kCodeTiles * 2 * kTileBytes;
@@ -85,7 +85,7 @@ __host__ __device__ inline TcSmem tc_smem(const Layout& l, int n_groups) {
                               : 0);
   m.bars = m.sums + 128 * kSumPitch * 4;
   m.groups = m.bars + 512;
-  m.total = m.groups + 4 * n_groups;
+  m.total = m.groups + 8 * chunks;
   return m;
 }
 
@@ -227,15 +227,15 @@ struct TcKernel {
   // Calls f(item's column block, expert, first row, end of rows) for every
   // pass of this CTA until it returns false.
   template <typename F>
-  __device__ static void passes(const TcArgs& a, const int32_t* active,
+  __device__ static void passes(const TcArgs& a, const int2* chunks,
                                 int n_items, int blocks, const F& f) {
 #pragma unroll 1
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-      const int g = active[item / blocks];
-      const int ex = a.map ? a.map[g] : g;
-      const int r1 = min(a.rows, a.offsets[g + 1]);
+      const int2 c = chunks[item / blocks];
+      const int ex = a.map ? a.map[c.x] : c.x;
+      const int r1 = chunk_end(a, c);
 #pragma unroll 1
-      for (int row = max(0, a.offsets[g]); row < r1; row += kNR)
+      for (int row = c.y; row < r1; row += kNR)
         if (!f(item % blocks, ex, row, r1)) return;
     }
   }
@@ -246,7 +246,7 @@ struct TcKernel {
     __shared__ int abort_word;
     __shared__ uint32_t tmem_word;
     volatile int* abort_flag = &abort_word;
-    const TcSmem m = tc_smem(a.l, a.n_groups);
+    const TcSmem m = tc_smem(a.l, a.chunks);
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const uint32_t sb = smem_u32(base);
@@ -281,25 +281,25 @@ struct TcKernel {
       tc::tmem_alloc(smem_u32(&tmem_word), tc::kTmemCols);
       tc::tmem_relinquish();
     }
-    int32_t* active = reinterpret_cast<int32_t*>(base + m.groups);
-    const int n_active = find_active<kTcWarps>(a, active);  // barriers within
+    int2* chunks = reinterpret_cast<int2*>(base + m.groups);
+    const int n_chunks = find_chunks<kTcWarps>(a, chunks);  // barriers within
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_word;
     const int blocks = (a.l.N + kCols - 1) / kCols;
-    const int n_items = n_active * blocks;
+    const int n_items = n_chunks * blocks;
     if (warp < kExpandWarps)
-      expand_codes(a, m, sb, b, active, n_items, blocks, tmem, warp, lane,
+      expand_codes(a, m, sb, b, chunks, n_items, blocks, tmem, warp, lane,
                    abort_flag);
     else if (warp < kExpandWarps + kAddWarps)
-      add_parts(a, reinterpret_cast<float*>(base + m.sums), b, active,
+      add_parts(a, reinterpret_cast<float*>(base + m.sums), b, chunks,
                 n_items, blocks, tmem, warp - kExpandWarps, lane, abort_flag);
     else if (warp < kCopyWarp)
-      multiply(a, sb, b, active, n_items, blocks, tmem, warp - kMmaWarp, lane,
+      multiply(a, sb, b, chunks, n_items, blocks, tmem, warp - kMmaWarp, lane,
                abort_flag);
     else
-      copy_rows(a, map, sb, b, active, n_items, blocks, lane, abort_flag);
+      copy_rows(a, map, sb, b, chunks, n_items, blocks, lane, abort_flag);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -310,7 +310,7 @@ struct TcKernel {
   // ---- codes to operands: two records of a tile of 64 rows at a time
   __device__ static void expand_codes(const TcArgs& a, const TcSmem& m,
                                       uint32_t sb, const Bars& b,
-                                      const int32_t* active, int n_items,
+                                      const int2* chunks, int n_items,
                                       int blocks, uint32_t tmem, int warp,
                                       int lane, volatile int* abort_flag) {
     const int tiles_k = a.l.tiles_k(), t = warp / 4 % 2, q = warp % 4;
@@ -324,10 +324,10 @@ struct TcKernel {
     int item = blockIdx.x, row = 0, r1 = 0, tile = 0, zslot = 0;
     const char *p0 = nullptr, *p1 = nullptr, *s0 = nullptr, *s1 = nullptr;
     const auto enter = [&] {
-      const int g = active[item / blocks];
-      const int ex = a.map ? a.map[g] : g;
-      row = max(0, a.offsets[g]);
-      r1 = min(a.rows, a.offsets[g + 1]);
+      const int2 chunk = chunks[item / blocks];
+      const int ex = a.map ? a.map[chunk.x] : chunk.x;
+      row = chunk.y;
+      r1 = chunk_end(a, chunk);
       s0 = record(a, ex, item % blocks, t, 2 * q) + lane * 16;
       s1 = record(a, ex, item % blocks, t, 2 * q + 1) + lane * 16;
     };
@@ -381,7 +381,7 @@ struct TcKernel {
 
     int slot = 0, st = 0;
     uint32_t phase = 1;
-    passes(a, active, n_items, blocks, [&](int, int, int, int) {
+    passes(a, chunks, n_items, blocks, [&](int, int, int, int) {
       uint32_t z[2][2];
       z[0][0] = z[0][1] = z[1][0] = z[1][1] = 0xbe00be00u;  // -8/64
 #pragma unroll 1
@@ -443,7 +443,7 @@ struct TcKernel {
   // ---- rows of x by TMA: 64 columns of the pass's rows at a time
   __device__ static void copy_rows(const TcArgs& a, const CUtensorMap* map,
                                    uint32_t sb, const Bars& b,
-                                   const int32_t* active, int n_items,
+                                   const int2* chunks, int n_items,
                                    int blocks, int lane,
                                    volatile int* abort_flag) {
     if (lane != 0) return;
@@ -452,7 +452,7 @@ struct TcKernel {
     long long filled = 0;
     uint32_t phase = 1;
     bool ok = true;
-    passes(a, active, n_items, blocks, [&](int, int, int row, int) {
+    passes(a, chunks, n_items, blocks, [&](int, int, int row, int) {
 #pragma unroll 1
       for (int k = 0; k < tiles_k; k += 2) {
         ok = (a.stall_after_fills < 0 || filled < a.stall_after_fills) &&
@@ -484,7 +484,7 @@ struct TcKernel {
 
   // ---- the matrix instructions: one partial sum for each group of W's rows
   __device__ static void multiply(const TcArgs& a, uint32_t sb, const Bars& b,
-                                  const int32_t* active, int n_items,
+                                  const int2* chunks, int n_items,
                                   int blocks, uint32_t tmem, int t, int lane,
                                   volatile int* abort_flag) {
     const int tiles_k = a.l.tiles_k();
@@ -494,7 +494,7 @@ struct TcKernel {
     int st = 0, xs = 0, part = 0;
     uint32_t phase = 0, x_phase = 0, p_phase = 1;
     bool full = false, x_full = false, empty = false;  // the next ones, as seen ahead
-    passes(a, active, n_items, blocks, [&](int, int, int row, int r1) {
+    passes(a, chunks, n_items, blocks, [&](int, int, int row, int r1) {
       const int n = (min(kNR, r1 - row) + 15) / 16 * 16;
       const uint32_t idesc =
           tc::make_idesc(128, 16, false) + ((n - 16) >> 3 << 17);
@@ -554,7 +554,7 @@ struct TcKernel {
 
   // ---- scale * partial sums, a thread per column of W, and the output
   __device__ static void add_parts(const TcArgs& a, float* sums,
-                                   const Bars& b, const int32_t* active,
+                                   const Bars& b, const int2* chunks,
                                    int n_items, int blocks, uint32_t tmem,
                                    int warp, int lane,
                                    volatile int* abort_flag) {
@@ -568,7 +568,7 @@ struct TcKernel {
     // After a wait that gave up the loops run on without waiting, so that
     // the warps meet at their barriers.
     bool ok = true;
-    passes(a, active, n_items, blocks, [&](int nb, int ex, int row, int r1) {
+    passes(a, chunks, n_items, blocks, [&](int nb, int ex, int row, int r1) {
       const int rows = min(kNR, r1 - row);
       const char* rec =
           record(a, ex, nb, t, 2 * q + (lane >> 4)) + (col & 7) * (4 * E) +
@@ -660,18 +660,19 @@ cudaError_t launch_tc(const TcArgs& a, const CUtensorMap& map,
   const cudaError_t e = launch::allow_shared<kernel>(d);
   if (e != cudaSuccess) return e;
   const int cols = TcKernel<DUAL, G, Z>::kCols;
-  const long long items = static_cast<long long>((a.l.N + cols - 1) / cols) *
-                          std::min(a.n_groups, a.rows);
+  const long long items =
+      static_cast<long long>((a.l.N + cols - 1) / cols) * a.chunks;
   const unsigned grid =
       static_cast<unsigned>(std::min<long long>(items, d.sms));
-  kernel<<<grid, kTcThreads, tc_smem(a.l, a.n_groups).total + 1024, s>>>(a,
+  kernel<<<grid, kTcThreads, tc_smem(a.l, a.chunks).total + 1024, s>>>(a,
                                                                         map);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_gmm_w4_tc(bool dual, const GmmArgs& g, cudaStream_t s) {
+cudaError_t launch_gmm_w4_tc(bool dual, GmmArgs g, cudaStream_t s) {
+  set_chunk(&g, kNR);
   Device d;
   cudaError_t e = launch::device(&d);
   if (e != cudaSuccess) return e;
@@ -680,7 +681,7 @@ cudaError_t launch_gmm_w4_tc(bool dual, const GmmArgs& g, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const TcArgs a = {g.offsets, g.map,    g.w0,        g.w1,
                     static_cast<__nv_bfloat16*>(g.out), g.status, g.l,
-                    g.n_experts, g.n_groups, g.rows,
+                    g.n_experts, g.n_groups, g.rows, g.chunk, g.chunks,
                     tc::g_stall_after_fills.load()};
 #define MOE_W4_CASE(GROUP)                                                  \
   if (g.l.group == GROUP) {                                                 \

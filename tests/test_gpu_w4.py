@@ -183,7 +183,10 @@ def test_swiglu(counts, H, F, dtype, group, zeros):
 @pytest.mark.parametrize("counts,H,F", [
     ([16], 8, 8), ([17, 0, 15], 72, 40), ([48], 64, 136), ([49, 97], 200, 328),
     ([33, 5], 1000, 264), ([60, 0, 60, 13], 264, 1416), ([250], 2056, 520),
-    ([13, 14, 40, 7, 31], 520, 2056)])
+    ([13, 14, 40, 7, 31], 520, 2056), ([1] * 8 + [300], 264, 136),
+    # enough items for the tensor cores' form: columns and row passes
+    ([1000, 0, 21], 8, 5000), ([48 * 40], 72, 2312), ([30] * 40, 328, 1032),
+    ([25] * 60 + [0, 96], 200, 520), ([700, 701], 1000, 1504)])
 @pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, True),
                                          (64, False), (128, True),
                                          (128, False)])
@@ -198,22 +201,22 @@ def test_swiglu_many_rows(counts, H, F, group, zeros):
 
 def test_many_rows_next_to_nonfinite_rows():
     """A pass may read rows of the next group; they stay apart."""
-    cfg, w4, x, off, doff, packs, ws = case([20, 30], 264, 136, 2, "bf16", 64,
-                                            True, seed=12)
+    cfg, w4, x, off, doff, packs, ws = case([620, 700], 264, 1416, 2, "bf16",
+                                            64, True, seed=12)
     h0, y0 = run_swiglu(cfg, w4, x, doff, packs)
     x = x.clone()
-    x[20:] = float("nan")
+    x[620:] = float("nan")
     h, y = run_swiglu(cfg, w4, x, doff, packs)
-    assert torch.equal(h[:20], h0[:20]) and torch.equal(y[:20], y0[:20])
-    assert h[20:].isnan().all() and y[20:].isnan().all()
+    assert torch.equal(h[:620], h0[:620]) and torch.equal(y[:620], y0[:620])
+    assert h[620:].isnan().all() and y[620:].isnan().all()
 
 
 def test_stalled_rows_time_out_and_context_survives():
     """The bounded waits of the many-row products: with the copies of x
     stopped, the kernel reports MOE_DEV_TIMEOUT and returns, and the next
     call is right."""
-    cfg, w4, x, off, doff, packs, ws = case([40, 60], 520, 264, 2, "bf16", 64,
-                                            False, seed=13)
+    cfg, w4, x, off, doff, packs, ws = case([600, 700], 520, 1416, 2, "bf16",
+                                            64, False, seed=13)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     try:
         moe.moe_test_stall_gemm_producer(3)
