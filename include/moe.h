@@ -963,11 +963,11 @@ moe_status_t moe_w4_dequantize(const moe_w4_t *opt, int32_t n, int32_t K,
 
 /* moe_gmm_gate_up_w4, moe_gmm_down_w4, moe_gmm_swiglu_w4 -- moe_gmm_gate_up,
  * moe_gmm_down and moe_gmm_swiglu with packed 4-bit weights: w_gate and w_up
- * are E matrices [H, F], w_down E matrices [F, H].  Made for few rows in a
- * group, one upward; any number is computed.  Any H and F that a cfg allows
- * (F >= 1).  Sums are float32; h and y_sorted are rounded to dtype.  A group
- * whose expert index is outside [0, E) is skipped and sets
- * MOE_DEV_BAD_INDEX. */
+ * are E matrices [H, F], w_down E matrices [F, H].  Any number of rows in a
+ * group, made for few, and any H and F that a cfg allows (F >= 1).  Sums are
+ * float32; h and y_sorted are rounded to dtype.  A group whose expert index
+ * is outside [0, E) is skipped and sets MOE_DEV_BAD_INDEX; MOE_DEV_TIMEOUT if
+ * a pipeline wait of the tensor-core form (many bf16 rows) gave up. */
 moe_status_t moe_gmm_gate_up_w4(const moe_config_t *cfg, const moe_w4_t *opt,
                                 int32_t n_groups, const int32_t *group_expert,
                                 const void *x_sorted,

@@ -5,15 +5,18 @@
 //   rstd_t = 1 / sqrt(mean_c v[t, c]^2 + eps)
 //   out = res_scale * x + gate * N(y; w_post),   h_next = N(out; w_next)
 //
-// One kernel serves the norm alone (moe_norm), the branch's end
+// Three entry points: the norm alone (moe_norm), the branch's end
 // (moe_block_out) and the branch's end with the weighted combine in front
-// (moe_combine_block_out).  A row is read once and kept, packed, in
-// registers over both reductions, so the traffic is each input once and each
-// output once; no product is large enough to matter and HBM bounds all of
-// it.  `y` and `out` are rounded to the layer's type where they are stored
-// and the norm that follows reads the rounded value: a backward pass that
-// starts from the stored tensors then differentiates what was computed.
-// Sums of squares are float32.
+// (moe_combine_block_out).  HBM bounds all of it, so a row is read once and
+// each output written once: a row is kept on chip over both reductions.  `y`
+// and `out` are rounded to the layer's type where they are stored and the
+// norm that follows reads the rounded value: a backward pass that starts from
+// the stored tensors then differentiates what was computed.  Sums of squares
+// are float32.
+//
+// Measured, bf16: 8192 x 7168 with a channel gate 78 us (470 MB, 6.0 TB/s);
+// 8192 x 5120 with one expert combined 81 us (420 MB, 5.2 TB/s); one token of
+// 7168 5.9 us a call, of which most is the call.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -27,8 +30,9 @@ using namespace block;
 
 enum Mode { kNormOnly = 0, kOut = 1, kCombineOut = 2 };
 
-// NV 16-byte words of the row per thread; WARP: a warp per row and several
-// rows per CTA, else one row per CTA.
+// Rows of up to 128 words (WARP: a warp per row, several rows per CTA), which
+// leave a scheduler many short rows to choose from, and rows too wide for the
+// streamed form below: NV 16-byte words of the row per thread, in registers.
 template <typename T, int NV, bool WARP, int MAXT, int MODE>
 __global__ void __launch_bounds__(MAXT)
     block_fwd_kernel(const FwdArgs a) {

@@ -3,8 +3,8 @@
 //   gate_up: h[r] = silu(x[r] Wg) * (x[r] Wu)      down: y[r] = h[r] Wd
 //   W[k, n] = (code - zero) * scale, over groups of rows of W
 //
-// What bounds it is the weights' bytes, each read once, as long as a group
-// has few rows.  So everything is arranged around that stream:
+// With few rows in a group the weights' bytes bound it, each read once.  So
+// everything is arranged around that stream:
 //
 // * A warp works on two records (16 columns each): of the gate and the up
 //   matrix, or two neighbours of the down matrix.  A matrix instruction
@@ -14,17 +14,26 @@
 // * Next comes the arithmetic of expanding codes: logic and shifts run at 16
 //   lanes a clock, so a tile of 64 rows of both records costs a scheduler 80
 //   clocks of masks and byte shifts (see expand()), beside 72 of matrix
-//   instructions and 32 bf16 multiply-adds, against 172 at full bandwidth.
+//   instructions and 64 of bf16 multiply-adds, against 172 at full bandwidth.
+//   Measured instruction costs: 2 clocks for a mask, shift or bf16 pair, 9
+//   for a matrix instruction, with little overlap of the two.
 // * Weights go from HBM to a ring in shared memory by asynchronous 16-byte
 //   copies, two steps of 256 rows ahead.  A lane reads back exactly what it
-//   copied itself, so that ring needs no barrier.  CTAs are persistent, one
-//   or two an SM, and the ring runs on across work items.
+//   copied itself, so that ring needs no barrier.  (Bulk copies issued by one
+//   warp were slower: about 1 KB each, 1300 us against 1000 us for the batch
+//   of 64 below.)  CTAs are persistent and the ring runs on across work
+//   items.
 // * A work item is a record pair of NW warps (neighbouring columns, which
 //   share the rows of x) with k split over KW warps, whose sums are added in
-//   warp order.  Many items: NW = 8 or 16; a few tokens leave few groups and
-//   few items, then NW = 1, KW = 8.
-// * More rows than 8 * NT of a group are further passes over its weights,
-//   which then come from L2.
+//   warp order, for one pass of up to 8 * NT rows.  Further rows of a group
+//   are further items, whose weights come from L2.
+//
+// Measured, DeepSeek-V3-shaped experts (7168 x 2048, groups of 128): one
+// token 46 us (8 experts, 182 MB: 3.9 TB/s; the copies alone take 41 us, the
+// launches and the tail of 6.7 items an SM are the rest); 16 tokens over 32
+// experts 142 us (5.1 TB/s; the copies alone 119 us, the arithmetic alone 145
+// us); 64 tokens, Zipf, 650 us (5.0 TB/s).  Llama4-Maverick-shaped, 16 tokens
+// one expert each, groups of 32 with zero points: 182 us (6.2 TB/s).
 //
 // float32 rows use the same instructions: a float is the exact sum of three
 // bf16 numbers (8 bits of its significand each), so three products with the
@@ -716,13 +725,14 @@ cudaError_t launch_shape(const GmmArgs& a, int tokens, cudaStream_t s) {
     return groups * ((a.l.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256)) *
            ((each + rows - 1) / rows);
   };
-  // A pass takes 8 rows (NT = 1), 16 (NT = 2) or 48 (tcgen05).  16 rows a
-  // group, 32 groups of 7168 x 2048: 298 us on NT = 2, 324 us on tcgen05; 24
-  // rows: 364 and 331 us.
+  // A pass takes 8 rows (NT = 1), 16 (NT = 2) or 48 (tcgen05).  32 groups of
+  // 7168 x 2048 with 16 rows each: 243 us on NT = 2, 324 us on tcgen05; 24
+  // rows: 332 and 333 us; 32 rows: 421 and 339 us; 64 rows: 748 and 602 us.
   const bool many = sizeof(T) == 2 && a.rows > 20 * groups;
   // Too few items for the SMs: 16 columns an item, and k over four warps.
-  // One token of 8 experts 46 us against 58 us; 4 tokens 132 us.  33 float32
-  // tokens over 7 experts: see below which is taken.
+  // 33 float32 tokens, three of 7 experts each, 1412 x 1004: 49 us, and 76 us
+  // in items of 128 columns; 4 tokens of 256 experts 132 us, and 158 us with k
+  // over eight warps.
   const long long wide = items(many ? 48 : a.rows <= 4 * groups ? 8 : 16);
   if (wide < (tokens <= 8 ? 4 : 1) * static_cast<long long>(d.sms))
     return launch_one<T, DUAL, 1, 4, 1, G, Z>(a, tokens, d, s);

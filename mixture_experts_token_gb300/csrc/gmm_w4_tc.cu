@@ -18,8 +18,17 @@
 //   and columns past K zeros; neither reaches a row that is written).
 //
 // A CTA per SM walks over items: 128 columns of the gate and the up matrix,
-// or 256 of the down matrix, of one group with rows.  Every wait is bounded;
+// or 256 of the down matrix, and 48 rows of one group.  Every wait is bounded;
 // one that gives up raises MOE_DEV_TIMEOUT and the CTA drains and returns.
+//
+// Measured, 7168 x 2048 experts, groups of 128: 1024 tokens over 256 experts
+// (32 rows each) 2.3 ms, 39% of the time its bytes need at 6.8 TB/s; 256
+// tokens over 32 experts (64 rows each) 602 us.  A tile of 64 rows of W takes
+// about 1000 clocks whatever the rows, and no one unit bounds it: without the
+// matrix instructions, the tensor memory traffic, the expansion or the copies
+// of x, one at a time, it stays within 10% of that, and with all of them gone
+// 560 clocks of hand-over between the roles are left.  Each role's warp has
+// about 150 dependent instructions a tile and 7 warps share a scheduler.
 #include <atomic>
 
 #include "gmm_w4.cuh"
