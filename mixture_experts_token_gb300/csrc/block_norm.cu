@@ -186,7 +186,10 @@ cudaError_t launch_mode(const FwdArgs& a, int mode, int threads,
 // with NV = 2, which halves the instructions of the reductions where a row
 // has over 512 words: 7168 bf16 columns and one expert 113 -> 81 us).  A row is, in queue order, y (or its k expert rows), x, and
 // a full gate.
-constexpr int kQueue = 8;
+// Words in flight: eight experts' and x, so that one row needs no second
+// round trip, or four rows of two.
+template <int MODE>
+constexpr int kQueueOf = MODE == kCombineOut ? 10 : 8;
 // Where the words of the coming rows are, for the combine: a ring of rows
 // whose entries are a word's address and its weight.
 struct Entry {
@@ -200,6 +203,7 @@ template <typename T, int NV, int MAXT, int MODE, bool FULL>
 __global__ void __launch_bounds__(MAXT) block_fwd_stream(const FwdArgs a) {
   using V = Vec<T>;
   constexpr int N = V::N;
+  constexpr int kQueue = kQueueOf<MODE>;
   extern __shared__ __align__(16) char queue[];
   __shared__ float red[2][32];
   __shared__ Entry table[MODE == kCombineOut ? kEntries : 1];
@@ -427,7 +431,7 @@ cudaError_t launch_stream(const FwdArgs& a, cudaStream_t s) {
   cudaError_t e = device(&d);
   if (e != cudaSuccess) return e;
   const int threads = ((a.n16 + NV - 1) / NV + 31) / 32 * 32;
-  const int bytes = kQueue * threads * NV * 16;
+  const int bytes = kQueueOf<MODE> * threads * NV * 16;
   constexpr auto kernel = block_fwd_stream<T, NV, MAXT, MODE, FULL>;
   int per_sm = 0;
   if ((e = launch::allow_shared<kernel>(d)) != cudaSuccess ||

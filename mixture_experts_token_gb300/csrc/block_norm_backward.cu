@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
 
   // one partial per CTA
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = POST ? 0 : 1; q < 2; ++q) {
     float* out =
         a.parts + (static_cast<long long>(blockIdx.x) * 2 + q) * a.n16 * N;
 #pragma unroll
@@ -222,6 +222,9 @@ __global__ void __launch_bounds__(MAXT)
   constexpr int W = 3 + POST + FULL;  // groups of copies of a row
   extern __shared__ __align__(16) char queue[];
   __shared__ float red[2][32];
+  // All CTAs of this grid are resident, so the column sums' can only take
+  // what they leave.
+  launch::let_next_start();
   const int group = threadIdx.x / threads, tid = threadIdx.x % threads;
   const int groups = blockDim.x / threads;
   const int t0 = blockIdx.x * groups + group, t_step = gridDim.x * groups;
@@ -437,13 +440,12 @@ __global__ void __launch_bounds__(MAXT)
   }
   copies_wait<0>();
 
-  launch::let_next_start();
   // One partial per CTA: this thread's columns, or the groups' added in
   // group order.
   float* cols = reinterpret_cast<float*>(queue);
   const int H = a.n16 * N;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = POST ? 0 : 1; q < 2; ++q) {
     float* out = a.parts + (static_cast<long long>(blockIdx.x) * 2 + q) * H;
     for (int g = 0; g < groups; ++g) {
       if (groups > 1) __syncthreads();
@@ -478,14 +480,15 @@ struct ColArgs {
 
 constexpr int kColThreads = 32;  // columns of a CTA
 constexpr int kColRows = 32;     // partials added side by side
+static_assert(kColThreads == 32 && kColRows == 32, "summed by warps");
 
-// Adds the CTAs' partials: blockIdx.y 0 the branch's column sums, 1 the next
-// norm's.
+// Adds the CTAs' partials: the next norm's column sums where blockIdx.y is
+// the last, else (with two) the branch's.
 __global__ void __launch_bounds__(kColThreads* kColRows)
     block_bwd_columns(const ColArgs a) {
-  __shared__ float part[kColRows][kColThreads];
-  const int c = blockIdx.x * kColThreads + threadIdx.x;
-  const int q = blockIdx.y;
+  __shared__ float part[kColRows][kColThreads + 1];
+  int c = blockIdx.x * kColThreads + threadIdx.x;
+  const int q = 2 - gridDim.y + blockIdx.y;
   launch::wait_for_previous();
   float s = 0.0f;
   if (c < a.H) {
@@ -496,9 +499,12 @@ __global__ void __launch_bounds__(kColThreads* kColRows)
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y != 0 || c >= a.H) return;
+  // 32 x 32 sums: a warp per column, its lanes' by halving
+  s = part[threadIdx.x][threadIdx.y];
 #pragma unroll
-  for (int i = 1; i < kColRows; ++i) s += part[i][threadIdx.x];
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  c = blockIdx.x * kColThreads + threadIdx.y;
+  if (threadIdx.x != 0 || c >= a.H) return;
   const auto put = [&](float* p, float v) {
     if (p) p[c] = a.accumulate ? p[c] + v : v;
   };
@@ -613,7 +619,7 @@ moe_status_t run(const moe_config_t& c, BwdArgs a, ColArgs ca, bool post,
           ? launch_rows<float>(a, post, parts, &ca.n_parts, s)
           : launch_rows<__nv_bfloat16>(a, post, parts, &ca.n_parts, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  const dim3 cols((c.H + kColThreads - 1) / kColThreads, 2);
+  const dim3 cols((c.H + kColThreads - 1) / kColThreads, post ? 2 : 1);
   return launch::overlapping(block_bwd_columns, cols,
                              dim3(kColThreads, kColRows), 0, s,
                              ca) == cudaSuccess
