@@ -88,54 +88,91 @@ __device__ __forceinline__ long long code_at(const Layout& l, int tile) {
   return l.step_at(tile / kPer) + tile % kPer * kTileBytes;
 }
 
-// One CTA per (column record, matrix).  grid.y strides over matrices.
+// A CTA packs four records (64 columns) of a matrix, 128 rows at a time:
+// codes come in rows of 64 bytes to shared memory and leave as whole words.
+// grid.y strides over matrices.  256 matrices of 7168 x 2048, 1.9 GB of
+// codes: 2.7 ms, and about 6 ms with a byte load for every code.
+constexpr int kPackRecords = 4;
+constexpr int kPackCols = kPackRecords * kTileN;
+constexpr int kPackK = 2 * kTileK;
 __global__ void __launch_bounds__(kThreads)
     pack_kernel(const uint8_t* __restrict__ codes,
                 const __nv_bfloat16* __restrict__ scales,
                 const uint8_t* __restrict__ zeros, int n_mats, Layout l,
-                char* __restrict__ packed) {
-  const int n0 = blockIdx.x * kTileN, G = l.groups();
+                bool wide, char* __restrict__ packed) {
+  // rows 4 bytes past 64: neighbouring rows start in neighbouring banks
+  __shared__ uint8_t rows[kPackK / 2][kPackCols + 4];
+  const int n0 = blockIdx.x * kPackCols, G = l.groups();
   const int E = kStepK / l.group;  // groups of a step
+  const int records = min(kPackRecords, l.tiles_n() - kPackRecords *
+                                            static_cast<int>(blockIdx.x));
   for (long long m = blockIdx.y; m < n_mats; m += gridDim.y) {
     const uint8_t* c = codes + m * (l.K / 2) * l.N;
     const __nv_bfloat16* sc = scales + m * G * l.N;
     const uint8_t* zp = l.zeros ? zeros + m * G * l.N : nullptr;
-    char* rec = packed + m * l.matrix() + blockIdx.x * l.record();
-    const int words = l.tiles_k() * 128;
-    for (int i = threadIdx.x; i < words; i += kThreads) {
-      const int tile = i >> 7, lane = (i >> 2) & 31, s = i & 3;
-      uint32_t v = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = tile * kTileK + nibble_k(lane, s, j);
-        const int n = n0 + nibble_n(lane, j);
-        uint32_t q = 8;
-        if (n < l.N) {
-          if (k < l.K) {
-            const uint32_t b = c[static_cast<long long>(k / 2) * l.N + n];
-            q = k & 1 ? b >> 4 : b & 15;
-          } else if (l.zeros) {
-            // the stored zero of k's group: 0 past the last group
-            const int g = k / l.group;
-            q = g < G ? zp[static_cast<long long>(g) * l.N + n] & 15 : 0;
-          }
-        } else if (l.zeros) {
-          q = 0;
+    char* rec0 = packed + m * l.matrix() +
+                 static_cast<long long>(blockIdx.x) * kPackRecords *
+                     l.record();
+    for (int k0 = 0; k0 < l.K; k0 += kPackK) {
+      __syncthreads();
+      const int r = threadIdx.x / 4, q = threadIdx.x % 4 * 16;
+      uint32_t v[4] = {0, 0, 0, 0};
+      if (2 * r + k0 < l.K) {
+        const uint8_t* src = c + (k0 / 2 + r) * static_cast<long long>(l.N) +
+                             n0 + q;
+        if (wide && n0 + q + 16 <= l.N) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+          v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        } else {
+          for (int i = 0; i < 16; ++i)
+            if (n0 + q + i < l.N)
+              v[i / 4] |= static_cast<uint32_t>(src[i]) << (8 * (i % 4));
         }
-        v |= q << (4 * j);
       }
-      *reinterpret_cast<uint32_t*>(rec + code_at(l, tile) + (i & 127) * 4) = v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint32_t*>(&rows[r][q + 4 * i]) = v[i];
+      __syncthreads();
+      const int tiles = min(2, l.tiles_k() - k0 / kTileK);
+      for (int i = threadIdx.x; i < records * tiles * 128; i += kThreads) {
+        const int rec = i / (tiles * 128), tile = i / 128 % tiles;
+        const int lane = (i >> 2) & 31, s = i & 3;
+        uint32_t word = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int kt = tile * kTileK + nibble_k(lane, s, j), k = k0 + kt;
+          const int col = rec * kTileN + nibble_n(lane, j), n = n0 + col;
+          uint32_t code = l.zeros ? 0 : 8;
+          if (n < l.N) {
+            if (k < l.K) {
+              const uint32_t b = rows[kt / 2][col];
+              code = k & 1 ? b >> 4 : b & 15;
+            } else if (l.zeros) {
+              // the stored zero of k's group: 0 past the last group
+              const int g = k / l.group;
+              code = g < G ? zp[static_cast<long long>(g) * l.N + n] & 15 : 0;
+            }
+          }
+          word |= code << (4 * j);
+        }
+        *reinterpret_cast<uint32_t*>(rec0 + rec * l.record() +
+                                     code_at(l, k0 / kTileK + tile) +
+                                     (i & 127) * 4) = word;
+      }
     }
-    for (int i = threadIdx.x; i < l.steps() * 16 * E; i += kThreads) {
-      const int step = i / (16 * E), j = i % (16 * E);
-      const int n = n0 + j / (2 * E) + 8 * (j & 1);
+    for (int i = threadIdx.x; i < records * l.steps() * 16 * E;
+         i += kThreads) {
+      const int rec = i / (l.steps() * 16 * E);
+      const int at = i - rec * (l.steps() * 16 * E);
+      const int step = at / (16 * E), j = at % (16 * E);
+      const int n = n0 + rec * kTileN + j / (2 * E) + 8 * (j & 1);
       const int g = step * E + j / 2 % E;
       const bool in = n < l.N && g < G;
-      const long long at = static_cast<long long>(g) * l.N + n;
-      char* so = rec + l.scales_at(step);
+      const long long from = static_cast<long long>(g) * l.N + n;
+      char* so = rec0 + rec * l.record() + l.scales_at(step);
       reinterpret_cast<__nv_bfloat16*>(so)[j] =
-          in ? sc[at] : __float2bfloat16(0.0f);
-      if (l.zeros) so[32 * E + j] = in ? zp[at] & 15 : 0;
+          in ? sc[from] : __float2bfloat16(0.0f);
+      if (l.zeros) so[32 * E + j] = in ? zp[from] & 15 : 0;
     }
   }
 }
@@ -227,9 +264,11 @@ moe_status_t moe_w4_pack(const moe_w4_t* opt, int32_t n, int32_t K, int32_t N,
       (zeros != nullptr) != (opt->zero_points != 0))
     return MOE_ERR_INVALID_ARG;
   const Layout l = layout(*opt, K, N);
-  pack_kernel<<<record_grid(l, n), kThreads, 0, stream>>>(
+  const dim3 grid((l.tiles_n() + kPackRecords - 1) / kPackRecords,
+                  n < 4096 ? n : 4096);
+  pack_kernel<<<grid, kThreads, 0, stream>>>(
       codes, static_cast<const __nv_bfloat16*>(scales), zeros, n, l,
-      static_cast<char*>(packed));
+      aligned16(codes) && N % 16 == 0, static_cast<char*>(packed));
   return launched();
 }
 
