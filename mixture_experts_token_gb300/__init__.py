@@ -221,9 +221,12 @@ def _ptr(t):
     """The device address of a tensor (or of an int or None, itself): what a
     c_void_p argument takes.  Plain ints convert faster than c_void_p
     objects, and a step of one token is mostly such conversions."""
-    if t is None or isinstance(t, int):
+    if t is None:
+        return None
+    try:
+        return t.data_ptr()
+    except AttributeError:
         return t
-    return t.data_ptr()
 
 
 def _nbytes(t):
@@ -673,54 +676,63 @@ def moe_layer_backward(cfg, x, logits, w_gate, w_up, w_down, dy, dx,
 # ------------------------------------------------------ block norms ------
 def moe_norm(cfg, opt, x, w, h, rstd=None, stream=None):
     """h = N(x; w), the norm before the block; rstd [T] for the backward."""
-    _check(lib().moe_norm(
-        ctypes.byref(cfg), ctypes.byref(opt), _ptr(x), _ptr(w), _ptr(h),
-        _ptr(rstd), _stream(stream)), "moe_norm")
+    st = (_lib or lib()).moe_norm(
+        cfg, opt, _ptr(x), _ptr(w), _ptr(h),
+        _ptr(rstd), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_norm")
 
 
 def moe_norm_backward(cfg, opt, x, w, rstd, dh, dres, dx, dw, accumulate,
                       workspace, stream=None):
-    _check(lib().moe_norm_backward(
-        ctypes.byref(cfg), ctypes.byref(opt), _ptr(x), _ptr(w), _ptr(rstd),
+    st = (_lib or lib()).moe_norm_backward(
+        cfg, opt, _ptr(x), _ptr(w), _ptr(rstd),
         _ptr(dh), _ptr(dres), _ptr(dx), _ptr(dw), int(accumulate),
-        _ptr(workspace), _nbytes(workspace), _stream(stream)),
-        "moe_norm_backward")
+        _ptr(workspace), _nbytes(workspace), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_norm_backward")
 
 
 def moe_block_out(cfg, opt, x, y, w_post, gate, w_next, out, h_next=None,
                   rstd_y=None, rstd_out=None, stream=None):
     """out = res_scale*x + gate*N(y; w_post) and h_next = N(out; w_next)."""
-    _check(lib().moe_block_out(
-        ctypes.byref(cfg), ctypes.byref(opt), _ptr(x), _ptr(y),
+    st = (_lib or lib()).moe_block_out(
+        cfg, opt, _ptr(x), _ptr(y),
         _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(out), _ptr(h_next),
-        _ptr(rstd_y), _ptr(rstd_out), _stream(stream)), "moe_block_out")
+        _ptr(rstd_y), _ptr(rstd_out), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_block_out")
 
 
 def moe_combine_block_out(cfg, opt, y_sorted, row_of, topk_w, x, w_post,
                           gate, w_next, y, out, h_next=None, rstd_y=None,
                           rstd_out=None, stream=None):
     """moe_block_out of moe_combine's rows; y (or None) receives them."""
-    _check(lib().moe_combine_block_out(
-        ctypes.byref(cfg), ctypes.byref(opt), _ptr(y_sorted), _ptr(row_of),
+    st = (_lib or lib()).moe_combine_block_out(
+        cfg, opt, _ptr(y_sorted), _ptr(row_of),
         _ptr(topk_w), _ptr(x), _ptr(w_post), _ptr(gate), _ptr(w_next),
         _ptr(y), _ptr(out), _ptr(h_next), _ptr(rstd_y), _ptr(rstd_out),
-        _stream(stream)), "moe_combine_block_out")
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_combine_block_out")
 
 
 def moe_block_out_backward(cfg, opt, y, w_post, gate, rstd_y, out, w_next,
                            rstd_out, dout, dh_next, dx, dy, dw_post, dgate,
                            dw_next, accumulate, workspace, stream=None):
-    _check(lib().moe_block_out_backward(
-        ctypes.byref(cfg), ctypes.byref(opt), _ptr(y), _ptr(w_post),
+    st = (_lib or lib()).moe_block_out_backward(
+        cfg, opt, _ptr(y), _ptr(w_post),
         _ptr(gate), _ptr(rstd_y), _ptr(out), _ptr(w_next), _ptr(rstd_out),
         _ptr(dout), _ptr(dh_next), _ptr(dx), _ptr(dy), _ptr(dw_post),
         _ptr(dgate), _ptr(dw_next), int(accumulate), _ptr(workspace),
-        _nbytes(workspace), _stream(stream)), "moe_block_out_backward")
+        _nbytes(workspace), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_block_out_backward")
 
 
 # ---------------------------------------------------- 4-bit weights ------
 def moe_w4_bytes(w4, n, K, N) -> int:
-    return int(lib().moe_w4_bytes(ctypes.byref(w4), n, K, N))
+    return int(lib().moe_w4_bytes(w4, n, K, N))
 
 
 def _float_type(t):
@@ -731,49 +743,60 @@ def _float_type(t):
 
 def moe_w4_quantize(w4, n, K, N, w, codes, scales, zeros=None, stream=None):
     """Codes, bf16 scales and (with zero points) zeros of w [n, K, N]."""
-    _check(lib().moe_w4_quantize(
-        ctypes.byref(w4), n, K, N, _float_type(w), _ptr(w), _ptr(codes),
-        _ptr(scales), _ptr(zeros), _stream(stream)), "moe_w4_quantize")
+    st = (_lib or lib()).moe_w4_quantize(
+        w4, n, K, N, _float_type(w), _ptr(w), _ptr(codes),
+        _ptr(scales), _ptr(zeros), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_w4_quantize")
 
 
 def moe_w4_pack(w4, n, K, N, codes, scales, zeros, packed, stream=None):
     """Lays 4-bit weights out for the products, into alloc_w4()'s buffer."""
-    _check(lib().moe_w4_pack(
-        ctypes.byref(w4), n, K, N, _ptr(codes), _ptr(scales), _ptr(zeros),
-        _ptr(packed), _stream(stream)), "moe_w4_pack")
+    st = (_lib or lib()).moe_w4_pack(
+        w4, n, K, N, _ptr(codes), _ptr(scales), _ptr(zeros),
+        _ptr(packed), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_w4_pack")
 
 
 def moe_w4_dequantize(w4, n, K, N, packed, w, stream=None):
-    _check(lib().moe_w4_dequantize(
-        ctypes.byref(w4), n, K, N, _ptr(packed), _float_type(w), _ptr(w),
-        _stream(stream)), "moe_w4_dequantize")
+    st = (_lib or lib()).moe_w4_dequantize(
+        w4, n, K, N, _ptr(packed), _float_type(w), _ptr(w),
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_w4_dequantize")
 
 
 def moe_gmm_gate_up_w4(cfg, w4, x_sorted, group_offsets, w_gate, w_up, h,
                        status_word=None, stream=None, n_groups=0,
                        group_expert=None):
-    _check(lib().moe_gmm_gate_up_w4(
-        ctypes.byref(cfg), ctypes.byref(w4), n_groups, _ptr(group_expert),
+    st = (_lib or lib()).moe_gmm_gate_up_w4(
+        cfg, w4, n_groups, _ptr(group_expert),
         _ptr(x_sorted), _ptr(group_offsets), _ptr(w_gate), _ptr(w_up),
-        _ptr(h), _ptr(status_word), _stream(stream)), "moe_gmm_gate_up_w4")
+        _ptr(h), _ptr(status_word), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_gmm_gate_up_w4")
 
 
 def moe_gmm_down_w4(cfg, w4, h, group_offsets, w_down, y_sorted,
                     status_word=None, stream=None, n_groups=0,
                     group_expert=None):
-    _check(lib().moe_gmm_down_w4(
-        ctypes.byref(cfg), ctypes.byref(w4), n_groups, _ptr(group_expert),
+    st = (_lib or lib()).moe_gmm_down_w4(
+        cfg, w4, n_groups, _ptr(group_expert),
         _ptr(h), _ptr(group_offsets), _ptr(w_down), _ptr(y_sorted),
-        _ptr(status_word), _stream(stream)), "moe_gmm_down_w4")
+        _ptr(status_word), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_gmm_down_w4")
 
 
 def moe_gmm_swiglu_w4(cfg, w4, x_sorted, group_offsets, w_gate, w_up, w_down,
                       h, y_sorted, status_word=None, stream=None):
-    _check(lib().moe_gmm_swiglu_w4(
-        ctypes.byref(cfg), ctypes.byref(w4), _ptr(x_sorted),
+    st = (_lib or lib()).moe_gmm_swiglu_w4(
+        cfg, w4, _ptr(x_sorted),
         _ptr(group_offsets), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(h),
-        _ptr(y_sorted), _ptr(status_word), _stream(stream)),
-        "moe_gmm_swiglu_w4")
+        _ptr(y_sorted), _ptr(status_word), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_gmm_swiglu_w4")
 
 
 class MoeLayerGraph:
