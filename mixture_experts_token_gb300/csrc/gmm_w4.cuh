@@ -29,11 +29,12 @@
 //   are further items, whose weights come from L2.
 //
 // Measured, DeepSeek-V3-shaped experts (7168 x 2048, groups of 128): one
-// token 46 us (8 experts, 182 MB: 3.9 TB/s; the copies alone take 41 us, the
-// launches and the tail of 6.7 items an SM are the rest); 16 tokens over 32
+// token 44.7 us (8 experts, 182 MB: 4.1 TB/s; the launches and the tail of
+// 6.7 items an SM are what it loses); 16 tokens over 32
 // experts 142 us (5.1 TB/s; the copies alone 119 us, the arithmetic alone 145
 // us); 64 tokens, Zipf, 650 us (5.0 TB/s).  Llama4-Maverick-shaped, 16 tokens
-// one expert each, groups of 32 with zero points: 182 us (6.2 TB/s).
+// one expert each, groups of 32 with zero points: 186 to 203 us, with where the
+// weights lie in memory (6.1 to 5.6 TB/s).
 //
 // float32 rows use the same instructions: a float is the exact sum of three
 // bf16 numbers (8 bits of its significand each), so three products with the
@@ -216,7 +217,8 @@ __device__ int find_chunks(const A& a, int2* chunks) {
 // The end of the chunk's rows.
 template <typename A>
 __device__ __forceinline__ int chunk_end(const A& a, int2 c) {
-  return min(min(a.rows, a.offsets[c.x + 1]), c.y + a.chunk);
+  const int end = min(a.rows, a.offsets[c.x + 1]);
+  return end - c.y > a.chunk ? c.y + a.chunk : end;
 }
 
 // The operands of 32 k of eight rows of x: P parts, two instructions each.
@@ -297,8 +299,10 @@ struct Kernel {
   static constexpr int kScaleRec = 8 * E * (Z ? 6 : 4);  // of a step
   static constexpr int kChunk = kTiles * kTileBytes + kScaleRec;
   static constexpr int kTilePair = 2 * kTileBytes;
-  // CTAs an SM has registers for
-  static constexpr int kPerSm = kWarps > 8 ? 1 : kWarps == 8 ? 2 : 4;
+  // CTAs an SM has registers for.  A fifth CTA of four warps (96 registers a
+  // thread) takes one bf16 token from 47.1 to 44.5 us; float32 rows, whose
+  // three parts need the registers, from 49 to 51 us.
+  static constexpr int kPerSm = kWarps == 8 ? 2 : sizeof(T) == 2 ? 5 : 4;
   // columns of an item
   static constexpr int kCols = DUAL ? NW * kTileN : 2 * NW * kTileN;
   static_assert(!kShareX || KW == 1, "x is shared by warps of the same k");
@@ -314,7 +318,7 @@ struct Kernel {
     m.x_slot = (kShareX ? 1 : kWarps) * x_rows * kPitch;
     m.scales = m.x + kXSlots * m.x_slot;
     m.sums = m.scales + kXSlots * kWarps * 2 * kScaleRec;
-    m.groups = m.sums + (KW > 1 ? kWarps * 2 * kRows * kTileN * 4 : 0);
+    m.groups = m.sums + (KW > 1 ? kWarps * 2 * x_rows * kTileN * 4 : 0);
     m.total = m.groups + 8 * chunks + 16;
     return m;
   }
@@ -628,29 +632,31 @@ struct Kernel {
       return;
     }
     float* sums = reinterpret_cast<float*>(base + m.sums);
-    constexpr int kRec = kRows * kTileN;
+    const int rec_floats = a.x_rows * kTileN;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int b = 0; b < NT; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sums[(warp * 2 + h) * kRec +
-               (8 * b + 2 * t + (i & 1)) * kTileN + c + 8 * (i >> 1)] =
-              acc[h][b][i];
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * b + 2 * t + (i & 1);
+          if (r < rows)
+            sums[(warp * 2 + h) * rec_floats + r * kTileN + c +
+                 8 * (i >> 1)] = acc[h][b][i];
+        }
     __syncthreads();
-    constexpr int kOut = NW * (DUAL ? 1 : 2) * kRec;
-    for (int i = threadIdx.x; i < kOut; i += kThreads) {
-      const int rec = i / kRec, r = i % kRec / kTileN, col = i % kTileN;
+    for (int i = threadIdx.x; i < rows * kCols; i += kThreads) {
+      const int r = i / kCols, rec = i % kCols / kTileN, col = i % kTileN;
       const int w = DUAL ? rec : rec >> 1, h = DUAL ? 0 : rec & 1;
-      const int n = n0 + rec * kTileN + col;
-      if (r >= rows || n >= a.l.N) continue;
+      const int n = n0 + i % kCols;
+      if (n >= a.l.N) continue;
       float v = 0.0f, u = 0.0f;
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
-        const float* p = sums + ((k * NW + w) * 2 + h) * kRec + i % kRec;
+        const float* p = sums + ((k * NW + w) * 2 + h) * rec_floats +
+                         r * kTileN + col;
         v += *p;
-        if (DUAL) u += p[kRec];
+        if (DUAL) u += p[rec_floats];
       }
       put(out + static_cast<long long>(row + r) * a.l.N + n,
           DUAL ? swiglu(v, u) : 64.0f * v);
