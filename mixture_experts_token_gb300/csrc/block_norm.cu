@@ -184,8 +184,8 @@ cudaError_t launch_mode(const FwdArgs& a, int mode, int threads,
 // memory that runs kQueue words ahead, across rows: a row's reductions leave
 // memory no pause.  A thread holds word tid of the row (and tid + blockDim.x
 // with NV = 2, which halves the instructions of the reductions where a row
-// has over 512 words: 7168 bf16 columns and one expert 113 -> 81 us).  A row is, in queue order, y (or its k expert rows), x, and
-// a full gate.
+// has over 512 words: 7168 bf16 columns and one expert 113 -> 81 us).  A row
+// is, in queue order, y (or its k expert rows), x, and a full gate.
 // Words in flight: eight experts' and x, so that one row needs no second
 // round trip, or four rows of two.
 template <int MODE>

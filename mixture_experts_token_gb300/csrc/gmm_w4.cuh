@@ -33,8 +33,8 @@
 // 6.7 items an SM are what it loses); 16 tokens over 32
 // experts 142 us (5.1 TB/s; the copies alone 119 us, the arithmetic alone 145
 // us); 64 tokens, Zipf, 650 us (5.0 TB/s).  Llama4-Maverick-shaped, 16 tokens
-// one expert each, groups of 32 with zero points: 186 to 203 us, with where the
-// weights lie in memory (6.1 to 5.6 TB/s).
+// one expert each, groups of 32 with zero points: 186 to 208 us, with where the
+// weights lie in memory (6.1 to 5.4 TB/s).
 //
 // float32 rows use the same instructions: a float is the exact sum of three
 // bf16 numbers (8 bits of its significand each), so three products with the
