@@ -543,7 +543,11 @@ cudaError_t launch_stream(const BwdArgs& a, int parts, int threads,
                           cudaStream_t s) {
   const int words = (a.dh ? 2 : 0) + (a.dout ? 1 : 0) + POST +
                     (GATE == MOE_GATE_FULL);
-  const int bytes = groups * S * words * threads * NV * 16;
+  // the same memory takes the columns that the groups add at the end
+  const int bytes =
+      std::max(groups * S * words * threads * NV * 16,
+               groups > 1 ? a.n16 * Vec<T>::N * static_cast<int>(sizeof(float))
+                          : 0);
   *grid = 0;
   if (bytes + 1024 > d.smem_cta) return cudaSuccess;
   constexpr auto kernel = block_bwd_stream<T, NV, MAXT, POST, GATE, S>;
@@ -553,7 +557,7 @@ cudaError_t launch_stream(const BwdArgs& a, int parts, int threads,
     e = launch::ctas_per_sm<kernel>(d, threads * groups, bytes, &per_sm);
   if (e != cudaSuccess) return e;
   const int rows = (a.T + groups - 1) / groups;
-  *grid = std::max(1, std::min({parts, rows, per_sm * d.sms}));
+  *grid = std::min({parts, rows, per_sm * d.sms});
   kernel<<<*grid, threads * groups, bytes, s>>>(a, threads);
   return cudaGetLastError();
 }
@@ -614,11 +618,14 @@ moe_status_t run(const moe_config_t& c, BwdArgs a, ColArgs ca, bool post,
   ca.parts = a.parts;
   ca.H = c.H;
   ca.w_offset = a.w_offset;
-  const cudaError_t e =
-      c.dtype == MOE_F32
-          ? launch_rows<float>(a, post, parts, &ca.n_parts, s)
-          : launch_rows<__nv_bfloat16>(a, post, parts, &ca.n_parts, s);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  // Without rows there are no partials, and every column sum is zero.
+  if (c.T > 0) {
+    const cudaError_t e =
+        c.dtype == MOE_F32
+            ? launch_rows<float>(a, post, parts, &ca.n_parts, s)
+            : launch_rows<__nv_bfloat16>(a, post, parts, &ca.n_parts, s);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
   const dim3 cols((c.H + kColThreads - 1) / kColThreads, post ? 2 : 1);
   return launch::overlapping(block_bwd_columns, cols,
                              dim3(kColThreads, kColRows), 0, s,

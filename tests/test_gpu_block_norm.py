@@ -349,3 +349,24 @@ def test_columns_off_16_bytes_and_other_stream():
                       s["w_next"], out, h, stream=side)
     side.synchronize()
     assert torch.equal(out, want["out"]) and torch.equal(h, want["h"])
+
+
+@pytest.mark.parametrize("H,dtype", [(8, "bf16"), (264, "bf16"),
+                                     (2048, "bf16"), (4104, "bf16"),
+                                     (16392, "bf16"), (1024, "f32")])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_norm_backward_without_rows(H, dtype, accumulate):
+    """No tokens: the row tensors are empty (their address is null) and the
+    column gradient is zero, or stays as it was."""
+    c, o = config(0, H, dtype), moe.make_block_norm()
+    e = torch.empty((0, H), dtype=DT[dtype], device="cuda")
+    r = torch.empty(0, device="cuda")
+    dw = torch.arange(H, dtype=torch.float32, device="cuda")
+    want = dw.clone() if accumulate else torch.zeros_like(dw)
+    ws = moe.layer_workspace(c, moe.MOE_WS_BLOCK_BACKWARD)
+    ws.fill_(0xAB)
+    w = torch.ones(H, device="cuda")
+    moe.moe_norm_backward(c, o, e, w, r, e, None, e, dw, accumulate, ws)
+    assert torch.equal(dw, want)
+    moe.moe_norm_backward(c, o, e, w, r, e, e, e, dw, accumulate, ws)
+    assert torch.equal(dw, want)
