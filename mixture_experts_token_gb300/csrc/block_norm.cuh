@@ -129,7 +129,8 @@ __device__ __forceinline__ void load_weight(const float* p, int c, bool vec,
 
 // Sum over the threads that hold a row, in every one of them, in a fixed
 // order: within a warp by halving, over warps in warp order.  `red` holds 32
-// floats and is used for one sum only between two barriers.
+// floats; sums that follow each other take different ones: nothing keeps a
+// warp from writing the next sum's place while another still reads this one's.
 template <bool WARP>
 __device__ __forceinline__ float row_sum(float s, float* red) {
 #pragma unroll

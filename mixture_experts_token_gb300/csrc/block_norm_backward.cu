@@ -57,6 +57,9 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) sum_post[u][i] = sum_next[u][i] = 0.0f;
 
+  // Row sums so far: they alternate between two buffers, so that a warp that
+  // is a sum ahead does not write what another still reads.
+  int sums = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const long long base = static_cast<long long>(t) * a.n16;
     int4 v[NV], dh[NV], go[NV], y[NV];
@@ -98,7 +101,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
           s = fmaf(d[u][i], vh, s);
         }
       }
-      s = row_sum<false>(s, red[0]) * a.inv_h;
+      s = row_sum<false>(s, red[sums++ & 1]) * a.inv_h;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         float fv[N], g[N];
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {
       }
     }
     if (post || token) {
-      s = row_sum<false>(s, red[1]);
+      s = row_sum<false>(s, red[sums++ & 1]);
       if (token && tid == 0) static_cast<float*>(a.dgate)[t] = s;
       s = post ? s * a.inv_h : 0.0f;
     }

@@ -370,3 +370,29 @@ def test_norm_backward_without_rows(H, dtype, accumulate):
     assert torch.equal(dw, want)
     moe.moe_norm_backward(c, o, e, w, r, e, e, e, dw, accumulate, ws)
     assert torch.equal(dw, want)
+
+
+# Rows too wide for the streamed kernels, and enough of them that every CTA
+# (at most 304) has two or three: float32 rows of 7168, bf16 rows of 16392 columns.
+WIDE = [(700, 7168, "f32"), (610, 16392, "bf16")]
+
+
+@pytest.mark.parametrize("T,H,dtype", WIDE)
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_backward_wide_rows(T, H, dtype, res):
+    """One row sum a row: each follows the last without another between."""
+    test_norm_backward(T, H, dtype, res)
+
+
+@pytest.mark.parametrize("T,H,dtype", WIDE)
+@pytest.mark.parametrize("kind,post,nxt", [
+    ("none", True, True), ("channel", False, True), ("full", True, False),
+    ("token", False, False), ("token", True, True)])
+def test_block_out_backward_wide_rows(T, H, dtype, kind, post, nxt):
+    s = tensors(T, H, dtype, kind, seed=14)
+    o = moe.make_block_norm(1e-5, 1.0, 0.9, GATES.index(kind))
+    got = backward(config(T, H, dtype), o, s, s["x"], kind, post, nxt)
+    check_backward(got, s, s["x"], kind, o, post, nxt)
+    again = backward(config(T, H, dtype), o, s, s["x"], kind, post, nxt)
+    for n in got:
+        assert got[n] is None or torch.equal(got[n], again[n]), n
