@@ -460,13 +460,12 @@ struct TcKernel {
     int xs = 0;
     long long filled = 0;
     uint32_t phase = 1;
-    bool ok = true;
     passes(a, chunks, n_items, blocks, [&](int, int, int row, int) {
 #pragma unroll 1
       for (int k = 0; k < tiles_k; k += 2) {
-        ok = (a.stall_after_fills < 0 || filled < a.stall_after_fills) &&
-             wait_one(b.x_empty + 8 * xs, phase, abort_flag, a.status);
-        if (!ok) return false;
+        if ((a.stall_after_fills >= 0 && filled >= a.stall_after_fills) ||
+            !wait_one(b.x_empty + 8 * xs, phase, abort_flag, a.status))
+          return false;
         const int n = min(2, tiles_k - k);
         mbar_expect_tx(b.x_full + 8 * xs, n * kXBytes);
         for (int i = 0; i < n; ++i)
@@ -480,15 +479,16 @@ struct TcKernel {
       }
       return true;
     });
-    // after a wait that gave up: this thread's own copies
-    if (!ok)
-      for (long long i = 0; i < filled && i < kXStages; ++i) {
-        if (--xs < 0) {
-          xs = kXStages - 1;
-          phase ^= 1;
-        }
-        tc::mbar_wait(b.x_full + 8 * xs, phase ^ 1, nullptr, a.status);
+    // This thread's last copies must have landed before the CTA ends.  The
+    // instructions that read them wait for them, unless a wait of any warp
+    // gave up: also after this thread's last fill.
+    for (long long i = 0; i < filled && i < kXStages; ++i) {
+      if (--xs < 0) {
+        xs = kXStages - 1;
+        phase ^= 1;
       }
+      tc::mbar_wait(b.x_full + 8 * xs, phase ^ 1, nullptr, a.status);
+    }
   }
 
   // ---- the matrix instructions: one partial sum for each group of W's rows
