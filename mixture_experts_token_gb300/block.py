@@ -60,7 +60,8 @@ class TrainBlock:
                                              device)
 
     def forward(self, x, gate=None):
-        """(out, h_next); keeps what backward() needs."""
+        """(out, h_next), h_next None without w_next; keeps what backward()
+        needs."""
         c, w = self.cfg, self.w
         self.x, self.gate = x, gate
         moe_norm(c, self.opt, x, w["w_pre"], self.h, self.rstd_x)
@@ -129,13 +130,16 @@ class DecodeBlock:
         self.w, self.offset = weights, logit_offset
         self.b = alloc_step_buffers(cfg, device)
         rows = dict(dtype=_row_type(cfg), device=device)
-        self.h, self.out, self.h_next = (
-            torch.empty((cfg.T, cfg.H), **rows) for _ in range(3))
+        self.h, self.out = (torch.empty((cfg.T, cfg.H), **rows)
+                            for _ in range(2))
+        self.h_next = None if weights["w_next"] is None else \
+            torch.empty((cfg.T, cfg.H), **rows)
         self.logits = torch.empty((cfg.T, cfg.E), dtype=torch.float32,
                                   device=device)
 
     def step(self, x, gate=None):
-        """(out, h_next) of rows x [T, H], in this object's buffers."""
+        """(out, h_next) of rows x [T, H], in this object's buffers; h_next is
+        None without w_next."""
         c, w, b = self.cfg, self.w, self.b
         moe_norm(c, self.opt, x, w["w_pre"], self.h)
         moe_router_logits(c, self.h, w["w_router"], self.offset, self.logits,

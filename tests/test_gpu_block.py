@@ -137,3 +137,78 @@ def test_decode_step(T, H, E, k, F, dtype, zeros):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(b.out, first)
+
+
+@pytest.mark.parametrize("post,nxt", [(False, True), (True, False),
+                                      (False, False)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_steps_without_a_norm(dtype, post, nxt):
+    """w_post, w_next or both absent, in the training and the decode step."""
+    T, H, E, k, F = 9, 128, 4, 2, 128
+    c = moe.make_config(T, H, E, k, F, 1, -1.0, dtype=dtype)
+    o = moe.make_block_norm(EPS, 0.0, 0.8, moe.MOE_GATE_CHANNEL)
+    w, normal = _weights(c, dtype, seed=2)
+    for n, there in (("w_post", post), ("w_next", nxt)):
+        if not there:
+            w[n] = None
+    x, gate = normal(T, H, std=2.0), normal(H, std=1.0, t=torch.float32)
+    dout, dh = normal(T, H, std=1.0), normal(T, H, std=1.0) if nxt else None
+
+    def check_forward(b, out, h_next, W):
+        h = block_ref.norm(f64(x), W["w_pre"], EPS)
+        y = _layer(c, h, b.logits.cpu().numpy(), W)
+        want, _ = block_ref.block_out(f64(x), y, W["w_post"], f64(gate),
+                                      "channel", EPS, 0.0, 0.8)
+        assert normwise(f64(out), want) <= TOL[dtype]
+        if nxt:
+            assert normwise(f64(h_next), block_ref.norm(
+                want, W["w_next"], EPS)) <= TOL[dtype]
+        else:
+            assert h_next is None
+        return h, y, want
+
+    W = {n: None if v is None else f64(v) for n, v in w.items()}
+    b = block.TrainBlock(c, o, w)
+    h, y, want = check_forward(b, *b.forward(x, gate), W)
+    got = b.backward(dout, dh)
+    back = {n: v for n, (v, _) in block_ref.block_out_backward(
+        y, W["w_post"], f64(gate), "channel", want, W["w_next"], f64(dout),
+        f64(dh) if nxt else None, EPS, 0.0, 0.8).items()}
+    lay = moe_ref.layer_backward_dropless(
+        moe_ref.MoEConfig(T, H, E, k, F, 1, -1.0), h, b.logits.cpu().numpy(),
+        W["w_gate"], W["w_up"], W["w_down"], back["dy"])
+    dx, dw_pre, _, _ = block_ref.norm_backward(
+        f64(x), W["w_pre"], lay.dx + lay.dlogits @ W["w_router"].T, EPS)
+    expect = {"dx": dx + back["dx"], "w_pre": dw_pre, "gate": back["dgate"],
+              "w_down": lay.dwd}
+    for n in ("w_post", "w_next"):
+        if w[n] is None:
+            assert got[n] is None
+        else:
+            expect[n] = back["d" + n]
+    for n, v in expect.items():
+        assert normwise(f64(got[n]), v) <= TOL[dtype], n
+
+    w4 = moe.make_w4(64, True)
+    for n in ("w_gate", "w_up", "w_down"):
+        q = block.quantize_experts(w4, w[n])
+        full = torch.empty_like(w[n], dtype=torch.float32)
+        moe.moe_w4_dequantize(w4, *w[n].shape, q, full)
+        w[n], W[n] = q, f64(full)
+    b = block.DecodeBlock(c, o, w4, w)
+    check_forward(b, *b.step(x, gate), W)
+
+
+def test_training_step_without_tokens():
+    """T = 0: no rows come out and every weight's gradient is zero."""
+    c = moe.make_config(0, 128, 4, 2, 128, 1, -1.0)
+    o = moe.make_block_norm(EPS, 0.0, 1.0, moe.MOE_GATE_CHANNEL)
+    w, normal = _weights(c, "bf16", seed=3)
+    x, gate = normal(0, 128), normal(128, t=torch.float32)
+    b = block.TrainBlock(c, o, w)
+    out, h_next = b.forward(x, gate)
+    got = b.backward(x.clone(), x.clone())
+    torch.cuda.synchronize()
+    assert out.shape == h_next.shape == got["dx"].shape == (0, 128)
+    for n in ("gate", "w_router", *(n for n in w)):
+        assert (got[n] == 0).all(), n
