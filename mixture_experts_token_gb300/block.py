@@ -11,6 +11,10 @@ of a decode batch with 4-bit expert weights.
 The arithmetic is in the library's kernels (include/moe.h); this module only
 sequences them and owns their buffers.  The router's own linear backward (two
 plain matrix products) uses torch.
+
+The kernels read a tensor's elements one after another from its address.  So
+a tensor that is not contiguous, or has another type, another number of
+elements or another device than the block's is refused with a ValueError.
 """
 from __future__ import annotations
 
@@ -23,11 +27,50 @@ from . import (MOE_F32, MOE_GATE_CHANNEL, MOE_GATE_FULL, MOE_GATE_NONE,
                moe_block_out, moe_block_out_backward, moe_combine_block_out,
                moe_gmm_swiglu_w4, moe_layer, moe_layer_backward, moe_norm,
                moe_norm_backward, moe_permute, moe_route, moe_router_logits,
-               moe_w4_pack, moe_w4_quantize)
+               moe_w4_bytes, moe_w4_pack, moe_w4_quantize)
 
 
 def _row_type(cfg):
     return torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16
+
+
+def _check(name, t, n, dtype, device):
+    """Refuses a tensor whose n elements are not where a kernel reads them."""
+    if not (t.is_contiguous() and t.numel() == n and t.dtype == dtype
+            and t.device.type == device.type):
+        raise ValueError(
+            f"{name}: needs {n} contiguous elements of {dtype} on "
+            f"{device.type}, not {tuple(t.shape)} of {t.dtype} on "
+            f"{t.device.type}, strides {t.stride()}")
+
+
+def _check_columns(cfg, w, device):
+    for n in ("w_pre", "w_post", "w_next"):
+        if n == "w_pre" or w[n] is not None:
+            _check(n, w[n], cfg.H, torch.float32, device)
+
+
+def _check_rows(cfg, device, **rows):
+    for name, t in rows.items():
+        if t is not None:
+            _check(name, t, cfg.T * cfg.H, _row_type(cfg), device)
+
+
+def _check_router(cfg, w, offset, device):
+    _check("w_router", w["w_router"], cfg.H * cfg.E, _row_type(cfg), device)
+    if offset is not None:
+        _check("logit_offset", offset, cfg.T * cfg.E, torch.float32, device)
+
+
+def _check_gate(cfg, opt, gate, device):
+    """The gate's form is opt's; where one of the two is missing, the library
+    refuses the call."""
+    if gate is not None and opt.gate_kind != MOE_GATE_NONE:
+        n, dt = {MOE_GATE_TOKEN: (cfg.T, torch.float32),
+                 MOE_GATE_CHANNEL: (cfg.H, torch.float32),
+                 MOE_GATE_FULL: (cfg.T * cfg.H, _row_type(cfg))}[
+                     opt.gate_kind]
+        _check("gate", gate, n, dt, device)
 
 
 class TrainBlock:
@@ -42,6 +85,12 @@ class TrainBlock:
                  mode=MOE_MODE_FALLBACK_LAYER, device="cuda"):
         self.cfg, self.opt, self.mode = cfg, opt, mode
         self.w, self.offset = weights, logit_offset
+        self.device = torch.device(device)
+        _check_columns(cfg, weights, self.device)
+        for n in ("w_gate", "w_up", "w_down"):
+            _check(n, weights[n], cfg.E * cfg.H * cfg.F, _row_type(cfg),
+                   self.device)
+        _check_router(cfg, weights, logit_offset, self.device)
         rows = dict(dtype=_row_type(cfg), device=device)
         f32 = dict(dtype=torch.float32, device=device)
         T, H = cfg.T, cfg.H
@@ -63,6 +112,8 @@ class TrainBlock:
         """(out, h_next), h_next None without w_next; keeps what backward()
         needs."""
         c, w = self.cfg, self.w
+        _check_rows(c, self.device, x=x)
+        _check_gate(c, self.opt, gate, self.device)
         self.x, self.gate = x, gate
         moe_norm(c, self.opt, x, w["w_pre"], self.h, self.rstd_x)
         moe_router_logits(c, self.h, w["w_router"], self.offset, self.logits,
@@ -78,6 +129,7 @@ class TrainBlock:
         """Gradients of <dout, out> + <dh_next, h_next>: a dict with dx and
         one entry for each weight and the gate."""
         c, w = self.cfg, self.w
+        _check_rows(c, self.device, dout=dout, dh_next=dh_next)
         like = torch.empty_like
         columns = {n: None if w[n] is None else like(w[n])
                    for n in ("w_pre", "w_post", "w_next")}
@@ -106,8 +158,10 @@ class TrainBlock:
 
 
 def quantize_experts(w4, w):
-    """Packed 4-bit matrices of expert weights w [E, K, N]."""
+    """Packed 4-bit matrices of expert weights w [E, K, N] (contiguous; a
+    transposed view is refused)."""
     E, K, N = w.shape
+    _check("w", w, E * K * N, w.dtype, torch.device("cuda"))
     G = -(-K // w4.group_size)
     codes = torch.empty((E, K // 2, N), dtype=torch.uint8, device=w.device)
     scales = torch.empty((E, G, N), dtype=torch.bfloat16, device=w.device)
@@ -128,6 +182,13 @@ class DecodeBlock:
                  device="cuda"):
         self.cfg, self.opt, self.w4 = cfg, opt, w4
         self.w, self.offset = weights, logit_offset
+        self.device = torch.device(device)
+        _check_columns(cfg, weights, self.device)
+        _check_router(cfg, weights, logit_offset, self.device)
+        for n, K, N in (("w_gate", cfg.H, cfg.F), ("w_up", cfg.H, cfg.F),
+                        ("w_down", cfg.F, cfg.H)):
+            _check(n, weights[n], moe_w4_bytes(w4, cfg.E, K, N), torch.uint8,
+                   self.device)
         self.b = alloc_step_buffers(cfg, device)
         rows = dict(dtype=_row_type(cfg), device=device)
         self.h, self.out = (torch.empty((cfg.T, cfg.H), **rows)
@@ -141,6 +202,8 @@ class DecodeBlock:
         """(out, h_next) of rows x [T, H], in this object's buffers; h_next is
         None without w_next."""
         c, w, b = self.cfg, self.w, self.b
+        _check_rows(c, self.device, x=x)
+        _check_gate(c, self.opt, gate, self.device)
         moe_norm(c, self.opt, x, w["w_pre"], self.h)
         moe_router_logits(c, self.h, w["w_router"], self.offset, self.logits,
                           b["status"])
