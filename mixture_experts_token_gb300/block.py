@@ -63,14 +63,15 @@ def _check_router(cfg, w, offset, device):
 
 
 def _check_gate(cfg, opt, gate, device):
-    """The gate's form is opt's; where one of the two is missing, the library
-    refuses the call."""
-    if gate is not None and opt.gate_kind != MOE_GATE_NONE:
-        n, dt = {MOE_GATE_TOKEN: (cfg.T, torch.float32),
-                 MOE_GATE_CHANNEL: (cfg.H, torch.float32),
-                 MOE_GATE_FULL: (cfg.T * cfg.H, _row_type(cfg))}[
-                     opt.gate_kind]
-        _check("gate", gate, n, dt, device)
+    """The gate's form is opt's; a gate that opt does not name, a missing one
+    and an unknown form are left for the library to refuse."""
+    if gate is None:
+        return
+    forms = {MOE_GATE_TOKEN: (cfg.T, torch.float32),
+             MOE_GATE_CHANNEL: (cfg.H, torch.float32),
+             MOE_GATE_FULL: (cfg.T * cfg.H, _row_type(cfg))}
+    if opt.gate_kind in forms:
+        _check("gate", gate, *forms[opt.gate_kind], device)
 
 
 class TrainBlock:

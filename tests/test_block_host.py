@@ -112,3 +112,15 @@ def test_steps_refuse_rows_and_gates_they_would_misread(m, kind, shape,
                      lambda: decode.step(x, bad)):
             with pytest.raises(ValueError, match="gate"):
                 call()
+
+
+@pytest.mark.parametrize("kind", [-1, 4])
+def test_an_unknown_gate_is_the_librarys_error(m, kind):
+    from mixture_experts_token_gb300 import block
+    c = m.make_config(3, 64, 4, 2, 32, 1)
+    b = block.TrainBlock(c, m.make_block_norm(gate=kind), weights(64, 4, 32),
+                         device="cpu")
+    x = torch.zeros(3, 64, dtype=torch.bfloat16)
+    with pytest.raises(m.MoeError) as err:
+        b.forward(x, x)
+    assert err.value.status == m.MOE_ERR_INVALID_ARG
