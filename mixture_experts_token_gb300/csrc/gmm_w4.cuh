@@ -312,8 +312,8 @@ struct Kernel {
   struct Smem {
     int x, x_slot, scales, sums, groups, total;
   };
-  __host__ __device__ static Smem smem(int x_rows, int chunks) {
-    Smem m;
+  __host__ __device__ static constexpr Smem smem(int x_rows, int chunks) {
+    Smem m = {};
     m.x = kWarps * kRing * kTilePair;
     m.x_slot = (kShareX ? 1 : kWarps) * x_rows * kPitch;
     m.scales = m.x + kXSlots * m.x_slot;
@@ -683,6 +683,10 @@ __global__ void __launch_bounds__(
 // than there are groups.  CTAs that take chunks of one group at the same time
 // share its weights in L2.
 constexpr int kMaxSplits = 512;
+constexpr int kMaxChunks = kMaxExperts + kMaxSplits;
+// Dynamic shared memory that every CTA may have: 227 KB, less 1 KB for the
+// kernels' own static arrays.
+constexpr int kMaxShared = 226 * 1024;
 inline void set_chunk(GmmArgs* a, int rows) {
   const long long most = static_cast<long long>(rows) * kMaxSplits;
   a->chunk = rows * static_cast<int>((a->rows + most - 1) / most);
@@ -693,16 +697,12 @@ template <typename T, bool DUAL, int NW, int KW, int NT, int G, bool Z>
 cudaError_t launch_one(GmmArgs a, int tokens, const Device& d,
                        cudaStream_t s) {
   using Ker = Kernel<T, DUAL, NW, KW, NT, G, Z>;
-  // routing gives a group at most one row of each token; float32 rows that
-  // every warp copies for itself fill shared memory sooner
+  // routing gives a group at most one row of each token
   a.x_rows = std::max(1, std::min(Ker::kRows, tokens));
   set_chunk(&a, a.x_rows);
-  int bytes = Ker::smem(a.x_rows, a.chunks).total;
-  while (bytes + 1024 > d.smem_sm && a.x_rows > 1) {
-    a.x_rows /= 2;
-    set_chunk(&a, a.x_rows);
-    bytes = Ker::smem(a.x_rows, a.chunks).total;
-  }
+  static_assert(Ker::smem(Ker::kRows, kMaxChunks).total <= kMaxShared,
+                "any call's shared memory fits a CTA");
+  const int bytes = Ker::smem(a.x_rows, a.chunks).total;
   constexpr auto kernel = gmm_w4_kernel<T, DUAL, NW, KW, NT, G, Z>;
   const cudaError_t e = launch::allow_shared<kernel>(d);
   if (e != cudaSuccess) return e;

@@ -85,8 +85,8 @@ struct TcArgs {
 struct TcSmem {
   int codes, zeros, sums, bars, groups, total;
 };
-__host__ __device__ inline TcSmem tc_smem(const Layout& l, int chunks) {
-  TcSmem m;
+__host__ __device__ constexpr TcSmem tc_smem(const Layout& l, int chunks) {
+  TcSmem m = {};
   m.codes = kXStages * 2 * kXBytes;
   m.zeros = m.codes + kExpandWarps * kCodeTiles * 2 * kTileBytes;
   m.sums = m.zeros + (l.zeros ? kExpandWarps * kZeroSlots * 2 * 16 *
@@ -97,6 +97,9 @@ __host__ __device__ inline TcSmem tc_smem(const Layout& l, int chunks) {
   m.total = m.groups + 8 * chunks;
   return m;
 }
+static_assert(tc_smem({0, 0, 32, true}, kMaxChunks).total + 1024 <=
+                  kMaxShared,
+              "any call's shared memory fits a CTA");
 
 // D (+)= A B over N16 * 16 of k, with A in tensor memory (8 columns for each
 // 16 of k) and B in shared memory (32 bytes, 2 in the descriptor); `leader`
