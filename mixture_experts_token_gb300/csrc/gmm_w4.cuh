@@ -97,16 +97,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
                "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst),
-               "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
-               "l"(src)
-               : "memory");
-}
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }

@@ -65,8 +65,8 @@ constexpr int kStageK = 128;       // rows of W in a stage: two tiles
 constexpr int kStages = 2;
 constexpr int kXStages = 4;        // further ahead: x comes from L2 or HBM
 constexpr int kXBytes = kNR * 128;  // 64 columns of x
-constexpr int kCodeTiles = 4;      // tiles of codes in flight, of each warp
-constexpr int kZeroSlots = kCodeTiles;  // zero points, with each tile
+// Tiles of codes, with their zero points, that each warp has in flight.
+constexpr int kCodeTiles = 4;
 constexpr int kTmemA = 256;        // columns: accumulators, then A
 constexpr int kSumPitch = kNR + 1;
 constexpr unsigned kSleepNs = 100;
@@ -89,7 +89,7 @@ __host__ __device__ constexpr TcSmem tc_smem(const Layout& l, int chunks) {
   TcSmem m = {};
   m.codes = kXStages * 2 * kXBytes;
   m.zeros = m.codes + kExpandWarps * kCodeTiles * 2 * kTileBytes;
-  m.sums = m.zeros + (l.zeros ? kExpandWarps * kZeroSlots * 2 * 16 *
+  m.sums = m.zeros + (l.zeros ? kExpandWarps * kCodeTiles * 2 * 16 *
                                     (kStepK / l.group)
                               : 0);
   m.bars = m.sums + 128 * kSumPitch * 4;
@@ -329,11 +329,11 @@ struct TcKernel {
     const int c = lane >> 2, turn = warp / 8;  // tile of a stage
     const uint32_t codes =
         sb + m.codes + warp * (kCodeTiles * 2 * kTileBytes) + lane * 16;
-    const uint32_t zeros = sb + m.zeros + warp * (kZeroSlots * 2 * 16 * E);
+    const uint32_t zeros = sb + m.zeros + warp * (kCodeTiles * 2 * 16 * E);
     const uint32_t a_at = tmem + kTmemA + t * 128 +
                           (static_cast<uint32_t>(32 * q) << 16);
     // the copying side, kCodeTiles tiles ahead
-    int item = blockIdx.x, row = 0, r1 = 0, tile = 0, zslot = 0;
+    int item = blockIdx.x, row = 0, r1 = 0, tile = 0;
     const char *p0 = nullptr, *p1 = nullptr, *s0 = nullptr, *s1 = nullptr;
     const auto enter = [&] {
       const int2 chunk = chunks[item / blocks];
@@ -371,7 +371,7 @@ struct TcKernel {
           const int at = tile % kTiles;  // the pointers are at this tile
           const int to = (min(tiles_k - tile + at, kTiles) - at) * kTileBytes +
                          32 * E;
-          const uint32_t d = zeros + zslot * (2 * 16 * E) + lane * 16;
+          const uint32_t d = zeros + in_slot * (2 * 16 * E) + lane * 16;
           copy16(d, p0 + to);
           copy16(d + 16 * E, p1 + to);
         }
@@ -386,7 +386,6 @@ struct TcKernel {
       }
       copies_commit();
       in_slot = in_slot == kCodeTiles - 1 ? 0 : in_slot + 1;
-      zslot = in_slot;
     };
 #pragma unroll 1
     for (int i = 0; i < kCodeTiles; ++i) copy_tile();
