@@ -100,8 +100,9 @@ __global__ void __launch_bounds__(kThreads)
                 const __nv_bfloat16* __restrict__ scales,
                 const uint8_t* __restrict__ zeros, int n_mats, Layout l,
                 bool wide, char* __restrict__ packed) {
-  // rows 4 bytes past 64: neighbouring rows start in neighbouring banks
-  __shared__ uint8_t rows[kPackK / 2][kPackCols + 4];
+  // written as words; rows 4 bytes past 64: neighbouring rows start in
+  // neighbouring banks
+  __shared__ __align__(4) uint8_t rows[kPackK / 2][kPackCols + 4];
   const int n0 = blockIdx.x * kPackCols, G = l.groups();
   const int E = kStepK / l.group;  // groups of a step
   const int records = min(kPackRecords, l.tiles_n() - kPackRecords *
