@@ -921,11 +921,13 @@ moe_status_t moe_block_out_backward(
  *               scale[k / group_size, n]
  * with codes 0..15, bf16 scales, and zero = 8 without zero points.  The
  * weights are constants: there is no gradient of them.
- *   w       [n, K, N] dtype          n matrices (one for each expert)
+ *   w       [n, K, N] dtype          n matrices (one for each expert), 16-byte
+ *                                    aligned
  *   codes   [n, K/2, N] uint8        row 2i in the low four bits, 2i+1 high
  *   scales  [n, G, N] bf16           G = ceil(K / group_size)
  *   zeros   [n, G, N] uint8, 0..15   NULL without zero points
  *   packed  moe_w4_bytes() bytes, 16-byte aligned: what the products read
+ * codes, scales and zeros may lie on any element's boundary.
  * K must be even; K, N <= 2^20.
  * ---------------------------------------------------------------------- */
 typedef struct {

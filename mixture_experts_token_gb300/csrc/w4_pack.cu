@@ -213,6 +213,10 @@ bool shape_ok(int n, int K, int N) {
 dim3 record_grid(const Layout& l, int n) {
   return dim3(l.tiles_n(), n < 4096 ? n : 4096);
 }
+// scales are read and written one by one: their natural alignment is enough
+bool ok_scales(const void* p) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 1) == 0;
+}
 moe_status_t launched() {
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -238,7 +242,7 @@ moe_status_t moe_w4_quantize(const moe_w4_t* opt, int32_t n, int32_t K,
       (dtype != MOE_F32 && dtype != MOE_BF16))
     return MOE_ERR_INVALID_ARG;
   if (n == 0) return MOE_OK;
-  if (!ok_ptr(w, true) || codes == nullptr || !ok_ptr(scales, false) ||
+  if (!ok_ptr(w, true) || codes == nullptr || !ok_scales(scales) ||
       (zeros != nullptr) != (opt->zero_points != 0))
     return MOE_ERR_INVALID_ARG;
   const Layout l = layout(*opt, K, N);
@@ -261,7 +265,7 @@ moe_status_t moe_w4_pack(const moe_w4_t* opt, int32_t n, int32_t K, int32_t N,
                          moe_stream_t stream) {
   if (!w4::options_ok(opt) || !shape_ok(n, K, N)) return MOE_ERR_INVALID_ARG;
   if (n == 0) return MOE_OK;
-  if (codes == nullptr || !ok_ptr(scales, false) || !ok_ptr(packed, true) ||
+  if (codes == nullptr || !ok_scales(scales) || !ok_ptr(packed, true) ||
       (zeros != nullptr) != (opt->zero_points != 0))
     return MOE_ERR_INVALID_ARG;
   const Layout l = layout(*opt, K, N);

@@ -339,3 +339,19 @@ def test_w4_sizes_and_arguments(m):
     c0 = cfg_of(m, F=0)
     assert lib.moe_gmm_swiglu_w4(ctypes.byref(c0), W, p, p, p, p, p, p, p,
                                  None, None) == bad
+
+
+def test_w4_scales_need_their_natural_alignment(m):
+    lib, p, W = m.lib(), ctypes.c_void_p(0x1000), ctypes.byref(m.make_w4(64))
+    odd, half = ctypes.c_void_p(0x1001), ctypes.c_void_p(0x1002)
+    # no matrices: a call that is accepted does nothing
+    for n, want in ((1, m.MOE_ERR_INVALID_ARG), (0, m.MOE_OK)):
+        assert lib.moe_w4_pack(W, n, 64, 16, p, odd, None, p, None) == want
+        assert lib.moe_w4_quantize(W, n, 64, 16, m.MOE_F32, p, p, odd, None,
+                                   None) == want
+    import torch
+    if not torch.cuda.is_available():     # past the checks, to a launch
+        assert lib.moe_w4_pack(W, 1, 64, 16, p, half, None, p,
+                               None) == m.MOE_ERR_CUDA
+        assert lib.moe_w4_quantize(W, 1, 64, 16, m.MOE_F32, p, p, half, None,
+                                   None) == m.MOE_ERR_CUDA

@@ -333,3 +333,27 @@ def test_offsets_past_32_bits():
     h, y = run_swiglu(cfg, w4, x, torch.tensor(off, dtype=torch.int32).cuda(),
                       packs)
     check_swiglu(x, [0, 2], [0], [w for _, w in one], h, y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_codes_scales_and_zeros_at_any_element(dtype):
+    """One matrix of several, and views whose addresses end in an odd byte
+    (codes, zeros) or half a word (scales): the bits of aligned copies."""
+    n, K, N, group = 1, 66, 17, 64
+    w = torch.randn(n, K, N, generator=torch.Generator().manual_seed(3))
+    w, w4, G = w.to(DT[dtype]).cuda(), moe.make_w4(group, True), 2
+
+    def run(skip):
+        def view(rows, dt):
+            t = torch.zeros(n * rows * N + skip, dtype=dt, device="cuda")
+            return t[skip:]
+        codes, zp = view(K // 2, torch.uint8), view(G, torch.uint8)
+        scales = view(G, torch.bfloat16)
+        assert codes.data_ptr() % 4 == skip
+        assert scales.data_ptr() % 4 == 2 * skip
+        moe.moe_w4_quantize(w4, n, K, N, w, codes, scales, zp)
+        packed = moe.alloc_w4(w4, n, K, N)
+        moe.moe_w4_pack(w4, n, K, N, codes, scales, zp, packed)
+        return codes, scales, zp, packed
+    for a, b in zip(run(0), run(1)):
+        assert torch.equal(a, b)
