@@ -396,3 +396,62 @@ def test_block_out_backward_wide_rows(T, H, dtype, kind, post, nxt):
     again = backward(config(T, H, dtype), o, s, s["x"], kind, post, nxt)
     for n in got:
         assert got[n] is None or torch.equal(got[n], again[n]), n
+
+
+# Rows enough that each CTA of the persistent kernels takes several: its queue
+# then runs across rows, the row sums' buffers alternate, a token's gate is
+# loaded a row ahead, and the combine's ring of rows (13 rows, or 4 of 32
+# experts) comes round.
+@pytest.mark.parametrize("T,H,dtype,kind,post,nxt", [
+    (2500, 4104, "bf16", "none", True, True),
+    (2500, 4104, "bf16", "token", True, True),
+    (2500, 4104, "bf16", "full", True, True),
+    (2500, 7168, "bf16", "channel", True, True),
+    (6000, 1032, "bf16", "token", True, True),
+    (6001, 1032, "bf16", "full", False, True),
+    (2500, 4104, "bf16", "token", False, True),
+    (2500, 4104, "bf16", "channel", True, False),
+    (2500, 4104, "bf16", "full", False, False),
+    (2500, 5120, "f32", "token", True, True)])
+def test_block_out_many_rows(T, H, dtype, kind, post, nxt):
+    s = tensors(T, H, dtype, kind, seed=15)
+    o = moe.make_block_norm(1e-5, 1.0, 0.9, GATES.index(kind))
+    got = forward(config(T, H, dtype), o, s, kind, post, nxt)
+    check_forward(got, s, f64(s["y"]), kind, o, post, nxt)
+
+
+@pytest.mark.parametrize("T,H,dtype", [(6000, 1032, "bf16"),
+                                       (2500, 7168, "bf16"),
+                                       (2500, 5120, "f32")])
+def test_norm_many_rows(T, H, dtype):
+    test_norm(T, H, dtype)
+
+
+@pytest.mark.parametrize("T,H,k,dtype,kind,post,nxt", [
+    (6000, 1032, 1, "bf16", "token", True, True),
+    (2500, 4104, 2, "bf16", "full", True, True),
+    (2500, 7168, 8, "bf16", "channel", True, True),
+    (2500, 4104, 32, "bf16", "full", True, True),
+    (2500, 4104, 32, "bf16", "token", False, True),
+    (2500, 7168, 1, "bf16", "none", True, False),
+    (2500, 7168, 1, "bf16", "token", False, False),
+    (2500, 4104, 2, "bf16", "full", False, False),
+    (2500, 5120, 3, "f32", "channel", True, True)])
+def test_combine_block_out_many_rows(T, H, k, dtype, kind, post, nxt):
+    s = tensors(T, H, dtype, kind, seed=16)
+    g = torch.Generator(device="cuda").manual_seed(17)
+    on = dict(generator=g, device="cuda")
+    ys = torch.randn(T * k, H, **on).to(DT[dtype])
+    row_of = torch.randperm(T * k, **on).int().reshape(T, k)
+    lost = torch.rand(T, k, **on) < 0.2
+    lost[T // 3] = lost[T - 1] = True       # tokens that lost every row
+    ys[row_of[lost].long()] = float("nan")  # and rows that are not read
+    row_of[lost] = -1
+    w = torch.rand(T, k, **on)
+    c = config(T, H, dtype, k)
+    o = moe.make_block_norm(1e-5, 1.0, 0.9, GATES.index(kind))
+    got = forward(c, o, s, kind, post, nxt, combine=(ys, row_of, w))
+    y = torch.empty_like(s["y"])
+    moe.moe_combine(c, ys, row_of, w, y)
+    assert torch.equal(got["y"], y)
+    check_forward(got, s, f64(y), kind, o, post, nxt)
