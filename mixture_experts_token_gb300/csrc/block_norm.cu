@@ -15,8 +15,10 @@
 // are float32.
 //
 // Measured, bf16: 8192 x 7168 with a channel gate 78 us (470 MB, 6.0 TB/s);
-// 8192 x 5120 with one expert combined 81 us (420 MB, 5.2 TB/s); one token of
-// 7168 5.9 us a call, of which most is the call.
+// 8192 x 5120 with one expert combined 81 us (420 MB, 5.2 TB/s); the norm
+// alone, 8192 x 7168, 44 us (235 MB, 5.4 TB/s); one token of 7168 5.9 us a
+// call, of which most is the call.  float32: 2047 x 5120 with a full gate 37 us
+// (210 MB, 5.6 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -32,7 +34,12 @@ enum Mode { kNormOnly = 0, kOut = 1, kCombineOut = 2 };
 
 // Rows of up to 128 words (WARP: a warp per row, several rows per CTA), which
 // leave a scheduler many short rows to choose from, and rows too wide for the
-// streamed form below: NV 16-byte words of the row per thread, in registers.
+// streamed form below (over 1280 words: more than 640 threads of two words do
+// not have registers for the column weights): NV 16-byte words of the row per
+// thread, in registers.  One row a CTA at a time: the end of the block with a
+// channel gate takes 45 us at 2048 x 7168 float32 (5.3 TB/s), 63 us at
+// 2048 x 16384 bf16 (4.3) and 80 us at 1024 x 32768 bf16 (3.3); the streamed
+// form 31 us at 2048 x 10240 bf16 (5.4).
 template <typename T, int NV, bool WARP, int MAXT, int MODE>
 __global__ void __launch_bounds__(MAXT)
     block_fwd_kernel(const FwdArgs a) {

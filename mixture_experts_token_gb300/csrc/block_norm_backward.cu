@@ -43,7 +43,14 @@ struct BwdArgs {
   bool vec_w;
 };
 
-// Rows wider than the streamed form holds: one row per CTA, in registers.
+// Rows wider than the streamed form holds (1280 words): one row per CTA, in
+// registers, which the column sums of four words a thread take most of.  bf16
+// spills: 376 bytes a thread with the branch up to 2048 words, 1756 (732
+// without it) above, where a thread has 64 registers.  Measured with a channel
+// gate: 2048 x 7168 float32 99 us (3.6 TB/s), 2048 x 16384 bf16 152 us (2.7),
+// 1024 x 32768 bf16 364 us (1.1); the norm alone 50, 75 and 159 us.  The
+// streamed form at its widest, 2048 x 10240 bf16, takes 88 us (2.9 TB/s; it
+// spills up to 196 bytes) and the norm alone 37 us (4.5).
 // POST: the branch's end is part of it; else only the norm of v.
 template <typename T, int NV, int MAXT, bool POST>
 __global__ void __launch_bounds__(MAXT) block_bwd_kernel(const BwdArgs a) {

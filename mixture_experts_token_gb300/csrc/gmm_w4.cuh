@@ -38,7 +38,9 @@
 //
 // float32 rows use the same instructions: a float is the exact sum of three
 // bf16 numbers (8 bits of its significand each), so three products with the
-// exact weights give float32 accuracy.
+// exact weights give float32 accuracy.  Every block of 16 columns splits the
+// rows again, and that bounds them: one token of the 7168 x 2048 experts 98 us,
+// 64 tokens of 32 experts (16 rows each) 849 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -290,7 +292,7 @@ struct Kernel {
   static constexpr int kChunk = kTiles * kTileBytes + kScaleRec;
   static constexpr int kTilePair = 2 * kTileBytes;
   // CTAs an SM has registers for.  A fifth CTA of four warps (96 registers a
-  // thread) takes one bf16 token from 47.1 to 44.5 us; float32 rows, whose
+  // thread) takes one bf16 token from 47.1 to 44.7 us; float32 rows, whose
   // three parts need the registers, from 49 to 51 us.
   static constexpr int kPerSm = kWarps == 8 ? 2 : sizeof(T) == 2 ? 5 : 4;
   // columns of an item

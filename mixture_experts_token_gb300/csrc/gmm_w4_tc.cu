@@ -22,13 +22,17 @@
 // one that gives up raises MOE_DEV_TIMEOUT and the CTA drains and returns.
 //
 // Measured, 7168 x 2048 experts, groups of 128: 1024 tokens over 256 experts
-// (32 rows each) 2.3 ms, 39% of the time its bytes need at 6.8 TB/s; 256
-// tokens over 32 experts (64 rows each) 602 us.  A tile of 64 rows of W takes
-// about 1000 clocks whatever the rows, and no one unit bounds it: without the
-// matrix instructions, the tensor memory traffic, the expansion or the copies
-// of x, one at a time, it stays within 10% of that, and with all of them gone
-// 560 clocks of hand-over between the roles are left.  Each role's warp has
-// about 150 dependent instructions a tile and 7 warps share a scheduler.
+// (32 rows each) 2.3 ms, of which its bytes need 39% at 6.8 TB/s; 256 tokens
+// over 32 experts (64 rows each) 602 us.  A tile of 64 rows of W takes about
+// 1000 clocks whatever the rows, and no one unit bounds it: without the matrix
+// instructions, the tensor memory traffic, the expansion or the copies of x,
+// one at a time, it stays within 10% of that, and with all of them gone 560
+// clocks are left.  Hand-overs are not what is left: stages of twice the rows
+// halved them and changed nothing (339 us both, 128 tokens of 32 experts).
+// Each role's warp has about 150 dependent instructions a tile, 7 warps share
+// a scheduler, and 864 threads leave each 72 registers, in which the adding
+// warps do not fit (52 to 88 bytes a thread spilled) and wait for the six
+// loads of a partial sum in turn.
 #include <atomic>
 
 #include "gmm_w4.cuh"

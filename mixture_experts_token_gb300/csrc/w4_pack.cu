@@ -2,6 +2,11 @@
 // (w4.cuh has the layout) and expanding again.  Work of loading a model, not
 // of a step: each kernel reads its input once and writes its output once
 // (the quantiser reads a group twice, the second time from the caches).
+// Measured, 256 bf16 matrices of 7168 x 2048 in groups of 128: quantise 6.0 ms
+// and expand 7.5 ms, 8.4 ms with zero points (1.4 ms of bytes at 6.8 TB/s),
+// pack 2.7 ms (0.57 ms).  Only packing was tuned: a thread of the quantiser
+// loads one value at a time, and the expander reads a word of codes anew for
+// each of its eight nibbles.
 #include <cuda_bf16.h>
 #include <math.h>
 
