@@ -38,9 +38,14 @@
 //
 // float32 rows use the same instructions: a float is the exact sum of three
 // bf16 numbers (8 bits of its significand each), so three products with the
-// exact weights give float32 accuracy.  Every block of 16 columns splits the
-// rows again, and that bounds them: one token of the 7168 x 2048 experts 98 us,
-// 64 tokens of 32 experts (16 rows each) 849 us.
+// exact weights give float32 accuracy.  A matrix instruction truncates what it
+// adds to, so the leading parts are summed apart from the others, over at most
+// 64 rows of W: their products are short, most of their sums exact, and what
+// the sums of the small parts lose is 2^-8 of what it would be in one sum.
+// (256 x 512, groups of 128: y is 1e-7 off, normwise; in one sum it was 1.4e-6
+// and always towards zero, for 0 to 3% less time.)  Every block of 16 columns
+// splits the rows again, and that bounds them: one token of the 7168 x 2048
+// experts 99 us, 64 tokens of 32 experts (16 rows each) 900 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -535,7 +540,10 @@ struct Kernel {
         w[i][r][0] = q.x, w[i][r][1] = q.y, w[i][r][2] = q.z;
         w[i][r][3] = q.w;
       }
-    float part[2][NT][4], s[2][2];
+    // of the leading part of x, and of the others
+    constexpr int kSums = Rows<T>::P > 1 ? 2 : 1;
+    constexpr int kSumK = kSums > 1 && G > kTileK ? kTileK : G;  // rows in one
+    float part[kSums][2][NT][4], s[2][2];
     uint32_t zero[2][2];
     constexpr int kHalves = 2 * TILES;
 #pragma unroll
@@ -555,10 +563,15 @@ struct Kernel {
             zero[r][1] = fma2(__byte_perm(z, 0, 0x4141), kPow127 | 0x80008000u, 0);
           }
         }
+      }
+      if (h == 0 || k % kSumK == 0) {
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
+        for (int q = 0; q < kSums; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) part[0][b][i] = part[1][b][i] = 0.0f;
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              part[q][0][b][i] = part[q][1][b][i] = 0.0f;
       }
       uint32_t op[2][2][4];
 #pragma unroll
@@ -579,17 +592,20 @@ struct Kernel {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              mma(part[r][b], op[r][i], o[2 * i], o[2 * i + 1], part[r][b]);
+            for (int r = 0; r < 2; ++r) {
+              float(&d)[4] = part[p == 0 ? 0 : kSums - 1][r][b];
+              mma(d, op[r][i], o[2 * i], o[2 * i + 1], d);
+            }
         }
-        if (h == kHalves - 1 || (k + 32) % G == 0) {  // a group ends
+        if (h == kHalves - 1 || (k + 32) % kSumK == 0) {  // a sum ends
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[r][b][i] =
-                  fmaf(s[r][i >> 1], part[r][b][i],
-                       acc[r][b][i]);
+            for (int i = 0; i < 4; ++i) {
+              float v = part[0][r][b][i];
+              if (kSums > 1) v += part[kSums - 1][r][b][i];
+              acc[r][b][i] = fmaf(s[r][i >> 1], v, acc[r][b][i]);
+            }
         }
       }
     }

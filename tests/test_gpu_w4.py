@@ -357,3 +357,28 @@ def test_codes_scales_and_zeros_at_any_element(dtype):
         return codes, scales, zp, packed
     for a, b in zip(run(0), run(1)):
         assert torch.equal(a, b)
+
+
+# each form of the kernel: k over four warps; 8 and 16 rows a pass
+@pytest.mark.parametrize("counts,H,F", [([30, 3, 16], 520, 260),
+                                        ([4] * 40, 512, 2056),
+                                        ([64] * 8, 520, 2056)])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False),
+                                         (128, True)])
+def test_float32_products_lean_neither_way(counts, H, F, group, zeros):
+    """Rounding to nearest errs to both sides alike; a sum that is truncated
+    once errs by half a unit in its last place towards zero on average, that
+    is 2^-24 of it.  The mean of the signed errors of the 10^4 and more outputs
+    has to be below that (their own scatter leaves about 1e-9 of it)."""
+    cfg, w4, x, off, doff, packs, ws = case(counts, H, F, len(counts), "f32",
+                                            group, zeros, seed=21)
+    h, y = run_swiglu(cfg, w4, x, doff, packs)
+    x64, h64 = f64(x), f64(h)
+    wh, wy = np.empty_like(h64), np.empty((off[-1], H))
+    for e in range(len(counts)):
+        r = slice(off[e], off[e + 1])
+        wh[r] = ref.silu(x64[r] @ ws[0][e]) * (x64[r] @ ws[1][e])
+        wy[r] = h64[r] @ ws[2][e]
+    for got, want, what in ((h64, wh, "h"), (f64(y), wy, "y")):
+        lean = ((got - want) * np.sign(want)).mean() / np.abs(want).mean()
+        assert abs(lean) < 2.0 ** -24, (what, lean)
