@@ -147,6 +147,58 @@ moe_status_t moe_route(const moe_config_t *cfg, const float *logits,
                        int32_t *status_word, moe_stream_t stream);
 
 /* ----------------------------------------------------------------------
+ * moe_route_scores -- routing by scores, a balancing bias and groups: a
+ * token's scores s are the softmax or the sigmoid of its E logits, and its
+ * experts rank by c = s + bias.  Of `groups` groups of E / groups consecutive
+ * experts the top_groups take part whose sums of their group_top largest c
+ * are largest (equal sums: the lower group); the k experts of largest c among
+ * them are chosen, equal c to the lower index.  Scores, sums and ranks are
+ * those of float64; without a bias the logits stand for c, but in sums of
+ * several: the same order, also where scores round to the same.  The weights
+ * are
+ *     w_j = scale * s_j / (renorm ? sum of the k chosen s : 1).
+ *   logits   in  [T, E] float32
+ *   bias     in  [E] float32 or NULL; not part of the weights
+ *   topk_idx out [T, k] int32, by descending c
+ *   topk_w   out [T, k] float32
+ *   status_word  in/out, device int32 or NULL.
+ * An expert whose logit or bias is NaN or infinite sets MOE_DEV_NONFINITE,
+ * has score 0, ranks behind all others of the groups that take part, and
+ * lets its group's sum be -infinity where it is one of the group_top.
+ * top_groups * (E / groups) must be at least k.
+ *
+ * moe_route_scores_backward -- dlogits [T, E] float32 from dtopk_w [T, k],
+ * the gradient of the weights at the experts chosen (the choice has none):
+ * with a_j = dtopk_w_j w_j, less w_j / scale * sum a with renorm,
+ *     sigmoid  dlogits_e = a_e (1 - s_e) at chosen experts, else 0
+ *     softmax  dlogits_e = (a_e at chosen experts) - s_e * sum a.
+ * A chosen index outside [0, E) is skipped.  A logit that is NaN or infinite
+ * gets no gradient.
+ * ---------------------------------------------------------------------- */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+typedef struct {
+  int32_t score;      /* moe_score_t                                       */
+  int32_t groups;     /* divides E, 1..64; 1: no groups                    */
+  int32_t top_groups; /* groups that take part, 1..groups                  */
+  int32_t group_top;  /* experts that make a group's sum, 1..min(4, E/groups) */
+  int32_t renorm;     /* 1: the chosen weights sum to scale                */
+  float scale;        /* of the weights; finite                            */
+} moe_route_scores_t;
+
+moe_status_t moe_route_scores(const moe_config_t *cfg,
+                              const moe_route_scores_t *opt,
+                              const float *logits, const float *bias,
+                              int32_t *topk_idx, float *topk_w,
+                              int32_t *status_word, moe_stream_t stream);
+moe_status_t moe_route_scores_backward(const moe_config_t *cfg,
+                                       const moe_route_scores_t *opt,
+                                       const float *logits,
+                                       const int32_t *topk_idx,
+                                       const float *dtopk_w, float *dlogits,
+                                       moe_stream_t stream);
+
+/* ----------------------------------------------------------------------
  * moe_check_overflow -- counts and the ragged overflow check [PR5920 Why,
  * How; PR4760 review: group_sizes per expert, experts_per_rank].
  *   topk_idx        in  [T, k] int32 (device)
@@ -987,6 +1039,113 @@ moe_status_t moe_gmm_swiglu_w4(const moe_config_t *cfg, const moe_w4_t *opt,
                                const void *w_gate, const void *w_up,
                                const void *w_down, void *h, void *y_sorted,
                                int32_t *status_word, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------
+ * Experts in microscaled 4-bit floating point, for serving: rows and weights
+ * both in 4 bits, multiplied by the block-scaled tensor-core instruction.  A
+ * code is a sign, two exponent bits and a mantissa bit: 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6.  A block of consecutive values along the reduction axis shares a
+ * scale:
+ *   block 32  a power of two, 2^(floor(log2 m) - 2) of the block's largest
+ *             magnitude m, not below 2^-127, as its exponent plus 127
+ *             (255: NaN);
+ *   block 16  a number of 4 exponent bits (bias 7) and 3 mantissa bits, m / 6
+ *             rounded to the nearest (at most 448; 0x7f: NaN).  The values
+ *             are multiplied beforehand by the reciprocal, rounded to float32,
+ *             of a float32 scale of the whole tensor.
+ * A code is the nearest to value / scale, ties to the even code, magnitudes
+ * over 6 to 6.  A block with a NaN or an infinity gets the NaN scale: all its
+ * values are NaN.  A block whose scale is 0 is 0.  The rounding has no
+ * gradient; these calls serve, and have no backward.
+ *   codes    [rows, K/2] uint8      column 2i in the low four bits; 16-byte
+ *                                   aligned
+ *   scales   [rows, moe_mx_scale_row()] uint8, one for each block of a row in
+ *                                   order, then up to three bytes that are
+ *                                   written as 0 and not read; 4-byte aligned
+ *   packed   moe_mx_bytes() bytes   weight matrices as the products read them;
+ *                                   16-byte aligned
+ * K must be a multiple of 32, at most 2^20.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t block; /* 32 or 16 values share a scale                         */
+  /* Tensor scales of the rows and of the activations h (blocks of 16; 1 with
+   * blocks of 32): normal and at most 1e38.                              */
+  float x_scale, h_scale;
+} moe_mx_t;
+
+/* Bytes of a row of scales (a multiple of 4), and of n packed matrices
+ * [K, N] (0 for an invalid argument; N <= 2^20). */
+int32_t moe_mx_scale_row(const moe_mx_t *opt, int32_t K);
+size_t moe_mx_bytes(const moe_mx_t *opt, int32_t n, int32_t K, int32_t N);
+
+/* moe_mx_quantize_rows -- codes and scales of x [R, K] dtype under the tensor
+ * scale `scale` (1 with blocks of 32); moe_mx_dequantize_rows -- their values,
+ * code * block scale * scale in float32, rounded to dtype once.  x is 16-byte
+ * aligned. */
+moe_status_t moe_mx_quantize_rows(const moe_mx_t *opt, int32_t R, int32_t K,
+                                  moe_dtype_t dtype, const void *x,
+                                  float scale, uint8_t *codes,
+                                  uint8_t *scales, moe_stream_t stream);
+moe_status_t moe_mx_dequantize_rows(const moe_mx_t *opt, int32_t R, int32_t K,
+                                    const uint8_t *codes,
+                                    const uint8_t *scales, float scale,
+                                    moe_dtype_t dtype, void *x,
+                                    moe_stream_t stream);
+
+/* moe_mx_quantize -- codes and scales of n weight matrices w [n, K, N] dtype
+ * (16-byte aligned), blocks along K: codes [n, N, K/2], scales [n, N, row],
+ * the order in which checkpoints hold them.  scale: [n] float32 (device),
+ * each matrix's tensor scale, or NULL for 1 (always with blocks of 32). */
+moe_status_t moe_mx_quantize(const moe_mx_t *opt, int32_t n, int32_t K,
+                             int32_t N, moe_dtype_t dtype, const void *w,
+                             const float *scale, uint8_t *codes,
+                             uint8_t *scales, moe_stream_t stream);
+
+/* moe_mx_pack -- lays codes and scales [n, N, ...] out for the products, once
+ * when a model is loaded; moe_mx_dequantize -- w [n, K, N] from packed. */
+moe_status_t moe_mx_pack(const moe_mx_t *opt, int32_t n, int32_t K, int32_t N,
+                         const uint8_t *codes, const uint8_t *scales,
+                         void *packed, moe_stream_t stream);
+moe_status_t moe_mx_dequantize(const moe_mx_t *opt, int32_t n, int32_t K,
+                               int32_t N, const void *packed,
+                               const float *scale, moe_dtype_t dtype, void *w,
+                               moe_stream_t stream);
+
+/* The products of moe_gmm_gate_up, moe_gmm_down and moe_gmm_swiglu with both
+ * operands in this form: w_gate and w_up are E packed matrices [H, F], w_down
+ * E packed matrices [F, H], *_scale [E] float32 (device) their tensor scales
+ * or NULL for 1 (always with blocks of 32).  H and F must be multiples of 32,
+ * else MOE_ERR_UNSUPPORTED.  Any number of rows in a group; rows behind the
+ * last group are left as they were.
+ *   moe_gmm_gate_up_mx  rows of x quantised under x_scale; h is quantised
+ *                       under h_scale from its float32 values, codes
+ *                       [T*k, F/2] and scales [T*k, row]
+ *   moe_gmm_down_mx     y_sorted [T*k, H] dtype, sums float32
+ *   moe_gmm_swiglu_mx   x_sorted [T*k, H] dtype, quantised on the way;
+ *                       workspace: moe_mx_workspace_bytes() bytes, 16-byte
+ *                       aligned
+ * A group whose expert index is outside [0, E) is skipped and sets
+ * MOE_DEV_BAD_INDEX; MOE_DEV_TIMEOUT if a pipeline wait gave up. */
+size_t moe_mx_workspace_bytes(const moe_config_t *cfg, const moe_mx_t *opt);
+moe_status_t moe_gmm_gate_up_mx(
+    const moe_config_t *cfg, const moe_mx_t *opt, int32_t n_groups,
+    const int32_t *group_expert, const uint8_t *x_codes,
+    const uint8_t *x_scales, const int32_t *group_offsets, const void *w_gate,
+    const void *w_up, const float *gate_scale, const float *up_scale,
+    uint8_t *h_codes, uint8_t *h_scales, int32_t *status_word,
+    moe_stream_t stream);
+moe_status_t moe_gmm_down_mx(const moe_config_t *cfg, const moe_mx_t *opt,
+                             int32_t n_groups, const int32_t *group_expert,
+                             const uint8_t *h_codes, const uint8_t *h_scales,
+                             const int32_t *group_offsets, const void *w_down,
+                             const float *down_scale, void *y_sorted,
+                             int32_t *status_word, moe_stream_t stream);
+moe_status_t moe_gmm_swiglu_mx(
+    const moe_config_t *cfg, const moe_mx_t *opt, const void *x_sorted,
+    const int32_t *group_offsets, const void *w_gate, const void *w_up,
+    const void *w_down, const float *gate_scale, const float *up_scale,
+    const float *down_scale, void *y_sorted, int32_t *status_word,
+    void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ----------------------------------------------------------------------
  * Host-side queries (no GPU work).

@@ -28,6 +28,7 @@ MOE_WS_PERMUTE, MOE_WS_CHUNKED, MOE_WS_LAYER = 0, 1, 2
 MOE_WS_GMM_BACKWARD, MOE_WS_LAYER_BACKWARD = 3, 4
 MOE_WS_BLOCK_BACKWARD = 5
 MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL = range(4)
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
 class MoeConfig(ctypes.Structure):
@@ -72,6 +73,19 @@ class MoeW4(ctypes.Structure):
     _fields_ = [("group_size", c_int32), ("zero_points", c_int32)]
 
 
+class MoeRouteScores(ctypes.Structure):
+    """moe_route_scores_t."""
+    _fields_ = [("score", c_int32), ("groups", c_int32),
+                ("top_groups", c_int32), ("group_top", c_int32),
+                ("renorm", c_int32), ("scale", c_float)]
+
+
+class MoeMx(ctypes.Structure):
+    """moe_mx_t."""
+    _fields_ = [("block", c_int32), ("x_scale", c_float),
+                ("h_scale", c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -100,6 +114,8 @@ def _declare(h):
     cfg = ctypes.POINTER(MoeConfig)
     opt = ctypes.POINTER(MoeBlockNorm)
     w4 = ctypes.POINTER(MoeW4)
+    scores = ctypes.POINTER(MoeRouteScores)
+    mx = ctypes.POINTER(MoeMx)
     i32 = c_int32
     sig = {
         "moe_router_logits": [cfg, P, P, P, P, P, P],
@@ -172,6 +188,18 @@ def _declare(h):
         "moe_gmm_gate_up_w4": [cfg, w4, i32, P, P, P, P, P, P, P, P],
         "moe_gmm_down_w4": [cfg, w4, i32, P, P, P, P, P, P, P],
         "moe_gmm_swiglu_w4": [cfg, w4, P, P, P, P, P, P, P, P, P],
+        "moe_route_scores": [cfg, scores, P, P, P, P, P, P],
+        "moe_route_scores_backward": [cfg, scores, P, P, P, P, P],
+        "moe_mx_quantize_rows": [mx, i32, i32, c_int, P, c_float, P, P, P],
+        "moe_mx_dequantize_rows": [mx, i32, i32, P, P, c_float, c_int, P, P],
+        "moe_mx_quantize": [mx, i32, i32, i32, c_int, P, P, P, P, P],
+        "moe_mx_pack": [mx, i32, i32, i32, P, P, P, P],
+        "moe_mx_dequantize": [mx, i32, i32, i32, P, P, c_int, P, P],
+        "moe_gmm_gate_up_mx": [cfg, mx, i32, P, P, P, P, P, P, P, P, P, P, P,
+                               P],
+        "moe_gmm_down_mx": [cfg, mx, i32, P, P, P, P, P, P, P, P, P],
+        "moe_gmm_swiglu_mx": [cfg, mx, P, P, P, P, P, P, P, P, P, P, P,
+                              c_size_t, P],
     }
     for name, args in sig.items():
         fn = getattr(h, name)
@@ -198,6 +226,12 @@ def _declare(h):
     h.moe_workspace_bytes.restype = c_size_t
     h.moe_w4_bytes.argtypes = [w4, i32, i32, i32]
     h.moe_w4_bytes.restype = c_size_t
+    h.moe_mx_bytes.argtypes = [mx, i32, i32, i32]
+    h.moe_mx_bytes.restype = c_size_t
+    h.moe_mx_scale_row.argtypes = [mx, i32]
+    h.moe_mx_scale_row.restype = c_int32
+    h.moe_mx_workspace_bytes.argtypes = [cfg, mx]
+    h.moe_mx_workspace_bytes.restype = c_size_t
     h.moe_validate_config.argtypes = [cfg]
     h.moe_validate_config.restype = c_int
     h.moe_row_dot_parts.argtypes = [cfg]
@@ -284,6 +318,16 @@ def make_block_norm(eps=1e-6, w_offset=0.0, res_scale=1.0,
 
 def make_w4(group_size=128, zero_points=False) -> MoeW4:
     return MoeW4(int(group_size), int(zero_points))
+
+
+def make_route_scores(score=MOE_SCORE_SOFTMAX, groups=1, top_groups=1,
+                      group_top=1, renorm=False, scale=1.0) -> MoeRouteScores:
+    return MoeRouteScores(int(score), int(groups), int(top_groups),
+                          int(group_top), int(renorm), float(scale))
+
+
+def make_mx(block=32, x_scale=1.0, h_scale=1.0) -> MoeMx:
+    return MoeMx(int(block), float(x_scale), float(h_scale))
 
 
 # --------------------------------------------------------- entry points ---
@@ -673,6 +717,28 @@ def moe_layer_backward(cfg, x, logits, w_gate, w_up, w_down, dy, dx,
             "capacity": info.capacity}
 
 
+# ------------------------------------------- routing by scores ----------
+def moe_route_scores(cfg, opt, logits, bias, topk_idx, topk_w,
+                     status_word=None, stream=None):
+    """Top-k by softmax or sigmoid scores plus a bias, within the best groups
+    of experts (opt: make_route_scores())."""
+    st = (_lib or lib()).moe_route_scores(
+        cfg, opt, _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_w),
+        _ptr(status_word), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_route_scores")
+
+
+def moe_route_scores_backward(cfg, opt, logits, topk_idx, dtopk_w, dlogits,
+                              stream=None):
+    """dlogits [T, E] from the gradient of moe_route_scores' weights."""
+    st = (_lib or lib()).moe_route_scores_backward(
+        cfg, opt, _ptr(logits), _ptr(topk_idx), _ptr(dtopk_w),
+        _ptr(dlogits), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_route_scores_backward")
+
+
 # ------------------------------------------------------ block norms ------
 def moe_norm(cfg, opt, x, w, h, rstd=None, stream=None):
     """h = N(x; w), the norm before the block; rstd [T] for the backward."""
@@ -843,6 +909,102 @@ class MoeLayerGraph:
             pass
 
 
+# ------------------------------------- microscaled 4-bit numbers ---------
+def moe_mx_bytes(mx, n, K, N) -> int:
+    return int(lib().moe_mx_bytes(mx, n, K, N))
+
+
+def moe_mx_scale_row(mx, K) -> int:
+    """Bytes of a row of scales."""
+    return int(lib().moe_mx_scale_row(mx, K))
+
+
+def moe_mx_workspace_bytes(cfg, mx) -> int:
+    return int(lib().moe_mx_workspace_bytes(cfg, mx))
+
+
+def moe_mx_quantize_rows(mx, R, K, x, scale, codes, scales, stream=None):
+    """Codes and block scales of rows x [R, K] under a tensor scale."""
+    st = (_lib or lib()).moe_mx_quantize_rows(
+        mx, R, K, _float_type(x), _ptr(x), scale, _ptr(codes), _ptr(scales),
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_mx_quantize_rows")
+
+
+def moe_mx_dequantize_rows(mx, R, K, codes, scales, scale, x, stream=None):
+    st = (_lib or lib()).moe_mx_dequantize_rows(
+        mx, R, K, _ptr(codes), _ptr(scales), scale, _float_type(x), _ptr(x),
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_mx_dequantize_rows")
+
+
+def moe_mx_quantize(mx, n, K, N, w, scale, codes, scales, stream=None):
+    """Codes and block scales (along K) of weights w [n, K, N]; scale: [n]
+    tensor scales or None."""
+    st = (_lib or lib()).moe_mx_quantize(
+        mx, n, K, N, _float_type(w), _ptr(w), _ptr(scale), _ptr(codes),
+        _ptr(scales), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_mx_quantize")
+
+
+def moe_mx_pack(mx, n, K, N, codes, scales, packed, stream=None):
+    """Lays weights out for the products, into alloc_mx()'s buffer."""
+    st = (_lib or lib()).moe_mx_pack(
+        mx, n, K, N, _ptr(codes), _ptr(scales), _ptr(packed),
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_mx_pack")
+
+
+def moe_mx_dequantize(mx, n, K, N, packed, scale, w, stream=None):
+    st = (_lib or lib()).moe_mx_dequantize(
+        mx, n, K, N, _ptr(packed), _ptr(scale), _float_type(w), _ptr(w),
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_mx_dequantize")
+
+
+def moe_gmm_gate_up_mx(cfg, mx, x_codes, x_scales, group_offsets, w_gate,
+                       w_up, gate_scale, up_scale, h_codes, h_scales,
+                       status_word=None, stream=None, n_groups=0,
+                       group_expert=None):
+    st = (_lib or lib()).moe_gmm_gate_up_mx(
+        cfg, mx, n_groups, _ptr(group_expert), _ptr(x_codes), _ptr(x_scales),
+        _ptr(group_offsets), _ptr(w_gate), _ptr(w_up), _ptr(gate_scale),
+        _ptr(up_scale), _ptr(h_codes), _ptr(h_scales), _ptr(status_word),
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_gmm_gate_up_mx")
+
+
+def moe_gmm_down_mx(cfg, mx, h_codes, h_scales, group_offsets, w_down,
+                    down_scale, y_sorted, status_word=None, stream=None,
+                    n_groups=0, group_expert=None):
+    st = (_lib or lib()).moe_gmm_down_mx(
+        cfg, mx, n_groups, _ptr(group_expert), _ptr(h_codes), _ptr(h_scales),
+        _ptr(group_offsets), _ptr(w_down), _ptr(down_scale), _ptr(y_sorted),
+        _ptr(status_word), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_gmm_down_mx")
+
+
+def moe_gmm_swiglu_mx(cfg, mx, x_sorted, group_offsets, w_gate, w_up, w_down,
+                      gate_scale, up_scale, down_scale, y_sorted, status_word,
+                      workspace, stream=None):
+    """The grouped SwiGLU FFN on packed microscaled experts; rows and h are
+    quantised on the way (workspace: mx_workspace())."""
+    st = (_lib or lib()).moe_gmm_swiglu_mx(
+        cfg, mx, _ptr(x_sorted), _ptr(group_offsets), _ptr(w_gate),
+        _ptr(w_up), _ptr(w_down), _ptr(gate_scale), _ptr(up_scale),
+        _ptr(down_scale), _ptr(y_sorted), _ptr(status_word), _ptr(workspace),
+        _nbytes(workspace), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_gmm_swiglu_mx")
+
+
 # ------------------------------------------------- buffer allocation ------
 def alloc_step_buffers(cfg, device="cuda"):
     """Device buffers for calling the entry points one by one (torch owns
@@ -897,3 +1059,29 @@ def alloc_w4(w4, n, K, N, device="cuda"):
     if b == 0 and n != 0:
         raise MoeError(MOE_ERR_INVALID_ARG, "moe_w4_bytes")
     return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+def alloc_mx(mx, n, K, N, device="cuda"):
+    """A buffer for n packed microscaled [K, N] matrices."""
+    import torch
+    b = moe_mx_bytes(mx, n, K, N)
+    if b == 0 and n != 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_mx_bytes")
+    return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+def alloc_mx_rows(mx, R, K, device="cuda"):
+    """Codes [R, K/2] and scales [R, row] of R quantised rows."""
+    import torch
+    row = moe_mx_scale_row(mx, K)
+    if row == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_mx_scale_row")
+    return (torch.empty((R, K // 2), dtype=torch.uint8, device=device),
+            torch.empty((R, row), dtype=torch.uint8, device=device))
+
+
+def mx_workspace(cfg, mx, device="cuda"):
+    """moe_gmm_swiglu_mx's workspace."""
+    import torch
+    n = moe_mx_workspace_bytes(cfg, mx)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)

@@ -1,0 +1,657 @@
+// Products of the routed rows with microscaled 4-bit experts on tcgen05, rows
+// and weights both in 4 bits (mx.cuh has the formats and the layout).
+//
+//   gate_up: h[r] = silu(x[r] Wg) * (x[r] Wu), quantised again
+//   down:    y[r] = h[r] Wd
+//
+// The block-scaled matrix instruction multiplies 64 of k of both operands and
+// their scales at once, so nothing is expanded.  128 columns of weights are
+// its M rows and the rows of x its N columns: a group of few rows costs few
+// columns, and one of any number of rows splits at any multiple of 16.
+//
+// A CTA an SM walks over items, a tile of 128 columns (of the gate and the up
+// matrix, or of the down matrix) for up to NT rows of one group:
+//   * a thread brings the weights' records by bulk copy and the rows' codes by
+//     TMA, 256 of k a stage (rows past the group's are other groups' or zeros;
+//     they reach only columns that are not written);
+//   * four warps, on every fourth stage each, bring the rows' scales into the
+//     order that tensor memory takes;
+//   * a warp copies a stage's scales to tensor memory and issues the matrix
+//     instructions; scales have two buffers there, and one is written again
+//     when the instructions of the stage but one before have completed;
+//   * four warps turn the sums into rows of the output, a thread a column,
+//     while the next item's sums go to the other accumulator.
+// Every wait is bounded; one that gives up raises MOE_DEV_TIMEOUT and the CTA
+// drains and returns.
+#pragma once
+
+#include <atomic>
+
+#include "chunks.cuh"
+#include "launch.cuh"
+#include "mx.cuh"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace tc {
+// The GEMMs' test hook (gmm_tc.cu): stop the producer after this many stage
+// fills (-1: never), so that the next wait runs out.
+extern std::atomic<long long> g_stall_after_fills;
+}  // namespace tc
+
+namespace mx {
+
+using launch::Device;
+
+struct GmmArgs {
+  const int32_t *offsets, *map;
+  const uint8_t* x_scales;
+  const char *w0, *w1;
+  const float *s0, *s1;  // the matrices' scales [E], or null
+  float x_scale;
+  float inv_out;         // gate_up: 1 / h_scale
+  uint8_t *h_codes, *h_scales;
+  void* y;
+  int32_t* status;
+  Layout l;
+  int n_experts, n_groups, rows, chunk, chunks;
+  bool f32;    // y's type
+  bool early;  // may start before the kernel that writes the rows has ended
+  long long stall_after_fills;  // tests of the timeout path only (-1: off)
+};
+
+// Which instance a call takes, and the launch (gmm_mx_*.cu).
+cudaError_t launch_gmm_mx_gate_up(const GmmArgs& a, const void* codes,
+                                  cudaStream_t s);
+cudaError_t launch_gmm_mx_down(const GmmArgs& a, const void* codes,
+                               cudaStream_t s);
+
+constexpr int kEpiWarps = 4;
+constexpr int kLoadWarp = kEpiWarps;
+constexpr int kMmaWarp = kLoadWarp + 1;
+constexpr int kScaleWarp = kMmaWarp + 1;
+constexpr int kScaleWarps = 4;
+constexpr int kWarps = kScaleWarp + kScaleWarps;
+constexpr int kGmmThreads = kWarps * 32;
+constexpr int kRowBox = 16;  // rows of one TMA copy
+constexpr int kMaxSplits = 512;
+constexpr int kMaxChunks = kMaxExperts + kMaxSplits;
+constexpr int kMaxShared = 226 * 1024;
+constexpr int kMaxStages = 8;
+constexpr int kBarBytes = 256;
+
+// ---------------------------------------------------------------- PTX ----
+// Bytes from global to shared memory, in one piece (16-byte aligned).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
+                                          uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// 32 rows of 16 bytes to four columns of all four quarters of the lanes.
+__device__ __forceinline__ void scales_to_tmem(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem),
+               "l"(desc)
+               : "memory");
+}
+// The matrix of 32 rows of 16 bytes, eight rows to a core matrix: no swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(16 >> 4) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+}
+// D (+)= A B over 64 of k, both 4-bit in shared memory, each block of BLOCK of
+// k times its scales in tensor memory.
+template <int BLOCK>
+__device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b,
+                                        uint32_t idesc, uint32_t sa,
+                                        uint32_t sb, uint32_t accumulate) {
+  if (BLOCK == 16)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of the block-scaled kinds: B's scale word's first
+// byte (bits 4-5), A and B of the 4-bit type (1 in bits 7-9 and 10-12), N >> 3
+// in bits 17-22, scales a power of two (bit 23), M >> 7 in bits 27-28, A's
+// scale word's first byte (bits 29-30).
+__device__ __forceinline__ uint32_t idesc_mx(int block, int n, int byte) {
+  return static_cast<uint32_t>(byte) << 4 | 1u << 7 | 1u << 10 |
+         static_cast<uint32_t>(n >> 3) << 17 | (block == 32 ? 1u << 23 : 0u) |
+         1u << 27 | static_cast<uint32_t>(byte) << 29;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
+// The registers of the loads before it are there.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
+                 "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// ------------------------------------------------------------- kernel ----
+template <bool DUAL, int BLOCK, int NT>
+struct Gmm {
+  static constexpr int kMats = DUAL ? 2 : 1;
+  static constexpr int kTiles = scale_tiles(BLOCK);  // of 128 rows, a stage
+  static constexpr int kRec = record_bytes(BLOCK);
+  static constexpr int kRowTiles = (NT + 127) / 128;
+  static constexpr int kX = kMats * kRec;             // the rows' codes
+  static constexpr int kXs = kX + NT * 128;           // and scales
+  static constexpr int kStage =
+      (kXs + kRowTiles * kTiles * kScaleTile + 1023) / 1024 * 1024;
+  static constexpr int kRoom = kMaxShared - 1024 - kBarBytes - 8 * kMaxChunks;
+  static constexpr int kStages =
+      kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
+  static_assert(kStages >= 3, "the scales' two buffers lag by two stages");
+  static_assert(kRec % 1024 == 0 && NT % 16 == 0, "swizzled tiles aligned");
+  // Tensor memory: accumulators [buffer][matrix][NT], then scales [buffer]
+  // of the weights [matrix][tile][4] and the rows [tile][row tile][4].
+  static constexpr int kAcc = kMats * NT;
+  static constexpr int kScaleA = 4 * kTiles;
+  static constexpr int kScales =
+      kMats * kScaleA + 4 * kTiles * kRowTiles;
+  static constexpr int kBuffers = 2 * kAcc + 2 * kScales <= 512 ? 2 : 1;
+  static constexpr int kScaleAt = kBuffers * kAcc;
+  static_assert(kScaleAt + 2 * kScales <= 512, "tensor memory");
+
+  static constexpr int shared_bytes(int chunks) {
+    return 1024 + kStages * kStage + kBarBytes + 8 * chunks;
+  }
+
+  // A stage is full when its copies and its rows' scales are there.
+  struct Bars {
+    uint32_t full, scales, empty, acc_full, acc_empty, done;
+  };
+  // Where a role stands: its item, and the ring's stage and phase.
+  struct Ring {
+    int st = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+  };
+  struct Item {
+    int tile, expert, row, rows;
+  };
+  __device__ static __forceinline__ Item item_at(const GmmArgs& a,
+                                                 const int2* chunks, int i,
+                                                 int tiles) {
+    const int2 c = chunks[i / tiles];
+    return {i % tiles, a.map ? a.map[c.x] : c.x, c.y, chunk_end(a, c) - c.y};
+  }
+  // Calls f(item) for the passes of up to NT rows of this CTA's items until
+  // it returns false.
+  template <typename F>
+  __device__ static __forceinline__ void passes(const GmmArgs& a,
+                                                const int2* chunks,
+                                                int n_items, int tiles,
+                                                const F& f) {
+#pragma unroll 1
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
+      Item it = item_at(a, chunks, i, tiles);
+      const int end = it.row + it.rows;
+#pragma unroll 1
+      for (; it.row < end; it.row += NT) {
+        it.rows = min(NT, end - it.row);
+        if (!f(it)) return;
+      }
+    }
+  }
+  __device__ static __forceinline__ bool wait_all(uint32_t bar, uint32_t phase,
+                                                  volatile int* abort_flag,
+                                                  int32_t* status) {
+    return __all_sync(0xffffffffu,
+                      tc::mbar_wait(bar, phase, abort_flag, status));
+  }
+
+  __device__ static void run(const GmmArgs& a, const CUtensorMap* map) {
+    extern __shared__ __align__(1024) char raw[];
+    char* base = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    __shared__ int abort_word;
+    __shared__ uint32_t tmem_word;
+    volatile int* abort_flag = &abort_word;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const uint32_t sb = tc::smem_u32(base);
+    Bars b;
+    b.full = sb + kStages * kStage;
+    b.scales = b.full + 8 * kStages;
+    b.empty = b.scales + 8 * kStages;
+    b.acc_full = b.empty + 8 * kStages;
+    b.acc_empty = b.acc_full + 8 * kBuffers;
+    b.done = b.acc_empty + 8 * kBuffers;
+    if (threadIdx.x == 0) {
+      abort_word = 0;
+      for (int i = 0; i < kStages; ++i) {
+        tc::mbar_init(b.full + 8 * i, 1);
+        tc::mbar_init(b.scales + 8 * i, 1);
+        tc::mbar_init(b.empty + 8 * i, 1);
+      }
+      for (int i = 0; i < kBuffers; ++i) {
+        tc::mbar_init(b.acc_full + 8 * i, 1);
+        tc::mbar_init(b.acc_empty + 8 * i, kEpiWarps);
+      }
+      tc::mbar_init(b.done, 1);
+      tc::fence_barrier_init();
+      tc::fence_proxy_async_smem();
+    }
+    if (warp == kMmaWarp) {
+      tc::tmem_alloc(tc::smem_u32(&tmem_word), tc::kTmemCols);
+      tc::tmem_relinquish();
+    }
+    int2* chunks =
+        reinterpret_cast<int2*>(base + kStages * kStage + kBarBytes);
+    const int n_chunks = find_chunks<kWarps>(a, chunks);  // barriers within
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    launch::let_next_start();
+    const uint32_t tmem = tmem_word;
+    const int tiles = a.l.tiles_n(), n_items = n_chunks * tiles;
+    if (warp < kEpiWarps)
+      write_out(a, b, chunks, n_items, tiles, tmem, warp, lane, abort_flag);
+    else if (warp == kLoadWarp)
+      load(a, map, sb, b, chunks, n_items, tiles, lane, abort_flag);
+    else if (warp == kMmaWarp)
+      multiply(a, sb, b, chunks, n_items, tiles, tmem, lane, abort_flag);
+    else
+      load_scales(a, sb, b, chunks, n_items, tiles, warp - kScaleWarp, lane,
+                  abort_flag);
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, tc::kTmemCols);
+  }
+
+  // ---- weights and the rows' codes
+  __device__ static void load(const GmmArgs& a, const CUtensorMap* map,
+                              uint32_t sb, const Bars& b, const int2* chunks,
+                              int n_items, int tiles, int lane,
+                              volatile int* abort_flag) {
+    if (lane != 0) return;
+    const int stages = a.l.stages();
+    Ring ring;
+    ring.phase = 1;
+    long long filled = 0;
+    const auto weights = [&](const Item& it, int s, int st) {
+      const long long at = it.expert * a.l.matrix() + it.tile * a.l.tile() +
+                           static_cast<long long>(s) * kRec;
+      const uint32_t dst = sb + st * kStage, bar = b.full + 8 * st;
+      const int boxes = (it.rows + kRowBox - 1) / kRowBox;
+      tc::mbar_expect_tx(bar, kMats * kRec + boxes * kRowBox * 128);
+      bulk_load(dst, a.w0 + at, kRec, bar);
+      if (DUAL) bulk_load(dst + kRec, a.w1 + at, kRec, bar);
+    };
+    const auto rows = [&](const Item& it, int s, int st) {
+      const uint32_t dst = sb + st * kStage + kX, bar = b.full + 8 * st;
+#pragma unroll 1
+      for (int r = 0; r < it.rows; r += kRowBox)
+        tc::tma_load_2d(dst + r * 128, map, bar, s * (kStageK / 2),
+                        it.row + r);
+    };
+    // The weights of the first stages do not wait for the kernel that writes
+    // the rows.
+    int ahead = 0;
+    if (a.stall_after_fills < 0)
+      passes(a, chunks, n_items, tiles, [&](const Item& it) {
+        for (int s = 0; s < stages && ahead < kStages; ++s, ++ahead)
+          weights(it, s, ahead);
+        return ahead < kStages;
+      });
+    launch::wait_for_previous();
+    passes(a, chunks, n_items, tiles, [&](const Item& it) {
+#pragma unroll 1
+      for (int s = 0; s < stages; ++s) {
+        if (a.stall_after_fills >= 0 && filled >= a.stall_after_fills)
+          return false;
+        if (filled >= ahead) {
+          if (!tc::mbar_wait(b.empty + 8 * ring.st, ring.phase, abort_flag,
+                             a.status))
+            return false;
+          weights(it, s, ring.st);
+        }
+        rows(it, s, ring.st);
+        ++filled;
+        ring.next();
+      }
+      return true;
+    });
+    // This thread's last copies must have landed before the CTA ends.  The
+    // instructions that read them wait for them, unless a wait of any warp
+    // gave up: also after this thread's last fill.
+    for (long long i = 0; i < filled && i < kStages; ++i) {
+      if (--ring.st < 0) {
+        ring.st = kStages - 1;
+        ring.phase ^= 1;
+      }
+      tc::mbar_wait(b.full + 8 * ring.st, ring.phase ^ 1, nullptr, a.status);
+    }
+  }
+
+  // ---- the rows' scales, a word of four at a time: every kScaleWarps-th
+  // stage is this warp's
+  __device__ static void load_scales(const GmmArgs& a, uint32_t sb,
+                                     const Bars& b, const int2* chunks,
+                                     int n_items, int tiles, int warp,
+                                     int lane, volatile int* abort_flag) {
+    constexpr int kWords = NT * kTiles / 32;
+    static_assert(NT * kTiles % 32 == 0, "whole words a lane");
+    const int stages = a.l.stages(), groups = a.l.K / BLOCK;
+    const int sr = scale_row(a.l.K, BLOCK);
+    Ring ring;
+    ring.phase = 1;
+    int turn = 0;
+    launch::wait_for_previous();
+    passes(a, chunks, n_items, tiles, [&](const Item& it) {
+#pragma unroll 1
+      for (int s = 0; s < stages; ++s, ring.next()) {
+        const bool mine = turn == warp;
+        turn = turn == kScaleWarps - 1 ? 0 : turn + 1;
+        if (!mine) continue;
+        uint32_t v[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const int r = (i * 32 + lane) / kTiles;
+          const int at = (s * kTiles + lane % kTiles) * 4;
+          v[i] = 0;
+          if (r < it.rows && at < groups) {
+            v[i] = *reinterpret_cast<const uint32_t*>(
+                a.x_scales + static_cast<long long>(it.row + r) * sr + at);
+            // what lies behind the row's last scale counts as zero
+            if (groups - at < 4) v[i] &= (1u << (8 * (groups - at))) - 1;
+          }
+        }
+        if (!wait_all(b.empty + 8 * ring.st, ring.phase, abort_flag,
+                      a.status))
+          return false;
+        const uint32_t dst =
+            sb + ring.st * kStage + kXs + lane % kTiles * kScaleTile;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const int r = (i * 32 + lane) / kTiles;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(
+                           dst + r / 128 * (kTiles * kScaleTile) +
+                           r % 32 * 16 + r % 128 / 32 * 4),
+                       "r"(v[i])
+                       : "memory");
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(b.scales + 8 * ring.st);
+      }
+      return true;
+    });
+  }
+
+  // ---- the matrix instructions
+  __device__ static void multiply(const GmmArgs& a, uint32_t sb,
+                                  const Bars& b, const int2* chunks,
+                                  int n_items, int tiles, uint32_t tmem,
+                                  int lane, volatile int* abort_flag) {
+    const int stages = a.l.stages();
+    const bool leader = lane == 0;
+    Ring ring, back1, back2;  // this stage and the two before it
+    int done = 0;             // stages so far, counted up to two
+    int buf = 0, sbuf = 0;
+    uint32_t acc_phase = 1;
+    passes(a, chunks, n_items, tiles, [&](const Item& it) {
+      const int n = (it.rows + 15) / 16 * 16;
+      const uint32_t idesc = idesc_mx(BLOCK, n, 0);
+      const uint32_t d = tmem + buf * kAcc;
+      if (!wait_all(b.acc_empty + 8 * buf, acc_phase, abort_flag, a.status))
+        return false;
+      tc::tc_fence_after();
+#pragma unroll 1
+      for (int s = 0; s < stages; ++s) {
+        if (!wait_all(b.full + 8 * ring.st, ring.phase, abort_flag,
+                      a.status) ||
+            !wait_all(b.scales + 8 * ring.st, ring.phase, abort_flag,
+                      a.status))
+          return false;
+        // the instructions that read these scales' buffer have completed
+        if (done == 2 && !wait_all(b.empty + 8 * back2.st, back2.phase,
+                                   abort_flag, a.status))
+          return false;
+        tc::tc_fence_after();
+        const uint32_t at = sb + ring.st * kStage;
+        const uint32_t sa = tmem + kScaleAt + sbuf * kScales;
+        const uint32_t sx = sa + kMats * kScaleA;
+        if (leader) {
+#pragma unroll
+          for (int m = 0; m < kMats; ++m)
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+              scales_to_tmem(
+                  sa + m * kScaleA + 4 * j,
+                  scale_desc(at + m * kRec + kCodeBytes + j * kScaleTile));
+#pragma unroll
+          for (int q = 0; q < kRowTiles; ++q)
+            if (q * 128 < n)
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j)
+                scales_to_tmem(sx + (j * kRowTiles + q) * 4,
+                               scale_desc(at + kXs +
+                                          (q * kTiles + j) * kScaleTile));
+          const uint64_t bd = tc::smem_desc(at + kX, 16, 1024);
+          const int steps = (a.l.K - s * kStageK + 63) / 64;
+#pragma unroll
+          for (int k = 0; k < kStageK / 64; ++k) {
+            if (k >= steps) break;
+            // four scales of 16 are a word's, two of 32 half of one
+            const int tile = BLOCK == 16 ? k : k / 2;
+            const uint32_t id =
+                BLOCK == 16 ? 0u : (k & 1) * (2u << 4 | 2u << 29);
+#pragma unroll
+            for (int m = 0; m < kMats; ++m)
+              umma_mx<BLOCK>(d + m * NT,
+                             tc::smem_desc(at + m * kRec, 16, 1024) + 2 * k,
+                             bd + 2 * k, idesc | id,
+                             sa + m * kScaleA + 4 * tile,
+                             sx + tile * kRowTiles * 4, s > 0 || k > 0);
+          }
+          tc::umma_commit(b.empty + 8 * ring.st);
+        }
+        __syncwarp();
+        sbuf ^= 1;
+        back2 = back1;
+        back1 = ring;
+        if (done < 2) ++done;
+        ring.next();
+      }
+      if (leader) tc::umma_commit(b.acc_full + 8 * buf);
+      __syncwarp();
+      if (++buf == kBuffers) {
+        buf = 0;
+        acc_phase ^= 1;
+      }
+      return true;
+    });
+    // drain: every instruction that this warp issued
+    if (leader) {
+      tc::umma_commit(b.done);
+      tc::mbar_wait(b.done, 0, nullptr, a.status);
+    }
+  }
+
+  // ---- sums to rows of the output, a thread a column of the weights
+  __device__ static void write_out(const GmmArgs& a, const Bars& b,
+                                   const int2* chunks, int n_items, int tiles,
+                                   uint32_t tmem, int warp, int lane,
+                                   volatile int* abort_flag) {
+    int buf = 0;
+    uint32_t phase = 0;
+    launch::wait_for_previous();
+    passes(a, chunks, n_items, tiles, [&](const Item& it) {
+      if (!wait_all(b.acc_full + 8 * buf, phase, abort_flag, a.status))
+        return false;
+      tc::tc_fence_after();
+      const int col0 = it.tile * kTileN + warp * 32;
+      const uint32_t at =
+          tmem + buf * kAcc + (static_cast<uint32_t>(warp * 32) << 16);
+      if (col0 < a.l.N) {  // N is a multiple of 32
+        const float t0 = a.x_scale * (a.s0 ? a.s0[it.expert] : 1.0f);
+        const float t1 = a.x_scale * (DUAL && a.s1 ? a.s1[it.expert] : 1.0f);
+#pragma unroll 1
+        for (int r = 0; r < it.rows; r += 16) {
+          uint32_t g[16], u[16];
+          tmem_ld16(at + r, g);
+          if (DUAL) tmem_ld16(at + NT + r, u);
+          tmem_ld_wait(g);
+          if (DUAL) {
+            tmem_ld_wait(u);
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+              if (r + i < it.rows)
+                write_h(a, it, col0, r + i, lane, t0, t1, g + i, u + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (r + i >= it.rows) break;
+              const long long o =
+                  static_cast<long long>(it.row + r + i) * a.l.N + col0 + lane;
+              const float v = t0 * __uint_as_float(g[i]);
+              if (a.f32)
+                put(static_cast<float*>(a.y) + o, v);
+              else
+                put(static_cast<__nv_bfloat16*>(a.y) + o, v);
+            }
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(b.acc_empty + 8 * buf);
+      if (++buf == kBuffers) {
+        buf = 0;
+        phase ^= 1;
+      }
+      return true;
+    });
+  }
+
+  // Eight rows of 32 columns of h: each lane has one column of all rows, a
+  // block is the warp's lanes or half of them.
+  __device__ static __forceinline__ void write_h(
+      const GmmArgs& a, const Item& it, int col0, int r, int lane, float t0,
+      float t1, const uint32_t* g, const uint32_t* u) {
+    const uint32_t mask =
+        BLOCK == 32 ? 0xffffffffu : lane < 16 ? 0xffffu : 0xffff0000u;
+    float q[8];
+    uint32_t byte = 0;  // the scale of row lane % 8
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float z = t0 * __uint_as_float(g[i]);
+      // z / (1 + exp(-z)); exp(-z) may be infinite
+      const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+      float h = z * s * (t1 * __uint_as_float(u[i]));
+      if (BLOCK == 16) h *= a.inv_out;
+      const Block blk = block_scale<BLOCK>(
+          __reduce_max_sync(mask, __float_as_uint(h) & 0x7fffffffu));
+      q[i] = over_scale<BLOCK>(h, blk);
+      if ((lane & 7) == i) byte = blk.byte;
+    }
+    // The codes of a column's eight rows are a word; words of eight rows by
+    // eight columns turn within eight lanes, halves, then bytes, then fours.
+    uint32_t w = encode8(q);
+    uint32_t p = __shfl_xor_sync(0xffffffffu, w, 4);
+    w = lane & 4 ? __byte_perm(w, p, 0x3276) : __byte_perm(w, p, 0x5410);
+    p = __shfl_xor_sync(0xffffffffu, w, 2);
+    w = lane & 2 ? __byte_perm(w, p, 0x3715) : __byte_perm(w, p, 0x6240);
+    p = __shfl_xor_sync(0xffffffffu, w, 1);
+    w = lane & 1 ? (w & 0xf0f0f0f0u) | (p >> 4 & 0x0f0f0f0fu)
+                 : (w & 0x0f0f0f0fu) | (p & 0x0f0f0f0fu) << 4;
+    const int i = r + (lane & 7);
+    if (i >= it.rows) return;
+    const long long row = it.row + i;
+    const int col = col0 + (lane & 24);
+    *reinterpret_cast<uint32_t*>(a.h_codes + row * (a.l.N / 2) + col / 2) = w;
+    if ((lane & (BLOCK == 32 ? 24 : 8)) == 0)
+      a.h_scales[row * scale_row(a.l.N, BLOCK) + col / BLOCK] =
+          static_cast<uint8_t>(byte);
+  }
+};
+
+template <bool DUAL, int BLOCK, int NT>
+__global__ void __launch_bounds__(kGmmThreads, 1)
+    gmm_mx_kernel(const GmmArgs a, const __grid_constant__ CUtensorMap map) {
+  Gmm<DUAL, BLOCK, NT>::run(a, &map);
+}
+
+// Rows of codes [rows, K/2], 16 rows of 128 bytes at a time.
+inline bool make_code_map(CUtensorMap* m, const void* base, int K,
+                          int64_t rows) {
+  tc::EncodeTiled fn = tc::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t box[2] = {128, kRowBox};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool DUAL, int BLOCK, int NT>
+cudaError_t launch_one(GmmArgs a, const void* codes, cudaStream_t s) {
+  using Ker = Gmm<DUAL, BLOCK, NT>;
+  // Chunks of as few passes of NT rows as leave at most kMaxSplits more than
+  // there are groups.
+  const long long most = static_cast<long long>(NT) * kMaxSplits;
+  a.chunk = NT * static_cast<int>((a.rows + most - 1) / most);
+  a.chunks = std::min(a.n_groups, a.rows) + a.rows / a.chunk;
+  static_assert(Ker::shared_bytes(kMaxChunks) <= kMaxShared,
+                "any call's shared memory fits a CTA");
+  Device d;
+  cudaError_t e = launch::device(&d);
+  if (e != cudaSuccess) return e;
+  constexpr auto kernel = gmm_mx_kernel<DUAL, BLOCK, NT>;
+  if ((e = launch::allow_shared<kernel>(d)) != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!make_code_map(&map, codes, a.l.K, a.rows)) return cudaErrorInvalidValue;
+  const long long items =
+      static_cast<long long>(a.l.tiles_n()) * a.chunks;
+  const unsigned grid =
+      static_cast<unsigned>(std::min<long long>(items, d.sms));
+  const int bytes = Ker::shared_bytes(a.chunks);
+  if (a.early)
+    return launch::overlapping(kernel, grid, kGmmThreads, bytes, s, a, map);
+  kernel<<<grid, kGmmThreads, bytes, s>>>(a, map);
+  return cudaGetLastError();
+}
+
+}  // namespace mx
+}  // namespace moe

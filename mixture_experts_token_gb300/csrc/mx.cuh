@@ -1,0 +1,163 @@
+// Microscaled 4-bit floating point (internal): the number formats, a block's
+// scale and codes, and the layout of weight matrices.
+//
+// A code is a sign, two exponent bits and a mantissa bit: 0, 0.5, 1, 1.5, 2,
+// 3, 4, 6.  Blocks of 32 along the reduction axis share a power of two (the
+// biased exponent in a byte, 255 for NaN), blocks of 16 a number of 4 exponent
+// and 3 mantissa bits (0x7f for NaN) under a float32 scale of the tensor.
+// Rows of codes: K/2 bytes, column 2i in the low four bits of byte i; rows of
+// scales: scale_row() bytes, one a block, zeros behind the last.
+//
+// A packed matrix [K, N] is, for each tile of 128 columns, one record after
+// another, a record for each 256 of K:
+//   codes   128 rows (columns of the matrix) of 128 bytes, 16-byte pieces
+//           exchanged as the tensor cores' 128-byte swizzle has it (piece p of
+//           row r lies at p ^ (r & 7))
+//   scales  tiles of 512 bytes, each 4 scales of 128 rows: those of row r are
+//           the word at (r % 32) * 16 + r / 32 * 4, the order in which 32 lanes
+//           of tensor memory take four columns
+// so that a product brings a record with one bulk copy and uses it in place.
+// What lies past the matrix has code 0 and scale 0.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "internal.h"
+
+namespace moe {
+namespace mx {
+
+constexpr int kStageK = 256;
+constexpr int kTileN = 128;
+constexpr int kCodeBytes = kTileN * kStageK / 2;
+constexpr int kScaleTile = 512;  // bytes: 4 scales of each of 128 rows
+constexpr float kCodeMax = 6.0f;
+
+__host__ __device__ constexpr int scale_tiles(int block) {  // of a record
+  return kStageK / block / 4;
+}
+__host__ __device__ constexpr int record_bytes(int block) {
+  return kCodeBytes + kScaleTile * scale_tiles(block);
+}
+__host__ __device__ inline int scale_row(int K, int block) {
+  return (K / block + 3) / 4 * 4;
+}
+
+struct Layout {
+  int K, N, block;
+  __host__ __device__ int stages() const {
+    return (K + kStageK - 1) / kStageK;
+  }
+  __host__ __device__ int tiles_n() const {
+    return (N + kTileN - 1) / kTileN;
+  }
+  __host__ __device__ long long tile() const {
+    return static_cast<long long>(stages()) * record_bytes(block);
+  }
+  __host__ __device__ long long matrix() const { return tile() * tiles_n(); }
+};
+
+inline bool scale_ok(int block, float s) {
+  return block == 32 ? s == 1.0f : s >= 1.17549435e-38f && s <= 1e38f;
+}
+inline bool options_ok(const moe_mx_t* o) {
+  return o != nullptr && (o->block == 16 || o->block == 32) &&
+         scale_ok(o->block, o->x_scale) && scale_ok(o->block, o->h_scale);
+}
+// Blocks do not straddle rows, and rows of codes are whole 16-byte pieces.
+inline bool length_ok(int K) {
+  return K >= 32 && K % 32 == 0 && K <= (1 << 20);
+}
+
+// ---------------------------------------------------------- numbers ------
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) {
+  *p = __float2bfloat16(v);
+}
+
+// Two codes in a byte, lo in the low four bits: nearest, ties to the even
+// code, magnitudes over 6 to 6.
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
+      "cvt.u32.u8 %0, t;\n\t}\n"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r;
+}
+// Eight codes, the first lowest.
+__device__ __forceinline__ uint32_t encode8(const float (&q)[8]) {
+  return encode2(q[0], q[1]) | encode2(q[2], q[3]) << 8 |
+         encode2(q[4], q[5]) << 16 | encode2(q[6], q[7]) << 24;
+}
+// The value of a code: 0, 1/2, then (1 + m/2) 2^(e-1).
+__device__ __forceinline__ float decode(uint32_t code) {
+  const uint32_t m = code & 7;
+  // exponent and mantissa where a float has them; the subnormal 1 is 2^-1
+  const uint32_t bits = m < 2 ? m * 0x3f000000u : (m << 22) + 0x3f000000u;
+  return __uint_as_float(bits | (code & 8) << 28);
+}
+// The value of a block's scale.
+template <int BLOCK>
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  if (BLOCK == 32)
+    return byte == 255   ? __uint_as_float(0x7fc00000u)
+           : byte == 0 ? __uint_as_float(0x00400000u)  // 2^-127
+                       : __uint_as_float(byte << 23);
+  const uint32_t m = byte & 7, e = byte >> 3 & 15;
+  if ((byte & 127) == 127) return __uint_as_float(0x7fc00000u);
+  return e == 0 ? static_cast<float>(m) * 0.001953125f  // 2^-9
+                : __uint_as_float((e + 120) << 23 | m << 20);
+}
+
+// A block's scale from the largest magnitude in it, as a float's bits (those
+// of an infinity or a NaN are the largest): the scale's byte, and what its
+// values are multiplied by (`inv`, and for blocks of 16 the scale `s`, with
+// which the quotient is corrected).
+struct Block {
+  uint32_t byte;
+  float s, inv;
+};
+template <int BLOCK>
+__device__ __forceinline__ Block block_scale(uint32_t most) {
+  Block b;
+  if (BLOCK == 32) {
+    // 2^(floor(log2 most) - 2): with the exponents' bias, the field less 2
+    const uint32_t e = most >> 23;
+    b.byte = e == 255 ? 255u : e > 2 ? e - 2 : 0u;
+    b.s = 0.0f;
+    b.inv = __uint_as_float((254u - min(b.byte, 253u)) << 23);
+  } else {
+    const bool finite = most < 0x7f800000u;
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\t"
+        "cvt.u32.u16 %0, t;\n\t}\n"
+        : "=r"(r)
+        : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(most), kCodeMax)));
+    b.byte = finite ? r & 127 : 127u;
+    b.s = finite ? scale_value<16>(b.byte) : 0.0f;
+    b.inv = b.s > 0.0f ? __frcp_rn(b.s) : 0.0f;
+  }
+  return b;
+}
+// v over the scale.  For blocks of 16 one step of correction makes the
+// quotient the nearest float: v = m s for a midpoint m between two codes must
+// give m itself, which the product with the reciprocal alone may miss.  (No
+// other v gives m: v and m s, of at most 7 bits, differ by more than half an
+// ulp of the quotient.)
+template <int BLOCK>
+__device__ __forceinline__ float over_scale(float v, const Block& b) {
+  const float q = v * b.inv;
+  // (the correction loses the sign of a zero)
+  return BLOCK == 32 ? q
+                     : copysignf(fmaf(fmaf(-q, b.s, v), b.inv, q), v);
+}
+
+}  // namespace mx
+}  // namespace moe

@@ -355,3 +355,131 @@ def test_w4_scales_need_their_natural_alignment(m):
                                None) == m.MOE_ERR_CUDA
         assert lib.moe_w4_quantize(W, 1, 64, 16, m.MOE_F32, p, p, half, None,
                                    None) == m.MOE_ERR_CUDA
+
+
+def test_route_scores_arguments(m):
+    lib, p, odd = m.lib(), ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1002)
+    bad = m.MOE_ERR_INVALID_ARG
+    c = cfg_of(m, E=12, k=3, S=1)
+    good = dict(groups=4, top_groups=2, group_top=2)
+
+    def fwd(cfg=c, x=p, b=None, i=p, w=p, **kw):
+        o = ctypes.byref(m.make_route_scores(**{**good, **kw}))
+        return lib.moe_route_scores(ctypes.byref(cfg), o, x, b, i, w, None,
+                                    None)
+
+    def bwd(x=p, i=p, d=p, g=p, **kw):
+        o = ctypes.byref(m.make_route_scores(**{**good, **kw}))
+        return lib.moe_route_scores_backward(ctypes.byref(c), o, x, i, d, g,
+                                             None)
+    for kw in (dict(score=2), dict(score=-1), dict(groups=5), dict(groups=0),
+               dict(groups=65), dict(top_groups=5), dict(top_groups=0),
+               dict(group_top=4), dict(group_top=0), dict(renorm=2),
+               dict(groups=6, top_groups=1),      # two experts for k = 3
+               dict(groups=1, group_top=5),
+               dict(scale=float("inf")), dict(scale=float("nan"))):
+        assert fwd(**kw) == bad and bwd(**kw) == bad, kw
+    for kw in (dict(x=None), dict(i=None), dict(x=odd), dict(i=odd)):
+        assert fwd(**kw) == bad and bwd(**kw) == bad, kw
+    assert fwd(w=None) == bad and fwd(b=odd) == bad
+    assert bwd(d=None) == bad and bwd(g=None) == bad
+    assert fwd(cfg=cfg_of(m, E=12, k=13)) == bad
+    assert lib.moe_route_scores(ctypes.byref(c), None, p, None, p, p, None,
+                                None) == bad
+    # nothing to do: nothing is looked at
+    assert fwd(cfg=cfg_of(m, E=12, k=3, S=1, T=0), x=None, i=None,
+               w=None) == m.MOE_OK
+    import torch
+    if not torch.cuda.is_available():     # past the checks, to a launch
+        assert fwd() == m.MOE_ERR_CUDA and bwd() == m.MOE_ERR_CUDA
+
+
+def test_mx_sizes_and_arguments(m):
+    lib, p, off = m.lib(), ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1008)
+    odd = ctypes.c_void_p(0x1002)
+    bad = m.MOE_ERR_INVALID_ARG
+    mx, nv = m.make_mx(32), m.make_mx(16, 0.5, 0.25)
+    # records of 128 columns by 256 of K: codes, and 1 or 2 KB of scales
+    assert m.moe_mx_bytes(mx, 3, 256, 128) == 3 * (16384 + 1024)
+    assert m.moe_mx_bytes(nv, 1, 288, 129) == 2 * 2 * (16384 + 2048)
+    assert m.moe_mx_bytes(mx, 0, 32, 1) == 0
+    for args in ((-1, 64, 16), (1, 48, 16), (1, 0, 16), (1, 64, 0),
+                 (1, 1 << 21, 16), (1, 64, 1 << 21)):
+        assert m.moe_mx_bytes(mx, *args) == 0, args
+    assert [m.moe_mx_scale_row(mx, K) for K in (32, 128, 160, 31, 0)] == \
+        [4, 4, 8, 0, 0]
+    assert [m.moe_mx_scale_row(nv, K) for K in (32, 64, 96)] == [4, 4, 8]
+    nan, inf = float("nan"), float("inf")
+    for o in (m.make_mx(8), m.make_mx(64), m.make_mx(32, 2.0),
+              m.make_mx(32, 1.0, 0.5), m.make_mx(16, 0.0), m.make_mx(16, nan),
+              m.make_mx(16, 1.0, inf), m.make_mx(16, -1.0),
+              m.make_mx(16, 1e-40)):
+        assert m.moe_mx_bytes(o, 1, 64, 16) == 0
+        assert lib.moe_mx_pack(ctypes.byref(o), 1, 64, 16, p, p, p,
+                               None) == bad
+    M, V = ctypes.byref(mx), ctypes.byref(nv)
+    rows = lambda o, *a: lib.moe_mx_quantize_rows(o, *a, None)  # noqa: E731
+    one = ctypes.c_float(1.0)
+    assert rows(M, 2, 64, 2, p, one, p, p) == bad
+    assert rows(M, -1, 64, 0, p, one, p, p) == bad
+    assert rows(M, 2, 48, 0, p, one, p, p) == bad
+    assert rows(M, 2, 64, 0, p, ctypes.c_float(0.5), p, p) == bad
+    assert rows(V, 2, 64, 0, p, ctypes.c_float(0.0), p, p) == bad
+    for a in ((None, p, p), (p, None, p), (p, p, None), (off, p, p),
+              (p, off, p), (p, p, odd)):
+        assert rows(M, 2, 64, 0, a[0], one, a[1], a[2]) == bad, a
+        assert lib.moe_mx_dequantize_rows(M, 2, 64, a[1], a[2], one, 0, a[0],
+                                          None) == bad, a
+        assert lib.moe_mx_quantize(M, 1, 64, 16, 0, a[0], None, a[1], a[2],
+                                   None) == bad, a
+    assert rows(M, 0, 64, 0, None, one, None, None) == m.MOE_OK
+    # a tensor scale where there is none, and one that no float is at
+    assert lib.moe_mx_quantize(M, 1, 64, 16, 0, p, p, p, p, None) == bad
+    assert lib.moe_mx_quantize(V, 1, 64, 16, 0, p, odd, p, p, None) == bad
+    assert lib.moe_mx_pack(M, 1, 64, 16, p, p, off, None) == bad
+    assert lib.moe_mx_pack(M, 1, 64, 16, off, p, p, None) == bad
+    assert lib.moe_mx_dequantize(M, 1, 64, 16, p, p, 0, p, None) == bad
+    assert lib.moe_mx_dequantize(M, 1, 64, 16, p, None, 3, p, None) == bad
+    assert lib.moe_mx_dequantize(M, 1, 64, 16, off, None, 0, p, None) == bad
+    # the products
+    c = cfg_of(m)
+    C = ctypes.byref(c)
+    up = lambda C, o, n, e, *a: lib.moe_gmm_gate_up_mx(  # noqa: E731
+        C, o, n, e, *a, None, None)
+    good = [p, p, p, p, p, None, None, p, p]
+    assert up(C, None, 0, None, *good) == bad
+    assert up(C, M, 3, None, *good) == bad         # groups without a map
+    assert up(C, M, 1025, p, *good) == bad
+    for i in (0, 1, 2, 3, 4, 7, 8):
+        a = list(good)
+        a[i] = None
+        assert up(C, M, 0, None, *a) == bad, i
+        a[i] = odd
+        assert up(C, M, 0, None, *a) == bad, i
+    for i in (5, 6):                               # no scales of matrices
+        a = list(good)
+        a[i] = p
+        assert up(C, M, 0, None, *a) == bad, i
+    down = lambda C, o, *a: lib.moe_gmm_down_mx(  # noqa: E731
+        C, o, 0, None, *a, None, None)
+    assert down(C, M, p, p, p, p, p, p) == bad     # a scale
+    assert down(C, V, p, p, p, p, odd, p) == bad
+    assert down(C, M, p, p, p, p, None, off) == bad
+    for bad_cfg, want in ((cfg_of(m, F=0), bad),
+                          (cfg_of(m, F=136), m.MOE_ERR_UNSUPPORTED),
+                          (cfg_of(m, H=72), m.MOE_ERR_UNSUPPORTED)):
+        B = ctypes.byref(bad_cfg)
+        assert up(B, M, 0, None, *good) == want
+        assert down(B, M, p, p, p, p, None, p) == want
+        assert m.moe_mx_workspace_bytes(bad_cfg, mx) == 0
+    need = m.moe_mx_workspace_bytes(c, mx)
+    assert need >= 128 * (64 + 128) * 17 // 32
+    ffn = lambda ws, n: lib.moe_gmm_swiglu_mx(  # noqa: E731
+        C, M, p, p, p, p, p, None, None, None, p, None, ws, n, None)
+    assert ffn(None, need) == m.MOE_ERR_WORKSPACE
+    assert ffn(p, need - 1) == m.MOE_ERR_WORKSPACE
+    assert ffn(off, need) == m.MOE_ERR_WORKSPACE
+    import torch
+    if not torch.cuda.is_available():     # past the checks, to a launch
+        assert ffn(p, need) == m.MOE_ERR_CUDA
+        assert up(C, M, 0, None, *good) == m.MOE_ERR_CUDA
