@@ -21,6 +21,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "internal.h"
 
@@ -79,28 +80,38 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) {
   *p = __float2bfloat16(v);
 }
 
-// Two codes in a byte, lo in the low four bits: nearest, ties to the even
+// Eight codes, the first in the lowest four bits: nearest, ties to the even
 // code, magnitudes over 6 to 6.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+__device__ __forceinline__ uint32_t encode8(const float (&q)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}\n"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}\n"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]),
+        "f"(q[6]), "f"(q[7]));
   return r;
 }
-// Eight codes, the first lowest.
-__device__ __forceinline__ uint32_t encode8(const float (&q)[8]) {
-  return encode2(q[0], q[1]) | encode2(q[2], q[3]) << 8 |
-         encode2(q[4], q[5]) << 16 | encode2(q[6], q[7]) << 24;
-}
-// The value of a code: 0, 1/2, then (1 + m/2) 2^(e-1).
-__device__ __forceinline__ float decode(uint32_t code) {
-  const uint32_t m = code & 7;
-  // exponent and mantissa where a float has them; the subnormal 1 is 2^-1
-  const uint32_t bits = m < 2 ? m * 0x3f000000u : (m << 22) + 0x3f000000u;
-  return __uint_as_float(bits | (code & 8) << 28);
+// The values of eight codes.
+__device__ __forceinline__ void decode8(uint32_t codes, float (&v)[8]) {
+  uint32_t h[4];  // pairs of halves, exactly
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 // The value of a block's scale.
 template <int BLOCK>
@@ -150,13 +161,34 @@ __device__ __forceinline__ Block block_scale(uint32_t most) {
 // quotient the nearest float: v = m s for a midpoint m between two codes must
 // give m itself, which the product with the reciprocal alone may miss.  (No
 // other v gives m: v and m s, of at most 7 bits, differ by more than half an
-// ulp of the quotient.)
+// ulp of the quotient.)  Written so that a zero keeps its sign.
 template <int BLOCK>
 __device__ __forceinline__ float over_scale(float v, const Block& b) {
   const float q = v * b.inv;
-  // (the correction loses the sign of a zero)
-  return BLOCK == 32 ? q
-                     : copysignf(fmaf(fmaf(-q, b.s, v), b.inv, q), v);
+  return BLOCK == 32 ? q : fmaf(-fmaf(q, b.s, -v), b.inv, q);
+}
+
+// Magnitudes, as bits whose order is theirs; those of a NaN or an infinity are
+// larger than any number's.
+__device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    most = max(most, __float_as_uint(v[j]) & 0x7fffffffu);
+  return most;
+}
+// of pairs of bf16 numbers: those of the pairs' low halves and high halves
+__device__ __forceinline__ uint32_t largest2(uint32_t most, uint32_t pair) {
+  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&most);
+  const uint32_t mag = pair & 0x7fff7fffu;
+  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&mag);
+  const __nv_bfloat162 m = __hmax2_nan(a, b);
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+// The largest magnitude of values that are multiplied by r, from that of the
+// values: rounding keeps order.
+__device__ __forceinline__ uint32_t scaled_bits(uint32_t most, float r) {
+  return __float_as_uint(__uint_as_float(most) * r) & 0x7fffffffu;
 }
 
 }  // namespace mx

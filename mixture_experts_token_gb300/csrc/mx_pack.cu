@@ -11,25 +11,43 @@ using namespace mx;
 
 constexpr int kThreads = 256;
 
+// Eight values as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+struct Eight;
 template <>
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Eight<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  }
+  __device__ __forceinline__ uint32_t most() const { return largest(v); }
+  __device__ __forceinline__ float at(int j) const { return v[j]; }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  __device__ __forceinline__ uint32_t most() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = largest2(m, w[i]);
+    return max(m << 16, m & 0xffff0000u);
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+  }
+};
 __device__ __forceinline__ void store8(const float (&v)[8], float* p) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -45,7 +63,38 @@ __device__ __forceinline__ void store8(const float (&v)[8],
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight values of a row a thread, so a block is two or four lanes.
+// Rows, eight values a thread and a piece; a CTA takes kPieces * kThreads
+// pieces in a row, all of which it loads before it uses one.
+constexpr int kPieces = 4;
+
+// The row and the place in it of a thread's pieces, kThreads apart.
+struct Place {
+  long long row;
+  uint32_t at, per_row;
+  __device__ __forceinline__ Place(long long first, int per_row)
+      : row(first / per_row), per_row(per_row) {
+    at = static_cast<uint32_t>(first - row * per_row) + threadIdx.x;
+    wrap();
+  }
+  __device__ __forceinline__ void next() {
+    at += kThreads;
+    if (per_row >= kThreads) {
+      if (at >= per_row) {
+        at -= per_row;
+        ++row;
+      }
+    } else {
+      wrap();
+    }
+  }
+  __device__ __forceinline__ void wrap() {
+    const uint32_t down = at / per_row;
+    row += down;
+    at -= down * per_row;
+  }
+};
+
+// A block is two or four lanes.
 template <int BLOCK, typename T>
 __global__ void __launch_bounds__(kThreads)
     quantize_rows_kernel(const T* __restrict__ x, long long pieces, int K,
@@ -54,36 +103,45 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kLanes = BLOCK / 8;
   launch::wait_for_previous();
   launch::let_next_start();
-  const int per_row = K / 8, sr = scale_row(K, BLOCK);
-  // pieces is a multiple of the lanes of a block: they leave together
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) +
-                     threadIdx.x;
-       i < pieces; i += static_cast<long long>(gridDim.x) * kThreads) {
-    float v[8];
-    load8(x + i * 8, v);
-    uint32_t most = 0;
+  const int sr = scale_row(K, BLOCK);
+  const long long first =
+      blockIdx.x * static_cast<long long>(kPieces * kThreads);
+  const bool all = first + kPieces * kThreads <= pieces;
+  Place place(first, K / 8);
+  Eight<T> v[kPieces];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (BLOCK == 16) v[j] *= r;
-      most = max(most, __float_as_uint(v[j]) & 0x7fffffffu);
-    }
-    const uint32_t mask =
-        ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
+  for (int p = 0; p < kPieces; ++p) {
+    const long long i = first + p * kThreads + threadIdx.x;
+    if (all || i < pieces)
+      v[p].load(x + i * 8);
+    else
+      v[p].zero();
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const long long i = first + p * kThreads + threadIdx.x;
+    uint32_t most = v[p].most();
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1)
-      most = max(most, __shfl_xor_sync(mask, most, o));
-    const Block b = block_scale<BLOCK>(most);
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const Block b =
+        block_scale<BLOCK>(BLOCK == 16 ? scaled_bits(most, r) : most);
+    float q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = over_scale<BLOCK>(v[j], b);
-    reinterpret_cast<uint32_t*>(codes)[i] = encode8(v);
-    if (threadIdx.x % kLanes == 0) {
-      const long long row = i / per_row;
-      const int at = static_cast<int>(i - row * per_row) / kLanes;
-      uint8_t* s = scales + row * sr;
-      s[at] = static_cast<uint8_t>(b.byte);
-      if (at == K / BLOCK - 1)
-        for (int j = at + 1; j < sr; ++j) s[j] = 0;
+    for (int j = 0; j < 8; ++j)
+      q[j] = over_scale<BLOCK>(BLOCK == 16 ? v[p].at(j) * r : v[p].at(j), b);
+    const uint32_t c = encode8(q);
+    if (all || i < pieces) {
+      reinterpret_cast<uint32_t*>(codes)[i] = c;
+      if (threadIdx.x % kLanes == 0) {
+        const int at = static_cast<int>(place.at) / kLanes;
+        uint8_t* s = scales + place.row * sr;
+        s[at] = static_cast<uint8_t>(b.byte);
+        if (at == K / BLOCK - 1)
+          for (int j = at + 1; j < sr; ++j) s[j] = 0;
+      }
     }
+    place.next();
   }
 }
 
@@ -93,79 +151,171 @@ __global__ void __launch_bounds__(kThreads)
                            const uint8_t* __restrict__ scales,
                            long long pieces, int K, float scale,
                            T* __restrict__ x) {
-  const int per_row = K / 8, sr = scale_row(K, BLOCK);
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) +
-                     threadIdx.x;
-       i < pieces; i += static_cast<long long>(gridDim.x) * kThreads) {
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    const long long row = i / per_row;
-    const int at = static_cast<int>(i - row * per_row) / (BLOCK / 8);
-    const float s = scale_value<BLOCK>(__ldg(scales + row * sr + at));
+  const int sr = scale_row(K, BLOCK);
+  const long long first =
+      blockIdx.x * static_cast<long long>(kPieces * kThreads);
+  Place place(first, K / 8);
+  uint32_t c[kPieces], byte[kPieces];
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const long long i = first + p * kThreads + threadIdx.x;
+    if (i < pieces) {
+      c[p] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
+      byte[p] = __ldg(scales + place.row * sr + place.at / (BLOCK / 8));
+    }
+    place.next();
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const long long i = first + p * kThreads + threadIdx.x;
+    if (i >= pieces) return;
+    const float s = scale_value<BLOCK>(byte[p]);
     float v[8];
+    decode8(c[p], v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = decode(c >> (4 * j) & 15) * s;  // exact
+      v[j] *= s;  // exact
       if (BLOCK == 16) v[j] *= scale;
     }
     store8(v, x + i * 8);
   }
 }
 
-// A weight matrix w [K, N] becomes N rows of codes: 64 columns and 256 of K
-// at a time through shared memory, read a row of w and written a row of codes
-// at a time.  A thread takes 32 of K of one column.
+// A weight matrix w [K, N] becomes N rows of codes: 64 columns and 256 of K at
+// a time through shared memory, read a row of w and written a row of codes at
+// a time.  A warp has 32 of K, a lane two neighbouring columns of them.
 constexpr int kTurnN = 64;
+template <typename T>
+struct Two;
+template <>
+struct Two<float> {
+  uint32_t m[2] = {0, 0};  // the largest magnitudes so far
+  static __device__ __forceinline__ float2 load(const float* p) {
+    return *reinterpret_cast<const float2*>(p);
+  }
+  __device__ __forceinline__ void look(const float* p) {
+    const uint2 f = *reinterpret_cast<const uint2*>(p);
+    m[0] = max(m[0], f.x & 0x7fffffffu);
+    m[1] = max(m[1], f.y & 0x7fffffffu);
+  }
+  __device__ __forceinline__ uint32_t most(int n) const { return m[n]; }
+};
+template <>
+struct Two<__nv_bfloat16> {
+  uint32_t m = 0;
+  static __device__ __forceinline__ float2 load(const __nv_bfloat16* p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+  }
+  __device__ __forceinline__ void look(const __nv_bfloat16* p) {
+    m = largest2(m, *reinterpret_cast<const uint32_t*>(p));
+  }
+  __device__ __forceinline__ uint32_t most(int n) const {
+    return n ? m & 0xffff0000u : m << 16;
+  }
+};
+
 template <int BLOCK, typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     quantize_weights_kernel(const T* __restrict__ w,
                             const float* __restrict__ scale, int n_mats,
                             int K, int N, uint8_t* __restrict__ codes,
                             uint8_t* __restrict__ scales) {
-  // an odd number of words a row: eight of k apart is four banks apart
-  extern __shared__ char raw[];
-  constexpr int kPitch = kTurnN + 4 / sizeof(T);
-  T* tile = reinterpret_cast<T*>(raw);
+  constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte piece
+  constexpr int kRow = kStageK / BLOCK;  // scales of a row here
+  static_assert(kThreads / 32 * 32 == kStageK, "a warp has 32 of K");
+  extern __shared__ __align__(16) char raw[];
+  T* tile = reinterpret_cast<T*>(raw);  // [256][64]
+  __shared__ __align__(16) char out[kTurnN * kStageK / 2];
+  __shared__ __align__(4) uint8_t out_s[kTurnN][kRow];
   const int n0 = blockIdx.x * kTurnN, k0 = blockIdx.y * kStageK;
   const int sr = scale_row(K, BLOCK);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k_here = min(kStageK, K - k0), n_here = min(kTurnN, N - n0);
+  // whole pieces, each in bounds and aligned
+  const bool wide = N % kPer == 0;
   for (long long m = blockIdx.z; m < n_mats; m += gridDim.z) {
     const float r = BLOCK == 16 && scale ? __frcp_rn(scale[m]) : 1.0f;
+    const T* src = w + (m * K + k0) * N + n0;
     __syncthreads();
-    for (int i = threadIdx.x; i < kStageK * kTurnN; i += kThreads) {
-      const int k = i / kTurnN, n = i % kTurnN;
-      if (k0 + k < K && n0 + n < N)
-        tile[k * kPitch + n] = w[(m * K + k0 + k) * N + n0 + n];
+    if (wide) {
+      constexpr int kIn = kStageK * kTurnN / kPer / kThreads;
+      uint4 v[kIn];
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) {
+        const int at = i * kThreads + threadIdx.x;
+        const int k = at / (kTurnN / kPer), n = at % (kTurnN / kPer) * kPer;
+        if (k < k_here && n < n_here)
+          v[i] = __ldg(reinterpret_cast<const uint4*>(
+              src + static_cast<long long>(k) * N + n));
+      }
+#pragma unroll
+      for (int i = 0; i < kIn; ++i)
+        reinterpret_cast<uint4*>(raw)[i * kThreads + threadIdx.x] = v[i];
+    } else {
+      for (int i = threadIdx.x; i < kStageK * kTurnN; i += kThreads) {
+        const int k = i / kTurnN, n = i % kTurnN;
+        if (k < k_here && n < n_here)
+          tile[i] = src[static_cast<long long>(k) * N + n];
+      }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kTurnN * (kStageK / 32); i += kThreads) {
-      const int n = i / (kStageK / 32), k = i % (kStageK / 32) * 32;
-      if (n0 + n >= N || k0 + k >= K) continue;
-      const long long row = m * N + n0 + n;
-      uint32_t out[4];
+    if (warp * 32 < k_here) {  // K is a multiple of 32
+      uint32_t c[2][4];
+      const T* col = tile + warp * 32 * kTurnN + 2 * lane;
 #pragma unroll
       for (int h = 0; h < 32 / BLOCK; ++h) {
-        float v[BLOCK];
-        uint32_t most = 0;
+        // read twice: held in registers, the values would cost warps
+        Two<T> two;
 #pragma unroll
-        for (int j = 0; j < BLOCK; ++j) {
-          v[j] = to_float(tile[(k + h * BLOCK + j) * kPitch + n]) * r;
-          most = max(most, __float_as_uint(v[j]) & 0x7fffffffu);
+        for (int j = 0; j < BLOCK; ++j)
+          two.look(col + (h * BLOCK + j) * kTurnN);
+        Block b[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          b[n] = block_scale<BLOCK>(BLOCK == 16 ? scaled_bits(two.most(n), r)
+                                                : two.most(n));
+          out_s[2 * lane + n][warp * (32 / BLOCK) + h] =
+              static_cast<uint8_t>(b[n].byte);
         }
-        const Block b = block_scale<BLOCK>(most);
 #pragma unroll
         for (int j = 0; j < BLOCK / 8; ++j) {
-          float q[8];
+          float q[2][8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q[e] = over_scale<BLOCK>(v[8 * j + e], b);
-          out[h * (BLOCK / 8) + j] = encode8(q);
+          for (int e = 0; e < 8; ++e) {
+            const float2 f =
+                Two<T>::load(col + (h * BLOCK + 8 * j + e) * kTurnN);
+            q[0][e] = over_scale<BLOCK>(BLOCK == 16 ? f.x * r : f.x, b[0]);
+            q[1][e] = over_scale<BLOCK>(BLOCK == 16 ? f.y * r : f.y, b[1]);
+          }
+          c[0][h * (BLOCK / 8) + j] = encode8(q[0]);
+          c[1][h * (BLOCK / 8) + j] = encode8(q[1]);
         }
-        const int at = (k0 + k) / BLOCK + h;
-        uint8_t* s = scales + row * sr;
-        s[at] = static_cast<uint8_t>(b.byte);
-        if (at == K / BLOCK - 1)
-          for (int j = at + 1; j < sr; ++j) s[j] = 0;
       }
-      *reinterpret_cast<uint4*>(codes + row * (K / 2) + (k0 + k) / 2) =
-          make_uint4(out[0], out[1], out[2], out[3]);
+      // pieces of a row change places by the row, so that lanes meet no bank
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        *reinterpret_cast<uint4*>(out + (2 * lane + n) * (kStageK / 2) +
+                                  ((warp ^ (lane & 7)) << 4)) =
+            make_uint4(c[n][0], c[n][1], c[n][2], c[n][3]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTurnN * 8; i += kThreads) {
+      const int n = i / 8, p = i % 8;
+      if (n < n_here && p * 32 < k_here)
+        *reinterpret_cast<uint4*>(codes + (m * N + n0 + n) * (K / 2) +
+                                  k0 / 2 + p * 16) =
+            *reinterpret_cast<const uint4*>(out + n * (kStageK / 2) +
+                                            ((p ^ (n >> 1 & 7)) << 4));
+    }
+    const int words = min(kRow, sr - k0 / BLOCK) / 4;  // zeros behind the last
+    for (int i = threadIdx.x; i < kTurnN * words; i += kThreads) {
+      const int n = i / words, at = i % words * 4;
+      uint32_t v = *reinterpret_cast<const uint32_t*>(&out_s[n][at]);
+      const int left = k_here / BLOCK - at;
+      if (left < 4) v &= (1u << (8 * left)) - 1;
+      if (n < n_here)
+        *reinterpret_cast<uint32_t*>(scales + (m * N + n0 + n) * sr +
+                                     k0 / BLOCK + at) = v;
     }
   }
 }
@@ -208,8 +358,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Records to w [K, N], a CTA for each: a thread expands eight of K of a
-// column, and the 128 columns of a row of w are written side by side.
+__device__ __forceinline__ void store2(float2 v, float* p) {
+  *reinterpret_cast<float2*>(p) = v;
+}
+__device__ __forceinline__ void store2(float2 v, __nv_bfloat16* p) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
+// Records to w [K, N], a CTA for each: a thread expands 32 of K of two
+// neighbouring columns, and a warp writes 64 columns of a row side by side.
 template <int BLOCK, typename T>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const char* __restrict__ packed,
@@ -217,6 +374,7 @@ __global__ void __launch_bounds__(kThreads)
                       T* __restrict__ w) {
   __shared__ __align__(16) char rec[record_bytes(BLOCK)];
   const int stage = blockIdx.x, n0 = blockIdx.y * kTileN;
+  const bool pairs = l.N % 2 == 0;
   for (long long m = blockIdx.z; m < n_mats; m += gridDim.z) {
     const char* src = packed + m * l.matrix() + blockIdx.y * l.tile() +
                       static_cast<long long>(stage) * record_bytes(BLOCK);
@@ -226,22 +384,48 @@ __global__ void __launch_bounds__(kThreads)
           __ldg(reinterpret_cast<const uint4*>(src) + i);
     __syncthreads();
     const float t = BLOCK == 16 && scale ? scale[m] : 1.0f;
-    for (int i = threadIdx.x; i < kTileN * (kStageK / 8); i += kThreads) {
-      const int r = i % kTileN, p = i / kTileN;  // column, eight of k
-      const int k = stage * kStageK + p * 8;
+    for (int i = threadIdx.x; i < kTileN / 2 * 8; i += kThreads) {
+      const int r = i % (kTileN / 2) * 2, p = i / (kTileN / 2);
+      const int k = stage * kStageK + p * 32;
       if (n0 + r >= l.N || k >= l.K) continue;
-      const uint32_t c = *reinterpret_cast<const uint32_t*>(
-          rec + r * 128 + ((p / 4 ^ (r & 7)) << 4) + p % 4 * 4);
-      const int g = p * 8 / BLOCK;
-      const float s = scale_value<BLOCK>(static_cast<uint8_t>(
-          rec[kCodeBytes + g / 4 * kScaleTile + r % 32 * 16 + r / 32 * 4 +
-              g % 4]));
+      uint32_t c[2][4];
+      float s[2][32 / BLOCK];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int row = r + n;
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            rec + row * 128 + ((p ^ (row & 7)) << 4));
+        c[n][0] = v.x, c[n][1] = v.y, c[n][2] = v.z, c[n][3] = v.w;
+#pragma unroll
+        for (int h = 0; h < 32 / BLOCK; ++h) {
+          const int g = p * (32 / BLOCK) + h;
+          s[n][h] = scale_value<BLOCK>(static_cast<uint8_t>(
+              rec[kCodeBytes + g / 4 * kScaleTile + row % 32 * 16 +
+                  row / 32 * 4 + g % 4]));
+        }
+      }
       T* out = w + (m * l.K + k) * l.N + n0 + r;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float v = decode(c >> (4 * j) & 15) * s;
-        if (BLOCK == 16) v *= t;
-        put(out + static_cast<long long>(j) * l.N, v);
+      for (int j = 0; j < 32; j += 8) {
+        float v[2][8];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          decode8(c[n][j / 8], v[n]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[n][i] *= s[n][j / BLOCK];
+            if (BLOCK == 16) v[n][i] *= t;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i, out += l.N) {
+          if (pairs) {
+            store2(make_float2(v[0][i], v[1][i]), out);
+          } else {
+            put(out, v[0][i]);
+            if (n0 + r + 1 < l.N) put(out + 1, v[1][i]);
+          }
+        }
       }
     }
   }
@@ -256,9 +440,13 @@ moe_status_t status_of(cudaError_t e) {
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 moe_status_t launched() { return status_of(cudaGetLastError()); }
+// What a grid holds, about 10^13 values: more than any memory does.
+bool grid_ok(long long pieces) {
+  return pieces <= static_cast<long long>(kPieces * kThreads) * 0x7fffffff;
+}
 unsigned row_grid(long long pieces) {
-  return static_cast<unsigned>(
-      std::min<long long>((pieces + kThreads - 1) / kThreads, 1 << 20));
+  return static_cast<unsigned>((pieces + kPieces * kThreads - 1) /
+                               (kPieces * kThreads));
 }
 dim3 record_grid(const Layout& l, int n) {
   return dim3(l.stages(), l.tiles_n(), n < 4096 ? n : 4096);
@@ -275,7 +463,7 @@ cudaError_t quantize_weights(int n, int K, int N, const void* w,
   if (e != cudaSuccess) return e;
   const dim3 grid((N + kTurnN - 1) / kTurnN, (K + kStageK - 1) / kStageK,
                   n < 4096 ? n : 4096);
-  const int bytes = kStageK * (kTurnN * sizeof(T) + 4);
+  const int bytes = kStageK * kTurnN * sizeof(T);
   kernel<<<grid, kThreads, bytes, s>>>(static_cast<const T*>(w), scale, n, K,
                                        N, codes, scales);
   return cudaGetLastError();
@@ -287,6 +475,7 @@ cudaError_t launch_mx_rows(int block, int R, int K, moe_dtype_t dtype,
                            const void* x, float scale, uint8_t* codes,
                            uint8_t* scales, cudaStream_t s) {
   const long long pieces = static_cast<long long>(R) * (K / 8);
+  if (!grid_ok(pieces)) return cudaErrorInvalidValue;
   const float r = 1.0f / scale;
   const unsigned grid = row_grid(pieces);
 #define MOE_MX_ROWS(B, T)                                                   \
@@ -336,6 +525,8 @@ moe_status_t moe_mx_quantize_rows(const moe_mx_t* opt, int32_t R, int32_t K,
   if (R == 0) return MOE_OK;
   if (!ok_ptr(x, true) || !ok_ptr(codes, true) || !ok_ptr(scales, false))
     return MOE_ERR_INVALID_ARG;
+  if (!grid_ok(static_cast<long long>(R) * (K / 8)))
+    return MOE_ERR_UNSUPPORTED;
   return status_of(launch_mx_rows(opt->block, R, K, dtype, x, scale, codes,
                                   scales, stream));
 }
@@ -352,6 +543,7 @@ moe_status_t moe_mx_dequantize_rows(const moe_mx_t* opt, int32_t R, int32_t K,
   if (!ok_ptr(codes, true) || !ok_ptr(scales, false) || !ok_ptr(x, true))
     return MOE_ERR_INVALID_ARG;
   const long long pieces = static_cast<long long>(R) * (K / 8);
+  if (!grid_ok(pieces)) return MOE_ERR_UNSUPPORTED;
 #define MOE_MX_ROWS(B, T)                                             \
   dequantize_rows_kernel<B, T><<<row_grid(pieces), kThreads, 0, stream>>>( \
       codes, scales, pieces, K, scale, static_cast<T*>(x))

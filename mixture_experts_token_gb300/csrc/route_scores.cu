@@ -10,24 +10,26 @@
 // whose order matters are nearer than that bound allows (about one row in a
 // thousand), again in float64.
 //
-// Forward, in float32: lane i holds the i-th run of EPL consecutive experts,
-// so that equal values go to the lower lane.  Each lane's two largest c give,
-// in k rounds of a warp maximum, a threshold that at least k values reach; the
-// few that do (and those within the error of it) are put in a row in shared
-// memory in the order of their experts, one to a lane, and each counts those
+// Forward, in float32: lane i holds the i-th run of EPL consecutive experts.
+// Each lane's two largest c give, in k rounds of a warp maximum, a threshold
+// that at least k values reach; the few that do (and those within the error of
+// it) are put in a row in shared memory, one to a lane, and each counts those
 // before it.  That is its rank: no list is sorted and no lane's values are
 // searched again.  Without a bias, and where no sum of scores is compared, the
-// logits rank, and there is no error to allow for.
+// logits rank, and there is no error to allow for; equal ones are told apart
+// where near ties are.
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 
+#include "launch.cuh"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxGroups = 64;
 constexpr int kMaxGroupTop = 4;
@@ -75,31 +77,60 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// e^x to 2^-22 and a little: the argument's product with log2 e in two parts.
+__device__ __forceinline__ float exp_near(float x) {
+  const float y = x * kLog2e;
+  // what y lacks: its own rounding, and that of the constant
+  const float rest = fmaf(x, kLog2e, -y) + x * 1.925963033500e-8f;
+  const float p = exp2_fast(y);
+  return fmaf(p * rest, 0.6931471806f, p);
+}
+
 // The weight of the chosen expert of logit l, in lanes where `chosen`; z is
 // the softmax's sum over all experts under the largest logit m.  Sums of
-// chosen scores are taken relative to the largest of them, so that they do not
-// vanish where all are small.
+// chosen scores are taken relative to the largest of them where all are small,
+// so that they do not vanish.
 __device__ __forceinline__ float weight(const Args& a, bool chosen, float l,
                                         float m, float z) {
   chosen = chosen && fabsf(l) <= FLT_MAX;
-  const float top = a.renorm ? warp_max(chosen ? l : -FLT_MAX) : 0.0f;
+  const float top = a.renorm ? warp_max(chosen ? l : -FLT_MAX) : m;
   float s = 0.0f;
   if (chosen) {
-    if (a.sigmoid)
-      s = expf(fminf(l, 0.0f) - (a.renorm ? fminf(top, 0.0f) : 0.0f)) /
-          (1.0f + expf(-fabsf(l)));
-    else
-      s = a.renorm ? expf(l - top) : expf(l - m) / z;
+    if (!a.sigmoid) {
+      s = expf(l - top);
+      if (!a.renorm) s /= z;
+    } else if (a.renorm && top < -60.0f) {
+      s = expf(l - top) / (1.0f + expf(l));
+    } else {
+      const float x = exp_near(fmaxf(-fabsf(l), -87.0f));
+      s = (l < 0.0f ? x : 1.0f) * rcp_fast(1.0f + x);
+    }
   }
   if (a.renorm) {
     const float sum = warp_sum(s);
-    s = sum > 0.0f ? s / sum : 0.0f;
+    s = sum > 0.0f ? __fdividef(s, sum) : 0.0f;
   }
   return a.scale * s;
 }
 
 // ------------------------------------------------------ in float64 -------
-// c of expert e; m and z as above.  Experts that are not finite rank last.
+// The largest logit m and the softmax's sum z; finite logits alone.
+__device__ void sums64(const Args& a, const float* row, int lane, float* m,
+                       double* z) {
+  float most = -INFINITY;
+  for (int e = lane; e < a.E; e += 32)
+    if (fabsf(row[e]) <= FLT_MAX) most = fmaxf(most, row[e]);
+  *m = warp_max(most);
+  double sum = 0.0;
+  if (!a.sigmoid) {
+    for (int e = lane; e < a.E; e += 32)
+      if (fabsf(row[e]) <= FLT_MAX)
+        sum += exp(static_cast<double>(row[e]) - static_cast<double>(*m));
+    sum = warp_sum(sum);
+  }
+  *z = sum;
+}
+// c of expert e.  Experts that are not finite rank last.
 __device__ double score64(const Args& a, const float* row, int e, float m,
                           double z) {
   const float l = row[e], b = a.bias ? a.bias[e] : 0.0f;
@@ -110,60 +141,140 @@ __device__ double score64(const Args& a, const float* row, int e, float m,
       a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - static_cast<double>(m)) / z;
   return s + b;
 }
+// What experts rank by: without a bias the logits, whose scores may round to
+// the same number.
+__device__ double rank_by64(const Args& a, const float* row, int e, float m,
+                            double z) {
+  if (a.bias) return score64(a, row, e, m, z);
+  return fabsf(row[e]) <= FLT_MAX ? static_cast<double>(row[e]) : -INFINITY;
+}
+// Numbers as integers of the same order (no NaN; one zero).
+__device__ __forceinline__ long long ordered64(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return b < 0 ? b ^ 0x7fffffffffffffffll : b;
+}
 
-// Ranks a row anew; lane j returns the j-th expert.
+// The rank of this lane's candidate e among those of the first `total` lanes.
+__device__ __noinline__ int rank_candidates64(const Args& a, const float* row,
+                                              int e, int total, int lane) {
+  float m = 0.0f;
+  double z = 1.0;
+  if (a.bias && !a.sigmoid) sums64(a, row, lane, &m, &z);
+  const long long v =
+      lane < total ? ordered64(rank_by64(a, row, e, m, z)) : LLONG_MIN;
+  int before = 0;
+  for (int j = 0; j < total; ++j) {
+    const long long other = __shfl_sync(kAll, v, j);
+    const int oe = __shfl_sync(kAll, e, j);
+    before += other > v || (other == v && oe < e);
+  }
+  return before;
+}
+
+// The largest of the lanes' numbers.
+__device__ __forceinline__ long long warp_max64(long long v) {
+  const int hi = __reduce_max_sync(kAll, static_cast<int>(v >> 32));
+  const uint32_t lo = __reduce_max_sync(
+      kAll, static_cast<int>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<long long>(hi) << 32 | lo;
+}
+
+// Whether the group of lane / lanes takes part, from the float64 sums of those
+// experts that the groups' largest c can be: one of the first `total` lanes
+// each, e its expert.  (Equal sums: the lower group.)
+__device__ __noinline__ bool keep_groups64(const Args& a, const float* row,
+                                           int e, int total, int lane,
+                                           int lanes) {
+  float m = 0.0f;
+  double z = 1.0;
+  if (!a.sigmoid) sums64(a, row, lane, &m, &z);
+  const int size = a.E / a.groups;
+  long long v = LLONG_MIN;
+  if (lane < total) v = ordered64(score64(a, row, e, m, z));
+  const int mine = lane < total ? e / size : -1;
+  long long sum = LLONG_MIN;  // of group `lane`
+  for (int g = 0; g < a.groups; ++g) {
+    long long left = mine == g ? v : LLONG_MIN;
+    double t = 0.0;
+    for (int j = 0; j < a.group_top; ++j) {
+      const long long best = warp_max64(left);
+      if (lane == __ffs(__ballot_sync(kAll, left == best)) - 1)
+        left = LLONG_MIN;
+      t += __longlong_as_double(best < 0 ? best ^ 0x7fffffffffffffffll : best);
+    }
+    if (lane == g) sum = ordered64(t);
+  }
+  int before = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const long long other = __shfl_sync(kAll, sum, g);
+    before += other > sum || (other == sum && g < lane);
+  }
+  const uint32_t keep =
+      __ballot_sync(kAll, lane < a.groups && before < a.top_groups);
+  return lane / lanes < a.groups && keep >> (lane / lanes) & 1;
+}
+
+// Ranks a row anew, groups and experts; lane j returns the j-th expert.  c:
+// room for the row's E numbers, as integers of their order.  Late rows of a
+// call wait for nothing else, so what counts is the time of one: float64
+// instructions are few and side by side.
 __device__ __noinline__ int rank64(const Args& a, const float* row, int lane,
-                                   float* max_logit, float* sum) {
-  const int per = (a.E + 31) / 32, first = lane * per;
+                                   long long* c, float* max_logit,
+                                   float* sum) {
   bool bad = false;
-  float m = -INFINITY;
-  for (int e = lane; e < a.E; e += 32) {
-    const float l = row[e];
-    const bool ok = fabsf(l) <= FLT_MAX;
-    bad |= !ok || (a.bias && !(fabsf(a.bias[e]) <= FLT_MAX));
-    if (ok) m = fmaxf(m, l);
-  }
-  m = warp_max(m);
-  double z = 0.0;
-  if (!a.sigmoid) {
-    for (int e = lane; e < a.E; e += 32)
-      if (fabsf(row[e]) <= FLT_MAX)
-        z += exp(static_cast<double>(row[e]) - static_cast<double>(m));
-    z = warp_sum(z);
-  }
-  *max_logit = m;
-  *sum = static_cast<float>(z);
+  for (int e = lane; e < a.E; e += 32)
+    bad |= !(fabsf(row[e]) <= FLT_MAX) ||
+           (a.bias && !(fabsf(a.bias[e]) <= FLT_MAX));
   if (__any_sync(kAll, bad) && lane == 0 && a.status)
     atomicOr(a.status, MOE_DEV_NONFINITE);
+  float m;
+  double z;
+  sums64(a, row, lane, &m, &z);
+  *max_logit = m;
+  *sum = static_cast<float>(z);
 
   // the groups that take part, a lane for two of them
   unsigned long long keep = ~0ull;
   const int size = a.E / a.groups;
+  __syncwarp();
   if (a.top_groups < a.groups) {
-    double total[2];
-    for (int h = 0; h < 2; ++h) {
-      const int g = h * 32 + lane;
-      total[h] = -INFINITY;
-      if (g >= a.groups) continue;
-      double top[kMaxGroupTop];
-      for (int j = 0; j < kMaxGroupTop; ++j) top[j] = -INFINITY;
-      for (int e = g * size; e < (g + 1) * size; ++e) {
-        double c = score64(a, row, e, m, z);
-        for (int j = 0; j < a.group_top; ++j)
-          if (c > top[j]) {
-            const double t = top[j];
-            top[j] = c;
-            c = t;
-          }
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32)
+      c[e] = ordered64(score64(a, row, e, m, z));
+    __syncwarp();
+    double total[2] = {-INFINITY, -INFINITY};
+    for (int g = 0; g < a.groups; ++g) {
+      // its group_top largest, one after another; equal ones one by one
+      double t = 0.0;
+      long long under = LLONG_MAX;  // none above it is left
+      int taken = 0;                // of those equal to it
+      for (int j = 0; j < a.group_top; ++j) {
+        long long best = LLONG_MIN;
+        int equal = 0;
+        for (int e = g * size + lane; e < (g + 1) * size; e += 32) {
+          const long long v = c[e];
+          if (v < under) best = max(best, v);
+          equal += v == under;
+        }
+        if (__reduce_add_sync(kAll, equal) > taken) {
+          ++taken;
+        } else {
+          under = warp_max64(best);
+          taken = 1;
+        }
+        const long long bits =
+            under < 0 ? under ^ 0x7fffffffffffffffll : under;
+        t += __longlong_as_double(bits);
       }
-      total[h] = top[0];
-      for (int j = 1; j < a.group_top; ++j) total[h] += top[j];
+      if (lane == (g & 31)) total[g >> 5] = t;
     }
+    const long long mine[2] = {ordered64(total[0]), ordered64(total[1])};
     int before[2] = {0, 0};
     for (int g = 0; g < a.groups; ++g) {
-      const double t = __shfl_sync(kAll, g < 32 ? total[0] : total[1], g & 31);
+      const long long t =
+          __shfl_sync(kAll, g < 32 ? mine[0] : mine[1], g & 31);
       for (int h = 0; h < 2; ++h)
-        if (t > total[h] || (t == total[h] && g < h * 32 + lane)) ++before[h];
+        before[h] += t > mine[h] || (t == mine[h] && g < h * 32 + lane);
     }
     keep = __ballot_sync(kAll, lane < a.groups && before[0] < a.top_groups);
     keep |= static_cast<unsigned long long>(__ballot_sync(
@@ -171,51 +282,101 @@ __device__ __noinline__ int rank64(const Args& a, const float* row, int lane,
             << 32;
   }
 
-  double c[32];
+  const int per = (a.E + 31) / 32, first = lane * per;
   uint32_t left = 0;  // this lane's experts that may be chosen yet
+  __syncwarp();  // c is written anew
   for (int i = 0; i < per; ++i) {
     const int e = first + i;
     if (e < a.E && keep >> (e / size) & 1) {
-      // without a bias the logits rank: their scores may round to the same
-      c[i] = a.bias                       ? score64(a, row, e, m, z)
-             : fabsf(row[e]) <= FLT_MAX ? static_cast<double>(row[e])
-                                          : -INFINITY;
+      if (!a.bias || a.top_groups == a.groups)  // else c holds it already
+        c[e] = ordered64(rank_by64(a, row, e, m, z));
       left |= 1u << i;
     }
   }
   int mine = 0;
   for (int j = 0; j < a.k; ++j) {
-    double best = -INFINITY;
+    long long best = LLONG_MIN;
     int at = kMaxExperts;
     for (int i = 0; i < per; ++i)
-      if (left >> i & 1 && (at == kMaxExperts || c[i] > best)) {
-        best = c[i];
-        at = first + i;
+      if (left >> i & 1) {
+        const long long v = c[first + i];
+        if (at == kMaxExperts || v > best) {
+          best = v;
+          at = first + i;
+        }
       }
-    for (int o = 16; o > 0; o >>= 1) {
-      const double other = __shfl_xor_sync(kAll, best, o);
-      const int oat = __shfl_xor_sync(kAll, at, o);
-      if (oat < kMaxExperts &&
-          (at == kMaxExperts || other > best || (other == best && oat < at))) {
-        best = other;
-        at = oat;
-      }
-    }
-    if (at >= first && at < first + per) left &= ~(1u << (at - first));
-    if (lane == j) mine = at;
+    const long long top = warp_max64(best);
+    const int e = __reduce_min_sync(
+        kAll, best == top ? static_cast<unsigned>(at) : kMaxExperts + 0u);
+    if (e >= first && e < first + per) left &= ~(1u << (e - first));
+    if (lane == j) mine = e;
   }
+  __syncwarp();
   return mine;
 }
 
 // ------------------------------------------------------ in float32 -------
-template <int EPL, int RANK>
-__global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
-  // a row's candidates (c, expert), and for groups that are not whole lanes
-  // its c
-  __shared__ float cand_c[kWarps][32];
-  __shared__ int cand_e[kWarps][32];
-  extern __shared__ float row_c[];
+// Experts e0 .. e0 + EPL - 1 of a row; -infinity past the last.
+template <int EPL, bool FULL>
+__device__ __forceinline__ void load_row(const float* row, int e0, int E,
+                                         bool wide, float (&c)[EPL]) {
+  if constexpr (EPL % 4 == 0) {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += 4) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (FULL || e0 + i < E)
+          v = __ldg(reinterpret_cast<const float4*>(row + e0 + i));
+        c[i] = v.x, c[i + 1] = v.y, c[i + 2] = v.z, c[i + 3] = v.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    c[i] = FULL || e0 + i < E ? __ldg(row + e0 + i) : -INFINITY;
+}
+
+// c of a logit l; m and inv: the softmax's largest logit and 1 / its sum.
+template <int RANK>
+__device__ __forceinline__ float rank_by(float l, float bias, float m,
+                                         float inv) {
+  if (RANK == kByLogit) return l;
+  const float s = RANK == kBySigmoid
+                      ? rcp_fast(1.0f + exp2_fast(-kLog2e * l))
+                      : exp2_fast((l - m) * kLog2e) * inv;
+  return s + bias;
+}
+
+// Puts the experts of the lanes' hits into the list, up to 32, in any order;
+// how many there are (33 or more: too many).
+__device__ __forceinline__ int collect(uint32_t hits, int e0, int lane,
+                                       int* list) {
+  int total = 0;
+  __syncwarp();
+#pragma unroll 1
+  for (uint32_t any; (any = __ballot_sync(kAll, hits != 0)) != 0;) {
+    const int at = total + __popc(any & ((1u << lane) - 1));
+    total += __popc(any);
+    if (hits != 0 && at < 32) list[at] = e0 + __ffs(hits) - 1;
+    if (total > 32) break;
+    hits &= hits - 1;
+  }
+  __syncwarp();
+  return total;
+}
+
+// FULL: E is 32 EPL.
+template <int EPL, int RANK, bool FULL>
+__global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
+    scores_kernel(const Args a) {
+  // a row's candidates, then (c, expert) by rank; the row's numbers, where
+  // groups are not whole lanes and in rank64()
+  __shared__ float cand_c[kWarps][33];
+  __shared__ int cand_e[kWarps][33];
+  extern __shared__ long long row_c[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long* mine64 = row_c + warp * (32 * EPL);
   const int size = a.E / a.groups;
   const bool select = a.top_groups < a.groups;
   // groups of whole lanes, a power of two of them
@@ -223,7 +384,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
   const bool whole = size % EPL == 0 && (lanes & (lanes - 1)) == 0 &&
                      a.group_top <= 2;
   const int e0 = lane * EPL;
-  const bool wide = EPL % 4 == 0 && a.E % 4 == 0 &&
+  const bool wide = EPL % 4 == 0 && (FULL || a.E % 4 == 0) &&
                     (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
   float bias[EPL], most_bias = 0.0f;
   if (RANK != kByLogit) {
@@ -236,35 +397,26 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
     }
     most_bias = warp_max(most_bias);
   }
-  for (long long t = blockIdx.x * static_cast<long long>(kWarps) + warp;
-       t < a.T; t += gridDim.x * static_cast<long long>(kWarps)) {
+  const long long step = gridDim.x * static_cast<long long>(kWarps);
+  long long t = blockIdx.x * static_cast<long long>(kWarps) + warp;
+  float next[EPL];
+  if (t < a.T)
+    load_row<EPL, FULL>(a.logits + t * a.E, e0, a.E, wide, next);
+#pragma unroll 1
+  for (; t < a.T; t += step) {
     const float* row = a.logits + t * a.E;
     float c[EPL];
-    bool again = most_bias == INFINITY;  // rank in float64
-    bool loaded = false;
-    if constexpr (EPL % 4 == 0) {
-      if (wide) {
-        loaded = true;
 #pragma unroll
-        for (int i = 0; i < EPL; i += 4) {
-          float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          if (e0 + i < a.E)
-            v = __ldg(reinterpret_cast<const float4*>(row + e0 + i));
-          c[i] = v.x, c[i + 1] = v.y, c[i + 2] = v.z, c[i + 3] = v.w;
-        }
-      }
-    }
-    if (!loaded) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        c[i] = e0 + i < a.E ? __ldg(row + e0 + i) : -INFINITY;
-    }
+    for (int i = 0; i < EPL; ++i) c[i] = next[i];
+    if (t + step < a.T)
+      load_row<EPL, FULL>(row + step * a.E, e0, a.E, wide, next);
+    bool again = RANK != kByLogit && most_bias == INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      again |= e0 + i < a.E && !(fabsf(c[i]) <= FLT_MAX);
+      again |= (FULL || e0 + i < a.E) && !(fabsf(c[i]) <= FLT_MAX);
 
     // scores, and the most that a c may be off by
-    float m = 0.0f, z = 1.0f, err = 0.0f;
+    float m = 0.0f, z = 1.0f, inv = 1.0f, err = 0.0f;
     if (RANK == kBySoftmax || (RANK == kByLogit && !a.sigmoid && !a.renorm)) {
       m = c[0];
 #pragma unroll
@@ -278,15 +430,14 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
         part += x;
       }
       z = warp_sum(part);
+      inv = rcp_fast(z);
     }
     if (RANK != kByLogit) {
-      const float inv = RANK == kBySoftmax ? rcp_fast(z) : 1.0f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const float s = RANK == kBySoftmax
-                            ? c[i] * inv
-                            : rcp_fast(1.0f + exp2_fast(-kLog2e * c[i]));
-        c[i] = e0 + i < a.E ? s + bias[i] : -INFINITY;
+        c[i] = RANK == kBySoftmax ? c[i] * inv + bias[i]
+                                  : rank_by<RANK>(c[i], bias[i], m, inv);
+        if (!FULL && e0 + i >= a.E) c[i] = -INFINITY;
       }
       // The sigmoid: 2^-22 of the exponential and what its argument's rounding
       // gives (a third of 2^-24), weighed by s (1 - s) <= 1/4, an ulp of the
@@ -295,8 +446,9 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
       // 2^-22, by 17 2^-24 from the arguments (far terms: 10 bits of them at
       // most weigh) and by 37 2^-24 from adding: below 2^-18.  Adding the
       // bias: half an ulp.
-      err = (RANK == kBySoftmax ? 3.8146973e-6f : 4.7683716e-7f) * inv +
-            1.1920929e-7f * (inv + most_bias);
+      const float most = RANK == kBySoftmax ? inv : 1.0f;
+      err = (RANK == kBySoftmax ? 3.8146973e-6f : 4.7683716e-7f) * most +
+            1.1920929e-7f * (most + most_bias);
     }
 
     // this lane's two largest
@@ -306,38 +458,54 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
       m2 = fmaxf(m2, fminf(m1, c[i]));
       m1 = fmaxf(m1, c[i]);
     }
+    bool kept = true;
     if (select) {
-      bool kept = false;
+      // sums of n c are off by n errors, and adding them by n (n - 1) / 2
+      const float group_err = a.group_top * (a.group_top + 1) * err;
       if (whole) {
         float g1 = m1, g2 = m2;
+#pragma unroll 1
         for (int o = 1; o < lanes; o <<= 1) {
           const float o1 = __shfl_xor_sync(kAll, g1, o);
           const float o2 = __shfl_xor_sync(kAll, g2, o);
           g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
           g1 = fmaxf(g1, o1);
         }
-        const float total = a.group_top == 2 ? g1 + g2 : g1;
-        const int mine = lane / lanes;
-        int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-          const float other = __shfl_sync(kAll, total, g * lanes & 31);
-          before += other > total || (other == total && g < mine);
+        // (one zero; lanes past the last expert are behind all groups)
+        uint32_t o = FULL || e0 < a.E
+                         ? ordered((a.group_top == 2 ? g1 + g2 : g1) + 0.0f)
+                         : 0u;
+        kept = false;
+        uint32_t last = 0;
+#pragma unroll 1
+        for (int g = 0; g < a.top_groups; ++g) {
+          last = __reduce_max_sync(kAll, o);
+          if (o == last) {
+            kept = true;
+            o = 0;
+          }
         }
-        const bool inside = e0 < a.E;
-        kept = inside && before < a.top_groups;
-        const float last = warp_min(kept ? total : INFINITY);
-        const float next = warp_max(inside && !kept ? total : -INFINITY);
-        // sums of n c are off by n errors, and adding them by n (n - 1) / 2
-        if (RANK != kByLogit)
-          again |= !(last - next > a.group_top * (a.group_top + 1) * err);
-        if (!kept) {
-          m1 = m2 = -INFINITY;
+        const uint32_t out = __reduce_max_sync(kAll, o);
+        // equal sums, or sums that the error may have exchanged
+        if (__popc(__ballot_sync(kAll, kept)) != a.top_groups * lanes ||
+            (RANK != kByLogit &&
+             !(unordered(last) - unordered(out) > group_err))) {
+          const float least = (a.group_top == 2 ? g2 : g1) - 2.0f * err;
+          uint32_t hits = 0;
 #pragma unroll
-          for (int i = 0; i < EPL; ++i) c[i] = -INFINITY;
+          for (int i = 0; i < EPL; ++i)
+            if (c[i] >= least) hits |= 1u << i;
+          const int n = collect(hits, e0, lane, cand_e[warp]);
+          if (n > 32)
+            again = true;
+          else
+            kept = keep_groups64(a, row, lane < n ? cand_e[warp][lane] : 0, n,
+                                 lane, lanes);
         }
+        if (!kept) m1 = m2 = -INFINITY;
       } else {
         // a lane a group (or two), over the row's c in shared memory
-        float* rc = row_c + warp * (32 * EPL);
+        float* rc = reinterpret_cast<float*>(mine64);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < EPL; ++i) rc[e0 + i] = c[i];
@@ -375,13 +543,14 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
         }
         const bool k0 = lane < a.groups && before[0] < a.top_groups;
         const bool k1 = 32 + lane < a.groups && before[1] < a.top_groups;
-        const float last = warp_min(
-            fminf(k0 ? total[0] : INFINITY, k1 ? total[1] : INFINITY));
-        const float next =
-            warp_max(fmaxf(lane < a.groups && !k0 ? total[0] : -INFINITY,
-                           32 + lane < a.groups && !k1 ? total[1] : -INFINITY));
-        if (RANK != kByLogit)
-          again |= !(last - next > a.group_top * (a.group_top + 1) * err);
+        if (RANK != kByLogit) {
+          const float last = warp_min(
+              fminf(k0 ? total[0] : INFINITY, k1 ? total[1] : INFINITY));
+          const float out = warp_max(
+              fmaxf(lane < a.groups && !k0 ? total[0] : -INFINITY,
+                    32 + lane < a.groups && !k1 ? total[1] : -INFINITY));
+          again |= !(last - out > group_err);
+        }
         const uint32_t low = __ballot_sync(kAll, k0);
         const uint32_t high = __ballot_sync(kAll, k1);
         m1 = m2 = -INFINITY;
@@ -397,70 +566,71 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const Args a) {
     }
 
     // a threshold that at least k values reach, if the lanes' pairs hold k
-    float bar = -INFINITY;
-    uint32_t o1 = ordered(m1), o2 = ordered(m2);
-    constexpr uint32_t kNone = 0x007fffffu;  // ordered(-infinity)
+    uint32_t o1 = ordered(m1), o2 = ordered(m2), reached = 0;
+#pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
-      const uint32_t best = __reduce_max_sync(kAll, o1);
-      bar = unordered(best);
-      if (o1 == best) {
+      reached = __reduce_max_sync(kAll, o1);
+      if (o1 == reached) {
         o1 = o2;
-        o2 = kNone;
+        o2 = 0;
       }
     }
     // values within twice the error of it stay, so that what is left out is
-    // surely behind; a threshold of -infinity leaves nothing out
-    bar = fmaxf(bar - 2.0f * err, -FLT_MAX);
-    int n = 0;
+    // surely behind; a threshold of -infinity (or none) leaves nothing out
+    const float bar = reached > ordered(-FLT_MAX)
+                          ? fmaxf(unordered(reached) - 2.0f * err, -FLT_MAX)
+                          : -FLT_MAX;
+    uint32_t hits = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) n += c[i] >= bar;
-    int at = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int below = __shfl_up_sync(kAll, at, o);
-      if (lane >= o) at += below;
-    }
-    const int total = __shfl_sync(kAll, at, 31);
-    at -= n;
+    for (int i = 0; i < EPL; ++i)
+      if (c[i] >= bar) hits |= 1u << i;
+    if (!kept) hits = 0;
+    const int total = collect(hits, e0, lane, cand_e[warp]);
     again |= total > 32 || total < a.k;
 
-    int e = 0, rank = 32;
+    int e = 0;
     float l = 0.0f;
     if (!__any_sync(kAll, again)) {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (c[i] >= bar) {
-          cand_c[warp][at] = c[i];
-          cand_e[warp][at++] = e0 + i;
-        }
-      __syncwarp();
-      const float v = lane < total ? cand_c[warp][lane] : -INFINITY;
-      int before = 0;
-      float gap = INFINITY;
-      for (int j = 0; j < total; ++j) {
-        const float other = __shfl_sync(kAll, v, j);
-        before += other > v || (other == v && j < lane);
-        if (RANK != kByLogit && j != lane) gap = fminf(gap, fabsf(other - v));
-      }
+      float v = -INFINITY;
       if (lane < total) {
         e = cand_e[warp][lane];
-        rank = before;
         l = __ldg(row + e);
+        v = rank_by<RANK>(l, RANK != kByLogit && a.bias ? __ldg(a.bias + e)
+                                                        : 0.0f,
+                          m, inv);
       }
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < total; ++j)
+        rank += __shfl_sync(kAll, v, j) > v;
+      // the list by rank: equal c leave a place empty
+      cand_c[warp][lane] = INFINITY;
+      __syncwarp();
+      if (lane < total) {
+        cand_c[warp][rank] = v;
+        cand_e[warp][rank] = e;
+      }
+      __syncwarp();
+      const float here = cand_c[warp][lane];
+      const float behind = __shfl_down_sync(kAll, here, 1);
       // nearer than the error allows, and before or among the k chosen
-      if (RANK != kByLogit) again = rank <= a.k && gap <= 2.0f * err;
-    }
-    if (__any_sync(kAll, again)) {
-      e = rank64(a, row, lane, &m, &z);
-      rank = lane;
+      if (__any_sync(kAll, lane < a.k && lane + 1 < total &&
+                               !(here - behind > 2.0f * err))) {
+        rank = rank_candidates64(a, row, e, total, lane);
+        if (lane < total) cand_e[warp][rank] = e;
+        __syncwarp();
+      }
+      e = cand_e[warp][lane];
+      l = lane < a.k ? __ldg(row + e) : 0.0f;
+    } else {
+      e = rank64(a, row, lane, mine64, &m, &z);
       l = lane < a.k ? row[e] : 0.0f;
       if (lane < a.k && a.bias && !(fabsf(a.bias[e]) <= FLT_MAX)) l = INFINITY;
     }
-    const float w = weight(a, rank < a.k, l, m, z);
-    if (rank < a.k) {
-      a.idx[t * a.k + rank] = e;
-      a.w[t * a.k + rank] = w;
+    const float w = weight(a, lane < a.k, l, m, z);
+    if (lane < a.k) {
+      a.idx[t * a.k + lane] = e;
+      a.w[t * a.k + lane] = w;
     }
   }
 }
@@ -476,48 +646,79 @@ struct BackArgs {
   float scale;
 };
 
-// A chosen expert a lane.  With sigmoid scores the row is zero but for the
-// chosen; with softmax scores lane i also has the i-th run of EPL experts.
-template <bool SIGMOID>
+// A chosen expert a lane, LANES lanes a token and so 32 / LANES tokens a warp.
+// With sigmoid scores the row is zero but for the chosen; with softmax scores
+// every lane also has its share of the row, one token after another.
+template <bool SIGMOID, int LANES>
 __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
     const BackArgs a) {
+  constexpr int kTokens = 32 / LANES;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tok = lane / LANES, j = lane % LANES;
   const bool wide =
       a.E % 4 == 0 &&
       ((reinterpret_cast<uintptr_t>(a.logits) |
         reinterpret_cast<uintptr_t>(a.dlogits)) & 15) == 0;
-  for (long long t = blockIdx.x * static_cast<long long>(kWarps) + warp;
-       t < a.T; t += gridDim.x * static_cast<long long>(kWarps)) {
-    const float* row = a.logits + t * a.E;
-    float* out = a.dlogits + t * a.E;
+  const auto token_sum = [](float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  };
+  for (long long t0 = (blockIdx.x * static_cast<long long>(kWarps) + warp) *
+                      kTokens;
+       t0 < a.T; t0 += gridDim.x * static_cast<long long>(kWarps) * kTokens) {
+    const long long t = t0 + tok;
+    const int here = static_cast<int>(min(static_cast<long long>(kTokens),
+                                          a.T - t0));
+    const bool on = tok < here && j < a.k;
     int e = -1 - lane;  // of no expert, and no other lane's
     float l = 0.0f, d = 0.0f;
-    if (lane < a.k) {
-      const int i = __ldg(a.idx + t * a.k + lane);
-      d = __ldg(a.dw + t * a.k + lane);
+    if (on) {
+      const int i = __ldg(a.idx + t * a.k + j);
+      d = __ldg(a.dw + t * a.k + j);
       if (i >= 0 && i < a.E) {
         e = i;
-        l = __ldg(row + e);
+        l = __ldg(a.logits + t * a.E + e);
+      }
+    }
+    float m = 0.0f, z = 1.0f;
+    if (SIGMOID) {
+      // zeros now, while the chosen logits come
+      float* out = a.dlogits + t0 * a.E;
+      const long long n = static_cast<long long>(here) * a.E;
+      if (wide)
+        for (long long i = lane * 4; i < n; i += 128)
+          *reinterpret_cast<float4*>(out + i) =
+              make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      else
+        for (long long i = lane; i < n; i += 32) out[i] = 0.0f;
+    } else {
+      for (int r = 0; r < here; ++r) {
+        const float* row = a.logits + (t0 + r) * a.E;
+        float most = -FLT_MAX;
+        for (int i = lane; i < a.E; i += 32) {
+          const float v = __ldg(row + i);
+          if (fabsf(v) <= FLT_MAX) most = fmaxf(most, v);
+        }
+        most = warp_max(most);
+        float sum = 0.0f;
+        for (int i = lane; i < a.E; i += 32) {
+          const float v = __ldg(row + i);
+          if (fabsf(v) <= FLT_MAX) sum += expf(v - most);
+        }
+        sum = warp_sum(sum);
+        if (tok == r) {
+          m = most;
+          z = sum;
+        }
       }
     }
     const bool finite = e >= 0 && fabsf(l) <= FLT_MAX;
-    float m = 0.0f, z = 1.0f;
-    if (!SIGMOID) {
-      m = -FLT_MAX;
-      for (int i = lane; i < a.E; i += 32) {
-        const float v = __ldg(row + i);
-        if (fabsf(v) <= FLT_MAX) m = fmaxf(m, v);
-      }
-      m = warp_max(m);
-      z = 0.0f;
-      for (int i = lane; i < a.E; i += 32) {
-        const float v = __ldg(row + i);
-        if (fabsf(v) <= FLT_MAX) z += expf(v - m);
-      }
-      z = warp_sum(z);
-    }
     // the weight over scale, as the forward has it
-    const float top = a.renorm ? warp_max(finite ? l : -FLT_MAX) : 0.0f;
+    float top = finite ? l : -FLT_MAX;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
     float w = 0.0f;
     if (finite) {
       if (SIGMOID)
@@ -527,56 +728,72 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
         w = a.renorm ? expf(l - top) : expf(l - m) / z;
     }
     if (a.renorm) {
-      const float sum = warp_sum(w);
+      const float sum = token_sum(w);
       w = sum > 0.0f ? w / sum : 0.0f;
     }
     float g = finite ? a.scale * d * w : 0.0f;
-    if (a.renorm) g -= w * warp_sum(g);
-    const float all = SIGMOID ? 0.0f : warp_sum(g);
+    if (a.renorm) g -= w * token_sum(g);
+    const float all = SIGMOID ? 0.0f : token_sum(g);
     // an index that stands twice has the sum of both
-    const uint32_t same = __match_any_sync(kAll, e);
-    if (__any_sync(kAll, (same & (same - 1)) != 0)) {
+    const uint32_t mine = (LANES == 32 ? kAll : (1u << LANES) - 1)
+                          << (tok * LANES);
+    const uint32_t same =
+        __match_any_sync(kAll, e) & mine & ~(1u << lane);
+    if (__any_sync(kAll, e >= 0 && same != 0)) {
       float sum = 0.0f;
-      for (int j = 0; j < a.k; ++j) {
-        const float other = __shfl_sync(kAll, g, j);
-        if (same >> j & 1) sum += other;
+      for (int i = 0; i < LANES; ++i) {
+        const float other = __shfl_sync(kAll, g, tok * LANES + i);
+        if (tok * LANES + i == lane || same >> (tok * LANES + i) & 1)
+          sum += other;
       }
       g = sum;
     }
-    if (wide) {
-      for (int i = lane * 4; i < a.E; i += 128) {
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (!SIGMOID) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(row + i));
-          const float f = -all / z;
-          o.x = fabsf(v.x) <= FLT_MAX ? f * expf(v.x - m) : 0.0f;
-          o.y = fabsf(v.y) <= FLT_MAX ? f * expf(v.y - m) : 0.0f;
-          o.z = fabsf(v.z) <= FLT_MAX ? f * expf(v.z - m) : 0.0f;
-          o.w = fabsf(v.w) <= FLT_MAX ? f * expf(v.w - m) : 0.0f;
+    if (!SIGMOID) {
+      for (int r = 0; r < here; ++r) {
+        const float* row = a.logits + (t0 + r) * a.E;
+        float* out = a.dlogits + (t0 + r) * a.E;
+        const float most = __shfl_sync(kAll, m, r * LANES);
+        const float f = __shfl_sync(kAll, -all / z, r * LANES);
+        if (wide) {
+          for (int i = lane * 4; i < a.E; i += 128) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(row + i));
+            float4 o;
+            o.x = fabsf(v.x) <= FLT_MAX ? f * expf(v.x - most) : 0.0f;
+            o.y = fabsf(v.y) <= FLT_MAX ? f * expf(v.y - most) : 0.0f;
+            o.z = fabsf(v.z) <= FLT_MAX ? f * expf(v.z - most) : 0.0f;
+            o.w = fabsf(v.w) <= FLT_MAX ? f * expf(v.w - most) : 0.0f;
+            *reinterpret_cast<float4*>(out + i) = o;
+          }
+        } else {
+          for (int i = lane; i < a.E; i += 32) {
+            const float v = __ldg(row + i);
+            out[i] = fabsf(v) <= FLT_MAX ? f * expf(v - most) : 0.0f;
+          }
         }
-        *reinterpret_cast<float4*>(out + i) = o;
-      }
-    } else {
-      for (int i = lane; i < a.E; i += 32) {
-        float o = 0.0f;
-        if (!SIGMOID) {
-          const float v = __ldg(row + i);
-          if (fabsf(v) <= FLT_MAX) o = -all / z * expf(v - m);
-        }
-        out[i] = o;
       }
     }
     __syncwarp();  // the chosen are written over what other lanes wrote
     if (finite)
-      out[e] = SIGMOID ? g * (1.0f / (1.0f + expf(l)))
-                       : g - all / z * expf(l - m);
+      a.dlogits[t * a.E + e] = SIGMOID ? g * (1.0f / (1.0f + expf(l)))
+                                       : g - all / z * expf(l - m);
   }
 }
 
-unsigned token_grid(int T) {
-  return static_cast<unsigned>(
-      std::min<long long>((static_cast<long long>(T) + kWarps - 1) / kWarps,
-                          1 << 14));
+template <bool SIGMOID>
+cudaError_t launch_backward(const BackArgs& a, cudaStream_t s) {
+  const int lanes = a.k <= 4 ? 4 : a.k <= 8 ? 8 : a.k <= 16 ? 16 : 32;
+  const int tokens = kWarps * 32 / lanes;  // of a CTA
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(
+      (static_cast<long long>(a.T) + tokens - 1) / tokens, 1 << 20));
+  if (lanes == 4)
+    scores_backward_kernel<SIGMOID, 4><<<grid, kThreads, 0, s>>>(a);
+  else if (lanes == 8)
+    scores_backward_kernel<SIGMOID, 8><<<grid, kThreads, 0, s>>>(a);
+  else if (lanes == 16)
+    scores_backward_kernel<SIGMOID, 16><<<grid, kThreads, 0, s>>>(a);
+  else
+    scores_backward_kernel<SIGMOID, 32><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 bool options_ok(const moe_config_t& c, const moe_route_scores_t* o) {
@@ -593,19 +810,35 @@ bool options_ok(const moe_config_t& c, const moe_route_scores_t* o) {
          static_cast<long long>(o->top_groups) * size >= c.k;
 }
 
+template <int EPL, int RANK, bool FULL>
+cudaError_t launch_scores(const Args& a, cudaStream_t s) {
+  constexpr auto kernel = scores_kernel<EPL, RANK, FULL>;
+  constexpr int kBytes = kWarps * 32 * EPL * sizeof(long long);
+  static_assert(kBytes + kWarps * 272 <= 48 * 1024, "no larger than any CTA's");
+  launch::Device d;
+  int per_sm = 1;
+  cudaError_t e = launch::device(&d);
+  if (e == cudaSuccess)
+    e = launch::ctas_per_sm<kernel>(d, kThreads, kBytes, &per_sm);
+  if (e != cudaSuccess) return e;
+  // CTAs that stay, so that a warp reads the bias once and the next row while
+  // it ranks one
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(
+      (static_cast<long long>(a.T) + kWarps - 1) / kWarps,
+      static_cast<long long>(per_sm) * d.sms));
+  kernel<<<grid, kThreads, kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+template <int EPL, bool FULL>
+cudaError_t launch_rank(const Args& a, cudaStream_t s) {
+  return a.by_logit  ? launch_scores<EPL, kByLogit, FULL>(a, s)
+         : a.sigmoid ? launch_scores<EPL, kBySigmoid, FULL>(a, s)
+                     : launch_scores<EPL, kBySoftmax, FULL>(a, s);
+}
 template <int EPL>
 cudaError_t launch_epl(const Args& a, cudaStream_t s) {
-  // the row's c, where groups are not whole lanes
-  const int bytes =
-      a.top_groups < a.groups ? kWarps * 32 * EPL * sizeof(float) : 0;
-  const unsigned grid = token_grid(a.T);
-  if (a.by_logit)
-    scores_kernel<EPL, kByLogit><<<grid, kThreads, bytes, s>>>(a);
-  else if (a.sigmoid)
-    scores_kernel<EPL, kBySigmoid><<<grid, kThreads, bytes, s>>>(a);
-  else
-    scores_kernel<EPL, kBySoftmax><<<grid, kThreads, bytes, s>>>(a);
-  return cudaGetLastError();
+  return a.E == 32 * EPL ? launch_rank<EPL, true>(a, s)
+                         : launch_rank<EPL, false>(a, s);
 }
 
 }  // namespace
@@ -678,12 +911,10 @@ moe_status_t moe_route_scores_backward(const moe_config_t* cfg,
     return MOE_ERR_INVALID_ARG;
   const BackArgs a = {logits, topk_idx, dtopk_w, dlogits, cfg->T, cfg->E,
                       cfg->k, opt->renorm != 0, opt->scale};
-  const unsigned grid = token_grid(cfg->T);
-  if (opt->score == MOE_SCORE_SIGMOID)
-    scores_backward_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    scores_backward_kernel<false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaError_t e = opt->score == MOE_SCORE_SIGMOID
+                            ? launch_backward<true>(a, stream)
+                            : launch_backward<false>(a, stream);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"
