@@ -26,6 +26,7 @@ GmmArgs args_of(const moe_config_t& c, const moe_mx_t& o, const Groups& g,
   a.n_experts = c.E;
   a.n_groups = g.n;
   a.rows = c.T * c.k;
+  a.tokens = c.T;
   a.f32 = c.dtype == MOE_F32;
   a.stall_after_fills = tc::g_stall_after_fills.load();
   return a;

@@ -17,8 +17,9 @@
 //   * four warps, on every fourth stage each, bring the rows' scales into the
 //     order that tensor memory takes;
 //   * a warp copies a stage's scales to tensor memory and issues the matrix
-//     instructions; scales have two buffers there, and one is written again
-//     when the instructions of the stage but one before have completed;
+//     instructions; scales have a buffer for each stage there, or as many as
+//     fit, and one is written again when the instructions that read it have
+//     completed;
 //   * four warps turn the sums into rows of the output, a thread a column,
 //     while the next item's sums go to the other accumulator.
 // Every wait is bounded; one that gives up raises MOE_DEV_TIMEOUT and the CTA
@@ -55,6 +56,7 @@ struct GmmArgs {
   int32_t* status;
   Layout l;
   int n_experts, n_groups, rows, chunk, chunks;
+  int tokens;  // routing gives a group at most one row of each
   bool f32;    // y's type
   bool early;  // may start before the kernel that writes the rows has ended
   long long stall_after_fills;  // tests of the timeout path only (-1: off)
@@ -73,7 +75,6 @@ constexpr int kScaleWarp = kMmaWarp + 1;
 constexpr int kScaleWarps = 4;
 constexpr int kWarps = kScaleWarp + kScaleWarps;
 constexpr int kGmmThreads = kWarps * 32;
-constexpr int kRowBox = 16;  // rows of one TMA copy
 constexpr int kMaxSplits = 512;
 constexpr int kMaxChunks = kMaxExperts + kMaxSplits;
 constexpr int kMaxShared = 226 * 1024;
@@ -102,6 +103,33 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
          (static_cast<uint64_t>(16 >> 4) << 16) |
          (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
 }
+// A bounded wait as tc::mbar_wait, but the clock is read only after many looks
+// in vain: reading it takes longer than most of these waits.
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag,
+                                              int32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t looks = 1;; ++looks) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((looks & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t t = tc::globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > tc::kWaitLimitNs) {
+        *abort_flag = 1;
+        if (status) atomicOr(status, MOE_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity,
+                                     volatile int* abort_flag,
+                                     int32_t* status) {
+  return tc::mbar_try_wait(bar, parity) ||
+         wait_long(bar, parity, abort_flag, status);
+}
+
 // D (+)= A B over 64 of k, both 4-bit in shared memory, each block of BLOCK of
 // k times its scales in tensor memory.
 template <int BLOCK>
@@ -162,25 +190,33 @@ struct Gmm {
   static constexpr int kMats = DUAL ? 2 : 1;
   static constexpr int kTiles = scale_tiles(BLOCK);  // of 128 rows, a stage
   static constexpr int kRec = record_bytes(BLOCK);
-  static constexpr int kRowTiles = (NT + 127) / 128;
+  // The rows' scales, tiles of 128 rows as the weights'.  (32 rows would fit
+  // the four columns of one tile, a column for each 64 of k; but the
+  // instruction wants its scales at a multiple of four columns.)
+  static constexpr int kRowTiles = (NT + 127) / 128 * kTiles;
+  // Rows of one TMA copy: few where rows are few; where they are many, small
+  // copies are what takes the time.
+  static constexpr int kRowBox = NT <= 64 ? 16 : NT / 2;
   static constexpr int kX = kMats * kRec;             // the rows' codes
   static constexpr int kXs = kX + NT * 128;           // and scales
   static constexpr int kStage =
-      (kXs + kRowTiles * kTiles * kScaleTile + 1023) / 1024 * 1024;
+      (kXs + kRowTiles * kScaleTile + 1023) / 1024 * 1024;
   static constexpr int kRoom = kMaxShared - 1024 - kBarBytes - 8 * kMaxChunks;
   static constexpr int kStages =
       kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
-  static_assert(kStages >= 3, "the scales' two buffers lag by two stages");
-  static_assert(kRec % 1024 == 0 && NT % 16 == 0, "swizzled tiles aligned");
+  static_assert(kStages >= 3, "copies stay ahead");
+  static_assert(kRec % 1024 == 0 && NT % 16 == 0 && kRowBox % 8 == 0,
+                "swizzled tiles aligned");
   // Tensor memory: accumulators [buffer][matrix][NT], then scales [buffer]
-  // of the weights [matrix][tile][4] and the rows [tile][row tile][4].
+  // of the weights [matrix][tile][4] and the rows [tile][4].
   static constexpr int kAcc = kMats * NT;
   static constexpr int kScaleA = 4 * kTiles;
-  static constexpr int kScales =
-      kMats * kScaleA + 4 * kTiles * kRowTiles;
+  static constexpr int kScales = kMats * kScaleA + 4 * kRowTiles;
   static constexpr int kBuffers = 2 * kAcc + 2 * kScales <= 512 ? 2 : 1;
   static constexpr int kScaleAt = kBuffers * kAcc;
-  static_assert(kScaleAt + 2 * kScales <= 512, "tensor memory");
+  static constexpr int kFit = (512 - kScaleAt) / kScales;
+  static constexpr int kScaleBufs = kFit < kStages ? kFit : kStages;
+  static_assert(kScaleBufs >= 2, "tensor memory");
 
   static constexpr int shared_bytes(int chunks) {
     return 1024 + kStages * kStage + kBarBytes + 8 * chunks;
@@ -231,8 +267,7 @@ struct Gmm {
   __device__ static __forceinline__ bool wait_all(uint32_t bar, uint32_t phase,
                                                   volatile int* abort_flag,
                                                   int32_t* status) {
-    return __all_sync(0xffffffffu,
-                      tc::mbar_wait(bar, phase, abort_flag, status));
+    return __all_sync(0xffffffffu, wait(bar, phase, abort_flag, status));
   }
 
   __device__ static void run(const GmmArgs& a, const CUtensorMap* map) {
@@ -337,8 +372,7 @@ struct Gmm {
         if (a.stall_after_fills >= 0 && filled >= a.stall_after_fills)
           return false;
         if (filled >= ahead) {
-          if (!tc::mbar_wait(b.empty + 8 * ring.st, ring.phase, abort_flag,
-                             a.status))
+          if (!wait(b.empty + 8 * ring.st, ring.phase, abort_flag, a.status))
             return false;
           weights(it, s, ring.st);
         }
@@ -396,15 +430,13 @@ struct Gmm {
         if (!wait_all(b.empty + 8 * ring.st, ring.phase, abort_flag,
                       a.status))
           return false;
-        const uint32_t dst =
-            sb + ring.st * kStage + kXs + lane % kTiles * kScaleTile;
+        const uint32_t dst = sb + ring.st * kStage + kXs;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
           const int r = (i * 32 + lane) / kTiles;
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(
-                           dst + r / 128 * (kTiles * kScaleTile) +
-                           r % 32 * 16 + r % 128 / 32 * 4),
-                       "r"(v[i])
+          const uint32_t at = (r / 128 * kTiles + lane % kTiles) * kScaleTile +
+                              r % 32 * 16 + r % 128 / 32 * 4;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + at), "r"(v[i])
                        : "memory");
         }
         tc::fence_proxy_async_smem();
@@ -415,15 +447,17 @@ struct Gmm {
     });
   }
 
-  // ---- the matrix instructions
+  // ---- the matrix instructions.  The whole warp runs the loop and one lane
+  // issues: the operands then are uniform.
   __device__ static void multiply(const GmmArgs& a, uint32_t sb,
                                   const Bars& b, const int2* chunks,
                                   int n_items, int tiles, uint32_t tmem,
                                   int lane, volatile int* abort_flag) {
     const int stages = a.l.stages();
     const bool leader = lane == 0;
-    Ring ring, back1, back2;  // this stage and the two before it
-    int done = 0;             // stages so far, counted up to two
+    Ring ring;
+    Ring back;     // where the buffer's last reader stood
+    int lead = 0;  // stages issued, counted up to kScaleBufs
     int buf = 0, sbuf = 0;
     uint32_t acc_phase = 1;
     passes(a, chunks, n_items, tiles, [&](const Item& it) {
@@ -432,7 +466,6 @@ struct Gmm {
       const uint32_t d = tmem + buf * kAcc;
       if (!wait_all(b.acc_empty + 8 * buf, acc_phase, abort_flag, a.status))
         return false;
-      tc::tc_fence_after();
 #pragma unroll 1
       for (int s = 0; s < stages; ++s) {
         if (!wait_all(b.full + 8 * ring.st, ring.phase, abort_flag,
@@ -440,14 +473,28 @@ struct Gmm {
             !wait_all(b.scales + 8 * ring.st, ring.phase, abort_flag,
                       a.status))
           return false;
-        // the instructions that read these scales' buffer have completed
-        if (done == 2 && !wait_all(b.empty + 8 * back2.st, back2.phase,
-                                   abort_flag, a.status))
-          return false;
+        // The instructions that read this buffer of scales have completed:
+        // with a buffer a stage those are the ones that freed the stage.
+        if (kScaleBufs < kStages) {
+          if (lead == kScaleBufs) {
+            if (!wait_all(b.empty + 8 * back.st, back.phase, abort_flag,
+                          a.status))
+              return false;
+            back.next();
+          } else {
+            ++lead;
+          }
+        }
         tc::tc_fence_after();
         const uint32_t at = sb + ring.st * kStage;
-        const uint32_t sa = tmem + kScaleAt + sbuf * kScales;
+        const uint32_t sa =
+            tmem + kScaleAt +
+            (kScaleBufs < kStages ? sbuf : ring.st) * kScales;
         const uint32_t sx = sa + kMats * kScaleA;
+        const uint64_t ad = tc::smem_desc(at, 16, 1024);
+        const uint64_t bd = tc::smem_desc(at + kX, 16, 1024);
+        const uint64_t sd = scale_desc(at);
+        const int steps = (a.l.K - s * kStageK + 63) / 64;
         if (leader) {
 #pragma unroll
           for (int m = 0; m < kMats; ++m)
@@ -455,17 +502,14 @@ struct Gmm {
             for (int j = 0; j < kTiles; ++j)
               scales_to_tmem(
                   sa + m * kScaleA + 4 * j,
-                  scale_desc(at + m * kRec + kCodeBytes + j * kScaleTile));
+                  sd + ((m * kRec + kCodeBytes + j * kScaleTile) >> 4));
 #pragma unroll
-          for (int q = 0; q < kRowTiles; ++q)
-            if (q * 128 < n)
-#pragma unroll
-              for (int j = 0; j < kTiles; ++j)
-                scales_to_tmem(sx + (j * kRowTiles + q) * 4,
-                               scale_desc(at + kXs +
-                                          (q * kTiles + j) * kScaleTile));
-          const uint64_t bd = tc::smem_desc(at + kX, 16, 1024);
-          const int steps = (a.l.K - s * kStageK + 63) / 64;
+          for (int j = 0; j < kRowTiles; ++j)
+            if (j / kTiles * 128 < n)
+              // tiles of one block's rows lie side by side
+              scales_to_tmem(sx + (j % kTiles * (kRowTiles / kTiles) +
+                                   j / kTiles) * 4,
+                             sd + ((kXs + j * kScaleTile) >> 4));
 #pragma unroll
           for (int k = 0; k < kStageK / 64; ++k) {
             if (k >= steps) break;
@@ -475,19 +519,16 @@ struct Gmm {
                 BLOCK == 16 ? 0u : (k & 1) * (2u << 4 | 2u << 29);
 #pragma unroll
             for (int m = 0; m < kMats; ++m)
-              umma_mx<BLOCK>(d + m * NT,
-                             tc::smem_desc(at + m * kRec, 16, 1024) + 2 * k,
+              umma_mx<BLOCK>(d + m * NT, ad + ((m * kRec >> 4) + 2 * k),
                              bd + 2 * k, idesc | id,
                              sa + m * kScaleA + 4 * tile,
-                             sx + tile * kRowTiles * 4, s > 0 || k > 0);
+                             sx + tile * (kRowTiles / kTiles * 4),
+                             s > 0 || k > 0);
           }
           tc::umma_commit(b.empty + 8 * ring.st);
         }
         __syncwarp();
-        sbuf ^= 1;
-        back2 = back1;
-        back1 = ring;
-        if (done < 2) ++done;
+        sbuf = sbuf == kScaleBufs - 1 ? 0 : sbuf + 1;
         ring.next();
       }
       if (leader) tc::umma_commit(b.acc_full + 8 * buf);
@@ -566,21 +607,39 @@ struct Gmm {
   __device__ static __forceinline__ void write_h(
       const GmmArgs& a, const Item& it, int col0, int r, int lane, float t0,
       float t1, const uint32_t* g, const uint32_t* u) {
-    const uint32_t mask =
-        BLOCK == 32 ? 0xffffffffu : lane < 16 ? 0xffffu : 0xffff0000u;
     float q[8];
-    uint32_t byte = 0;  // the scale of row lane % 8
+    uint32_t most = 0;  // of row lane % 8, this lane's block
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float z = t0 * __uint_as_float(g[i]);
       // z / (1 + exp(-z)); exp(-z) may be infinite
       const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-      float h = z * s * (t1 * __uint_as_float(u[i]));
-      if (BLOCK == 16) h *= a.inv_out;
-      const Block blk = block_scale<BLOCK>(
-          __reduce_max_sync(mask, __float_as_uint(h) & 0x7fffffffu));
-      q[i] = over_scale<BLOCK>(h, blk);
-      if ((lane & 7) == i) byte = blk.byte;
+      q[i] = z * s * (t1 * __uint_as_float(u[i]));
+      if (BLOCK == 16) q[i] *= a.inv_out;
+      const uint32_t bits = __float_as_uint(q[i]) & 0x7fffffffu;
+      uint32_t m;
+      if (BLOCK == 32) {
+        m = __reduce_max_sync(0xffffffffu, bits);
+      } else {
+        // (halves apart by masks of their own would run one after the other
+        // behind a check of the masks, many times slower)
+        const uint32_t lo =
+            __reduce_max_sync(0xffffffffu, lane < 16 ? bits : 0u);
+        const uint32_t hi =
+            __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : bits);
+        m = lane < 16 ? lo : hi;
+      }
+      if ((lane & 7) == i) most = m;
+    }
+    // each scale once, then to its block's lanes
+    const Block own = block_scale<BLOCK>(most);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      Block b;
+      const int from = (lane & 16) + i;
+      b.inv = __shfl_sync(0xffffffffu, own.inv, from);
+      b.s = BLOCK == 16 ? __shfl_sync(0xffffffffu, own.s, from) : 0.0f;
+      q[i] = over_scale<BLOCK>(q[i], b);
     }
     // The codes of a column's eight rows are a word; words of eight rows by
     // eight columns turn within eight lanes, halves, then bytes, then fours.
@@ -599,7 +658,7 @@ struct Gmm {
     *reinterpret_cast<uint32_t*>(a.h_codes + row * (a.l.N / 2) + col / 2) = w;
     if ((lane & (BLOCK == 32 ? 24 : 8)) == 0)
       a.h_scales[row * scale_row(a.l.N, BLOCK) + col / BLOCK] =
-          static_cast<uint8_t>(byte);
+          static_cast<uint8_t>(own.byte);
   }
 };
 
@@ -609,15 +668,15 @@ __global__ void __launch_bounds__(kGmmThreads, 1)
   Gmm<DUAL, BLOCK, NT>::run(a, &map);
 }
 
-// Rows of codes [rows, K/2], 16 rows of 128 bytes at a time.
+// Rows of codes [rows, K/2], `box` rows of 128 bytes at a time.
 inline bool make_code_map(CUtensorMap* m, const void* base, int K,
-                          int64_t rows) {
+                          int64_t rows, int box_rows) {
   tc::EncodeTiled fn = tc::encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2),
                               static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
-  const cuuint32_t box[2] = {128, kRowBox};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -641,7 +700,8 @@ cudaError_t launch_one(GmmArgs a, const void* codes, cudaStream_t s) {
   constexpr auto kernel = gmm_mx_kernel<DUAL, BLOCK, NT>;
   if ((e = launch::allow_shared<kernel>(d)) != cudaSuccess) return e;
   CUtensorMap map;
-  if (!make_code_map(&map, codes, a.l.K, a.rows)) return cudaErrorInvalidValue;
+  if (!make_code_map(&map, codes, a.l.K, a.rows, Ker::kRowBox))
+    return cudaErrorInvalidValue;
   const long long items =
       static_cast<long long>(a.l.tiles_n()) * a.chunks;
   const unsigned grid =
