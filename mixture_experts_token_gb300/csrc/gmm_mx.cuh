@@ -14,12 +14,10 @@
 //   * a thread brings the weights' records by bulk copy and the rows' codes by
 //     TMA, 256 of k a stage (rows past the group's are other groups' or zeros;
 //     they reach only columns that are not written);
-//   * four warps, on every fourth stage each, bring the rows' scales into the
-//     order that tensor memory takes;
-//   * a warp copies a stage's scales to tensor memory and issues the matrix
-//     instructions; scales have a buffer for each stage there, or as many as
-//     fit, and one is written again when the instructions that read it have
-//     completed;
+//   * four warps, one for each quarter of the lanes of tensor memory, write a
+//     stage's scales there, those of the weights from shared memory and those
+//     of the rows from global memory;
+//   * a warp issues the matrix instructions;
 //   * four warps turn the sums into rows of the output, a thread a column,
 //     while the next item's sums go to the other accumulator.
 // Every wait is bounded; one that gives up raises MOE_DEV_TIMEOUT and the CTA
@@ -91,17 +89,40 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-// 32 rows of 16 bytes to four columns of all four quarters of the lanes.
-__device__ __forceinline__ void scales_to_tmem(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem),
-               "l"(desc)
-               : "memory");
+// Columns of this warp's quarter of the lanes, 8 or 16 at a time.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[N]) {
+  static_assert(N == 8 || N % 16 == 0, "columns of scales");
+  if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, "
+        "%6, %7, %8};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7])
+        : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+      asm volatile(
+          "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, "
+          "%6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at + i),
+          "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]),
+          "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7]),
+          "r"(r[i + 8]), "r"(r[i + 9]), "r"(r[i + 10]), "r"(r[i + 11]),
+          "r"(r[i + 12]), "r"(r[i + 13]), "r"(r[i + 14]), "r"(r[i + 15])
+          : "memory");
+  }
 }
-// The matrix of 32 rows of 16 bytes, eight rows to a core matrix: no swizzle.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
-         (static_cast<uint64_t>(16 >> 4) << 16) |
-         (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
 }
 // A bounded wait as tc::mbar_wait, but the clock is read only after many looks
 // in vain: reading it takes longer than most of these waits.
@@ -190,17 +211,15 @@ struct Gmm {
   static constexpr int kMats = DUAL ? 2 : 1;
   static constexpr int kTiles = scale_tiles(BLOCK);  // of 128 rows, a stage
   static constexpr int kRec = record_bytes(BLOCK);
-  // The rows' scales, tiles of 128 rows as the weights'.  (32 rows would fit
-  // the four columns of one tile, a column for each 64 of k; but the
-  // instruction wants its scales at a multiple of four columns.)
+  // Tiles of the rows' scales, as the weights'.  (32 rows would fit the four
+  // columns of one tile, a column for each 64 of k; but the instruction wants
+  // its scales at a multiple of four columns.)
   static constexpr int kRowTiles = (NT + 127) / 128 * kTiles;
   // Rows of one TMA copy: few where rows are few; where they are many, small
   // copies are what takes the time.
   static constexpr int kRowBox = NT <= 64 ? 16 : NT / 2;
-  static constexpr int kX = kMats * kRec;             // the rows' codes
-  static constexpr int kXs = kX + NT * 128;           // and scales
-  static constexpr int kStage =
-      (kXs + kRowTiles * kScaleTile + 1023) / 1024 * 1024;
+  static constexpr int kX = kMats * kRec;  // the rows' codes
+  static constexpr int kStage = kX + NT * 128;
   static constexpr int kRoom = kMaxShared - 1024 - kBarBytes - 8 * kMaxChunks;
   static constexpr int kStages =
       kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
@@ -208,10 +227,12 @@ struct Gmm {
   static_assert(kRec % 1024 == 0 && NT % 16 == 0 && kRowBox % 8 == 0,
                 "swizzled tiles aligned");
   // Tensor memory: accumulators [buffer][matrix][NT], then scales [buffer]
-  // of the weights [matrix][tile][4] and the rows [tile][4].
+  // of the weights [matrix][tile][4] and the rows [tile][4], both from a
+  // multiple of 16 columns.
   static constexpr int kAcc = kMats * NT;
   static constexpr int kScaleA = 4 * kTiles;
-  static constexpr int kScales = kMats * kScaleA + 4 * kRowTiles;
+  static constexpr int kScaleX = (kMats * kScaleA + 15) / 16 * 16;
+  static constexpr int kScales = kScaleX + (4 * kRowTiles + 15) / 16 * 16;
   static constexpr int kBuffers = 2 * kAcc + 2 * kScales <= 512 ? 2 : 1;
   static constexpr int kScaleAt = kBuffers * kAcc;
   static constexpr int kFit = (512 - kScaleAt) / kScales;
@@ -222,16 +243,17 @@ struct Gmm {
     return 1024 + kStages * kStage + kBarBytes + 8 * chunks;
   }
 
-  // A stage is full when its copies and its rows' scales are there.
+  // Scales have barriers of their own, one for each of their buffers.
   struct Bars {
     uint32_t full, scales, empty, acc_full, acc_empty, done;
   };
-  // Where a role stands: its item, and the ring's stage and phase.
+  // Where a role stands in a ring of N buffers.
+  template <int N = kStages>
   struct Ring {
     int st = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void next() {
-      if (++st == kStages) {
+      if (++st == N) {
         st = 0;
         phase ^= 1;
       }
@@ -282,7 +304,7 @@ struct Gmm {
     Bars b;
     b.full = sb + kStages * kStage;
     b.scales = b.full + 8 * kStages;
-    b.empty = b.scales + 8 * kStages;
+    b.empty = b.scales + 8 * kScaleBufs;
     b.acc_full = b.empty + 8 * kStages;
     b.acc_empty = b.acc_full + 8 * kBuffers;
     b.done = b.acc_empty + 8 * kBuffers;
@@ -290,9 +312,10 @@ struct Gmm {
       abort_word = 0;
       for (int i = 0; i < kStages; ++i) {
         tc::mbar_init(b.full + 8 * i, 1);
-        tc::mbar_init(b.scales + 8 * i, 1);
         tc::mbar_init(b.empty + 8 * i, 1);
       }
+      for (int i = 0; i < kScaleBufs; ++i)
+        tc::mbar_init(b.scales + 8 * i, kScaleWarps);
       for (int i = 0; i < kBuffers; ++i) {
         tc::mbar_init(b.acc_full + 8 * i, 1);
         tc::mbar_init(b.acc_empty + 8 * i, kEpiWarps);
@@ -321,7 +344,7 @@ struct Gmm {
     else if (warp == kMmaWarp)
       multiply(a, sb, b, chunks, n_items, tiles, tmem, lane, abort_flag);
     else
-      load_scales(a, sb, b, chunks, n_items, tiles, warp - kScaleWarp, lane,
+      load_scales(a, sb, b, chunks, n_items, tiles, tmem, warp & 3, lane,
                   abort_flag);
     __syncwarp();
     tc::tc_fence_before();
@@ -337,7 +360,7 @@ struct Gmm {
                               volatile int* abort_flag) {
     if (lane != 0) return;
     const int stages = a.l.stages();
-    Ring ring;
+    Ring<> ring;
     ring.phase = 1;
     long long filled = 0;
     const auto weights = [&](const Item& it, int s, int st) {
@@ -394,54 +417,113 @@ struct Gmm {
     }
   }
 
-  // ---- the rows' scales, a word of four at a time: every kScaleWarps-th
-  // stage is this warp's
+  // ---- scales to tensor memory.  The instruction reads them from every
+  // quarter of the lanes, so each of the four warps writes all of them to its
+  // own quarter.  (The tensor cores can copy them from shared memory to all
+  // quarters, but a copy of 512 bytes takes its turn among the matrix
+  // instructions: 45 clocks, beside 60 to 90 for one of those.)
   __device__ static void load_scales(const GmmArgs& a, uint32_t sb,
                                      const Bars& b, const int2* chunks,
-                                     int n_items, int tiles, int warp,
-                                     int lane, volatile int* abort_flag) {
-    constexpr int kWords = NT * kTiles / 32;
-    static_assert(NT * kTiles % 32 == 0, "whole words a lane");
+                                     int n_items, int tiles, uint32_t tmem,
+                                     int quarter, int lane,
+                                     volatile int* abort_flag) {
+    constexpr int kRows = (NT + 31) / 32;  // rows a lane
     const int stages = a.l.stages(), groups = a.l.K / BLOCK;
     const int sr = scale_row(a.l.K, BLOCK);
-    Ring ring;
-    ring.phase = 1;
-    int turn = 0;
+    const bool wide =
+        sr % (4 * kTiles) == 0 &&
+        (reinterpret_cast<uintptr_t>(a.x_scales) & (4 * kTiles - 1)) == 0;
+    const uint32_t out =
+        tmem + kScaleAt + (static_cast<uint32_t>(32 * quarter) << 16);
+    Ring<> ring, back;
+    Ring<kScaleBufs> sring;
+    int lead = 0;  // stages so far, counted up to kScaleBufs
+    // The words of rows lane, lane + 32, .. of a stage; zeros past the rows.
+    const auto load = [&](const Item& it, int s, uint32_t (&v)[kRows][kTiles]) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = i * 32 + lane;
+        const uint8_t* p = a.x_scales +
+                           static_cast<long long>(it.row + r) * sr +
+                           s * (4 * kTiles);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) v[i][j] = 0;
+        if (r >= it.rows) continue;
+        if (wide) {
+          if constexpr (kTiles == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p);
+            v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            v[i][0] = w.x, v[i][1] = w.y;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+            if ((s * kTiles + j) * 4 < groups)
+              v[i][j] = *reinterpret_cast<const uint32_t*>(p + 4 * j);
+        }
+      }
+      // what lies behind a row's last scale counts as zero
+      if (s == stages - 1 && groups % 4 != 0) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+          if ((s * kTiles + j) * 4 + 4 > groups) {
+            const int left = groups - (s * kTiles + j) * 4;
+            const uint32_t mask = left > 0 ? (1u << (8 * left)) - 1 : 0u;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) v[i][j] &= mask;
+          }
+      }
+    };
     launch::wait_for_previous();
     passes(a, chunks, n_items, tiles, [&](const Item& it) {
+      uint32_t next[kRows][kTiles];
+      load(it, 0, next);
 #pragma unroll 1
-      for (int s = 0; s < stages; ++s, ring.next()) {
-        const bool mine = turn == warp;
-        turn = turn == kScaleWarps - 1 ? 0 : turn + 1;
-        if (!mine) continue;
-        uint32_t v[kWords];
+      for (int s = 0; s < stages; ++s) {
+        // rows' columns: [tile][128 rows][4]
+        uint32_t x[kRowTiles * 4];
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          const int r = (i * 32 + lane) / kTiles;
-          const int at = (s * kTiles + lane % kTiles) * 4;
-          v[i] = 0;
-          if (r < it.rows && at < groups) {
-            v[i] = *reinterpret_cast<const uint32_t*>(
-                a.x_scales + static_cast<long long>(it.row + r) * sr + at);
-            // what lies behind the row's last scale counts as zero
-            if (groups - at < 4) v[i] &= (1u << (8 * (groups - at))) - 1;
-          }
-        }
-        if (!wait_all(b.empty + 8 * ring.st, ring.phase, abort_flag,
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+          for (int i = 0; i < kRowTiles / kTiles * 4; ++i)
+            x[j * (kRowTiles / kTiles * 4) + i] = i < kRows ? next[i][j] : 0u;
+        if (s + 1 < stages) load(it, s + 1, next);
+        if (!wait_all(b.full + 8 * ring.st, ring.phase, abort_flag,
                       a.status))
           return false;
-        const uint32_t dst = sb + ring.st * kStage + kXs;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          const int r = (i * 32 + lane) / kTiles;
-          const uint32_t at = (r / 128 * kTiles + lane % kTiles) * kScaleTile +
-                              r % 32 * 16 + r % 128 / 32 * 4;
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + at), "r"(v[i])
-                       : "memory");
+        // The instructions that read this buffer have completed: with one for
+        // each stage, before the stage was filled again.
+        if (kScaleBufs < kStages) {
+          if (lead == kScaleBufs) {
+            if (!wait_all(b.empty + 8 * back.st, back.phase, abort_flag,
+                          a.status))
+              return false;
+            back.next();
+          } else {
+            ++lead;
+          }
         }
-        tc::fence_proxy_async_smem();
+        uint32_t w[kMats * kScaleA];
+        const uint32_t from = sb + ring.st * kStage + kCodeBytes + lane * 16;
+#pragma unroll
+        for (int m = 0; m < kMats; ++m)
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j) {
+            const uint4 v = lds16(from + m * kRec + j * kScaleTile);
+            uint32_t* to = w + (m * kTiles + j) * 4;
+            to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+          }
+        tc::tc_fence_after();
+        tmem_st(out + sring.st * kScales, w);
+        tmem_st(out + sring.st * kScales + kScaleX, x);
+        tmem_st_wait();
+        tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(b.scales + 8 * ring.st);
+        if (lane == 0) tc::mbar_arrive(b.scales + 8 * sring.st);
+        ring.next();
+        sring.next();
       }
       return true;
     });
@@ -455,10 +537,9 @@ struct Gmm {
                                   int lane, volatile int* abort_flag) {
     const int stages = a.l.stages();
     const bool leader = lane == 0;
-    Ring ring;
-    Ring back;     // where the buffer's last reader stood
-    int lead = 0;  // stages issued, counted up to kScaleBufs
-    int buf = 0, sbuf = 0;
+    Ring<> ring;
+    Ring<kScaleBufs> sring;
+    int buf = 0;
     uint32_t acc_phase = 1;
     passes(a, chunks, n_items, tiles, [&](const Item& it) {
       const int n = (it.rows + 15) / 16 * 16;
@@ -470,46 +551,17 @@ struct Gmm {
       for (int s = 0; s < stages; ++s) {
         if (!wait_all(b.full + 8 * ring.st, ring.phase, abort_flag,
                       a.status) ||
-            !wait_all(b.scales + 8 * ring.st, ring.phase, abort_flag,
+            !wait_all(b.scales + 8 * sring.st, sring.phase, abort_flag,
                       a.status))
           return false;
-        // The instructions that read this buffer of scales have completed:
-        // with a buffer a stage those are the ones that freed the stage.
-        if (kScaleBufs < kStages) {
-          if (lead == kScaleBufs) {
-            if (!wait_all(b.empty + 8 * back.st, back.phase, abort_flag,
-                          a.status))
-              return false;
-            back.next();
-          } else {
-            ++lead;
-          }
-        }
         tc::tc_fence_after();
         const uint32_t at = sb + ring.st * kStage;
-        const uint32_t sa =
-            tmem + kScaleAt +
-            (kScaleBufs < kStages ? sbuf : ring.st) * kScales;
-        const uint32_t sx = sa + kMats * kScaleA;
+        const uint32_t sa = tmem + kScaleAt + sring.st * kScales;
+        const uint32_t sx = sa + kScaleX;
         const uint64_t ad = tc::smem_desc(at, 16, 1024);
         const uint64_t bd = tc::smem_desc(at + kX, 16, 1024);
-        const uint64_t sd = scale_desc(at);
         const int steps = (a.l.K - s * kStageK + 63) / 64;
         if (leader) {
-#pragma unroll
-          for (int m = 0; m < kMats; ++m)
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j)
-              scales_to_tmem(
-                  sa + m * kScaleA + 4 * j,
-                  sd + ((m * kRec + kCodeBytes + j * kScaleTile) >> 4));
-#pragma unroll
-          for (int j = 0; j < kRowTiles; ++j)
-            if (j / kTiles * 128 < n)
-              // tiles of one block's rows lie side by side
-              scales_to_tmem(sx + (j % kTiles * (kRowTiles / kTiles) +
-                                   j / kTiles) * 4,
-                             sd + ((kXs + j * kScaleTile) >> 4));
 #pragma unroll
           for (int k = 0; k < kStageK / 64; ++k) {
             if (k >= steps) break;
@@ -528,8 +580,8 @@ struct Gmm {
           tc::umma_commit(b.empty + 8 * ring.st);
         }
         __syncwarp();
-        sbuf = sbuf == kScaleBufs - 1 ? 0 : sbuf + 1;
         ring.next();
+        sring.next();
       }
       if (leader) tc::umma_commit(b.acc_full + 8 * buf);
       __syncwarp();
