@@ -1059,9 +1059,13 @@ moe_status_t moe_gmm_swiglu_w4(const moe_config_t *cfg, const moe_w4_t *opt,
  * gradient; these calls serve, and have no backward.
  *   codes    [rows, K/2] uint8      column 2i in the low four bits; 16-byte
  *                                   aligned
- *   scales   [rows, moe_mx_scale_row()] uint8, one for each block of a row in
- *                                   order, then up to three bytes that are
- *                                   written as 0 and not read; 4-byte aligned
+ *   scales   of weights: [rows, moe_mx_scale_row()] uint8, one for each block
+ *            of a row in order, then up to three bytes that are written as 0
+ *            and not read; 4-byte aligned.  Of the rows of x and h:
+ *            [ceil(K/256), rows, 256/block] uint8, those of 256 columns at a
+ *            time (moe_mx_row_scale_bytes() in all; behind a row's last one
+ *            they are written as 0 or not written, and not read); 16-byte
+ *            aligned
  *   packed   moe_mx_bytes() bytes   weight matrices as the products read them;
  *                                   16-byte aligned
  * K must be a multiple of 32, at most 2^20.
@@ -1073,9 +1077,11 @@ typedef struct {
   float x_scale, h_scale;
 } moe_mx_t;
 
-/* Bytes of a row of scales (a multiple of 4), and of n packed matrices
- * [K, N] (0 for an invalid argument; N <= 2^20). */
+/* Bytes of a row of a weight matrix's scales (a multiple of 4), of the scales
+ * of R rows, and of n packed matrices [K, N] (0 for an invalid argument;
+ * N <= 2^20). */
 int32_t moe_mx_scale_row(const moe_mx_t *opt, int32_t K);
+size_t moe_mx_row_scale_bytes(const moe_mx_t *opt, int32_t R, int32_t K);
 size_t moe_mx_bytes(const moe_mx_t *opt, int32_t n, int32_t K, int32_t N);
 
 /* moe_mx_quantize_rows -- codes and scales of x [R, K] dtype under the tensor
@@ -1119,7 +1125,7 @@ moe_status_t moe_mx_dequantize(const moe_mx_t *opt, int32_t n, int32_t K,
  * last group are left as they were.
  *   moe_gmm_gate_up_mx  rows of x quantised under x_scale; h is quantised
  *                       under h_scale from its float32 values, codes
- *                       [T*k, F/2] and scales [T*k, row]
+ *                       [T*k, F/2] and the rows' scales
  *   moe_gmm_down_mx     y_sorted [T*k, H] dtype, sums float32
  *   moe_gmm_swiglu_mx   x_sorted [T*k, H] dtype, quantised on the way;
  *                       workspace: moe_mx_workspace_bytes() bytes, 16-byte

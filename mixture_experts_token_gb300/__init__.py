@@ -230,6 +230,8 @@ def _declare(h):
     h.moe_mx_bytes.restype = c_size_t
     h.moe_mx_scale_row.argtypes = [mx, i32]
     h.moe_mx_scale_row.restype = c_int32
+    h.moe_mx_row_scale_bytes.argtypes = [mx, i32, i32]
+    h.moe_mx_row_scale_bytes.restype = c_size_t
     h.moe_mx_workspace_bytes.argtypes = [cfg, mx]
     h.moe_mx_workspace_bytes.restype = c_size_t
     h.moe_validate_config.argtypes = [cfg]
@@ -915,8 +917,13 @@ def moe_mx_bytes(mx, n, K, N) -> int:
 
 
 def moe_mx_scale_row(mx, K) -> int:
-    """Bytes of a row of scales."""
+    """Bytes of a row of a weight matrix's scales."""
     return int(lib().moe_mx_scale_row(mx, K))
+
+
+def moe_mx_row_scale_bytes(mx, R, K) -> int:
+    """Bytes of the scales of R rows."""
+    return int(lib().moe_mx_row_scale_bytes(mx, R, K))
 
 
 def moe_mx_workspace_bytes(cfg, mx) -> int:
@@ -1071,13 +1078,25 @@ def alloc_mx(mx, n, K, N, device="cuda"):
 
 
 def alloc_mx_rows(mx, R, K, device="cuda"):
-    """Codes [R, K/2] and scales [R, row] of R quantised rows."""
+    """Codes [R, K/2] and scales [ceil(K/256), R, 256/block] of R quantised
+    rows.  (Both hold those of weight matrices, R = n * N, too.)"""
+    import torch
+    if moe_mx_scale_row(mx, K) == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_mx_scale_row")
+    u8 = dict(dtype=torch.uint8, device=device)
+    return (torch.empty((R, K // 2), **u8),
+            torch.empty((-(-K // 256), R, 256 // mx.block), **u8))
+
+
+def alloc_mx_codes(mx, n, K, N, device="cuda"):
+    """Codes [n, N, K/2] and scales [n, N, row] of n weight matrices."""
     import torch
     row = moe_mx_scale_row(mx, K)
     if row == 0:
         raise MoeError(MOE_ERR_INVALID_ARG, "moe_mx_scale_row")
-    return (torch.empty((R, K // 2), dtype=torch.uint8, device=device),
-            torch.empty((R, row), dtype=torch.uint8, device=device))
+    u8 = dict(dtype=torch.uint8, device=device)
+    return (torch.empty((n, N, K // 2), **u8),
+            torch.empty((n, N, row), **u8))
 
 
 def mx_workspace(cfg, mx, device="cuda"):

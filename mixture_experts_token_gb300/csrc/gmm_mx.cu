@@ -90,9 +90,9 @@ Workspace carve(void* base, const moe_config_t& c, const moe_mx_t& o,
   Workspace w;
   const size_t rows = static_cast<size_t>(c.T) * c.k;
   w.x_codes = cv.take<uint8_t>(rows * (c.H / 2));
-  w.x_scales = cv.take<uint8_t>(rows * scale_row(c.H, o.block));
+  w.x_scales = cv.take<uint8_t>(row_scale_bytes(o.block, rows, c.H));
   w.h_codes = cv.take<uint8_t>(rows * (c.F / 2));
-  w.h_scales = cv.take<uint8_t>(rows * scale_row(c.F, o.block));
+  w.h_scales = cv.take<uint8_t>(row_scale_bytes(o.block, rows, c.F));
   *bytes = cv.off;
   return w;
 }
@@ -122,11 +122,11 @@ moe_status_t moe_gmm_gate_up_mx(
   Groups g;
   const moe_status_t st = check(cfg, opt, n_groups, group_expert, &g);
   if (st != MOE_OK || cfg->T == 0) return st;
-  if (!ok_ptr(x_codes, true) || !ok_ptr(x_scales, false) ||
+  if (!ok_ptr(x_codes, true) || !ok_ptr(x_scales, true) ||
       !ok_ptr(group_offsets, false) || !ok_ptr(w_gate, true) ||
       !ok_ptr(w_up, true) || !scales_ok(*opt, gate_scale) ||
       !scales_ok(*opt, up_scale) || !ok_ptr(h_codes, true) ||
-      !ok_ptr(h_scales, false))
+      !ok_ptr(h_scales, true))
     return MOE_ERR_INVALID_ARG;
   return status_of(gate_up(*cfg, *opt, g, x_codes, x_scales, group_offsets,
                            w_gate, w_up, gate_scale, up_scale, h_codes,
@@ -142,7 +142,7 @@ moe_status_t moe_gmm_down_mx(const moe_config_t* cfg, const moe_mx_t* opt,
   Groups g;
   const moe_status_t st = check(cfg, opt, n_groups, group_expert, &g);
   if (st != MOE_OK || cfg->T == 0) return st;
-  if (!ok_ptr(h_codes, true) || !ok_ptr(h_scales, false) ||
+  if (!ok_ptr(h_codes, true) || !ok_ptr(h_scales, true) ||
       !ok_ptr(group_offsets, false) || !ok_ptr(w_down, true) ||
       !scales_ok(*opt, down_scale) || !ok_ptr(y_sorted, true))
     return MOE_ERR_INVALID_ARG;

@@ -429,10 +429,6 @@ struct Gmm {
                                      volatile int* abort_flag) {
     constexpr int kRows = (NT + 31) / 32;  // rows a lane
     const int stages = a.l.stages(), groups = a.l.K / BLOCK;
-    const int sr = scale_row(a.l.K, BLOCK);
-    const bool wide =
-        sr % (4 * kTiles) == 0 &&
-        (reinterpret_cast<uintptr_t>(a.x_scales) & (4 * kTiles - 1)) == 0;
     const uint32_t out =
         tmem + kScaleAt + (static_cast<uint32_t>(32 * quarter) << 16);
     Ring<> ring, back;
@@ -443,37 +439,31 @@ struct Gmm {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = i * 32 + lane;
-        const uint8_t* p = a.x_scales +
-                           static_cast<long long>(it.row + r) * sr +
-                           s * (4 * kTiles);
+        const uint8_t* p =
+            a.x_scales + (static_cast<long long>(s) * a.rows + it.row + r) *
+                             (4 * kTiles);
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) v[i][j] = 0;
         if (r >= it.rows) continue;
-        if (wide) {
-          if constexpr (kTiles == 4) {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
-            v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(p);
-            v[i][0] = w.x, v[i][1] = w.y;
-          }
+        if constexpr (kTiles == 4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(p);
+          v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
         } else {
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j)
-            if ((s * kTiles + j) * 4 < groups)
-              v[i][j] = *reinterpret_cast<const uint32_t*>(p + 4 * j);
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          v[i][0] = w.x, v[i][1] = w.y;
         }
       }
       // what lies behind a row's last scale counts as zero
-      if (s == stages - 1 && groups % 4 != 0) {
+      if (s == stages - 1 && groups % (4 * kTiles) != 0) {
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-          if ((s * kTiles + j) * 4 + 4 > groups) {
-            const int left = groups - (s * kTiles + j) * 4;
+        for (int j = 0; j < kTiles; ++j) {
+          const int left = groups - (s * kTiles + j) * 4;
+          if (left < 4) {
             const uint32_t mask = left > 0 ? (1u << (8 * left)) - 1 : 0u;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) v[i][j] &= mask;
           }
+        }
       }
     };
     launch::wait_for_previous();
@@ -709,7 +699,7 @@ struct Gmm {
     const int col = col0 + (lane & 24);
     *reinterpret_cast<uint32_t*>(a.h_codes + row * (a.l.N / 2) + col / 2) = w;
     if ((lane & (BLOCK == 32 ? 24 : 8)) == 0)
-      a.h_scales[row * scale_row(a.l.N, BLOCK) + col / BLOCK] =
+      a.h_scales[row_scale_at(BLOCK, a.rows, row, col / BLOCK)] =
           static_cast<uint8_t>(own.byte);
   }
 };

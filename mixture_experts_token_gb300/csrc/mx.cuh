@@ -6,7 +6,10 @@
 // biased exponent in a byte, 255 for NaN), blocks of 16 a number of 4 exponent
 // and 3 mantissa bits (0x7f for NaN) under a float32 scale of the tensor.
 // Rows of codes: K/2 bytes, column 2i in the low four bits of byte i; rows of
-// scales: scale_row() bytes, one a block, zeros behind the last.
+// scales of a weight matrix: scale_row() bytes, one a block, zeros behind the
+// last.  The scales of the products' rows lie by 256 of K: for each of those,
+// for each row, its 256 / block, so that what a product wants of 32 rows at a
+// time lies together.
 //
 // A packed matrix [K, N] is, for each tile of 128 columns, one record after
 // another, a record for each 256 of K:
@@ -42,6 +45,17 @@ __host__ __device__ constexpr int record_bytes(int block) {
 }
 __host__ __device__ inline int scale_row(int K, int block) {
   return (K / block + 3) / 4 * 4;
+}
+
+// Where the scale of block `at` of a row is, of R rows.
+__host__ __device__ inline long long row_scale_at(int block, long long R,
+                                                  long long row, int at) {
+  const int per = kStageK / block;
+  return (at / per * R + row) * per + at % per;
+}
+__host__ __device__ inline long long row_scale_bytes(int block, long long R,
+                                                     int K) {
+  return (K + kStageK - 1) / kStageK * R * (kStageK / block);
 }
 
 struct Layout {

@@ -97,13 +97,13 @@ struct Place {
 // A block is two or four lanes.
 template <int BLOCK, typename T>
 __global__ void __launch_bounds__(kThreads)
-    quantize_rows_kernel(const T* __restrict__ x, long long pieces, int K,
-                         float r, uint8_t* __restrict__ codes,
+    quantize_rows_kernel(const T* __restrict__ x, int R, int K, float r,
+                         uint8_t* __restrict__ codes,
                          uint8_t* __restrict__ scales) {
   constexpr int kLanes = BLOCK / 8;
   launch::wait_for_previous();
   launch::let_next_start();
-  const int sr = scale_row(K, BLOCK);
+  const long long pieces = static_cast<long long>(R) * (K / 8);
   const long long first =
       blockIdx.x * static_cast<long long>(kPieces * kThreads);
   const bool all = first + kPieces * kThreads <= pieces;
@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(kThreads)
       reinterpret_cast<uint32_t*>(codes)[i] = c;
       if (threadIdx.x % kLanes == 0) {
         const int at = static_cast<int>(place.at) / kLanes;
-        uint8_t* s = scales + place.row * sr;
-        s[at] = static_cast<uint8_t>(b.byte);
-        if (at == K / BLOCK - 1)
-          for (int j = at + 1; j < sr; ++j) s[j] = 0;
+        uint8_t* s = scales + row_scale_at(BLOCK, R, place.row, at);
+        *s = static_cast<uint8_t>(b.byte);
+        if (at == K / BLOCK - 1)  // zeros to the end of the 256
+          for (int j = at + 1; j % (kStageK / BLOCK) != 0; ++j) *++s = 0;
       }
     }
     place.next();
@@ -148,10 +148,9 @@ __global__ void __launch_bounds__(kThreads)
 template <int BLOCK, typename T>
 __global__ void __launch_bounds__(kThreads)
     dequantize_rows_kernel(const uint8_t* __restrict__ codes,
-                           const uint8_t* __restrict__ scales,
-                           long long pieces, int K, float scale,
-                           T* __restrict__ x) {
-  const int sr = scale_row(K, BLOCK);
+                           const uint8_t* __restrict__ scales, int R, int K,
+                           float scale, T* __restrict__ x) {
+  const long long pieces = static_cast<long long>(R) * (K / 8);
   const long long first =
       blockIdx.x * static_cast<long long>(kPieces * kThreads);
   Place place(first, K / 8);
@@ -161,7 +160,8 @@ __global__ void __launch_bounds__(kThreads)
     const long long i = first + p * kThreads + threadIdx.x;
     if (i < pieces) {
       c[p] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-      byte[p] = __ldg(scales + place.row * sr + place.at / (BLOCK / 8));
+      byte[p] = __ldg(scales + row_scale_at(BLOCK, R, place.row,
+                                            place.at / (BLOCK / 8)));
     }
     place.next();
   }
@@ -480,7 +480,7 @@ cudaError_t launch_mx_rows(int block, int R, int K, moe_dtype_t dtype,
   const unsigned grid = row_grid(pieces);
 #define MOE_MX_ROWS(B, T)                                                   \
   return launch::overlapping(quantize_rows_kernel<B, T>, grid, kThreads, 0, \
-                             s, static_cast<const T*>(x), pieces, K, r,     \
+                             s, static_cast<const T*>(x), R, K, r,          \
                              codes, scales)
   if (block == 16) {
     if (dtype == MOE_F32) MOE_MX_ROWS(16, float);
@@ -511,6 +511,11 @@ size_t moe_mx_bytes(const moe_mx_t* opt, int32_t n, int32_t K, int32_t N) {
   return static_cast<size_t>(Layout{K, N, opt->block}.matrix()) * n;
 }
 
+size_t moe_mx_row_scale_bytes(const moe_mx_t* opt, int32_t R, int32_t K) {
+  if (!mx::options_ok(opt) || !rows_ok(R, K)) return 0;
+  return static_cast<size_t>(row_scale_bytes(opt->block, R, K));
+}
+
 int32_t moe_mx_scale_row(const moe_mx_t* opt, int32_t K) {
   return mx::options_ok(opt) && length_ok(K) ? scale_row(K, opt->block) : 0;
 }
@@ -523,7 +528,7 @@ moe_status_t moe_mx_quantize_rows(const moe_mx_t* opt, int32_t R, int32_t K,
       !scale_ok(opt->block, scale))
     return MOE_ERR_INVALID_ARG;
   if (R == 0) return MOE_OK;
-  if (!ok_ptr(x, true) || !ok_ptr(codes, true) || !ok_ptr(scales, false))
+  if (!ok_ptr(x, true) || !ok_ptr(codes, true) || !ok_ptr(scales, true))
     return MOE_ERR_INVALID_ARG;
   if (!grid_ok(static_cast<long long>(R) * (K / 8)))
     return MOE_ERR_UNSUPPORTED;
@@ -540,13 +545,13 @@ moe_status_t moe_mx_dequantize_rows(const moe_mx_t* opt, int32_t R, int32_t K,
       !scale_ok(opt->block, scale))
     return MOE_ERR_INVALID_ARG;
   if (R == 0) return MOE_OK;
-  if (!ok_ptr(codes, true) || !ok_ptr(scales, false) || !ok_ptr(x, true))
+  if (!ok_ptr(codes, true) || !ok_ptr(scales, true) || !ok_ptr(x, true))
     return MOE_ERR_INVALID_ARG;
   const long long pieces = static_cast<long long>(R) * (K / 8);
   if (!grid_ok(pieces)) return MOE_ERR_UNSUPPORTED;
 #define MOE_MX_ROWS(B, T)                                             \
   dequantize_rows_kernel<B, T><<<row_grid(pieces), kThreads, 0, stream>>>( \
-      codes, scales, pieces, K, scale, static_cast<T*>(x))
+      codes, scales, R, K, scale, static_cast<T*>(x))
   if (opt->block == 16) {
     if (dtype == MOE_F32)
       MOE_MX_ROWS(16, float);

@@ -425,6 +425,9 @@ def test_mx_sizes_and_arguments(m):
     assert rows(M, 2, 48, 0, p, one, p, p) == bad
     assert rows(M, 2, 64, 0, p, ctypes.c_float(0.5), p, p) == bad
     assert rows(V, 2, 64, 0, p, ctypes.c_float(0.0), p, p) == bad
+    assert m.moe_mx_row_scale_bytes(mx, 3, 288) == 2 * 3 * 8
+    assert m.moe_mx_row_scale_bytes(nv, 3, 256) == 3 * 16
+    assert m.moe_mx_row_scale_bytes(nv, 3, 40) == 0
     for a in ((None, p, p), (p, None, p), (p, p, None), (off, p, p),
               (p, off, p), (p, p, odd)):
         assert rows(M, 2, 64, 0, a[0], one, a[1], a[2]) == bad, a
@@ -447,6 +450,7 @@ def test_mx_sizes_and_arguments(m):
     up = lambda C, o, n, e, *a: lib.moe_gmm_gate_up_mx(  # noqa: E731
         C, o, n, e, *a, None, None)
     good = [p, p, p, p, p, None, None, p, p]
+    assert rows(M, 2, 64, 0, p, one, p, off) == bad
     assert up(C, None, 0, None, *good) == bad
     assert up(C, M, 3, None, *good) == bad         # groups without a map
     assert up(C, M, 1025, p, *good) == bad

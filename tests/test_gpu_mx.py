@@ -34,6 +34,12 @@ def make(block, x_scale=0.011, h_scale=0.013):
                                 (1.0, 1.0)))
 
 
+def by_row(scales):
+    """Scales [steps, R, 256/block] of rows as [R, ..] in their order."""
+    s = np8(scales).transpose(1, 0, 2)
+    return s.reshape(s.shape[0], -1)
+
+
 def hard_rows(R, K, dtype, seed, unit=1.0):
     """Rows of unlike sizes, with ties (multiples of a quarter of a power of
     two), zeros, extremes and blocks of one value."""
@@ -64,10 +70,13 @@ def test_rows_bit_for_bit(R, K, block, dtype, scale):
     mx = make(block)
     x = hard_rows(R, K, DT[dtype], R + K, scale)
     codes, scales = moe.alloc_mx_rows(mx, R, K)
+    assert scales.numel() == moe.moe_mx_row_scale_bytes(mx, R, K)
     scales.fill_(0xAB)
     moe.moe_mx_quantize_rows(mx, R, K, x.cuda(), scale, codes, scales)
     want, ws = ref.quantize_rows(x.float().numpy(), block, scale)
-    assert np.array_equal(np8(scales), ws)
+    got = by_row(scales)
+    assert np.array_equal(got[:, :K // block], ws[:, :K // block])
+    assert not got[:, K // block:].any()
     nan = 255 if block == 32 else 127
     fine = np.repeat(ws[:, :K // block] != nan, block // 2, 1)
     assert np.array_equal(np8(codes)[fine], want[fine])
@@ -90,7 +99,7 @@ def matrices(n, K, N, block, dtype="f32", seed=0, std=0.02):
     scale = None
     if block == 16:
         scale = (w.float().abs().amax((1, 2)) / (448 * 6)).cuda()
-    codes, scales = moe.alloc_mx_rows(mx, n * N, K)
+    codes, scales = moe.alloc_mx_codes(mx, n, K, N)
     scales.fill_(0xAB)
     moe.moe_mx_quantize(mx, n, K, N, w.cuda(), scale, codes, scales)
     packed = moe.alloc_mx(mx, n, K, N)
@@ -98,10 +107,9 @@ def matrices(n, K, N, block, dtype="f32", seed=0, std=0.02):
     moe.moe_mx_pack(mx, n, K, N, codes, scales, packed)
     values = np.empty((n, K, N))
     for e in range(n):
-        rows = slice(e * N, (e + 1) * N)
         t = 1.0 if scale is None else float(scale[e])
-        values[e] = ref.dequantize_rows(np8(codes)[rows], np8(scales)[rows],
-                                        block, t).T
+        values[e] = ref.dequantize_rows(np8(codes[e]), np8(scales[e]), block,
+                                        t).T
     return packed, scale, values, (w, codes, scales)
 
 
@@ -117,8 +125,8 @@ def test_weights_bit_for_bit(n, K, N, block, dtype):
         rows = w[e].float().T.contiguous().numpy()
         want, ws = ref.quantize_rows(
             rows, block, 1.0 if scale is None else float(scale[e]))
-        assert np.array_equal(np8(scales)[e * N:(e + 1) * N], ws)
-        assert np.array_equal(np8(codes)[e * N:(e + 1) * N], want)
+        assert np.array_equal(np8(scales[e]), ws)
+        assert np.array_equal(np8(codes[e]), want)
     for out in (torch.float32, torch.bfloat16):
         v = torch.empty((n, K, N), dtype=out, device="cuda")
         moe.moe_mx_dequantize(mx, n, K, N, packed, scale, v)
@@ -131,7 +139,7 @@ def test_weights_of_a_checkpoint():
     mx, n, K, N = make(32), 1, 160, 8
     packed, _, values, (w, codes, scales) = matrices(n, K, N, 32)
     again = moe.alloc_mx(mx, n, K, N)
-    scales[:, 5:] = 255
+    scales[:, :, 5:] = 255
     moe.moe_mx_pack(mx, n, K, N, codes, scales, again)
     assert torch.equal(again, packed)
 
@@ -198,10 +206,10 @@ class Case:
 
     def check(self, xq, hq, y, experts=None, off=None):
         mx, off = self.mx, off or self.off
-        x = ref.dequantize_rows(np8(xq[0]), np8(xq[1]), self.block,
+        hs = by_row(hq[1])
+        x = ref.dequantize_rows(np8(xq[0]), by_row(xq[1]), self.block,
                                 mx.x_scale)
-        h = ref.dequantize_rows(np8(hq[0]), np8(hq[1]), self.block,
-                                mx.h_scale)
+        h = ref.dequantize_rows(np8(hq[0]), hs, self.block, mx.h_scale)
         wg, wu, wd = self.w
         for i, e in enumerate(experts or range(len(off) - 1)):
             a, z = off[i], off[i + 1]
@@ -213,7 +221,7 @@ class Case:
             s = ref.silu(g)
             tol = (1.1 * eg + 8 * 2.0 ** -23 * np.abs(s)) \
                 * (np.abs(u) + eu) + np.abs(s) * eu + 1e-30
-            self.check_h(h[a:z], np8(hq[1])[a:z], s * u, tol)
+            self.check_h(h[a:z], hs[a:z], s * u, tol)
             m = np.abs(h[a:z]) @ np.abs(wd[e])
             close(y[a:z], h[a:z] @ wd[e], REL * m + 1e-30, ("y", i))
 
@@ -304,7 +312,7 @@ def test_rows_past_the_end_and_empty_call(block):
     xq, hq, y = c.steps()
     c.check(xq, hq, y)
     assert (y[7:] == 7).all()
-    assert (hq[0][7:] == 0x77).all() and (hq[1][7:] == 0x77).all()
+    assert (hq[0][7:] == 0x77).all() and (hq[1][:, 7:] == 0x77).all()
     assert torch.equal(c.whole(), y)
     c.offsets = torch.zeros_like(c.offsets)
     assert (c.whole() == 7).all()
