@@ -56,7 +56,8 @@ struct GmmArgs {
   int n_experts, n_groups, rows, chunk, chunks;
   int tokens;  // routing gives a group at most one row of each
   bool f32;    // y's type
-  bool early;  // may start before the kernel that writes the rows has ended
+  bool early;  // may read all but the rows before the kernel that writes those
+               // has ended
   long long stall_after_fills;  // tests of the timeout path only (-1: off)
 };
 
@@ -328,6 +329,10 @@ struct Gmm {
       tc::tmem_alloc(tc::smem_u32(&tmem_word), tc::kTmemCols);
       tc::tmem_relinquish();
     }
+    // Offsets and weights were final before the kernel that writes the rows
+    // began, where this one may start early; else nothing is read before all
+    // kernels before it have ended.
+    if (!a.early) launch::wait_for_previous();
     int2* chunks =
         reinterpret_cast<int2*>(base + kStages * kStage + kBarBytes);
     const int n_chunks = find_chunks<kWarps>(a, chunks);  // barriers within
@@ -749,10 +754,7 @@ cudaError_t launch_one(GmmArgs a, const void* codes, cudaStream_t s) {
   const unsigned grid =
       static_cast<unsigned>(std::min<long long>(items, d.sms));
   const int bytes = Ker::shared_bytes(a.chunks);
-  if (a.early)
-    return launch::overlapping(kernel, grid, kGmmThreads, bytes, s, a, map);
-  kernel<<<grid, kGmmThreads, bytes, s>>>(a, map);
-  return cudaGetLastError();
+  return launch::overlapping(kernel, grid, kGmmThreads, bytes, s, a, map);
 }
 
 }  // namespace mx

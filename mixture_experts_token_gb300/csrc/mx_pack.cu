@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(kThreads)
     dequantize_rows_kernel(const uint8_t* __restrict__ codes,
                            const uint8_t* __restrict__ scales, int R, int K,
                            float scale, T* __restrict__ x) {
+  launch::wait_for_previous();
+  launch::let_next_start();
   const long long pieces = static_cast<long long>(R) * (K / 8);
   const long long first =
       blockIdx.x * static_cast<long long>(kPieces * kThreads);
@@ -549,9 +551,11 @@ moe_status_t moe_mx_dequantize_rows(const moe_mx_t* opt, int32_t R, int32_t K,
     return MOE_ERR_INVALID_ARG;
   const long long pieces = static_cast<long long>(R) * (K / 8);
   if (!grid_ok(pieces)) return MOE_ERR_UNSUPPORTED;
+  cudaError_t e;
 #define MOE_MX_ROWS(B, T)                                             \
-  dequantize_rows_kernel<B, T><<<row_grid(pieces), kThreads, 0, stream>>>( \
-      codes, scales, R, K, scale, static_cast<T*>(x))
+  e = launch::overlapping(dequantize_rows_kernel<B, T>, row_grid(pieces), \
+                          kThreads, 0, stream, codes, scales, R, K, scale, \
+                          static_cast<T*>(x))
   if (opt->block == 16) {
     if (dtype == MOE_F32)
       MOE_MX_ROWS(16, float);
@@ -563,7 +567,7 @@ moe_status_t moe_mx_dequantize_rows(const moe_mx_t* opt, int32_t R, int32_t K,
     MOE_MX_ROWS(32, __nv_bfloat16);
   }
 #undef MOE_MX_ROWS
-  return launched();
+  return status_of(e);
 }
 
 moe_status_t moe_mx_quantize(const moe_mx_t* opt, int32_t n, int32_t K,

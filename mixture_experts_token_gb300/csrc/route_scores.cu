@@ -93,21 +93,30 @@ __device__ __forceinline__ float exp_near(float x) {
 __device__ __forceinline__ float weight(const Args& a, bool chosen, float l,
                                         float m, float z) {
   chosen = chosen && fabsf(l) <= FLT_MAX;
-  const float top = a.renorm ? warp_max(chosen ? l : -FLT_MAX) : m;
   float s = 0.0f;
-  if (chosen) {
-    if (!a.sigmoid) {
+  if (a.sigmoid && (!a.renorm || __any_sync(kAll, chosen && l > -60.0f))) {
+    const float x = exp_near(fmaxf(-fabsf(l), -87.0f));
+    if (chosen) s = (l < 0.0f ? x : 1.0f) * rcp_fast(1.0f + x);
+  } else {
+    const float top = a.renorm ? warp_max(chosen ? l : -FLT_MAX) : m;
+    if (chosen) {
       s = expf(l - top);
-      if (!a.renorm) s /= z;
-    } else if (a.renorm && top < -60.0f) {
-      s = expf(l - top) / (1.0f + expf(l));
-    } else {
-      const float x = exp_near(fmaxf(-fabsf(l), -87.0f));
-      s = (l < 0.0f ? x : 1.0f) * rcp_fast(1.0f + x);
+      if (a.sigmoid)
+        s /= 1.0f + expf(l);
+      else if (!a.renorm)
+        s /= z;
     }
   }
   if (a.renorm) {
-    const float sum = warp_sum(s);
+    // lanes past the k-th have nothing
+    float sum = s;
+    if (a.k > 8) {
+      sum += __shfl_xor_sync(kAll, sum, 16);
+      sum += __shfl_xor_sync(kAll, sum, 8);
+    }
+    sum += __shfl_xor_sync(kAll, sum, 4);
+    sum += __shfl_xor_sync(kAll, sum, 2);
+    sum += __shfl_xor_sync(kAll, sum, 1);
     s = sum > 0.0f ? __fdividef(s, sum) : 0.0f;
   }
   return a.scale * s;
@@ -386,6 +395,8 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
   const int e0 = lane * EPL;
   const bool wide = EPL % 4 == 0 && (FULL || a.E % 4 == 0) &&
                     (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
+  launch::wait_for_previous();
+  launch::let_next_start();
   float bias[EPL], most_bias = 0.0f;
   if (RANK != kByLogit) {
 #pragma unroll
@@ -464,8 +475,9 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
       const float group_err = a.group_top * (a.group_top + 1) * err;
       if (whole) {
         float g1 = m1, g2 = m2;
-#pragma unroll 1
-        for (int o = 1; o < lanes; o <<= 1) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          if (o >= lanes) break;
           const float o1 = __shfl_xor_sync(kAll, g1, o);
           const float o2 = __shfl_xor_sync(kAll, g2, o);
           g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
                          : 0u;
         kept = false;
         uint32_t last = 0;
-#pragma unroll 1
+#pragma unroll 4
         for (int g = 0; g < a.top_groups; ++g) {
           last = __reduce_max_sync(kAll, o);
           if (o == last) {
@@ -664,23 +676,38 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
     for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
   };
-  for (long long t0 = (blockIdx.x * static_cast<long long>(kWarps) + warp) *
-                      kTokens;
-       t0 < a.T; t0 += gridDim.x * static_cast<long long>(kWarps) * kTokens) {
+  launch::wait_for_previous();
+  launch::let_next_start();
+  const long long step =
+      gridDim.x * static_cast<long long>(kWarps) * kTokens;
+  long long t0 = (blockIdx.x * static_cast<long long>(kWarps) + warp) *
+                 kTokens;
+  // An expert of no lane's choice, and no other lane's, where there is none.
+  const auto choice = [&](long long first, int* e, float* d) {
+    *e = -1 - lane;
+    *d = 0.0f;
+    const long long t = first + tok;
+    if (t < a.T && j < a.k) {
+      const int i = __ldg(a.idx + t * a.k + j);
+      *d = __ldg(a.dw + t * a.k + j);
+      if (i >= 0 && i < a.E) *e = i;
+    }
+  };
+  const auto logit = [&](long long first, int e) {
+    return e >= 0 ? __ldg(a.logits + (first + tok) * a.E + e) : 0.0f;
+  };
+  // the next tokens' choices and their logits come while these are worked on
+  int next_e;
+  float next_d, next_l;
+  choice(t0, &next_e, &next_d);
+  next_l = logit(t0, next_e);
+  for (; t0 < a.T; t0 += step) {
     const long long t = t0 + tok;
     const int here = static_cast<int>(min(static_cast<long long>(kTokens),
                                           a.T - t0));
-    const bool on = tok < here && j < a.k;
-    int e = -1 - lane;  // of no expert, and no other lane's
-    float l = 0.0f, d = 0.0f;
-    if (on) {
-      const int i = __ldg(a.idx + t * a.k + j);
-      d = __ldg(a.dw + t * a.k + j);
-      if (i >= 0 && i < a.E) {
-        e = i;
-        l = __ldg(a.logits + t * a.E + e);
-      }
-    }
+    const int e = next_e;
+    const float l = next_l, d = next_d;
+    choice(t0 + step, &next_e, &next_d);
     float m = 0.0f, z = 1.0f;
     if (SIGMOID) {
       // zeros now, while the chosen logits come
@@ -713,6 +740,7 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
         }
       }
     }
+    next_l = logit(t0 + step, next_e);
     const bool finite = e >= 0 && fabsf(l) <= FLT_MAX;
     // the weight over scale, as the forward has it
     float top = finite ? l : -FLT_MAX;
@@ -779,21 +807,27 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
   }
 }
 
+template <bool SIGMOID, int LANES>
+cudaError_t launch_backward_of(const BackArgs& a, cudaStream_t s) {
+  constexpr auto kernel = scores_backward_kernel<SIGMOID, LANES>;
+  constexpr int kTokens = kWarps * 32 / LANES;  // of a CTA
+  launch::Device d;
+  int per_sm = 1;
+  cudaError_t e = launch::device(&d);
+  if (e == cudaSuccess)
+    e = launch::ctas_per_sm<kernel>(d, kThreads, 0, &per_sm);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(
+      (static_cast<long long>(a.T) + kTokens - 1) / kTokens,
+      static_cast<long long>(per_sm) * d.sms));
+  return launch::overlapping(kernel, grid, kThreads, 0, s, a);
+}
 template <bool SIGMOID>
 cudaError_t launch_backward(const BackArgs& a, cudaStream_t s) {
-  const int lanes = a.k <= 4 ? 4 : a.k <= 8 ? 8 : a.k <= 16 ? 16 : 32;
-  const int tokens = kWarps * 32 / lanes;  // of a CTA
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(
-      (static_cast<long long>(a.T) + tokens - 1) / tokens, 1 << 20));
-  if (lanes == 4)
-    scores_backward_kernel<SIGMOID, 4><<<grid, kThreads, 0, s>>>(a);
-  else if (lanes == 8)
-    scores_backward_kernel<SIGMOID, 8><<<grid, kThreads, 0, s>>>(a);
-  else if (lanes == 16)
-    scores_backward_kernel<SIGMOID, 16><<<grid, kThreads, 0, s>>>(a);
-  else
-    scores_backward_kernel<SIGMOID, 32><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.k <= 4    ? launch_backward_of<SIGMOID, 4>(a, s)
+         : a.k <= 8  ? launch_backward_of<SIGMOID, 8>(a, s)
+         : a.k <= 16 ? launch_backward_of<SIGMOID, 16>(a, s)
+                     : launch_backward_of<SIGMOID, 32>(a, s);
 }
 
 bool options_ok(const moe_config_t& c, const moe_route_scores_t* o) {
@@ -826,8 +860,7 @@ cudaError_t launch_scores(const Args& a, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(std::min<long long>(
       (static_cast<long long>(a.T) + kWarps - 1) / kWarps,
       static_cast<long long>(per_sm) * d.sms));
-  kernel<<<grid, kThreads, kBytes, s>>>(a);
-  return cudaGetLastError();
+  return launch::overlapping(kernel, grid, kThreads, kBytes, s, a);
 }
 template <int EPL, bool FULL>
 cudaError_t launch_rank(const Args& a, cudaStream_t s) {
