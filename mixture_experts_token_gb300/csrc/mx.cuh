@@ -158,16 +158,24 @@ __device__ __forceinline__ Block block_scale(uint32_t most) {
     b.s = 0.0f;
     b.inv = __uint_as_float((254u - min(b.byte, 253u)) << 23);
   } else {
+    // The quotient by 6 and the reciprocal, each an approximation and one
+    // Newton step: the nearest float but for an ulp at most, and m / 6 exact
+    // where it is the middle of two scales (as a middle of two codes below).
     const bool finite = most < 0x7f800000u;
-    uint32_t r;
+    const float m = __uint_as_float(most), q = m * (1.0f / kCodeMax);
+    const float sixth = fmaf(fmaf(-q, kCodeMax, m), 1.0f / kCodeMax, q);
+    uint32_t r, h;
     asm("{\n\t.reg .b16 t;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 t, %2, %3;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, t;\n\t"
         "cvt.u32.u16 %0, t;\n\t}\n"
-        : "=r"(r)
-        : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(most), kCodeMax)));
-    b.byte = finite ? r & 127 : 127u;
-    b.s = finite ? scale_value<16>(b.byte) : 0.0f;
-    b.inv = b.s > 0.0f ? __frcp_rn(b.s) : 0.0f;
+        : "=r"(r), "=r"(h)
+        : "f"(0.0f), "f"(finite ? sixth : 0.0f));
+    b.byte = finite ? r : 127u;
+    b.s = __low2float(*reinterpret_cast<const __half2*>(&h));
+    float inv;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(b.s));
+    b.inv = b.s > 0.0f ? fmaf(fmaf(-b.s, inv, 1.0f), inv, inv) : 0.0f;
   }
   return b;
 }
