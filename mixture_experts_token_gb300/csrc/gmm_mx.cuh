@@ -18,10 +18,16 @@
 //     stage's scales there, those of the weights from shared memory and those
 //     of the rows from global memory;
 //   * a warp issues the matrix instructions;
-//   * four warps turn the sums into rows of the output, a thread a column,
-//     while the next item's sums go to the other accumulator.
+//   * four warps, or sixteen, turn the sums into rows of the output, a thread a
+//     column, while the next item's sums go to the other accumulator.
 // Every wait is bounded; one that gives up raises MOE_DEV_TIMEOUT and the CTA
 // drains and returns.
+//
+// With many rows a group, what a CTA brings and reads for a matrix instruction
+// bounds it, so two SMs work on one item as a pair: 256 columns of weights, half
+// of them in each CTA, and the rows' codes halved between them, which the
+// instruction reads from both.  One CTA's warp issues for both; the other's
+// passes on that its scales are written and its sums are read.
 #pragma once
 
 #include <atomic>
@@ -67,13 +73,7 @@ cudaError_t launch_gmm_mx_gate_up(const GmmArgs& a, const void* codes,
 cudaError_t launch_gmm_mx_down(const GmmArgs& a, const void* codes,
                                cudaStream_t s);
 
-constexpr int kEpiWarps = 4;
-constexpr int kLoadWarp = kEpiWarps;
-constexpr int kMmaWarp = kLoadWarp + 1;
-constexpr int kScaleWarp = kMmaWarp + 1;
 constexpr int kScaleWarps = 4;
-constexpr int kWarps = kScaleWarp + kScaleWarps;
-constexpr int kGmmThreads = kWarps * 32;
 constexpr int kMaxSplits = 512;
 constexpr int kMaxChunks = kMaxExperts + kMaxSplits;
 constexpr int kMaxShared = 226 * 1024;
@@ -153,7 +153,30 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity,
 }
 
 // D (+)= A B over 64 of k, both 4-bit in shared memory, each block of BLOCK of
-// k times its scales in tensor memory.
+// k times its scales in tensor memory; of a pair of CTAs, A's rows and D's in
+// halves, B's columns too, and the scales of B whole in both.
+template <int BLOCK>
+__device__ __forceinline__ void umma_mx_pair(uint32_t d, uint64_t a,
+                                             uint64_t b, uint32_t idesc,
+                                             uint32_t sa, uint32_t sb,
+                                             uint32_t accumulate) {
+  if (BLOCK == 16)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
 template <int BLOCK>
 __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b,
                                         uint32_t idesc, uint32_t sa,
@@ -179,10 +202,9 @@ __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b,
 // byte (bits 4-5), A and B of the 4-bit type (1 in bits 7-9 and 10-12), N >> 3
 // in bits 17-22, scales a power of two (bit 23), M >> 7 in bits 27-28, A's
 // scale word's first byte (bits 29-30).
-__device__ __forceinline__ uint32_t idesc_mx(int block, int n, int byte) {
-  return static_cast<uint32_t>(byte) << 4 | 1u << 7 | 1u << 10 |
-         static_cast<uint32_t>(n >> 3) << 17 | (block == 32 ? 1u << 23 : 0u) |
-         1u << 27 | static_cast<uint32_t>(byte) << 29;
+__device__ __forceinline__ uint32_t idesc_mx(int block, int m, int n) {
+  return 1u << 7 | 1u << 10 | static_cast<uint32_t>(n >> 3) << 17 |
+         (block == 32 ? 1u << 23 : 0u) | static_cast<uint32_t>(m >> 7) << 27;
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
@@ -207,8 +229,20 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
 }
 
 // ------------------------------------------------------------- kernel ----
-template <bool DUAL, int BLOCK, int NT>
+template <bool DUAL, int BLOCK, int NT, bool PAIR>
 struct Gmm {
+  static constexpr int kCtas = PAIR ? 2 : 1;  // of an item
+  // Warps for each quarter of the lanes, which share an item's rows.  Many rows
+  // of both matrices leave tensor memory no second accumulator, and the matrix
+  // instructions wait while it is read: 10.8 us of an item's 29 with one warp
+  // a quarter, 7 of 25 with four.
+  static constexpr int kRowParts = !PAIR ? 1 : DUAL ? 4 : 2;
+  static constexpr int kEpiWarps = 4 * kRowParts;
+  static constexpr int kLoadWarp = kEpiWarps;
+  static constexpr int kMmaWarp = kLoadWarp + 1;
+  static constexpr int kScaleWarp = kMmaWarp + 1;
+  static constexpr int kWarps = kScaleWarp + kScaleWarps;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kMats = DUAL ? 2 : 1;
   static constexpr int kTiles = scale_tiles(BLOCK);  // of 128 rows, a stage
   static constexpr int kRec = record_bytes(BLOCK);
@@ -218,14 +252,15 @@ struct Gmm {
   static constexpr int kRowTiles = (NT + 127) / 128 * kTiles;
   // Rows of one TMA copy: few where rows are few; where they are many, small
   // copies are what takes the time.
-  static constexpr int kRowBox = NT <= 64 ? 16 : NT / 2;
+  static constexpr int kRowBox = NT <= 64 ? 16 : NT / (2 * kCtas);
   static constexpr int kX = kMats * kRec;  // the rows' codes
-  static constexpr int kStage = kX + NT * 128;
+  static constexpr int kStage = kX + NT / kCtas * 128;
   static constexpr int kRoom = kMaxShared - 1024 - kBarBytes - 8 * kMaxChunks;
   static constexpr int kStages =
       kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
   static_assert(kStages >= 3, "copies stay ahead");
-  static_assert(kRec % 1024 == 0 && NT % 16 == 0 && kRowBox % 8 == 0,
+  static_assert(kRec % 1024 == 0 && NT % (16 * kCtas) == 0 &&
+                    kRowBox % 8 == 0 && NT / kCtas % kRowBox == 0,
                 "swizzled tiles aligned");
   // Tensor memory: accumulators [buffer][matrix][NT], then scales [buffer]
   // of the weights [matrix][tile][4] and the rows [tile][4], both from a
@@ -267,7 +302,16 @@ struct Gmm {
                                                  const int2* chunks, int i,
                                                  int tiles) {
     const int2 c = chunks[i / tiles];
-    return {i % tiles, a.map ? a.map[c.x] : c.x, c.y, chunk_end(a, c) - c.y};
+    return {i % tiles * kCtas + rank(), a.map ? a.map[c.x] : c.x, c.y,
+            chunk_end(a, c) - c.y};
+  }
+  // This CTA of its pair.
+  __device__ static __forceinline__ int rank() {
+    return PAIR ? blockIdx.x & 1 : 0;
+  }
+  // Columns of the instruction for so many rows.
+  __device__ static __forceinline__ int columns(int rows) {
+    return (rows + 16 * kCtas - 1) / (16 * kCtas) * (16 * kCtas);
   }
   // Calls f(item) for the passes of up to NT rows of this CTA's items until
   // it returns false.
@@ -277,7 +321,7 @@ struct Gmm {
                                                 int n_items, int tiles,
                                                 const F& f) {
 #pragma unroll 1
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
+    for (int i = blockIdx.x / kCtas; i < n_items; i += gridDim.x / kCtas) {
       Item it = item_at(a, chunks, i, tiles);
       const int end = it.row + it.rows;
 #pragma unroll 1
@@ -315,19 +359,25 @@ struct Gmm {
         tc::mbar_init(b.full + 8 * i, 1);
         tc::mbar_init(b.empty + 8 * i, 1);
       }
+      // (the first CTA's count both CTAs' warps)
       for (int i = 0; i < kScaleBufs; ++i)
-        tc::mbar_init(b.scales + 8 * i, kScaleWarps);
+        tc::mbar_init(b.scales + 8 * i, kScaleWarps * kCtas);
       for (int i = 0; i < kBuffers; ++i) {
         tc::mbar_init(b.acc_full + 8 * i, 1);
-        tc::mbar_init(b.acc_empty + 8 * i, kEpiWarps);
+        tc::mbar_init(b.acc_empty + 8 * i, kEpiWarps * kCtas);
       }
       tc::mbar_init(b.done, 1);
       tc::fence_barrier_init();
       tc::fence_proxy_async_smem();
     }
     if (warp == kMmaWarp) {
-      tc::tmem_alloc(tc::smem_u32(&tmem_word), tc::kTmemCols);
-      tc::tmem_relinquish();
+      if (PAIR) {
+        tc::tmem_alloc_pair(tc::smem_u32(&tmem_word), tc::kTmemCols);
+        tc::tmem_relinquish_pair();
+      } else {
+        tc::tmem_alloc(tc::smem_u32(&tmem_word), tc::kTmemCols);
+        tc::tmem_relinquish();
+      }
     }
     // Offsets and weights were final before the kernel that writes the rows
     // began, where this one may start early; else nothing is read before all
@@ -338,10 +388,12 @@ struct Gmm {
     const int n_chunks = find_chunks<kWarps>(a, chunks);  // barriers within
     tc::tc_fence_before();
     __syncthreads();
+    if (PAIR) tc::cluster_sync();  // both CTAs' barriers exist
     tc::tc_fence_after();
     launch::let_next_start();
     const uint32_t tmem = tmem_word;
-    const int tiles = a.l.tiles_n(), n_items = n_chunks * tiles;
+    const int tiles = (a.l.tiles_n() + kCtas - 1) / kCtas;
+    const int n_items = n_chunks * tiles;
     if (warp < kEpiWarps)
       write_out(a, b, chunks, n_items, tiles, tmem, warp, lane, abort_flag);
     else if (warp == kLoadWarp)
@@ -354,8 +406,15 @@ struct Gmm {
     __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
+    // neither CTA leaves while the other may still use what is its
+    if (PAIR) tc::cluster_sync();
     tc::tc_fence_after();
-    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, tc::kTmemCols);
+    if (warp == kMmaWarp) {
+      if (PAIR)
+        tc::tmem_dealloc_pair(tmem, tc::kTmemCols);
+      else
+        tc::tmem_dealloc(tmem, tc::kTmemCols);
+    }
   }
 
   // ---- weights and the rows' codes
@@ -369,20 +428,25 @@ struct Gmm {
     ring.phase = 1;
     long long filled = 0;
     const auto weights = [&](const Item& it, int s, int st) {
-      const long long at = it.expert * a.l.matrix() + it.tile * a.l.tile() +
+      // (the second of a pair may be past the last tile: it has the last
+      // again, and writes nothing)
+      const int tile = PAIR ? min(it.tile, a.l.tiles_n() - 1) : it.tile;
+      const long long at = it.expert * a.l.matrix() + tile * a.l.tile() +
                            static_cast<long long>(s) * kRec;
       const uint32_t dst = sb + st * kStage, bar = b.full + 8 * st;
-      const int boxes = (it.rows + kRowBox - 1) / kRowBox;
+      const int boxes =
+          (columns(it.rows) / kCtas + kRowBox - 1) / kRowBox;
       tc::mbar_expect_tx(bar, kMats * kRec + boxes * kRowBox * 128);
       bulk_load(dst, a.w0 + at, kRec, bar);
       if (DUAL) bulk_load(dst + kRec, a.w1 + at, kRec, bar);
     };
     const auto rows = [&](const Item& it, int s, int st) {
       const uint32_t dst = sb + st * kStage + kX, bar = b.full + 8 * st;
+      const int n = columns(it.rows) / kCtas;
 #pragma unroll 1
-      for (int r = 0; r < it.rows; r += kRowBox)
+      for (int r = 0; r < n; r += kRowBox)
         tc::tma_load_2d(dst + r * 128, map, bar, s * (kStageK / 2),
-                        it.row + r);
+                        it.row + rank() * n + r);
     };
     // The weights of the first stages do not wait for the kernel that writes
     // the rows.
@@ -500,23 +564,24 @@ struct Gmm {
             ++lead;
           }
         }
-        uint32_t w[kMats * kScaleA];
+        tc::tc_fence_after();
+        tmem_st(out + sring.st * kScales + kScaleX, x);
         const uint32_t from = sb + ring.st * kStage + kCodeBytes + lane * 16;
 #pragma unroll
-        for (int m = 0; m < kMats; ++m)
+        for (int m = 0; m < kMats; ++m) {
+          uint32_t w[kScaleA];
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
             const uint4 v = lds16(from + m * kRec + j * kScaleTile);
-            uint32_t* to = w + (m * kTiles + j) * 4;
-            to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+            w[4 * j] = v.x, w[4 * j + 1] = v.y;
+            w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
           }
-        tc::tc_fence_after();
-        tmem_st(out + sring.st * kScales, w);
-        tmem_st(out + sring.st * kScales + kScaleX, x);
+          tmem_st(out + sring.st * kScales + m * kScaleA, w);
+        }
         tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(b.scales + 8 * sring.st);
+        if (lane == 0) arrive(b.scales + 8 * sring.st);
         ring.next();
         sring.next();
       }
@@ -531,14 +596,15 @@ struct Gmm {
                                   int n_items, int tiles, uint32_t tmem,
                                   int lane, volatile int* abort_flag) {
     const int stages = a.l.stages();
+    if (PAIR && rank() != 0) return;  // the first CTA's issues for both
     const bool leader = lane == 0;
     Ring<> ring;
     Ring<kScaleBufs> sring;
     int buf = 0;
     uint32_t acc_phase = 1;
     passes(a, chunks, n_items, tiles, [&](const Item& it) {
-      const int n = (it.rows + 15) / 16 * 16;
-      const uint32_t idesc = idesc_mx(BLOCK, n, 0);
+      const uint32_t idesc =
+          idesc_mx(BLOCK, kTileN * kCtas, columns(it.rows));
       const uint32_t d = tmem + buf * kAcc;
       if (!wait_all(b.acc_empty + 8 * buf, acc_phase, abort_flag, a.status))
         return false;
@@ -565,20 +631,25 @@ struct Gmm {
             const uint32_t id =
                 BLOCK == 16 ? 0u : (k & 1) * (2u << 4 | 2u << 29);
 #pragma unroll
-            for (int m = 0; m < kMats; ++m)
-              umma_mx<BLOCK>(d + m * NT, ad + ((m * kRec >> 4) + 2 * k),
-                             bd + 2 * k, idesc | id,
-                             sa + m * kScaleA + 4 * tile,
-                             sx + tile * (kRowTiles / kTiles * 4),
-                             s > 0 || k > 0);
+            for (int m = 0; m < kMats; ++m) {
+              const uint64_t am = ad + ((m * kRec >> 4) + 2 * k);
+              const uint32_t sm = sa + m * kScaleA + 4 * tile;
+              const uint32_t st = sx + tile * (kRowTiles / kTiles * 4);
+              if (PAIR)
+                umma_mx_pair<BLOCK>(d + m * NT, am, bd + 2 * k, idesc | id,
+                                    sm, st, s > 0 || k > 0);
+              else
+                umma_mx<BLOCK>(d + m * NT, am, bd + 2 * k, idesc | id, sm, st,
+                               s > 0 || k > 0);
+            }
           }
-          tc::umma_commit(b.empty + 8 * ring.st);
+          commit(b.empty + 8 * ring.st);
         }
         __syncwarp();
         ring.next();
         sring.next();
       }
-      if (leader) tc::umma_commit(b.acc_full + 8 * buf);
+      if (leader) commit(b.acc_full + 8 * buf);
       __syncwarp();
       if (++buf == kBuffers) {
         buf = 0;
@@ -588,11 +659,32 @@ struct Gmm {
     });
     // drain: every instruction that this warp issued
     if (leader) {
-      tc::umma_commit(b.done);
+      if (PAIR)
+        tc::umma_commit_pair(b.done);
+      else
+        tc::umma_commit(b.done);
       tc::mbar_wait(b.done, 0, nullptr, a.status);
     }
   }
-
+  // Arrives on a barrier of the CTA that issues.  What it tells of is in
+  // tensor memory or was brought there by copies, and complete; so nothing
+  // waits for a release to the whole cluster, which takes longer than a stage
+  // (about 1 us each: 8192 rows' products then took 1.5 times theirs).
+  __device__ static __forceinline__ void arrive(uint32_t bar) {
+    if (PAIR)
+      asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                       tc::map_to_rank(bar, 0))
+                   : "memory");
+    else
+      tc::mbar_arrive(bar);
+  }
+  // Arrives, in both CTAs of a pair, when all instructions so far are done.
+  __device__ static __forceinline__ void commit(uint32_t bar) {
+    if (PAIR)
+      tc::umma_commit_pair_mc(bar);
+    else
+      tc::umma_commit(bar);
+  }
   // ---- sums to rows of the output, a thread a column of the weights
   __device__ static void write_out(const GmmArgs& a, const Bars& b,
                                    const int2* chunks, int n_items, int tiles,
@@ -602,45 +694,84 @@ struct Gmm {
     uint32_t phase = 0;
     launch::wait_for_previous();
     passes(a, chunks, n_items, tiles, [&](const Item& it) {
+      const float t0 = a.x_scale * (a.s0 ? a.s0[it.expert] : 1.0f);
+      float t1 = a.x_scale * (DUAL && a.s1 ? a.s1[it.expert] : 1.0f);
+      if (DUAL && BLOCK == 16) t1 *= a.inv_out;
       if (!wait_all(b.acc_full + 8 * buf, phase, abort_flag, a.status))
         return false;
       tc::tc_fence_after();
-      const int col0 = it.tile * kTileN + warp * 32;
+      const int quarter = warp & 3;
+      const int col0 = it.tile * kTileN + quarter * 32;
       const uint32_t at =
-          tmem + buf * kAcc + (static_cast<uint32_t>(warp * 32) << 16);
+          tmem + buf * kAcc + (static_cast<uint32_t>(quarter * 32) << 16);
       if (col0 < a.l.N) {  // N is a multiple of 32
-        const float t0 = a.x_scale * (a.s0 ? a.s0[it.expert] : 1.0f);
-        const float t1 = a.x_scale * (DUAL && a.s1 ? a.s1[it.expert] : 1.0f);
+        if constexpr (DUAL && PAIR) {
+          // h of this warp's rows, then the sums are free, then the codes
+          constexpr int kRows = NT / kRowParts;
+          static_assert(kRows % 16 == 0, "whole loads");
+          const int r0 = warp / 4 * kRows;
+          float h[kRows];
+#pragma unroll
+          for (int r = 0; r < kRows; r += 16)
+            if (r0 + r < it.rows) {
+              uint32_t g[16], u[16];
+              tmem_ld16(at + r0 + r, g);
+              tmem_ld16(at + NT + r0 + r, u);
+              tmem_ld_wait(g);
+              tmem_ld_wait(u);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                h[r + i] = swiglu(__uint_as_float(g[i]), __uint_as_float(u[i]), t0,
+                                  t1);
+            }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(b.acc_empty + 8 * buf);
+#pragma unroll
+          for (int r = 0; r < kRows; r += 8)
+            if (r0 + r < it.rows) write_h(a, it, col0, r0 + r, lane, h + r);
+        } else {
+          const int r1 = min(it.rows, (warp / 4 + 1) * (NT / kRowParts));
 #pragma unroll 1
-        for (int r = 0; r < it.rows; r += 16) {
-          uint32_t g[16], u[16];
-          tmem_ld16(at + r, g);
-          if (DUAL) tmem_ld16(at + NT + r, u);
-          tmem_ld_wait(g);
-          if (DUAL) {
-            tmem_ld_wait(u);
+          for (int r = warp / 4 * (NT / kRowParts); r < r1; r += 16) {
+            uint32_t g[16], u[16];
+            tmem_ld16(at + r, g);
+            if (DUAL) tmem_ld16(at + NT + r, u);
+            tmem_ld_wait(g);
+            if (DUAL) {
+              tmem_ld_wait(u);
 #pragma unroll
-            for (int i = 0; i < 16; i += 8)
-              if (r + i < it.rows)
-                write_h(a, it, col0, r + i, lane, t0, t1, g + i, u + i);
-          } else {
+              for (int i = 0; i < 16; i += 8)
+                if (r + i < it.rows) {
+                  float h[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (r + i >= it.rows) break;
-              const long long o =
-                  static_cast<long long>(it.row + r + i) * a.l.N + col0 + lane;
-              const float v = t0 * __uint_as_float(g[i]);
-              if (a.f32)
-                put(static_cast<float*>(a.y) + o, v);
-              else
-                put(static_cast<__nv_bfloat16*>(a.y) + o, v);
+                  for (int j = 0; j < 8; ++j)
+                    h[j] = swiglu(__uint_as_float(g[i + j]),
+                                  __uint_as_float(u[i + j]), t0, t1);
+                  write_h(a, it, col0, r + i, lane, h);
+                }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                if (r + i >= it.rows) break;
+                const long long o =
+                    static_cast<long long>(it.row + r + i) * a.l.N + col0 +
+                    lane;
+                const float v = t0 * __uint_as_float(g[i]);
+                if (a.f32)
+                  put(static_cast<float*>(a.y) + o, v);
+                else
+                  put(static_cast<__nv_bfloat16*>(a.y) + o, v);
+              }
             }
           }
         }
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(b.acc_empty + 8 * buf);
+      if (!(DUAL && PAIR && col0 < a.l.N)) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(b.acc_empty + 8 * buf);
+      }
       if (++buf == kBuffers) {
         buf = 0;
         phase ^= 1;
@@ -649,20 +780,27 @@ struct Gmm {
     });
   }
 
+  // silu(t0 g) t1 u, silu(z) = z / (1 + exp(-z)); exp(-z) may be infinite.
+  // (t1 includes the reciprocal of h's scale: one rounding of h less.)
+  __device__ static __forceinline__ float swiglu(float g, float u, float t0,
+                                                 float t1) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * (t0 * -1.44269504f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return t0 * g * s * (t1 * u);
+  }
+
   // Eight rows of 32 columns of h: each lane has one column of all rows, a
   // block is the warp's lanes or half of them.
-  __device__ static __forceinline__ void write_h(
-      const GmmArgs& a, const Item& it, int col0, int r, int lane, float t0,
-      float t1, const uint32_t* g, const uint32_t* u) {
+  __device__ static __forceinline__ void write_h(const GmmArgs& a,
+                                                 const Item& it, int col0,
+                                                 int r, int lane,
+                                                 const float* h) {
     float q[8];
     uint32_t most = 0;  // of row lane % 8, this lane's block
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float z = t0 * __uint_as_float(g[i]);
-      // z / (1 + exp(-z)); exp(-z) may be infinite
-      const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-      q[i] = z * s * (t1 * __uint_as_float(u[i]));
-      if (BLOCK == 16) q[i] *= a.inv_out;
+      q[i] = h[i];
       const uint32_t bits = __float_as_uint(q[i]) & 0x7fffffffu;
       uint32_t m;
       if (BLOCK == 32) {
@@ -710,9 +848,24 @@ struct Gmm {
 };
 
 template <bool DUAL, int BLOCK, int NT>
-__global__ void __launch_bounds__(kGmmThreads, 1)
+__global__ void __launch_bounds__(Gmm<DUAL, BLOCK, NT, false>::kThreads, 1)
     gmm_mx_kernel(const GmmArgs a, const __grid_constant__ CUtensorMap map) {
-  Gmm<DUAL, BLOCK, NT>::run(a, &map);
+  Gmm<DUAL, BLOCK, NT, false>::run(a, &map);
+}
+template <bool DUAL, int BLOCK, int NT>
+__global__ void __cluster_dims__(2, 1, 1) 
+    __launch_bounds__(Gmm<DUAL, BLOCK, NT, true>::kThreads, 1)
+    gmm_mx_pair_kernel(const GmmArgs a,
+                       const __grid_constant__ CUtensorMap map) {
+  Gmm<DUAL, BLOCK, NT, true>::run(a, &map);
+}
+
+template <bool DUAL, int BLOCK, int NT, bool PAIR>
+constexpr auto kernel_of() {
+  if constexpr (PAIR)
+    return gmm_mx_pair_kernel<DUAL, BLOCK, NT>;
+  else
+    return gmm_mx_kernel<DUAL, BLOCK, NT>;
 }
 
 // Rows of codes [rows, K/2], `box` rows of 128 bytes at a time.
@@ -731,9 +884,9 @@ inline bool make_code_map(CUtensorMap* m, const void* base, int K,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool DUAL, int BLOCK, int NT>
+template <bool DUAL, int BLOCK, int NT, bool PAIR = false>
 cudaError_t launch_one(GmmArgs a, const void* codes, cudaStream_t s) {
-  using Ker = Gmm<DUAL, BLOCK, NT>;
+  using Ker = Gmm<DUAL, BLOCK, NT, PAIR>;
   // Chunks of as few passes of NT rows as leave at most kMaxSplits more than
   // there are groups.
   const long long most = static_cast<long long>(NT) * kMaxSplits;
@@ -744,17 +897,18 @@ cudaError_t launch_one(GmmArgs a, const void* codes, cudaStream_t s) {
   Device d;
   cudaError_t e = launch::device(&d);
   if (e != cudaSuccess) return e;
-  constexpr auto kernel = gmm_mx_kernel<DUAL, BLOCK, NT>;
+  constexpr auto kernel = kernel_of<DUAL, BLOCK, NT, PAIR>();
   if ((e = launch::allow_shared<kernel>(d)) != cudaSuccess) return e;
   CUtensorMap map;
   if (!make_code_map(&map, codes, a.l.K, a.rows, Ker::kRowBox))
     return cudaErrorInvalidValue;
   const long long items =
-      static_cast<long long>(a.l.tiles_n()) * a.chunks;
-  const unsigned grid =
-      static_cast<unsigned>(std::min<long long>(items, d.sms));
+      static_cast<long long>((a.l.tiles_n() + Ker::kCtas - 1) / Ker::kCtas) *
+      a.chunks;
+  const unsigned grid = static_cast<unsigned>(
+      std::min<long long>(items, d.sms / Ker::kCtas) * Ker::kCtas);
   const int bytes = Ker::shared_bytes(a.chunks);
-  return launch::overlapping(kernel, grid, kGmmThreads, bytes, s, a, map);
+  return launch::overlapping(kernel, grid, Ker::kThreads, bytes, s, a, map);
 }
 
 }  // namespace mx

@@ -11,7 +11,7 @@ static cudaError_t pick(const GmmArgs& a, const void* codes, cudaStream_t s) {
   if (a.tokens <= 16) return launch_one<true, BLOCK, 16>(a, codes, s);
   if (a.tokens <= 64 || a.rows <= 48 * groups)
     return launch_one<true, BLOCK, 64>(a, codes, s);
-  return launch_one<true, BLOCK, 96>(a, codes, s);
+  return launch_one<true, BLOCK, 192, true>(a, codes, s);
 }
 cudaError_t launch_gmm_mx_gate_up(const GmmArgs& a, const void* codes,
                                   cudaStream_t s) {
