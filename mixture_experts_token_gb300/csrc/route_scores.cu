@@ -409,18 +409,12 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
     most_bias = warp_max(most_bias);
   }
   const long long step = gridDim.x * static_cast<long long>(kWarps);
-  long long t = blockIdx.x * static_cast<long long>(kWarps) + warp;
-  float next[EPL];
-  if (t < a.T)
-    load_row<EPL, FULL>(a.logits + t * a.E, e0, a.E, wide, next);
 #pragma unroll 1
-  for (; t < a.T; t += step) {
+  for (long long t = blockIdx.x * static_cast<long long>(kWarps) + warp;
+       t < a.T; t += step) {
     const float* row = a.logits + t * a.E;
     float c[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = next[i];
-    if (t + step < a.T)
-      load_row<EPL, FULL>(row + step * a.E, e0, a.E, wide, next);
+    load_row<EPL, FULL>(row, e0, a.E, wide, c);
     bool again = RANK != kByLogit && most_bias == INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
@@ -855,8 +849,7 @@ cudaError_t launch_scores(const Args& a, cudaStream_t s) {
   if (e == cudaSuccess)
     e = launch::ctas_per_sm<kernel>(d, kThreads, kBytes, &per_sm);
   if (e != cudaSuccess) return e;
-  // CTAs that stay, so that a warp reads the bias once and the next row while
-  // it ranks one
+  // CTAs that stay, so that a warp reads the bias once
   const unsigned grid = static_cast<unsigned>(std::min<long long>(
       (static_cast<long long>(a.T) + kWarps - 1) / kWarps,
       static_cast<long long>(per_sm) * d.sms));
