@@ -67,11 +67,22 @@ struct GmmArgs {
   long long stall_after_fills;  // tests of the timeout path only (-1: off)
 };
 
-// Which instance a call takes, and the launch (gmm_mx_*.cu).
+// The launch of either product (gmm_mx_*.cu).
 cudaError_t launch_gmm_mx_gate_up(const GmmArgs& a, const void* codes,
                                   cudaStream_t s);
 cudaError_t launch_gmm_mx_down(const GmmArgs& a, const void* codes,
                                cudaStream_t s);
+
+// Whether passes of 192 rows on SM pairs are faster than passes of 64 on single
+// SMs: by the mean rows of a group, where groups can have more than 64 (routing
+// gives a group at most one row of each token).  32 experts of 7168 x 2048, both
+// products, singles against pairs: 32 rows a group 167 and 179 us, 64 rows 194
+// and 192, 128 rows 300 and 211, 512 rows 968 and 535.  (Passes of 16 rows
+// gained nothing: 113 us for one row a group, 114 in passes of 64.)
+inline bool many_rows(const GmmArgs& a) {
+  return a.tokens > 64 &&
+         a.rows > 48ll * std::min(a.n_groups, a.rows);
+}
 
 constexpr int kScaleWarps = 4;
 constexpr int kMaxSplits = 512;
@@ -252,7 +263,7 @@ struct Gmm {
   static constexpr int kRowTiles = (NT + 127) / 128 * kTiles;
   // Rows of one TMA copy: few where rows are few; where they are many, small
   // copies are what takes the time.
-  static constexpr int kRowBox = NT <= 64 ? 16 : NT / (2 * kCtas);
+  static constexpr int kRowBox = PAIR ? NT / 4 : 16;
   static constexpr int kX = kMats * kRec;  // the rows' codes
   static constexpr int kStage = kX + NT / kCtas * 128;
   static constexpr int kRoom = kMaxShared - 1024 - kBarBytes - 8 * kMaxChunks;
@@ -884,7 +895,7 @@ inline bool make_code_map(CUtensorMap* m, const void* base, int K,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool DUAL, int BLOCK, int NT, bool PAIR = false>
+template <bool DUAL, int BLOCK, int NT, bool PAIR>
 cudaError_t launch_one(GmmArgs a, const void* codes, cudaStream_t s) {
   using Ker = Gmm<DUAL, BLOCK, NT, PAIR>;
   // Chunks of as few passes of NT rows as leave at most kMaxSplits more than

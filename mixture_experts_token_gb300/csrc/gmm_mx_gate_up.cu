@@ -7,11 +7,8 @@ namespace mx {
 
 template <int BLOCK>
 static cudaError_t pick(const GmmArgs& a, const void* codes, cudaStream_t s) {
-  const long long groups = std::min(a.n_groups, a.rows);
-  if (a.tokens <= 16) return launch_one<true, BLOCK, 16>(a, codes, s);
-  if (a.tokens <= 64 || a.rows <= 48 * groups)
-    return launch_one<true, BLOCK, 64>(a, codes, s);
-  return launch_one<true, BLOCK, 192, true>(a, codes, s);
+  return many_rows(a) ? launch_one<true, BLOCK, 192, true>(a, codes, s)
+                      : launch_one<true, BLOCK, 64, false>(a, codes, s);
 }
 cudaError_t launch_gmm_mx_gate_up(const GmmArgs& a, const void* codes,
                                   cudaStream_t s) {
