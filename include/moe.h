@@ -1100,8 +1100,9 @@ moe_status_t moe_mx_dequantize_rows(const moe_mx_t *opt, int32_t R, int32_t K,
 
 /* moe_mx_quantize -- codes and scales of n weight matrices w [n, K, N] dtype
  * (16-byte aligned), blocks along K: codes [n, N, K/2], scales [n, N, row],
- * the order in which checkpoints hold them.  scale: [n] float32 (device),
- * each matrix's tensor scale, or NULL for 1 (always with blocks of 32). */
+ * the order in which checkpoints hold them.  scale: [n] float32 (device), each
+ * matrix's tensor scale (finite, above 2^-126), or NULL for 1 (always with
+ * blocks of 32). */
 moe_status_t moe_mx_quantize(const moe_mx_t *opt, int32_t n, int32_t K,
                              int32_t N, moe_dtype_t dtype, const void *w,
                              const float *scale, uint8_t *codes,
@@ -1196,12 +1197,13 @@ int32_t moe_gmm_kernel_choice(const moe_config_t *cfg, int32_t n_groups,
 const char *moe_status_string(moe_status_t status);
 
 /* For tests of failure detection only: with fills >= 0 the TMA producers of
- * the bf16 GEMM, of the router's cluster form and of the two-SM weight
- * gradient stop after that many pipeline-stage fills, so the MMA warp's
- * bounded wait runs out (about 2 s): the kernel then sets MOE_DEV_TIMEOUT in
- * the status word, stops its other roles, drains its copies and MMAs, frees
- * its tensor memory and returns, and the CUDA context stays usable.  -1
- * restores normal operation.  Process-wide; not for production use. */
+ * the bf16 GEMM, of the router's cluster form, of the two-SM weight gradient
+ * and of the 4-bit products stop after that many pipeline-stage fills, so the
+ * MMA warp's bounded wait runs out (about 2 s): the kernel then sets
+ * MOE_DEV_TIMEOUT in the status word, stops its other roles, drains its copies
+ * and MMAs, frees its tensor memory and returns, and the CUDA context stays
+ * usable.  -1 restores normal operation.  Process-wide; not for production
+ * use. */
 void moe_test_stall_gemm_producer(int64_t fills);
 
 #ifdef __cplusplus

@@ -10,7 +10,7 @@
 // columns, and one of any number of rows splits at any multiple of 16.
 //
 // A CTA an SM walks over items, a tile of 128 columns (of the gate and the up
-// matrix, or of the down matrix) for up to NT rows of one group:
+// matrix, or of the down matrix) for up to NT = 64 rows of one group:
 //   * a thread brings the weights' records by bulk copy and the rows' codes by
 //     TMA, 256 of k a stage (rows past the group's are other groups' or zeros;
 //     they reach only columns that are not written);
@@ -18,16 +18,25 @@
 //     stage's scales there, those of the weights from shared memory and those
 //     of the rows from global memory;
 //   * a warp issues the matrix instructions;
-//   * four warps, or sixteen, turn the sums into rows of the output, a thread a
-//     column, while the next item's sums go to the other accumulator.
+//   * four warps, or eight or sixteen, turn the sums into rows of the output, a
+//     thread a column, while the next item's sums go to the other accumulator,
+//     if there is one.
 // Every wait is bounded; one that gives up raises MOE_DEV_TIMEOUT and the CTA
 // drains and returns.
 //
 // With many rows a group, what a CTA brings and reads for a matrix instruction
-// bounds it, so two SMs work on one item as a pair: 256 columns of weights, half
-// of them in each CTA, and the rows' codes halved between them, which the
-// instruction reads from both.  One CTA's warp issues for both; the other's
-// passes on that its scales are written and its sums are read.
+// bounds it, so two SMs work on one item as a pair: up to 192 rows by 256 columns
+// of weights, half of the columns in each CTA, and the rows' codes halved
+// between them, which the instruction reads from both.  One CTA's warp issues
+// for both.
+//
+// Measured with blocks of 16, quantising the rows and both products: one token,
+// 8 experts of 7168 x 2048, 198 MB, 42 us (4.7 TB/s; 128 items leave 24 of 152
+// SMs idle in the first product); 64 tokens over 146 such experts 546 to 581 us
+// (5.7 to 6.1 TB/s, with where the buffers lie); 16 experts of 5120 x 8192, 163
+// to 173 us.  32768 rows over 32 experts of 7168 x 2048, 987 us: gate and up 471
+// (4.1 PFLOP/s), down 391 (2.5 PFLOP/s), quantising the rows 139.  On 2048
+// tokens over 16 experts the tensor pipe is 43% busy in gate and up, 26% in down.
 #pragma once
 
 #include <atomic>
@@ -246,7 +255,9 @@ struct Gmm {
   // Warps for each quarter of the lanes, which share an item's rows.  Many rows
   // of both matrices leave tensor memory no second accumulator, and the matrix
   // instructions wait while it is read: 10.8 us of an item's 29 with one warp
-  // a quarter, 7 of 25 with four.
+  // a quarter, 7 of 25 with four, 4 of 22 as it is now (32768 rows; a run that
+  // read no sums subtracted).  Down has a second one: 397, 391, 422, 453 us with
+  // one to four.
   static constexpr int kRowParts = !PAIR ? 1 : DUAL ? 4 : 2;
   static constexpr int kEpiWarps = 4 * kRowParts;
   static constexpr int kLoadWarp = kEpiWarps;
@@ -678,9 +689,9 @@ struct Gmm {
     }
   }
   // Arrives on a barrier of the CTA that issues.  What it tells of is in
-  // tensor memory or was brought there by copies, and complete; so nothing
-  // waits for a release to the whole cluster, which takes longer than a stage
-  // (about 1 us each: 8192 rows' products then took 1.5 times theirs).
+  // tensor memory or was brought by copies, and complete; so nothing waits for
+  // a release to the whole cluster, which takes longer than a stage (gate and
+  // up of 32768 rows, at that step: 727 us with it, 612 without).
   __device__ static __forceinline__ void arrive(uint32_t bar) {
     if (PAIR)
       asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(

@@ -1,6 +1,10 @@
 // Microscaled 4-bit numbers (mx.cuh): quantising rows and weight matrices,
 // laying matrices out for the products, and expanding both again.  Each
-// kernel reads its input once and writes its output once, so bytes bound it.
+// kernel reads its input once and writes its output once.  Measured: 8192 x
+// 7168 bf16 rows, blocks of 32, quantised 28 to 31 us, expanded 23 to 24 (148 MB
+// each, 22 us at 6.8 TB/s); eight bf16 matrices of 7168 x 2048, blocks of 16,
+// quantised 71 us (301 MB, 44 us), packed 22 (132 MB, 19), expanded 49 (301 MB,
+// 44).  Quantising is bound by issue (slots 72 to 81% busy), the others by bytes.
 #include "launch.cuh"
 #include "mx.cuh"
 

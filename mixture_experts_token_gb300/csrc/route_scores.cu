@@ -18,6 +18,13 @@
 // searched again.  Without a bias, and where no sum of scores is compared, the
 // logits rank, and there is no error to allow for; equal ones are told apart
 // where near ties are.
+//
+// Measured, 256 experts in 8 groups, 4 kept, 8 chosen, sigmoid with a bias:
+// 65536 tokens 50 us (the bytes need 10.5; 607 instructions a token, issue slots
+// 69% busy), one token 3.6 us.  A row that float64 ranks adds 1.3 us where
+// candidates are near, 3.6 where group sums are, 17 to 20 in rank64().  The
+// gradient, 65536 tokens: 22 us (73 MB must move, 10.8 us; 105 MB, 15.5 us, if
+// HBM reads 64 bytes for a chosen logit).
 #include <float.h>
 #include <limits.h>
 #include <math.h>

@@ -292,6 +292,32 @@ def test_products_of_more_items_than_sms(counts, H, F, block):
 
 
 @pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("counts", [
+    # chunks of two passes of 64 rows, and of two of a pair's 192
+    [30] * 1000 + [5000], [60000, 0, 41000]])
+def test_more_rows_than_work_items(block, counts):
+    c = Case(counts, 32, 64, "bf16", block, seed=17)
+    xq, hq, y = c.steps()
+    assert c.status.item() == 0
+    c.check(xq, hq, y)
+    assert torch.equal(c.whole(), y)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("counts,H,F", [
+    ([384, 385], 512, 128), ([191, 0, 200, 97], 288, 416), ([208], 32, 32),
+    ([1000], 4128, 160), ([130] * 40, 256, 1312)])
+def test_products_on_pairs(counts, H, F, block):
+    """Many rows a group: odd numbers of column tiles, halves of rows that end
+    inside a copy, one stage and many."""
+    c = Case(counts, H, F, "bf16", block, seed=18)
+    xq, hq, y = c.steps()
+    assert c.status.item() == 0
+    c.check(xq, hq, y)
+    assert torch.equal(c.whole(), y)
+
+
+@pytest.mark.parametrize("block", [16, 32])
 def test_many_experts_one_token(block):
     E, k, H, F = 200, 6, 160, 96
     counts = np.zeros(E, dtype=int)
@@ -407,8 +433,10 @@ def test_calls_that_share_a_workspace_in_order():
         assert torch.equal(a, b)
 
 
-def test_stalled_copies_time_out_and_context_survives():
-    c = Case([60, 70], 1056, 416, "bf16", 16, seed=13)
+@pytest.mark.parametrize("counts", [[60, 70], [300, 290]])
+def test_stalled_copies_time_out_and_context_survives(counts):
+    """Single CTAs and pairs, in which one's waits end the other's."""
+    c = Case(counts, 1056, 416, "bf16", 16, seed=13)
     try:
         moe.moe_test_stall_gemm_producer(3)
         c.whole()
