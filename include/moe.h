@@ -173,7 +173,7 @@ moe_status_t moe_route(const moe_config_t *cfg, const float *logits,
  *     sigmoid  dlogits_e = a_e (1 - s_e) at chosen experts, else 0
  *     softmax  dlogits_e = (a_e at chosen experts) - s_e * sum a.
  * A chosen index outside [0, E) is skipped.  A logit that is NaN or infinite
- * gets no gradient.
+ * gets no gradient.  dlogits and logits are different memory.
  * ---------------------------------------------------------------------- */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 

@@ -30,13 +30,14 @@
 // between them, which the instruction reads from both.  One CTA's warp issues
 // for both.
 //
-// Measured with blocks of 16, quantising the rows and both products: one token,
-// 8 experts of 7168 x 2048, 198 MB, 42 us (4.7 TB/s; 128 items leave 24 of 152
-// SMs idle in the first product); 64 tokens over 146 such experts 546 to 581 us
-// (5.7 to 6.1 TB/s, with where the buffers lie); 16 experts of 5120 x 8192, 163
-// to 173 us.  32768 rows over 32 experts of 7168 x 2048, 987 us: gate and up 471
-// (4.1 PFLOP/s), down 391 (2.5 PFLOP/s), quantising the rows 139.  On 2048
-// tokens over 16 experts the tensor pipe is 43% busy in gate and up, 26% in down.
+// Measured, quantising the rows and both products: one token, 8 experts of 7168
+// x 2048, blocks of 16, 198 MB, 42 us (4.7 TB/s; 128 items leave 24 of 152 SMs
+// idle in the first product); 64 tokens over 146 such experts, blocks of 32, 546
+// to 581 us (5.7 to 6.1 TB/s, with where the buffers lie); 16 experts of 5120 x
+// 8192, a row each, 160 to 173.  32768 rows over 32 experts of 7168 x 2048, blocks
+// of 16, 990 us: gate and up 471 (4.1 PFLOP/s), down 391 (2.5 PFLOP/s), quantising
+// the rows 139.  On 2048 tokens over 16 experts the tensor pipe is 43% busy in
+// gate and up, 26% in down.
 #pragma once
 
 #include <atomic>

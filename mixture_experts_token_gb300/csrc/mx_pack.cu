@@ -4,7 +4,8 @@
 // 7168 bf16 rows, blocks of 32, quantised 28 to 31 us, expanded 23 to 24 (148 MB
 // each, 22 us at 6.8 TB/s); eight bf16 matrices of 7168 x 2048, blocks of 16,
 // quantised 71 us (301 MB, 44 us), packed 22 (132 MB, 19), expanded 49 (301 MB,
-// 44).  Quantising is bound by issue (slots 72 to 81% busy), the others by bytes.
+// 44).  Rows both ways and quantising matrices are bound by issue (slots 72 to 81%
+// busy), the others by bytes.
 #include "launch.cuh"
 #include "mx.cuh"
 
@@ -22,8 +23,8 @@ template <>
 struct Eight<float> {
   float v[8];
   __device__ __forceinline__ void load(const float* p) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *(reinterpret_cast<const float4*>(p) + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
@@ -38,7 +39,7 @@ template <>
 struct Eight<__nv_bfloat16> {
   uint32_t w[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
   }
   __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
@@ -68,7 +69,9 @@ __device__ __forceinline__ void store8(const float (&v)[8],
 }
 
 // Rows, eight values a thread and a piece; a CTA takes kPieces * kThreads
-// pieces in a row, all of which it loads before it uses one.
+// pieces in a row, all of which it loads before it uses one.  (Plain loads:
+// those of constant memory may not see what the kernel before writes while
+// this one has begun.)
 constexpr int kPieces = 4;
 
 // The row and the place in it of a thread's pieces, kThreads apart.
@@ -101,9 +104,8 @@ struct Place {
 // A block is two or four lanes.
 template <int BLOCK, typename T>
 __global__ void __launch_bounds__(kThreads)
-    quantize_rows_kernel(const T* __restrict__ x, int R, int K, float r,
-                         uint8_t* __restrict__ codes,
-                         uint8_t* __restrict__ scales) {
+    quantize_rows_kernel(const T* x, int R, int K, float r, uint8_t* codes,
+                         uint8_t* scales) {
   constexpr int kLanes = BLOCK / 8;
   launch::wait_for_previous();
   launch::let_next_start();
@@ -151,9 +153,8 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int BLOCK, typename T>
 __global__ void __launch_bounds__(kThreads)
-    dequantize_rows_kernel(const uint8_t* __restrict__ codes,
-                           const uint8_t* __restrict__ scales, int R, int K,
-                           float scale, T* __restrict__ x) {
+    dequantize_rows_kernel(const uint8_t* codes, const uint8_t* scales, int R,
+                           int K, float scale, T* x) {
   launch::wait_for_previous();
   launch::let_next_start();
   const long long pieces = static_cast<long long>(R) * (K / 8);
@@ -165,9 +166,9 @@ __global__ void __launch_bounds__(kThreads)
   for (int p = 0; p < kPieces; ++p) {
     const long long i = first + p * kThreads + threadIdx.x;
     if (i < pieces) {
-      c[p] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-      byte[p] = __ldg(scales + row_scale_at(BLOCK, R, place.row,
-                                            place.at / (BLOCK / 8)));
+      c[p] = reinterpret_cast<const uint32_t*>(codes)[i];
+      byte[p] = scales[row_scale_at(BLOCK, R, place.row,
+                                    place.at / (BLOCK / 8))];
     }
     place.next();
   }

@@ -342,7 +342,7 @@ __device__ __forceinline__ void load_row(const float* row, int e0, int E,
       for (int i = 0; i < EPL; i += 4) {
         float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (FULL || e0 + i < E)
-          v = __ldg(reinterpret_cast<const float4*>(row + e0 + i));
+          v = *reinterpret_cast<const float4*>(row + e0 + i);
         c[i] = v.x, c[i + 1] = v.y, c[i + 2] = v.z, c[i + 3] = v.w;
       }
       return;
@@ -350,7 +350,7 @@ __device__ __forceinline__ void load_row(const float* row, int e0, int E,
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i)
-    c[i] = FULL || e0 + i < E ? __ldg(row + e0 + i) : -INFINITY;
+    c[i] = FULL || e0 + i < E ? row[e0 + i] : -INFINITY;
 }
 
 // c of a logit l; m and inv: the softmax's largest logit and 1 / its sum.
@@ -607,10 +607,9 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
       float v = -INFINITY;
       if (lane < total) {
         e = cand_e[warp][lane];
-        l = __ldg(row + e);
-        v = rank_by<RANK>(l, RANK != kByLogit && a.bias ? __ldg(a.bias + e)
-                                                        : 0.0f,
-                          m, inv);
+        l = row[e];
+        v = rank_by<RANK>(
+            l, RANK != kByLogit && a.bias ? a.bias[e] : 0.0f, m, inv);
       }
       int rank = 0;
 #pragma unroll 4
@@ -634,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
         __syncwarp();
       }
       e = cand_e[warp][lane];
-      l = lane < a.k ? __ldg(row + e) : 0.0f;
+      l = lane < a.k ? row[e] : 0.0f;
     } else {
       e = rank64(a, row, lane, mine64, &m, &z);
       l = lane < a.k ? row[e] : 0.0f;
@@ -689,13 +688,13 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
     *d = 0.0f;
     const long long t = first + tok;
     if (t < a.T && j < a.k) {
-      const int i = __ldg(a.idx + t * a.k + j);
-      *d = __ldg(a.dw + t * a.k + j);
+      const int i = a.idx[t * a.k + j];
+      *d = a.dw[t * a.k + j];
       if (i >= 0 && i < a.E) *e = i;
     }
   };
   const auto logit = [&](long long first, int e) {
-    return e >= 0 ? __ldg(a.logits + (first + tok) * a.E + e) : 0.0f;
+    return e >= 0 ? a.logits[(first + tok) * a.E + e] : 0.0f;
   };
   // the next tokens' choices and their logits come while these are worked on
   int next_e;
@@ -725,13 +724,13 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
         const float* row = a.logits + (t0 + r) * a.E;
         float most = -FLT_MAX;
         for (int i = lane; i < a.E; i += 32) {
-          const float v = __ldg(row + i);
+          const float v = row[i];
           if (fabsf(v) <= FLT_MAX) most = fmaxf(most, v);
         }
         most = warp_max(most);
         float sum = 0.0f;
         for (int i = lane; i < a.E; i += 32) {
-          const float v = __ldg(row + i);
+          const float v = row[i];
           if (fabsf(v) <= FLT_MAX) sum += expf(v - most);
         }
         sum = warp_sum(sum);
@@ -785,7 +784,7 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
         const float f = __shfl_sync(kAll, -all / z, r * LANES);
         if (wide) {
           for (int i = lane * 4; i < a.E; i += 128) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(row + i));
+            const float4 v = *reinterpret_cast<const float4*>(row + i);
             float4 o;
             o.x = fabsf(v.x) <= FLT_MAX ? f * expf(v.x - most) : 0.0f;
             o.y = fabsf(v.y) <= FLT_MAX ? f * expf(v.y - most) : 0.0f;
@@ -795,7 +794,7 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
           }
         } else {
           for (int i = lane; i < a.E; i += 32) {
-            const float v = __ldg(row + i);
+            const float v = row[i];
             out[i] = fabsf(v) <= FLT_MAX ? f * expf(v - most) : 0.0f;
           }
         }
@@ -940,7 +939,8 @@ moe_status_t moe_route_scores_backward(const moe_config_t* cfg,
   if (!options_ok(*cfg, opt)) return MOE_ERR_INVALID_ARG;
   if (cfg->T == 0) return MOE_OK;
   if (!ok_ptr(logits, false) || !ok_ptr(topk_idx, false) ||
-      !ok_ptr(dtopk_w, false) || !ok_ptr(dlogits, false))
+      !ok_ptr(dtopk_w, false) || !ok_ptr(dlogits, false) ||
+      dlogits == logits)  // a row is written while it is read
     return MOE_ERR_INVALID_ARG;
   const BackArgs a = {logits, topk_idx, dtopk_w, dlogits, cfg->T, cfg->E,
                       cfg->k, opt->renorm != 0, opt->scale};

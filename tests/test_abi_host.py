@@ -368,7 +368,9 @@ def test_route_scores_arguments(m):
         return lib.moe_route_scores(ctypes.byref(cfg), o, x, b, i, w, None,
                                     None)
 
-    def bwd(x=p, i=p, d=p, g=p, **kw):
+    other = ctypes.c_void_p(0x2000)
+
+    def bwd(x=p, i=p, d=p, g=other, **kw):
         o = ctypes.byref(m.make_route_scores(**{**good, **kw}))
         return lib.moe_route_scores_backward(ctypes.byref(c), o, x, i, d, g,
                                              None)
@@ -383,6 +385,7 @@ def test_route_scores_arguments(m):
         assert fwd(**kw) == bad and bwd(**kw) == bad, kw
     assert fwd(w=None) == bad and fwd(b=odd) == bad
     assert bwd(d=None) == bad and bwd(g=None) == bad
+    assert bwd(g=p) == bad                # over the logits
     assert fwd(cfg=cfg_of(m, E=12, k=13)) == bad
     assert lib.moe_route_scores(ctypes.byref(c), None, p, None, p, p, None,
                                 None) == bad

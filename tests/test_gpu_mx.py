@@ -433,6 +433,50 @@ def test_calls_that_share_a_workspace_in_order():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("block", [16, 32])
+def test_calls_at_once_on_three_streams(block):
+    """Each with a workspace of its own: a few rows, singles, pairs."""
+    cases = [Case(n, 512, 256, "bf16", block, seed=20 + i) for i, n in
+             enumerate(([1], [30, 0, 50], [300, 290]))]
+    want = [c.whole() for c in cases]
+    room = [moe.mx_workspace(c.cfg, c.mx) for c in cases]
+    outs = [torch.zeros_like(y) for y in want]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, ws, y, s in zip(cases, room, outs, streams):
+            moe.moe_gmm_swiglu_mx(c.cfg, c.mx, c.x, c.offsets, *c.packs,
+                                  *c.scales, y, c.status, ws, stream=s)
+    torch.cuda.synchronize()
+    for c, a, b in zip(cases, outs, want):
+        assert torch.equal(a, b) and c.status.item() == 0
+
+
+def test_inputs_written_by_the_kernel_before():
+    """Rows and offsets that torch writes on the stream just before a call."""
+    c = Case([40, 25, 7], 512, 256, "bf16", 16, seed=30)
+    offsets = [torch.tensor(o, dtype=torch.int32).cuda()
+               for o in ([0, 40, 65, 72], [0, 0, 1, 72], [0, 72, 72, 72])]
+    rows = [c.x.clone(), -c.x, c.x.flip(0).contiguous()]
+    ws = moe.mx_workspace(c.cfg, c.mx)
+
+    def call(x, o):
+        y = torch.zeros_like(x)
+        moe.moe_gmm_swiglu_mx(c.cfg, c.mx, x, o, *c.packs, *c.scales, y,
+                              c.status, ws)
+        return y
+    want = []
+    for x, o in zip(rows, offsets):
+        torch.cuda.synchronize()
+        want.append(call(x, o))
+    x, o = torch.zeros_like(c.x), torch.zeros_like(offsets[0])
+    for _ in range(10):
+        for i in range(3):
+            x.copy_(rows[i])
+            o.copy_(offsets[i])
+            assert torch.equal(call(x, o), want[i])
+
+
 @pytest.mark.parametrize("counts", [[60, 70], [300, 290]])
 def test_stalled_copies_time_out_and_context_survives(counts):
     """Single CTAs and pairs, in which one's waits end the other's."""

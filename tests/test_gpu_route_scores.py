@@ -272,3 +272,57 @@ def test_forward_and_backward_in_a_graph(sigmoid):
         wd = ref.route_backward(new.numpy(), want, dw.cpu().double().numpy(),
                                 sigmoid, True, 2.5)
         assert np.allclose(dl.cpu().numpy(), wd, rtol=1e-4, atol=1e-6)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_two_calls_at_once(sigmoid):
+    """Calls on two streams that overlap, each with memory of its own."""
+    g = torch.Generator().manual_seed(12)
+    T, E, k = 3000, 256, 8
+    cfg = moe.make_config(T, 8, E, k, 0, 1)
+    opt = moe.make_route_scores(SCORES[sigmoid], 8, 4, 2, True, 2.5)
+    bias = (torch.randn(E, generator=g) * 0.05).cuda()
+    dw = torch.randn(T, k, generator=g).cuda()
+    xs = [torch.randn(T, E, generator=g).cuda() for _ in range(2)]
+    outs = [(torch.zeros(T, k, dtype=torch.int32).cuda(),
+             torch.zeros(T, k).cuda(), torch.zeros(T, E).cuda())
+            for _ in range(4)]
+
+    def step(x, o, **kw):
+        moe.moe_route_scores(cfg, opt, x, bias, o[0], o[1], **kw)
+        moe.moe_route_scores_backward(cfg, opt, x, o[0], dw, o[2], **kw)
+    for x, o in zip(xs, outs):
+        step(x, o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(20):
+        for x, o, s in zip(xs, outs[2:], streams):
+            step(x, o, stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(outs[:2], outs[2:]):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+
+
+def test_inputs_written_by_the_kernel_before():
+    """Logits that change between calls, by torch and by the backward."""
+    g = torch.Generator().manual_seed(13)
+    T, E, k = 2000, 64, 6
+    cfg = moe.make_config(T, 8, E, k, 0, 1)
+    opt = moe.make_route_scores(moe.MOE_SCORE_SOFTMAX, 1, 1, 1, False, 1.0)
+    src = [torch.randn(T, E, generator=g).cuda() for _ in range(4)]
+    x, dl = torch.zeros(T, E).cuda(), torch.zeros(T, E).cuda()
+    dw = torch.ones(T, k).cuda()
+    idx = [torch.zeros(T, k, dtype=torch.int32).cuda() for _ in range(8)]
+    w = torch.zeros(T, k).cuda()
+    grads = []
+    for i in range(4):
+        x.copy_(src[i])
+        moe.moe_route_scores(cfg, opt, x, None, idx[i], w)
+        moe.moe_route_scores_backward(cfg, opt, x, idx[i], dw, dl)
+        moe.moe_route_scores(cfg, opt, dl, None, idx[4 + i], w)
+        grads.append(dl.clone())
+    torch.cuda.synchronize()
+    for got, rows in zip(idx, src + grads):
+        want = np.argsort(-rows.cpu().numpy(), 1, kind="stable")[:, :k]
+        assert np.array_equal(got.cpu().numpy(), want)
