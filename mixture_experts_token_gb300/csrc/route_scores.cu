@@ -10,14 +10,13 @@
 // whose order matters are nearer than that bound allows (about one row in a
 // thousand), again in float64.
 //
-// Forward, in float32: lane i holds the i-th run of EPL consecutive experts.
-// Each lane's two largest c give, in k rounds of a warp maximum, a threshold
-// that at least k values reach; the few that do (and those within the error of
-// it) are put in a row in shared memory, one to a lane, and each counts those
-// before it.  That is its rank: no list is sorted and no lane's values are
-// searched again.  Without a bias, and where no sum of scores is compared, the
-// logits rank, and there is no error to allow for; equal ones are told apart
-// where near ties are.
+// Forward, in float32: lane i holds the i-th run of EPL consecutive experts,
+// and its three largest c with the expert's place in the lowest bits.  k rounds
+// of a warp maximum take the chosen in order, the lane that has one bringing its
+// next.  Where a lane could have brought a fourth, or two that follow each other
+// are nearer than the errors of c and of those bits allow, all that reach the
+// k-th are put in a row and ranked in float64.  Without a bias, and where no sum
+// of scores is compared, the logits rank, and the bits are the only error.
 //
 // Measured, 256 experts in 8 groups, 4 kept, 8 chosen, sigmoid with a bias:
 // 65536 tokens 50 us (the bytes need 10.5; 607 instructions a token, issue slots
@@ -54,18 +53,16 @@ struct Args {
   float scale;
 };
 
-__device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t o) {
-  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
-}
+// The warp's largest and smallest (a NaN only if all are).
 __device__ __forceinline__ float warp_max(float v) {
-  return unordered(__reduce_max_sync(kAll, ordered(v)));
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ float warp_min(float v) {
-  return unordered(__reduce_min_sync(kAll, ordered(v)));
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 template <typename T>
 __device__ __forceinline__ T warp_sum(T v) {
@@ -364,6 +361,33 @@ __device__ __forceinline__ float rank_by(float l, float bias, float m,
   return s + bias;
 }
 
+// A lane's three largest of v, with the place in the lowest bits.
+template <int EPL>
+struct Top {
+  float a = -INFINITY, b = -INFINITY, c = -INFINITY;
+  static __device__ __forceinline__ float key(float v, int i) {
+    return __uint_as_float(
+        (__float_as_uint(fmaxf(v, -FLT_MAX)) & ~(EPL - 1u)) | i);
+  }
+  __device__ __forceinline__ Top() {}
+  __device__ __forceinline__ explicit Top(const float (&v)[EPL]) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      float k = key(v[i], i);
+      const float under = fminf(a, k);
+      a = fmaxf(a, k);
+      if (EPL < 2) continue;
+      k = under;
+      const float third = fminf(b, k);
+      b = fmaxf(b, k);
+      if (EPL > 2) c = fmaxf(c, third);
+    }
+  }
+};
+// What a key may be off by, of its magnitude: EPL - 1 units in the last place.
+template <int EPL>
+constexpr float kKeyErr = EPL * 1.1920929e-7f;
+
 // Puts the experts of the lanes' hits into the list, up to 32, in any order;
 // how many there are (33 or more: too many).
 __device__ __forceinline__ int collect(uint32_t hits, int e0, int lane,
@@ -386,10 +410,10 @@ __device__ __forceinline__ int collect(uint32_t hits, int e0, int lane,
 template <int EPL, int RANK, bool FULL>
 __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
     scores_kernel(const Args a) {
-  // a row's candidates, then (c, expert) by rank; the row's numbers, where
-  // groups are not whole lanes and in rank64()
-  __shared__ float cand_c[kWarps][33];
-  __shared__ int cand_e[kWarps][33];
+  // the chosen, a key and its lane's first expert; candidates of a closer look;
+  // the row's numbers, where groups are not whole lanes and in rank64()
+  __shared__ float2 chosen[kWarps][32];
+  __shared__ int cand_e[kWarps][32];
   extern __shared__ long long row_c[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long* mine64 = row_c + warp * (32 * EPL);
@@ -422,13 +446,14 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
     const float* row = a.logits + t * a.E;
     float c[EPL];
     load_row<EPL, FULL>(row, e0, a.E, wide, c);
-    bool again = RANK != kByLogit && most_bias == INFINITY;
+    float nan = RANK != kByLogit && most_bias == INFINITY ? NAN : 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      again |= (FULL || e0 + i < a.E) && !(fabsf(c[i]) <= FLT_MAX);
+      if (FULL || e0 + i < a.E) nan = fmaf(c[i], 0.0f, nan);
+    bool again = nan != 0.0f;  // a logit or a bias is not finite
 
     // scores, and the most that a c may be off by
-    float m = 0.0f, z = 1.0f, inv = 1.0f, err = 0.0f;
+    float m = 0.0f, z = 1.0f, inv = 1.0f, err = 0.0f, most = 0.0f;
     if (RANK == kBySoftmax || (RANK == kByLogit && !a.sigmoid && !a.renorm)) {
       m = c[0];
 #pragma unroll
@@ -458,24 +483,18 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
       // 2^-22, by 17 2^-24 from the arguments (far terms: 10 bits of them at
       // most weigh) and by 37 2^-24 from adding: below 2^-18.  Adding the
       // bias: half an ulp.
-      const float most = RANK == kBySoftmax ? inv : 1.0f;
+      most = RANK == kBySoftmax ? inv : 1.0f;
       err = (RANK == kBySoftmax ? 3.8146973e-6f : 4.7683716e-7f) * most +
             1.1920929e-7f * (most + most_bias);
     }
 
-    // this lane's two largest
-    float m1 = -INFINITY, m2 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      m2 = fmaxf(m2, fminf(m1, c[i]));
-      m1 = fmaxf(m1, c[i]);
-    }
+    Top<EPL> top(c);
     bool kept = true;
     if (select) {
       // sums of n c are off by n errors, and adding them by n (n - 1) / 2
       const float group_err = a.group_top * (a.group_top + 1) * err;
       if (whole) {
-        float g1 = m1, g2 = m2;
+        float g1 = top.a, g2 = top.b;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           if (o >= lanes) break;
@@ -484,26 +503,30 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
           g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
           g1 = fmaxf(g1, o1);
         }
-        // (one zero; lanes past the last expert are behind all groups)
-        uint32_t o = FULL || e0 < a.E
-                         ? ordered((a.group_top == 2 ? g1 + g2 : g1) + 0.0f)
-                         : 0u;
+        // (lanes past the last expert are behind all groups)
+        float o = FULL || e0 < a.E ? (a.group_top == 2 ? g1 + g2 : g1)
+                                   : -INFINITY;
         kept = false;
-        uint32_t last = 0;
+        float last = 0.0f;
 #pragma unroll 4
         for (int g = 0; g < a.top_groups; ++g) {
-          last = __reduce_max_sync(kAll, o);
+          last = warp_max(o);
           if (o == last) {
             kept = true;
-            o = 0;
+            o = -INFINITY;
           }
         }
-        const uint32_t out = __reduce_max_sync(kAll, o);
-        // equal sums, or sums that the error may have exchanged
+        const float out = warp_max(o);
+        // equal sums, or sums that the errors may have exchanged
+        const float keys =
+            kKeyErr<EPL> * (RANK == kByLogit
+                                ? fabsf(last) + fabsf(out)
+                                : 2 * a.group_top * (most + most_bias));
         if (__popc(__ballot_sync(kAll, kept)) != a.top_groups * lanes ||
-            (RANK != kByLogit &&
-             !(unordered(last) - unordered(out) > group_err))) {
-          const float least = (a.group_top == 2 ? g2 : g1) - 2.0f * err;
+            !(last - out > group_err + keys + FLT_MIN)) {
+          const float g = a.group_top == 2 ? g2 : g1;
+          const float least =
+              g - 2.0f * (err + kKeyErr<EPL> * fabsf(g) + FLT_MIN);
           uint32_t hits = 0;
 #pragma unroll
           for (int i = 0; i < EPL; ++i)
@@ -515,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
             kept = keep_groups64(a, row, lane < n ? cand_e[warp][lane] : 0, n,
                                  lane, lanes);
         }
-        if (!kept) m1 = m2 = -INFINITY;
+        if (!kept) top = Top<EPL>();
       } else {
         // a lane a group (or two), over the row's c in shared memory
         float* rc = reinterpret_cast<float*>(mine64);
@@ -566,73 +589,80 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
         }
         const uint32_t low = __ballot_sync(kAll, k0);
         const uint32_t high = __ballot_sync(kAll, k1);
-        m1 = m2 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
           const int g = (e0 + i) / size;
           if (g >= a.groups || !((g < 32 ? low >> g : high >> (g - 32)) & 1))
             c[i] = -INFINITY;
-          m2 = fmaxf(m2, fminf(m1, c[i]));
-          m1 = fmaxf(m1, c[i]);
         }
+        top = Top<EPL>(c);
       }
     }
 
-    // a threshold that at least k values reach, if the lanes' pairs hold k
-    uint32_t o1 = ordered(m1), o2 = ordered(m2), reached = 0;
+    // The largest left in the warp, k times: its lane brings the next.
+    float reached = 0.0f, behind = -INFINITY;
+    {
+      float o1 = top.a, o2 = top.b, o3 = top.c;
+      __syncwarp();
 #pragma unroll 4
-    for (int j = 0; j < a.k; ++j) {
-      reached = __reduce_max_sync(kAll, o1);
-      if (o1 == reached) {
-        o1 = o2;
-        o2 = 0;
+      for (int j = 0; j < a.k; ++j) {
+        reached = warp_max(o1);
+        if (o1 == reached) {
+          chosen[warp][j] = make_float2(o1, __int_as_float(e0));
+          o1 = o2;
+          o2 = o3;
+          o3 = -INFINITY;
+        }
       }
+      behind = fmaxf(warp_max(o1), -FLT_MAX);
     }
-    // values within twice the error of it stay, so that what is left out is
-    // surely behind; a threshold of -infinity (or none) leaves nothing out
-    const float bar = reached > ordered(-FLT_MAX)
-                          ? fmaxf(unordered(reached) - 2.0f * err, -FLT_MAX)
-                          : -FLT_MAX;
-    uint32_t hits = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (c[i] >= bar) hits |= 1u << i;
-    if (!kept) hits = 0;
-    const int total = collect(hits, e0, lane, cand_e[warp]);
-    again |= total > 32 || total < a.k;
+    again |= !(reached > -3.4e38f);  // fewer than k
 
     int e = 0;
     float l = 0.0f;
     if (!__any_sync(kAll, again)) {
-      float v = -INFINITY;
-      if (lane < total) {
-        e = cand_e[warp][lane];
-        l = row[e];
-        v = rank_by<RANK>(
-            l, RANK != kByLogit && a.bias ? a.bias[e] : 0.0f, m, inv);
-      }
-      int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < total; ++j)
-        rank += __shfl_sync(kAll, v, j) > v;
-      // the list by rank: equal c leave a place empty
-      cand_c[warp][lane] = INFINITY;
-      __syncwarp();
-      if (lane < total) {
-        cand_c[warp][rank] = v;
-        cand_e[warp][rank] = e;
+      // Keys that reach the k-th, equal ones and those that their lane did not
+      // bring among them: as many as were chosen.
+      int n = (top.a >= reached) + (top.b >= reached) + (top.c >= reached);
+      if (EPL > 3 && __any_sync(kAll, n == 3)) {
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          n += kept && Top<EPL>::key(c[i], i) >= reached;
       }
       __syncwarp();
-      const float here = cand_c[warp][lane];
-      const float behind = __shfl_down_sync(kAll, here, 1);
-      // nearer than the error allows, and before or among the k chosen
-      if (__any_sync(kAll, lane < a.k && lane + 1 < total &&
-                               !(here - behind > 2.0f * err))) {
-        rank = rank_candidates64(a, row, e, total, lane);
-        if (lane < total) cand_e[warp][rank] = e;
-        __syncwarp();
+      const float2 own = chosen[warp][lane];
+      float next = __shfl_down_sync(kAll, own.x, 1);
+      if (lane == a.k - 1) next = behind;
+      e = __float_as_int(own.y) + (__float_as_uint(own.x) & (EPL - 1u));
+      // nearer than the errors allow, before or among the k chosen
+      const bool near =
+          lane < a.k &&
+          !(own.x - next > 2.0f * err + FLT_MIN +
+                               kKeyErr<EPL> * (fabsf(own.x) + fabsf(next)));
+      if (__any_sync(kAll, near) || __reduce_add_sync(kAll, n) != a.k) {
+        // what is left out is surely behind
+        const float bar = fmaxf(
+            reached - 2.0f * (err + kKeyErr<EPL> * fabsf(reached) + FLT_MIN),
+            -FLT_MAX);
+        uint32_t hits = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (c[i] >= bar) hits |= 1u << i;
+        if (!kept) hits = 0;
+        const int total = collect(hits, e0, lane, cand_e[warp]);
+        again = total > 32 || total < a.k;
+        if (!again) {
+          const int mine = lane < total ? cand_e[warp][lane] : 0;
+          const int rank = rank_candidates64(a, row, mine, total, lane);
+          __syncwarp();
+          if (lane < total) cand_e[warp][rank] = mine;
+          __syncwarp();
+          e = cand_e[warp][lane];
+        }
       }
-      e = cand_e[warp][lane];
+    }
+    if (!__any_sync(kAll, again)) {
       l = lane < a.k ? row[e] : 0.0f;
     } else {
       e = rank64(a, row, lane, mine64, &m, &z);
@@ -848,7 +878,7 @@ template <int EPL, int RANK, bool FULL>
 cudaError_t launch_scores(const Args& a, cudaStream_t s) {
   constexpr auto kernel = scores_kernel<EPL, RANK, FULL>;
   constexpr int kBytes = kWarps * 32 * EPL * sizeof(long long);
-  static_assert(kBytes + kWarps * 272 <= 48 * 1024, "no larger than any CTA's");
+  static_assert(kBytes + kWarps * 384 <= 48 * 1024, "no larger than any CTA's");
   launch::Device d;
   int per_sm = 1;
   cudaError_t e = launch::device(&d);
