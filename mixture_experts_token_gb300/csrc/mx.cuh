@@ -190,6 +190,36 @@ __device__ __forceinline__ float over_scale(float v, const Block& b) {
   return BLOCK == 32 ? q : fmaf(-fmaf(q, b.s, -v), b.inv, q);
 }
 
+// Two numbers an instruction: quantising is bound by the instructions issued.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+// over_scale() of r v for two v, each with a block (r: 1 with blocks of 32), in
+// the same steps with the signs of v, the reciprocal and the remainder turned.
+template <int BLOCK>
+__device__ __forceinline__ float2 over_scale2(float2 v, float r,
+                                              const Block& b,
+                                              const Block& c) {
+  if (BLOCK == 32) return mul2(v, make_float2(b.inv, c.inv));
+  const float2 inv = make_float2(-b.inv, -c.inv);
+  const float2 minus = mul2(v, make_float2(-r, -r)), q = mul2(minus, inv);
+  return fma2(fma2(q, make_float2(b.s, c.s), minus), inv, q);
+}
+
 // Magnitudes, as bits whose order is theirs; those of a NaN or an infinity are
 // larger than any number's.
 __device__ __forceinline__ uint32_t largest(const float (&v)[8]) {

@@ -134,8 +134,12 @@ __global__ void __launch_bounds__(kThreads)
         block_scale<BLOCK>(BLOCK == 16 ? scaled_bits(most, r) : most);
     float q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      q[j] = over_scale<BLOCK>(BLOCK == 16 ? v[p].at(j) * r : v[p].at(j), b);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 two = over_scale2<BLOCK>(
+          make_float2(v[p].at(j), v[p].at(j + 1)), r, b, b);
+      q[j] = two.x;
+      q[j + 1] = two.y;
+    }
     const uint32_t c = encode8(q);
     if (all || i < pieces) {
       reinterpret_cast<uint32_t*>(codes)[i] = c;
@@ -180,9 +184,11 @@ __global__ void __launch_bounds__(kThreads)
     float v[8];
     decode8(c[p], v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] *= s;  // exact
-      if (BLOCK == 16) v[j] *= scale;
+    for (int j = 0; j < 8; j += 2) {
+      float2 two = mul2(make_float2(v[j], v[j + 1]), make_float2(s, s));  // exact
+      if (BLOCK == 16) two = mul2(two, make_float2(scale, scale));
+      v[j] = two.x;
+      v[j + 1] = two.y;
     }
     store8(v, x + i * 8);
   }
@@ -289,10 +295,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
           float q[2][8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 f =
-                Two<T>::load(col + (h * BLOCK + 8 * j + e) * kTurnN);
-            q[0][e] = over_scale<BLOCK>(BLOCK == 16 ? f.x * r : f.x, b[0]);
-            q[1][e] = over_scale<BLOCK>(BLOCK == 16 ? f.y * r : f.y, b[1]);
+            const float2 f = over_scale2<BLOCK>(
+                Two<T>::load(col + (h * BLOCK + 8 * j + e) * kTurnN), r, b[0],
+                b[1]);
+            q[0][e] = f.x;
+            q[1][e] = f.y;
           }
           c[0][h * (BLOCK / 8) + j] = encode8(q[0]);
           c[1][h * (BLOCK / 8) + j] = encode8(q[1]);

@@ -94,18 +94,20 @@ __device__ __forceinline__ float exp_near(float x) {
 // the softmax's sum over all experts under the largest logit m.  Sums of
 // chosen scores are taken relative to the largest of them where all are small,
 // so that they do not vanish.
+template <int RANK>
 __device__ __forceinline__ float weight(const Args& a, bool chosen, float l,
                                         float m, float z) {
+  const bool sigmoid = RANK == kByLogit ? a.sigmoid : RANK == kBySigmoid;
   chosen = chosen && fabsf(l) <= FLT_MAX;
   float s = 0.0f;
-  if (a.sigmoid && (!a.renorm || __any_sync(kAll, chosen && l > -60.0f))) {
+  if (sigmoid && (!a.renorm || __any_sync(kAll, chosen && l > -60.0f))) {
     const float x = exp_near(fmaxf(-fabsf(l), -87.0f));
     if (chosen) s = (l < 0.0f ? x : 1.0f) * rcp_fast(1.0f + x);
   } else {
     const float top = a.renorm ? warp_max(chosen ? l : -FLT_MAX) : m;
     if (chosen) {
       s = expf(l - top);
-      if (a.sigmoid)
+      if (sigmoid)
         s /= 1.0f + expf(l);
       else if (!a.renorm)
         s /= z;
@@ -669,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
       l = lane < a.k ? row[e] : 0.0f;
       if (lane < a.k && a.bias && !(fabsf(a.bias[e]) <= FLT_MAX)) l = INFINITY;
     }
-    const float w = weight(a, lane < a.k, l, m, z);
+    const float w = weight<RANK>(a, lane < a.k, l, m, z);
     if (lane < a.k) {
       a.idx[t * a.k + lane] = e;
       a.w[t * a.k + lane] = w;
