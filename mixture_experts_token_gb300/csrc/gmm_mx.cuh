@@ -14,8 +14,8 @@
 //   * a thread brings the weights' records by bulk copy and the rows' codes by
 //     TMA, 256 of k a stage (rows past the group's are other groups' or zeros;
 //     they reach only columns that are not written);
-//   * four warps, one for each quarter of the lanes of tensor memory, write a
-//     stage's scales there, those of the weights from shared memory and those
+//   * four warps (or eight in turn), one for each quarter of the lanes of tensor
+//     memory, write a stage's scales there, those of the weights from shared memory and those
 //     of the rows from global memory;
 //   * a warp issues the matrix instructions;
 //   * four warps, or eight or sixteen, turn the sums into rows of the output, a
@@ -264,7 +264,13 @@ struct Gmm {
   static constexpr int kLoadWarp = kEpiWarps;
   static constexpr int kMmaWarp = kLoadWarp + 1;
   static constexpr int kScaleWarp = kMmaWarp + 1;
-  static constexpr int kWarps = kScaleWarp + kScaleWarps;
+  // Four warps write scales to tensor memory; where rows are many, whose stages
+  // are short, two such teams do so in turn, each every other stage (down, 32768
+  // rows: 391 us with one, 360 with two, 338 with the rows' scales written before
+  // the stage is there, 346 with four).  Gate and up have no registers for two:
+  // 455 us against 438.
+  static constexpr int kTeams = PAIR && !DUAL ? 2 : 1;
+  static constexpr int kWarps = kScaleWarp + kScaleWarps * kTeams;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kMats = DUAL ? 2 : 1;
   static constexpr int kTiles = scale_tiles(BLOCK);  // of 128 rows, a stage
@@ -424,8 +430,8 @@ struct Gmm {
     else if (warp == kMmaWarp)
       multiply(a, sb, b, chunks, n_items, tiles, tmem, lane, abort_flag);
     else
-      load_scales(a, sb, b, chunks, n_items, tiles, tmem, warp & 3, lane,
-                  abort_flag);
+      load_scales(a, sb, b, chunks, n_items, tiles, tmem, warp & 3,
+                  (warp - kScaleWarp) / kScaleWarps, lane, abort_flag);
     __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
@@ -517,7 +523,7 @@ struct Gmm {
   __device__ static void load_scales(const GmmArgs& a, uint32_t sb,
                                      const Bars& b, const int2* chunks,
                                      int n_items, int tiles, uint32_t tmem,
-                                     int quarter, int lane,
+                                     int quarter, int team, int lane,
                                      volatile int* abort_flag) {
     constexpr int kRows = (NT + 31) / 32;  // rows a lane
     const int stages = a.l.stages(), groups = a.l.K / BLOCK;
@@ -561,9 +567,20 @@ struct Gmm {
     launch::wait_for_previous();
     passes(a, chunks, n_items, tiles, [&](const Item& it) {
       uint32_t next[kRows][kTiles];
-      load(it, 0, next);
+      if (kTeams == 1 || team < stages) load(it, team, next);
 #pragma unroll 1
       for (int s = 0; s < stages; ++s) {
+        if (kTeams > 1 && s % kTeams != team) {  // another team's
+          if (kScaleBufs < kStages) {
+            if (lead == kScaleBufs)
+              back.next();
+            else
+              ++lead;
+          }
+          ring.next();
+          sring.next();
+          continue;
+        }
         // rows' columns: [tile][128 rows][4]
         uint32_t x[kRowTiles * 4];
 #pragma unroll
@@ -571,24 +588,26 @@ struct Gmm {
 #pragma unroll
           for (int i = 0; i < kRowTiles / kTiles * 4; ++i)
             x[j * (kRowTiles / kTiles * 4) + i] = i < kRows ? next[i][j] : 0u;
-        if (s + 1 < stages) load(it, s + 1, next);
-        if (!wait_all(b.full + 8 * ring.st, ring.phase, abort_flag,
-                      a.status))
-          return false;
-        // The instructions that read this buffer have completed: with one for
-        // each stage, before the stage was filled again.
-        if (kScaleBufs < kStages) {
-          if (lead == kScaleBufs) {
-            if (!wait_all(b.empty + 8 * back.st, back.phase, abort_flag,
-                          a.status))
-              return false;
-            back.next();
-          } else {
-            ++lead;
-          }
+        if (s + kTeams < stages) load(it, s + kTeams, next);
+        // The instructions that read this buffer must have completed: with a
+        // buffer for each stage, they had before the stage was filled again.
+        const auto filled = [&] {
+          return wait_all(b.full + 8 * ring.st, ring.phase, abort_flag,
+                          a.status);
+        };
+        if (kScaleBufs == kStages) {
+          if (!filled()) return false;
+        } else if (lead == kScaleBufs) {
+          if (!wait_all(b.empty + 8 * back.st, back.phase, abort_flag,
+                        a.status))
+            return false;
+          back.next();
+        } else {
+          ++lead;
         }
         tc::tc_fence_after();
         tmem_st(out + sring.st * kScales + kScaleX, x);
+        if (kScaleBufs < kStages && !filled()) return false;
         const uint32_t from = sb + ring.st * kStage + kCodeBytes + lane * 16;
 #pragma unroll
         for (int m = 0; m < kMats; ++m) {
