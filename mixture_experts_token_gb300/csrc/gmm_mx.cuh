@@ -85,10 +85,11 @@ cudaError_t launch_gmm_mx_down(const GmmArgs& a, const void* codes,
 
 // Whether passes of 192 rows on SM pairs are faster than passes of 64 on single
 // SMs: by the mean rows of a group, where groups can have more than 64 (routing
-// gives a group at most one row of each token).  32 experts of 7168 x 2048, both
-// products, singles against pairs: 32 rows a group 167 and 179 us, 64 rows 194
-// and 192, 128 rows 300 and 211, 512 rows 968 and 535.  (Passes of 16 rows
-// gained nothing: 113 us for one row a group, 114 in passes of 64.)
+// gives a group at most one row of each token).  32 experts of 7168 x 2048, rows
+// quantised and both products, singles against pairs: 32 rows a group 169 and 171
+// us, 48 rows 173 and 177, 64 rows 194 and 181, 128 rows 300 and 198, 1024 rows
+// 1872 and 890.  (Passes of 16 rows gained nothing: 113 us for one row a group, 114
+// in passes of 64.)
 inline bool many_rows(const GmmArgs& a) {
   return a.tokens > 64 &&
          a.rows > 48ll * std::min(a.n_groups, a.rows);
@@ -838,26 +839,28 @@ struct Gmm {
                                                  const Item& it, int col0,
                                                  int r, int lane,
                                                  const float* h) {
+    // The largest magnitudes of eight rows, each over the block's lanes: pairs of
+    // lanes share out the rows and halve them, until lane % 8 has its row's.
     float q[8];
-    uint32_t most = 0;  // of row lane % 8, this lane's block
+    uint32_t part[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       q[i] = h[i];
-      const uint32_t bits = __float_as_uint(q[i]) & 0x7fffffffu;
-      uint32_t m;
-      if (BLOCK == 32) {
-        m = __reduce_max_sync(0xffffffffu, bits);
-      } else {
-        // (halves apart by masks of their own would run one after the other
-        // behind a check of the masks, many times slower)
-        const uint32_t lo =
-            __reduce_max_sync(0xffffffffu, lane < 16 ? bits : 0u);
-        const uint32_t hi =
-            __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : bits);
-        m = lane < 16 ? lo : hi;
-      }
-      if ((lane & 7) == i) most = m;
+      part[i] = __float_as_uint(q[i]) & 0x7fffffffu;
     }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4 / o; ++i) {
+        const uint32_t even = part[2 * i], odd = part[2 * i + 1];
+        const uint32_t other =
+            __shfl_xor_sync(0xffffffffu, lane & o ? even : odd, o);
+        part[i] = max(lane & o ? odd : even, other);
+      }
+    uint32_t most = part[0];
+#pragma unroll
+    for (int o = 8; o < BLOCK; o <<= 1)
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     // each scale once, then to its block's lanes
     const Block own = block_scale<BLOCK>(most);
 #pragma unroll
