@@ -636,7 +636,9 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
       const float2 own = chosen[warp][lane];
       float next = __shfl_down_sync(kAll, own.x, 1);
       if (lane == a.k - 1) next = behind;
-      e = __float_as_int(own.y) + (__float_as_uint(own.x) & (EPL - 1u));
+      e = min(__float_as_int(own.y) +
+                  static_cast<int>(__float_as_uint(own.x) & (EPL - 1u)),
+              a.E - 1);  // (of lanes that have one no change)
       // nearer than the errors allow, before or among the k chosen
       const bool near =
           lane < a.k &&

@@ -33,7 +33,8 @@ def log_scores(logits, sigmoid):
         if sigmoid:
             return np.minimum(x, 0) - np.log1p(np.exp(-np.abs(x)))
         m = x.max()
-        return x - (m + np.log(np.exp(x - m).sum()))
+        # (m + log would lose log where m is large: ulp(3e38) is 4e22)
+        return (x - m) - np.log(np.exp(x - m).sum())
 
 
 def order(c):

@@ -145,6 +145,36 @@ def test_large_bias_leaves_no_choice_to_rounding():
     check(x, bias, 8, False, 4, 2, 2, True, 1.0)
 
 
+@pytest.mark.parametrize("E,groups,top_groups,group_top",
+                         [(256, 1, 1, 1), (256, 8, 4, 1), (60, 1, 1, 1),
+                          (60, 4, 2, 2), (1000, 1, 1, 1), (28, 1, 1, 1)])
+@pytest.mark.parametrize("score,shift", [("logit", 0.0), ("sigmoid", -0.5),
+                                         ("softmax", -1.0)])
+def test_zeros_and_subnormals_between_other_rows(E, groups, top_groups,
+                                                 group_top, score, shift):
+    """c of zero, of both signs, below the smallest normal number, as low as
+    numbers go and beyond, in rows that one warp has one after another."""
+    g = torch.Generator().manual_seed(14)
+    kinds = [torch.randn(E, generator=g), torch.zeros(E),
+             torch.arange(E) * 1e-44, -torch.arange(E) * 1e-42,
+             torch.where(torch.arange(E) % 2 == 0, 0.0, -0.0),
+             torch.full((E,), -3.4028234e38), torch.full((E,), -3.4e38),
+             3e38 - torch.arange(E) * 1e36 * (600 / E)]
+    x = torch.stack(kinds * 40).float()
+    x = x.repeat(16, 1)
+    bias = None if score == "logit" else torch.full((E,), shift)
+    opt = (6, score != "softmax", groups, top_groups, group_top, False, 1.0)
+    idx, w, st = call(x, bias, *opt)
+    want, ww = ref.route(x[:len(kinds)].numpy(),
+                         None if bias is None else bias.numpy(), *opt)
+    # the last kind ends in infinities
+    assert not torch.isfinite(kinds[-1]).all()
+    assert st == moe.MOE_DEV_NONFINITE
+    assert np.array_equal(idx, np.tile(want, (40 * 16, 1)))
+    ww = np.tile(ww, (40 * 16, 1))
+    assert np.all(np.abs(w - ww) <= 1e-6 * np.abs(ww) + 1e-37)
+
+
 def test_unaligned_logits_and_other_stream():
     g = torch.Generator().manual_seed(5)
     flat = torch.randn(33 * 128 + 1, generator=g).cuda()
