@@ -34,10 +34,11 @@
 // x 2048, blocks of 16, 198 MB, 42 us (4.7 TB/s; 128 items leave 24 of 152 SMs
 // idle in the first product); 64 tokens over 146 such experts, blocks of 32, 546
 // to 581 us (5.7 to 6.1 TB/s, with where the buffers lie); 16 experts of 5120 x
-// 8192, a row each, 160 to 173.  32768 rows over 32 experts of 7168 x 2048, blocks
-// of 16, 990 us: gate and up 471 (4.1 PFLOP/s), down 391 (2.5 PFLOP/s), quantising
-// the rows 139.  On 2048 tokens over 16 experts the tensor pipe is 43% busy in
-// gate and up, 26% in down.
+// 8192, a row each, 160 to 174.  32768 rows over 32 experts of 7168 x 2048, blocks
+// of 16, 896 us: quantising the rows 125, gate and up 438 (4.4 PFLOP/s), down 338
+// (2.8 PFLOP/s).  Of 444 and 338, 385 and 297 are left if nothing reads the sums,
+// 369 and 266 without matrix instructions, 235 and 217 if scales are not loaded
+// either.
 #pragma once
 
 #include <atomic>
@@ -257,9 +258,9 @@ struct Gmm {
   // Warps for each quarter of the lanes, which share an item's rows.  Many rows
   // of both matrices leave tensor memory no second accumulator, and the matrix
   // instructions wait while it is read: 10.8 us of an item's 29 with one warp
-  // a quarter, 7 of 25 with four, 4 of 22 as it is now (32768 rows; a run that
-  // read no sums subtracted).  Down has a second one: 397, 391, 422, 453 us with
-  // one to four.
+  // a quarter, 7 of 25 with four (32768 rows; a run that read no sums
+  // subtracted), 2.5 of 21 as it is now.  Down has a second one: 397, 391, 422,
+  // 453 us with one to four, at that step.
   static constexpr int kRowParts = !PAIR ? 1 : DUAL ? 4 : 2;
   static constexpr int kEpiWarps = 4 * kRowParts;
   static constexpr int kLoadWarp = kEpiWarps;
