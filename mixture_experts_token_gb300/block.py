@@ -265,25 +265,25 @@ _EXPERTS = ("w_gate", "w_up", "w_down")
 
 class DecodeBlock:
     """The block over cfg.T tokens with 4-bit experts (w_gate, w_up, w_down
-    packed; the other weights as TrainBlock's).  ``quant`` says how they are
+    packed; the other weights as TrainBlock's).  ``w4`` says how they are
     held: make_w4()'s, or make_mx()'s, whose tensor scales are w_gate_scale,
     w_up_scale and w_down_scale (absent or None: 1).  The step enqueues its
     calls and waits for nothing, so torch.cuda.graph can capture it."""
 
-    def __init__(self, cfg, opt, quant, weights, logit_offset=None,
+    def __init__(self, cfg, opt, w4, weights, logit_offset=None,
                  device="cuda", route=None, bias=None):
-        self.cfg, self.opt, self.quant = cfg, opt, quant
+        self.cfg, self.opt, self.w4 = cfg, opt, w4
         self.w, self.offset = weights, logit_offset
         self.route, self.bias = route, bias
         self.device = torch.device(device)
-        self.mx = isinstance(quant, MoeMx)
+        self.mx = isinstance(w4, MoeMx)
         _check_route(cfg, route, bias, self.device)
         _check_columns(cfg, weights, self.device)
         _check_router(cfg, weights, logit_offset, self.device)
         size = moe_mx_bytes if self.mx else moe_w4_bytes
         for n, K, N in (("w_gate", cfg.H, cfg.F), ("w_up", cfg.H, cfg.F),
                         ("w_down", cfg.F, cfg.H)):
-            _check(n, weights[n], size(quant, cfg.E, K, N), torch.uint8,
+            _check(n, weights[n], size(w4, cfg.E, K, N), torch.uint8,
                    self.device)
         self.scales = [weights.get(n + "_scale") for n in _EXPERTS]
         for n, s in zip(_EXPERTS, self.scales):
@@ -300,17 +300,17 @@ class DecodeBlock:
         self.logits = torch.empty((cfg.T, cfg.E), dtype=torch.float32,
                                   device=device)
         if self.mx:
-            self.ws = mx_workspace(cfg, quant, device)
+            self.ws = mx_workspace(cfg, w4, device)
 
     def _products(self):
         c, w, b = self.cfg, self.w, self.b
         packed = [w[n] for n in _EXPERTS]
         if self.mx:
-            moe_gmm_swiglu_mx(c, self.quant, b["x_sorted"],
+            moe_gmm_swiglu_mx(c, self.w4, b["x_sorted"],
                               b["group_offsets"], *packed, *self.scales,
                               b["y_sorted"], b["status"], self.ws)
         else:
-            moe_gmm_swiglu_w4(c, self.quant, b["x_sorted"],
+            moe_gmm_swiglu_w4(c, self.w4, b["x_sorted"],
                               b["group_offsets"], *packed, b["h"],
                               b["y_sorted"], b["status"])
 

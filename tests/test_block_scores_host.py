@@ -60,6 +60,21 @@ def test_scales_belong_to_microscaled_experts(m):
                           {**q, "w_up_scale": torch.ones(4)}, device="cpu")
 
 
+def test_experts_are_given_by_name_as_before(m):
+    from mixture_experts_token_gb300 import block
+    c, o, w4 = m.make_config(3, 64, 4, 2, 32, 1), m.make_block_norm(), \
+        m.make_w4(32)
+    w = weights(64, 4, 32)
+    q = {**w, **{n: m.alloc_w4(w4, *w[n].shape, "cpu")
+                 for n in ("w_gate", "w_up", "w_down")}}
+    made = block.DecodeBlock(cfg=c, opt=o, w4=w4, weights=q, device="cpu")
+    assert made.w4 is w4
+    mx = m.make_mx(32)
+    made = block.DecodeBlock(cfg=c, opt=o, w4=mx, weights=mx_weights(m, mx, w),
+                             device="cpu")
+    assert made.w4 is mx
+
+
 def test_a_capped_pass_is_the_layers(m):
     from mixture_experts_token_gb300 import block
     c = m.make_config(3, 64, 4, 2, 32, 1)
