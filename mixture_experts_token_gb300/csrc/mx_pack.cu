@@ -5,7 +5,7 @@
 // each, 22 us at 6.8 TB/s); eight bf16 matrices of 7168 x 2048, blocks of 16,
 // quantised 71 us (301 MB, 44 us), packed 22 (132 MB, 19), expanded 49 (301 MB,
 // 44).  Rows both ways and quantising matrices are bound by issue (slots 72 to 81%
-// busy), the others by bytes.
+// busy, with one number an instruction), the others by bytes.
 #include "launch.cuh"
 #include "mx.cuh"
 
