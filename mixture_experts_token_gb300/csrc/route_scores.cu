@@ -533,10 +533,11 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
           const float g = a.group_top == 2 ? g2 : g1;
           const float least =
               g - 2.0f * (err + kKeyErr<EPL> * fabsf(g) + FLT_MIN);
+          // (behind the last expert c and `least` are both -infinity)
           uint32_t hits = 0;
 #pragma unroll
           for (int i = 0; i < EPL; ++i)
-            if (c[i] >= least) hits |= 1u << i;
+            if ((FULL || e0 + i < a.E) && c[i] >= least) hits |= 1u << i;
           const int n = collect(hits, e0, lane, cand_e[warp]);
           if (n > 32)
             again = true;

@@ -175,6 +175,33 @@ def test_zeros_and_subnormals_between_other_rows(E, groups, top_groups,
     assert np.all(np.abs(w - ww) <= 1e-6 * np.abs(ww) + 1e-37)
 
 
+# E, groups, group_top: groups of whole lanes that end before the warp does,
+# with one to sixteen experts a lane
+@pytest.mark.parametrize("E,groups,group_top", [
+    (16, 8, 1), (24, 3, 2), (28, 7, 1), (48, 3, 2), (48, 6, 1), (96, 3, 2),
+    (112, 7, 2), (160, 5, 2), (192, 6, 1), (240, 15, 2), (448, 7, 2)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_near_groups_that_leave_lanes_empty(E, groups, group_top, sigmoid,
+                                            with_bias):
+    """Equal and nearly equal group sums: what is looked at more closely ends
+    with the last expert, of the last token and of the bias too."""
+    g = torch.Generator().manual_seed(15)
+    size = E // groups
+    x = torch.randn(24, E, generator=g)
+    x[:8] = x[:8, :size].repeat(1, groups)          # equal sums
+    x[8:16] = x[8:16, :size].repeat(1, groups)      # sums an ulp apart
+    odd = x[8:16, size::2 * size]                   # every other group's first
+    x[8:16, size::2 * size] = torch.nextafter(odd, torch.tensor(9.0))
+    x[16] = 0.0
+    bias = torch.full((E,), 0.25) if with_bias else None
+    for top_groups in {1, groups - 1}:
+        k = min(top_groups * size, 4)
+        opt = (k, sigmoid, groups, top_groups, group_top, True, 1.0)
+        check(x, bias, *opt)
+        check(x[15:16].clone(), bias, *opt)         # a single token
+
+
 def test_unaligned_logits_and_other_stream():
     g = torch.Generator().manual_seed(5)
     flat = torch.randn(33 * 128 + 1, generator=g).cuda()
