@@ -415,7 +415,8 @@ moe_status_t moe_permute_planned(const moe_config_t *cfg, const void *x,
  * moe_permute_scatter: x_sorted, uniq_tokens, expand_idx and the rest of
  *   uniq_offsets, from row_of, uniq_offsets and the workspace that
  *   moe_permute_tables wrote (same cfg).  Order the two on the device
- *   (same stream, or an event) before the scatter runs.
+ *   (same stream, or an event) before the scatter runs.  x may be written
+ *   between the two.
  * ---------------------------------------------------------------------- */
 moe_status_t moe_permute_tables(const moe_config_t *cfg,
                                 const int32_t *topk_idx, int32_t capped,

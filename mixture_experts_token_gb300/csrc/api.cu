@@ -291,7 +291,7 @@ cudaError_t pipelined_passes(const moe_config_t& c, const void* x,
     if ((e = launch_permute_scatter(
              sc, static_cast<const char*>(x) + o * row_bytes,
              b.row_of + o * c.k, tb.uniq_offsets, b.x_sorted, tb.uniq_tokens,
-             tb.expand_idx, tb.pws, s)) != cudaSuccess ||
+             tb.expand_idx, tb.pws, s, true)) != cudaSuccess ||
         (e = stamp(tr, trace_slot(i, 1), s)) != cudaSuccess ||
         (c.F > 0 &&
          (e = launch_gmm1(sc, identity_groups(sc), b.x_sorted,
@@ -330,8 +330,8 @@ cudaError_t capped_pass_tabled(const moe_config_t& c, const void* x,
   cudaError_t e;
   if ((e = stamp(tr, trace_slot(0, 0), s)) != cudaSuccess ||
       (e = launch_permute_scatter(c, x, row_of, tb.uniq_offsets, b.x_sorted,
-                                  tb.uniq_tokens, tb.expand_idx, tb.pws, s)) !=
-          cudaSuccess ||
+                                  tb.uniq_tokens, tb.expand_idx, tb.pws, s,
+                                  true)) != cudaSuccess ||
       (e = stamp(tr, trace_slot(0, 1), s)) != cudaSuccess ||
       (c.F > 0 &&
        (e = launch_gmm1(c, groups, b.x_sorted, tb.group_offsets, wg, wu, b.h,
@@ -720,7 +720,7 @@ moe_status_t moe_permute_scatter(const moe_config_t* cfg, const void* x,
       carve_permute_scratch(cv, cfg->T, cfg->E, cfg->k, cfg->S);
   return cuda_status(launch_permute_scatter(*cfg, x, row_of, uniq_offsets,
                                             x_sorted, uniq_tokens, expand_idx,
-                                            ws, stream));
+                                            ws, stream, false));
 }
 
 moe_status_t moe_gmm_swiglu_mapped(const moe_config_t* cfg, int32_t n_groups,

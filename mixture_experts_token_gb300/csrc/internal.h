@@ -83,7 +83,9 @@ cudaError_t launch_permute(const moe_config_t& c, const void* x,
 // The two halves of launch_permute: the counting-sort tables (row_of,
 // sorted_token, group_offsets, n_dropped, and the scatter's tables in ws),
 // then the row copy with the dedup indices.  uniq_offsets is complete after
-// the scatter.  Between the two, ws must not be reused.
+// the scatter.  Between the two, ws must not be reused.  x_final: x was final
+// before the kernel ahead of the scatter on s began, so that the scatter may
+// read it before that kernel has ended.
 cudaError_t launch_permute_tables(const moe_config_t& c,
                                   const int32_t* topk_idx, int64_t cap,
                                   int32_t* row_of, int32_t* sorted_token,
@@ -95,7 +97,8 @@ cudaError_t launch_permute_scatter(const moe_config_t& c, const void* x,
                                    const int32_t* row_of,
                                    int32_t* uniq_offsets, void* x_sorted,
                                    int32_t* uniq_tokens, int32_t* expand_idx,
-                                   const PermuteScratch& ws, cudaStream_t s);
+                                   const PermuteScratch& ws, cudaStream_t s,
+                                   bool x_final);
 cudaError_t launch_plan(const moe_config_t& c, const int32_t* counts,
                         int32_t* divert, int32_t* slot_of,
                         int32_t* group_expert, int32_t* shard_after,

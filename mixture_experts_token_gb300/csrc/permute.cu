@@ -29,7 +29,8 @@
 // Kernels 2 to 5 are programmatic dependent launches: each may start once
 // its predecessor has started, does the work that needs none of its
 // predecessor's output (assign: the lane masks from the routing indices;
-// scatter: the read of x[t]), and then waits for its predecessor to finish.
+// scatter: the read of x[t], where x was final before kernel 1 began), and
+// then waits for its predecessor to finish.
 // launch_permute_tables runs kernels 1 to 4, launch_permute_scatter kernel 5
 // (a caller may run the two on different streams, ordered by an event, so
 // that one chunk's tables overlap the previous chunk's expert FFN);
@@ -366,11 +367,24 @@ inline bool inline_uniq(int nb, int S) {
   return static_cast<long long>(nb) * S <= kInlineUniqCounts;
 }
 
+// Sixteen bytes of a row, by an ordinary load: the read-only path is for
+// memory that nothing writes while the kernel runs, and the kernel before
+// this one may write x after this one has begun.
+__device__ __forceinline__ int4 load_row(const int4* p) {
+  int4 v;
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // One CTA per token, or per (token, column slice) when there are too few
 // tokens to keep every SM busy: the row's 16-byte chunks are split into
 // contiguous slices, one CTA each, and only the slice-0 CTA of a token
 // writes its index outputs.  The first part of the CTA's slice (all of it
-// up to 16 KB) is read before the wait for the tables.  Dedup position of
+// up to 16 KB) is read before the wait for the tables, if x is then final
+// (x_final): the kernel before this one need not be one of the tables', and
+// may write x after letting this one start.  Dedup position of
 // (t, j) in shard s: the members of shards before s, plus those of s in
 // the token blocks before t's, plus t's rank among its block's members.
 // With inline_uniq the first two come from the block_ucnt counts as assign
@@ -378,7 +392,7 @@ inline bool inline_uniq(int nb, int S) {
 // scanned them.
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(
     const int4* __restrict__ x, int n16, int k, int S, int nb,
-    int inline_uniq, const int32_t* __restrict__ row_of,
+    int inline_uniq, int x_final, const int32_t* __restrict__ row_of,
     const int32_t* __restrict__ block_ucnt, const int32_t* __restrict__ urank,
     int32_t* __restrict__ uniq_offsets, int4* __restrict__ x_sorted,
     int32_t* __restrict__ expand_idx, int32_t* __restrict__ uniq_tokens,
@@ -397,10 +411,11 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(
   const int end = min(n16r, begin + per_split);
   const int4* src = x + static_cast<long long>(t) * n16r;
   int4 v[kScatterUnroll];
+  if (!x_final) wait_for_producer();
 #pragma unroll
   for (int u = 0; u < kScatterUnroll; ++u) {
     const int c = begin + tid + u * kScatterThreads;
-    if (c < end) v[u] = __ldg(src + c);
+    if (c < end) v[u] = load_row(src + c);
   }
   for (int q = tid; q < S; q += kScatterThreads) {
     tot[q] = 0;
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(
 #pragma unroll
       for (int u = 0; u < kScatterUnroll; ++u) {
         const int c = c0 + u * kScatterThreads;
-        if (c < end) v[u] = __ldg(src + c);
+        if (c < end) v[u] = load_row(src + c);
       }
     }
     for (int j = 0; j < k; ++j) {
@@ -561,7 +576,8 @@ cudaError_t launch_permute_scatter(const moe_config_t& c, const void* x,
                                    const int32_t* row_of,
                                    int32_t* uniq_offsets, void* x_sorted,
                                    int32_t* uniq_tokens, int32_t* expand_idx,
-                                   const PermuteScratch& ws, cudaStream_t s) {
+                                   const PermuteScratch& ws, cudaStream_t s,
+                                   bool x_final) {
   if (c.T == 0) return cudaSuccess;
   const int nb = (c.T + TB - 1) / TB;
   const int n16 = c.H * elem_bytes(c.dtype) / 16;
@@ -581,7 +597,7 @@ cudaError_t launch_permute_scatter(const moe_config_t& c, const void* x,
                                static_cast<unsigned>(splits)),
                           kScatterThreads, 0, s,
                           static_cast<const int4*>(x), n16, c.k, c.S, nb,
-                          inline_uniq(nb, c.S) ? 1 : 0, row_of,
+                          inline_uniq(nb, c.S) ? 1 : 0, x_final ? 1 : 0, row_of,
                           ws.block_ucnt, ws.urank, uniq_offsets,
                           static_cast<int4*>(x_sorted), expand_idx,
                           uniq_tokens, per);
@@ -601,7 +617,7 @@ cudaError_t launch_permute(const moe_config_t& c, const void* x,
                             status, s, plan);
   if (e != cudaSuccess) return e;
   return launch_permute_scatter(c, x, row_of, uniq_offsets, x_sorted,
-                                uniq_tokens, expand_idx, ws, s);
+                                uniq_tokens, expand_idx, ws, s, true);
 }
 
 }  // namespace moe

@@ -229,3 +229,54 @@ def test_permute_split_random(i):
         bufs = gpu_permute(cfg, x, idx, capped)
         p = ref.permute_indices(oi, wl.E, wl.S, C if capped else None)
         compare_permutation(bufs, p, x.cpu())
+
+
+@pytest.mark.parametrize("writer", ["mx expand", "mx down", "w4 down"])
+def test_rows_written_between_the_two_halves(writer):
+    """x comes from one of the library's own kernels, directly before
+    moe_permute_scatter and after moe_permute_tables."""
+    import mixture_experts_token_gb300 as moe
+    T, H, E, k, F = 2048, 2048, 16, 4, 512
+    g = torch.Generator().manual_seed(3)
+    cfg = moe.make_config(T, H, E, k, F, 2)
+    idx = torch.rand(T, E, generator=g).topk(k).indices.int().cuda()
+    b = moe.alloc_step_buffers(cfg)
+    one = moe.make_config(T, H, 1, 1, F, 1)        # a product of one expert
+    off = torch.tensor([0, T], dtype=torch.int32).cuda()
+    mx, w4 = moe.make_mx(32), moe.make_w4(128)
+    w = torch.randn(1, F, H, generator=g).bfloat16().cuda()
+    codes, scales = moe.alloc_mx_codes(mx, 1, F, H)
+    moe.moe_mx_quantize(mx, 1, F, H, w, None, codes, scales)
+    packed = moe.alloc_mx(mx, 1, F, H)
+    moe.moe_mx_pack(mx, 1, F, H, codes, scales, packed)
+    c4 = torch.randint(0, 256, (1, F // 2, H), generator=g,
+                       dtype=torch.uint8).cuda()
+    packed4 = moe.alloc_w4(w4, 1, F, H)
+    moe.moe_w4_pack(w4, 1, F, H, c4, torch.ones((1, F // 128, H)).bfloat16()
+                    .cuda(), None, packed4)
+    K = H if writer == "mx expand" else F
+    rows = [torch.randn(T, K, generator=g).bfloat16().cuda()
+            for _ in range(2)]
+    q = []
+    for r in rows:
+        q.append(moe.alloc_mx_rows(mx, T, K))
+        moe.moe_mx_quantize_rows(mx, T, K, r, 1.0, *q[-1])
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    for i in range(8):
+        moe.moe_permute_tables(cfg, idx, False, b["row_of"],
+                               b["sorted_token"], b["group_offsets"],
+                               b["uniq_offsets"], b["n_dropped"],
+                               b["permute_ws"])
+        x.zero_()
+        if writer == "mx expand":
+            moe.moe_mx_dequantize_rows(mx, T, H, *q[i % 2], 1.0, x)
+        elif writer == "mx down":
+            moe.moe_gmm_down_mx(one, mx, *q[i % 2], off, packed, None, x)
+        else:
+            moe.moe_gmm_down_w4(one, w4, rows[i % 2], off, packed4, x)
+        moe.moe_permute_scatter(cfg, x, b["row_of"], b["uniq_offsets"],
+                                b["x_sorted"], b["uniq_tokens"],
+                                b["expand_idx"], b["permute_ws"])
+        torch.cuda.synchronize()
+        assert x.abs().sum(1).min() > 0
+        assert torch.equal(b["x_sorted"], x[b["sorted_token"].long()]), i
