@@ -94,27 +94,50 @@ __device__ __forceinline__ float exp_near(float x) {
   return fmaf(p * rest, 0.6931471806f, p);
 }
 
+// The weight of the chosen expert of logit l, in lanes where `chosen`, where
+// a score or its share is below e^kFar: in float64, since float32 would lose
+// it before the scale brings it back.  z and m as below.
+constexpr float kFar = -80.0f;
+__device__ __noinline__ float far_weight(const Args& a, bool chosen, float l,
+                                         float m, float z) {
+  // the score's logarithm
+  double v = -INFINITY;
+  if (chosen) {
+    v = l;
+    v = a.sigmoid ? fmin(v, 0.0) - log1p(exp(-fabs(v)))
+                  : v - static_cast<double>(m) - log(static_cast<double>(z));
+  }
+  double top = 0.0, sum = 1.0;
+  if (a.renorm) {
+    top = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      top = fmax(top, __shfl_xor_sync(kAll, top, o));
+    sum = warp_sum(chosen ? exp(v - top) : 0.0);
+  }
+  return chosen ? static_cast<float>(a.scale * (exp(v - top) / sum)) : 0.0f;
+}
+
 // The weight of the chosen expert of logit l, in lanes where `chosen`; z is
-// the softmax's sum over all experts under the largest logit m.  Sums of
-// chosen scores are taken relative to the largest of them where all are small,
-// so that they do not vanish.
+// the softmax's sum over all experts under the largest logit m.
 template <int RANK>
 __device__ __forceinline__ float weight(const Args& a, bool chosen, float l,
                                         float m, float z) {
   const bool sigmoid = RANK == kByLogit ? a.sigmoid : RANK == kBySigmoid;
   chosen = chosen && fabsf(l) <= FLT_MAX;
   float s = 0.0f;
-  if (sigmoid && (!a.renorm || __any_sync(kAll, chosen && l > -60.0f))) {
+  if (sigmoid) {
+    if (__any_sync(kAll, chosen && l < kFar))
+      return far_weight(a, chosen, l, m, z);
     const float x = exp_near(fmaxf(-fabsf(l), -87.0f));
     if (chosen) s = (l < 0.0f ? x : 1.0f) * rcp_fast(1.0f + x);
   } else {
-    const float top = a.renorm ? warp_max(chosen ? l : -FLT_MAX) : m;
+    const float x = l - (a.renorm ? warp_max(chosen ? l : -FLT_MAX) : m);
+    if (__any_sync(kAll, chosen && x < kFar))
+      return far_weight(a, chosen, l, m, z);
     if (chosen) {
-      s = expf(l - top);
-      if (sigmoid)
-        s /= 1.0f + expf(l);
-      else if (!a.renorm)
-        s /= z;
+      s = expf(x);
+      if (!a.renorm) s /= z;
     }
   }
   if (a.renorm) {

@@ -118,6 +118,35 @@ def test_far_logits(sigmoid):
 
 
 @pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scale", [1.0, 1e30, -3e38])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_scores_below_float32_beside_others(sigmoid, renorm, scale,
+                                            with_bias):
+    """Chosen scores of which some are too small for float32 and others are
+    not, also under a scale that brings them back: each weight to 1e-6 of
+    itself.  Logits are multiples of an eighth, whose differences are exact;
+    2^-149 is the smallest step of the result."""
+    x = torch.tensor([
+        [-59, -70, -100, -130, -200, -1000],
+        [-59.125, -59.25, -87.5, -87.625, -95, -103],
+        [-0.5, -86.5, -87.5, -88.5, -104.5, -110],
+        [200, 120, 113, 96, 90, 5], [-100] * 6,
+        [-79.875, -80, -80.125, -80.25, -81, -82],
+        [3e38, 0, -1, -100, -1e30, -3e38], [0, -1, -2, -3, -4, -5]])
+    x = torch.cat([x, torch.full((len(x), 10), -2000.0)], 1)
+    x[6, 6:] = -3.2e38
+    bias = torch.zeros(16) if with_bias else None
+    opt = (6, sigmoid, 1, 1, 1, renorm, scale)
+    idx, w, st = call(x, bias, *opt)
+    want, ww = ref.route(x.numpy(), None if bias is None else bias.numpy(),
+                         *opt)
+    assert st == 0 and np.array_equal(idx, want)
+    assert np.all(np.abs(w - ww) <= 1e-6 * np.abs(ww) + 2.0 ** -149), \
+        np.argwhere(np.abs(w - ww) > 1e-6 * np.abs(ww))
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
 @pytest.mark.parametrize("groups,top_groups,group_top", [(1, 1, 1), (4, 2, 2),
                                                          (3, 1, 1)])
 def test_nonfinite_logits_and_bias(sigmoid, groups, top_groups, group_top):
