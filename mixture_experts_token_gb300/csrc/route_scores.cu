@@ -85,15 +85,6 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
-// e^x to 2^-22 and a little: the argument's product with log2 e in two parts.
-__device__ __forceinline__ float exp_near(float x) {
-  const float y = x * kLog2e;
-  // what y lacks: its own rounding, and that of the constant
-  const float rest = fmaf(x, kLog2e, -y) + x * 1.925963033500e-8f;
-  const float p = exp2_fast(y);
-  return fmaf(p * rest, 0.6931471806f, p);
-}
-
 // The weight of the chosen expert of logit l, in lanes where `chosen`, where
 // a score or its share is below e^kFar: in float64, since float32 would lose
 // it before the scale brings it back.  z and m as below.
@@ -129,7 +120,7 @@ __device__ __forceinline__ float weight(const Args& a, bool chosen, float l,
   if (sigmoid) {
     if (__any_sync(kAll, chosen && l < kFar))
       return far_weight(a, chosen, l, m, z);
-    const float x = exp_near(fmaxf(-fabsf(l), -87.0f));
+    const float x = expf(-fabsf(l));
     if (chosen) s = (l < 0.0f ? x : 1.0f) * rcp_fast(1.0f + x);
   } else {
     const float x = l - (a.renorm ? warp_max(chosen ? l : -FLT_MAX) : m);

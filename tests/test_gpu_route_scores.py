@@ -117,6 +117,23 @@ def test_far_logits(sigmoid):
     check(x, None, 5, sigmoid, 1, 1, 1, True, 1.0, status=status)
 
 
+def test_sigmoid_over_its_range():
+    """The weight of one expert is the sigmoid of its logit: the exponential
+    and the reciprocal within an ulp (2^-23), a sum and a product rounded
+    (2^-24 each)."""
+    g = torch.Generator().manual_seed(16)
+    x = torch.cat([torch.linspace(-79.99, 40, 150_001),
+                   torch.randn(20_000, generator=g) * 3,
+                   torch.logspace(-30, 38, 2000), -torch.logspace(-30, 1.9,
+                                                                  2000)])
+    idx, w, st = call(x[:, None].contiguous(), None, 1, True, 1, 1, 1, False,
+                      1.0)
+    v = x.double().numpy()
+    want = np.exp(np.minimum(v, 0)) / (1 + np.exp(-np.abs(v)))
+    assert st == 0 and not idx.any()
+    assert np.all(np.abs(w[:, 0] - want) <= 3 * 2.0 ** -23 * want)
+
+
 @pytest.mark.parametrize("sigmoid", [True, False])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("scale", [1.0, 1e30, -3e38])
