@@ -711,6 +711,48 @@ struct BackArgs {
   float scale;
 };
 
+// A chosen expert's gradient where a weight, one less a score or the weight's
+// gradient is out of float32's range on the way: in float64, and with the
+// sigmoid's 1 - s in it.  All lanes of the warp.
+template <bool SIGMOID, int LANES>
+__device__ __noinline__ float far_gradient(const BackArgs& a, bool finite,
+                                           float l, float d, float m,
+                                           float z) {
+  const auto token_sum = [](double v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  };
+  double v = -INFINITY;  // the score's logarithm
+  if (finite) {
+    v = l;
+    v = SIGMOID ? fmin(v, 0.0) - log1p(exp(-fabs(v)))
+                : v - static_cast<double>(m) - log(static_cast<double>(z));
+  }
+  double top = 0.0;
+  if (a.renorm) {
+    top = v;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+      top = fmax(top, __shfl_xor_sync(kAll, top, o));
+  }
+  double w = finite ? exp(v - top) : 0.0;
+  double g = finite ? static_cast<double>(a.scale) * d : 0.0;
+  if (a.renorm) {
+    const double sum = token_sum(w);
+    if (finite) w /= sum;
+    g -= token_sum(w * g);
+  }
+  g *= w;
+  if (SIGMOID && finite) g /= 1.0 + exp(static_cast<double>(l));
+  return static_cast<float>(g);
+}
+// f e^x, x <= 0, also where e^x alone is below float32's range.
+__device__ __forceinline__ float times_exp(float f, float x) {
+  const float root = expf(0.5f * x);
+  return f * root * root;
+}
+
 // A chosen expert a lane, LANES lanes a token and so 32 / LANES tokens a warp.
 // With sigmoid scores the row is zero but for the chosen; with softmax scores
 // every lane also has its share of the row, one token after another.
@@ -812,8 +854,13 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
       const float sum = token_sum(w);
       w = sum > 0.0f ? w / sum : 0.0f;
     }
-    float g = finite ? a.scale * d * w : 0.0f;
+    float g = finite ? a.scale * d : 0.0f;
+    const bool far = __any_sync(
+        kAll, finite && (w < 1e-30f || fabsf(g) > 1e30f ||
+                         (SIGMOID && fabsf(l) > -kFar)));
+    g *= w;
     if (a.renorm) g -= w * token_sum(g);
+    if (far) g = far_gradient<SIGMOID, LANES>(a, finite, l, d, m, z);
     const float all = SIGMOID ? 0.0f : token_sum(g);
     // an index that stands twice has the sum of both
     const uint32_t mine = (LANES == 32 ? kAll : (1u << LANES) - 1)
@@ -839,24 +886,25 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
           for (int i = lane * 4; i < a.E; i += 128) {
             const float4 v = *reinterpret_cast<const float4*>(row + i);
             float4 o;
-            o.x = fabsf(v.x) <= FLT_MAX ? f * expf(v.x - most) : 0.0f;
-            o.y = fabsf(v.y) <= FLT_MAX ? f * expf(v.y - most) : 0.0f;
-            o.z = fabsf(v.z) <= FLT_MAX ? f * expf(v.z - most) : 0.0f;
-            o.w = fabsf(v.w) <= FLT_MAX ? f * expf(v.w - most) : 0.0f;
+            o.x = fabsf(v.x) <= FLT_MAX ? times_exp(f, v.x - most) : 0.0f;
+            o.y = fabsf(v.y) <= FLT_MAX ? times_exp(f, v.y - most) : 0.0f;
+            o.z = fabsf(v.z) <= FLT_MAX ? times_exp(f, v.z - most) : 0.0f;
+            o.w = fabsf(v.w) <= FLT_MAX ? times_exp(f, v.w - most) : 0.0f;
             *reinterpret_cast<float4*>(out + i) = o;
           }
         } else {
           for (int i = lane; i < a.E; i += 32) {
             const float v = row[i];
-            out[i] = fabsf(v) <= FLT_MAX ? f * expf(v - most) : 0.0f;
+            out[i] = fabsf(v) <= FLT_MAX ? times_exp(f, v - most) : 0.0f;
           }
         }
       }
     }
     __syncwarp();  // the chosen are written over what other lanes wrote
     if (finite)
-      a.dlogits[t * a.E + e] = SIGMOID ? g * (1.0f / (1.0f + expf(l)))
-                                       : g - all / z * expf(l - m);
+      a.dlogits[t * a.E + e] = !SIGMOID ? g - times_exp(all / z, l - m)
+                               : far    ? g
+                                        : g * (1.0f / (1.0f + expf(l)));
   }
 }
 

@@ -93,7 +93,9 @@ def route_backward(logits, idx, dw, sigmoid, renorm, scale):
         else:
             np.add.at(ds, ch, scale * dw[t])
         if sigmoid:
-            out[t] = ds * s * (1 - s)
+            with np.errstate(over="ignore", invalid="ignore"):
+                rest = 1 / (1 + np.exp(x))  # 1 - s would round to 0
+            out[t] = np.where(np.isfinite(x), ds * s * rest, 0.0)
         else:
             out[t] = s * (ds - (ds * s).sum())
     return out

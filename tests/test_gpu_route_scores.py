@@ -345,6 +345,45 @@ def test_backward_unaligned_nonfinite_and_odd_indexes(sigmoid):
 
 
 @pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scale", [1.0, 1e30, -3e38])
+@pytest.mark.parametrize("E", [16, 19])
+def test_backward_of_scores_below_float32_beside_others(sigmoid, renorm,
+                                                        scale, E):
+    """Scores, and what they lack of 1, that are too small for float32 without
+    the scale: test_backward's bound of each entry by its own score (and by
+    1 - s), with the smallest step of the result.  Logits are multiples of an
+    eighth, whose differences are exact."""
+    x = torch.tensor([
+        [-59, -70, -100, -130, -150, -1000],
+        [-59.125, -59.25, -87.5, -87.625, -95, -103],
+        [-0.5, -86.5, -87.5, -88.5, -104.5, -110],
+        [100, 89, 88.5, 95, 81, 5], [-100] * 6, [140, 130, 100, 90, 85, 81],
+        [-79.875, -80, -80.125, -80.25, -81, -82], [0, -1, -2, -3, -4, -5]])
+    g = torch.Generator().manual_seed(17)
+    x = torch.cat([x, torch.randint(-160, 0, (len(x), E - 6), generator=g)
+                   + x[:, :1]], 1)
+    dw = (torch.rand(len(x), 6, generator=g) - 0.5) * 0.1
+    idx = torch.arange(6).repeat(len(x), 1)
+    idx[:, 3] = E - 2                                # one of the others
+    got = back(x, idx, dw, sigmoid, renorm, scale)
+    want = ref.route_backward(x.numpy(), idx.numpy(), dw.double().numpy(),
+                              sigmoid, renorm, scale)
+    x64 = x.double().numpy()
+    s = np.exp(np.stack([ref.log_scores(r, sigmoid) for r in x64]))
+    ch = np.take_along_axis(s, idx.numpy(), 1)
+    terms = abs(scale) * np.abs(dw.double().numpy())
+    terms = terms.max(1, keepdims=True) * 2 / ch.sum(1, keepdims=True) \
+        if renorm else terms.max(1, keepdims=True) if sigmoid else \
+        (terms * ch).sum(1, keepdims=True) + terms.max(1, keepdims=True)
+    tol = 4e-6 * terms * s + 2.0 ** -149
+    if sigmoid:
+        tol = 4e-6 * terms * s / (1 + np.exp(x64)) + 2.0 ** -149
+    assert np.all(np.abs(got - want) <= tol), \
+        np.argwhere(np.abs(got - want) > tol)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
 def test_forward_and_backward_in_a_graph(sigmoid):
     """Captured once, replayed on other logits."""
     g = torch.Generator().manual_seed(9)
