@@ -385,6 +385,44 @@ def test_large_and_zero_products(block):
     assert (y[1] == 0).all()
 
 
+# powers of two on the scales of x, the gate, up and down matrices and h, with
+# values to match: the product of two scales that float32 rounds coarsely or
+# not at all, with rows and up's sums that make up for it; that is infinite;
+# that is large; h far over its scale's range
+@pytest.mark.parametrize("powers", [
+    (-70, -50, 100, -20, -90), (50, -50, 50, 60, 100), (60, -60, -60, 110, 0),
+    (0, 0, 0, 0, -110), (-100, 100, 100, -30, 0), (100, -100, -100, -40, -100)])
+@pytest.mark.parametrize("counts", [[9, 0, 5], [5, 0, 200]])
+def test_tensor_scales_near_the_ends_of_float32(counts, powers):
+    c = Case(counts, 288, 160, "f32", 16, seed=31)
+    two = [2.0 ** p for p in powers]
+    c.mx = moe.make_mx(16, 0.011 * two[0], 0.013 * two[4])
+    c.x = c.x * two[0]
+    c.x[1] = 0
+    for i in range(3):
+        c.scales[i], c.w[i] = c.scales[i] * two[1 + i], c.w[i] * two[1 + i]
+        assert c.scales[i].min() >= 2.0 ** -126
+        assert c.scales[i].isfinite().all()
+    xq, hq, y = c.steps()
+    hs = by_row(hq[1])
+    x = ref.dequantize_rows(np8(xq[0]), by_row(xq[1]), 16, c.mx.x_scale)
+    h = ref.dequantize_rows(np8(hq[0]), hs, 16, c.mx.h_scale)
+    for e in range(len(counts)):
+        r = slice(c.off[e], c.off[e + 1])
+        if counts[e] == 0:
+            continue
+        g, u = x[r] @ c.w[0][e], x[r] @ c.w[1][e]
+        eg, eu = (REL * (np.abs(x[r]) @ np.abs(w[e])) for w in c.w[:2])
+        s = ref.silu(g)
+        tol = (1.1 * eg + 8 * 2.0 ** -23 * np.abs(s)) * (np.abs(u) + eu) \
+            + np.abs(s) * eu
+        c.check_h(h[r], hs[r], s * u, tol)
+        close(y[r], h[r] @ c.w[2][e],
+              REL * (np.abs(h[r]) @ np.abs(c.w[2][e])), ("y", e))
+    assert c.status.item() == 0 and (y[1] == 0).all()
+    assert torch.equal(c.whole(), y)
+
+
 def test_h_beyond_float32_is_nan():
     """A row whose h overflows float32 is NaN, the others are not."""
     c = Case([4], 64, 64, "f32", 32, seed=6, std=1.0)
