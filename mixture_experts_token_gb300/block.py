@@ -245,14 +245,16 @@ def quantize_experts(w4, w):
 def quantize_experts_mx(mx, w):
     """(packed, scales) of expert weights w [E, K, N] (contiguous) in
     microscaled 4-bit floating point.  With blocks of 16 the scales [E] float32
-    put each expert's largest magnitude at the largest value that a block can
-    hold, 448 * 6; with blocks of 32 there are none."""
+    put each expert's largest finite magnitude at the largest value that a block
+    can hold, 448 * 6; with blocks of 32 there are none."""
     E, K, N = w.shape
     _check("w", w, E * K * N, w.dtype, torch.device("cuda"))
     scale = None
     if mx.block == 16:
-        # an expert of zeros: any scale
-        scale = (w.abs().amax((1, 2)).float() / (448 * 6)).clamp_(min=2e-38)
+        # an expert of zeros: any scale; a weight that is not finite spoils its
+        # block, not its expert's scale
+        most = w.abs().nan_to_num_(0.0, 0.0, 0.0).amax((1, 2)).float()
+        scale = (most / (448 * 6)).clamp_(min=2e-38)
     codes, scales = alloc_mx_codes(mx, E, K, N, w.device)
     packed = alloc_mx(mx, E, K, N, w.device)
     moe_mx_quantize(mx, E, K, N, w, scale, codes, scales)

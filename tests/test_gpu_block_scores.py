@@ -157,3 +157,22 @@ def test_decode_step(T, H, E, k, F, dtype, size):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(b.out, want[0]) and torch.equal(b.h_next, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+def test_weights_that_are_not_finite_spoil_their_block_alone(dtype, bad):
+    g = torch.Generator().manual_seed(5)
+    w = (torch.randn(3, 96, 40, generator=g) * 0.02).to(dtype).cuda()
+    mx = moe.make_mx(16)
+    clean, scale = block.quantize_experts_mx(mx, w)
+    broken = w.clone()
+    broken[1, 35, 7] = float(bad)
+    q, s = block.quantize_experts_mx(mx, broken)
+    assert torch.equal(s, scale)
+    a, b = (torch.empty_like(w, dtype=torch.float32) for _ in range(2))
+    moe.moe_mx_dequantize(mx, *w.shape, clean, scale, a)
+    moe.moe_mx_dequantize(mx, *w.shape, q, s, b)
+    assert b[1, 32:48, 7].isnan().all()
+    b[1, 32:48, 7] = a[1, 32:48, 7]
+    assert torch.equal(a, b)
