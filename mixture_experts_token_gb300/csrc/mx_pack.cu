@@ -522,7 +522,9 @@ extern "C" {
 
 size_t moe_mx_bytes(const moe_mx_t* opt, int32_t n, int32_t K, int32_t N) {
   if (!mx::options_ok(opt) || !matrix_ok(n, K, N)) return 0;
-  return static_cast<size_t>(Layout{K, N, opt->block}.matrix()) * n;
+  const size_t each = static_cast<size_t>(Layout{K, N, opt->block}.matrix());
+  if (n > 0 && each > SIZE_MAX / n) return 0;  // no such number of bytes
+  return each * n;
 }
 
 size_t moe_mx_row_scale_bytes(const moe_mx_t* opt, int32_t R, int32_t K) {

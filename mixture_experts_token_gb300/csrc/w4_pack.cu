@@ -236,7 +236,9 @@ extern "C" {
 
 size_t moe_w4_bytes(const moe_w4_t* opt, int32_t n, int32_t K, int32_t N) {
   if (!w4::options_ok(opt) || !shape_ok(n, K, N)) return 0;
-  return static_cast<size_t>(layout(*opt, K, N).matrix()) * n;
+  const size_t each = static_cast<size_t>(layout(*opt, K, N).matrix());
+  if (n > 0 && each > SIZE_MAX / n) return 0;  // no such number of bytes
+  return each * n;
 }
 
 moe_status_t moe_w4_quantize(const moe_w4_t* opt, int32_t n, int32_t K,

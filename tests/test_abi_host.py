@@ -490,3 +490,19 @@ def test_mx_sizes_and_arguments(m):
     if not torch.cuda.is_available():     # past the checks, to a launch
         assert ffn(p, need) == m.MOE_ERR_CUDA
         assert up(C, M, 0, None, *good) == m.MOE_ERR_CUDA
+
+
+def test_sizes_of_packed_matrices_do_not_wrap(m):
+    """2^31 - 1 matrices of 2^20 x 2^20 have more bytes than 64 bits count."""
+    most, side = (1 << 31) - 1, 1 << 20
+    for o in (m.make_mx(32), m.make_mx(16)):
+        one = m.moe_mx_bytes(o, 1, side, side)
+        fit = ((1 << 64) - 1) // one
+        assert 0 < fit < most
+        assert m.moe_mx_bytes(o, fit, side, side) == fit * one
+        assert m.moe_mx_bytes(o, fit + 1, side, side) == 0
+        assert m.moe_mx_bytes(o, most, side, side) == 0
+    w4 = m.make_w4(128)
+    one = m.moe_w4_bytes(w4, 1, side, side)
+    assert one > 0 and one * most < 1 << 64 or \
+        m.moe_w4_bytes(w4, most, side, side) == 0
