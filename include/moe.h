@@ -172,8 +172,13 @@ moe_status_t moe_route(const moe_config_t *cfg, const float *logits,
  * with a_j = dtopk_w_j w_j, less w_j / scale * sum a with renorm,
  *     sigmoid  dlogits_e = a_e (1 - s_e) at chosen experts, else 0
  *     softmax  dlogits_e = (a_e at chosen experts) - s_e * sum a.
- * A chosen index outside [0, E) is skipped.  A logit that is NaN or infinite
- * gets no gradient.  dlogits and logits are different memory.
+ * A chosen index outside [0, E) is skipped: its expert is as one that was not
+ * chosen.  A logit that is NaN or infinite gets no gradient.  The bias is not an
+ * input: an expert that was chosen although its bias is NaN or infinite (fewer
+ * than k of the groups that take part had both finite; the forward has set
+ * MOE_DEV_NONFINITE) counts here with the score of its logit, unless the caller
+ * puts an index outside [0, E) in its place.  dlogits and logits are different
+ * memory.
  * ---------------------------------------------------------------------- */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 

@@ -384,6 +384,30 @@ def test_backward_of_scores_below_float32_beside_others(sigmoid, renorm,
 
 
 @pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_backward_beside_a_bias_that_is_not_finite(sigmoid, renorm):
+    """Experts chosen for want of others, whose weight is 0: with their indexes
+    taken out the gradient is that of the weights."""
+    g = torch.Generator().manual_seed(18)
+    T, E, k = 9, 12, 5
+    x = torch.randn(T, E, generator=g)
+    bias = torch.randn(E, generator=g) * 0.1
+    bias[3:] = torch.tensor([float("nan"), float("inf"), float("-inf")] * 3)
+    opt = (k, sigmoid, 1, 1, 1, renorm, 2.5)
+    idx, w, st = call(x, bias, *opt)
+    want, ww = ref.route(x.numpy(), bias.numpy(), *opt)
+    assert st == moe.MOE_DEV_NONFINITE and np.array_equal(idx, want)
+    lost = idx >= 3
+    assert (lost.sum(1) == 2).all() and not w[lost].any()
+    dw = torch.randn(T, k, generator=g)
+    got = back(x, torch.from_numpy(np.where(lost, -1, idx)), dw, sigmoid,
+               renorm, 2.5)
+    dl = ref.route_backward(x.numpy(), idx[:, :3], dw[:, :3].double().numpy(),
+                            sigmoid, renorm, 2.5)
+    assert np.allclose(got, dl, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
 def test_forward_and_backward_in_a_graph(sigmoid):
     """Captured once, replayed on other logits."""
     g = torch.Generator().manual_seed(9)
