@@ -134,6 +134,65 @@ def test_weights_bit_for_bit(n, K, N, block, dtype):
             values.astype(np.float32)).to(out))
 
 
+@pytest.mark.parametrize("K,N", [(32, 10), (288, 9), (544, 72), (256, 16)])
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1.0, 0.011])
+def test_hard_weights_bit_for_bit(K, N, block, dtype, scale):
+    """Ties, zeros, extremes, NaN and infinities as columns of a matrix, with
+    odd and even numbers of them; a matrix of zeros beside them."""
+    scale = scale if block == 16 else 1.0
+    mx = make(block)
+    rows = hard_rows(N, K, DT[dtype], K + N, scale)
+    w = torch.stack([rows.T, torch.zeros(K, N).to(rows.dtype)]).contiguous()
+    t = torch.tensor([scale, 1.0]).cuda() if block == 16 else None
+    codes, scales = moe.alloc_mx_codes(mx, 2, K, N)
+    scales.fill_(0xAB)
+    moe.moe_mx_quantize(mx, 2, K, N, w.cuda(), t, codes, scales)
+    want, ws = ref.quantize_rows(rows.float().numpy(), block, scale)
+    assert np.array_equal(np8(scales[0]), ws)
+    nan = 255 if block == 32 else 127
+    fine = np.repeat(ws[:, :K // block] != nan, block // 2, 1)
+    assert np.array_equal(np8(codes[0])[fine], want[fine])
+    zero, zs = ref.quantize_rows(np.zeros((N, K), np.float32), block, 1.0)
+    assert np.array_equal(np8(codes[1]), zero)
+    assert np.array_equal(np8(scales[1]), zs)
+    packed = moe.alloc_mx(mx, 2, K, N)
+    moe.moe_mx_pack(mx, 2, K, N, codes, scales, packed)
+    for out in (torch.float32, torch.bfloat16):
+        v = torch.empty((2, K, N), dtype=out, device="cuda")
+        moe.moe_mx_dequantize(mx, 2, K, N, packed, t, v)
+        # the last product is rounded to float32
+        values = torch.from_numpy(ref.dequantize_rows(want, ws, block, scale)
+                                  .astype(np.float32)).to(out).T
+        got = v.cpu()
+        assert torch.equal(got[0].isnan(), values.isnan())
+        assert torch.equal(got[0].nan_to_num(), values.nan_to_num())
+        assert (got[1] == 0).all()
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_more_matrices_than_a_grid_has(block):
+    """5000 small ones: a CTA takes a second matrix."""
+    n, K, N = 5000, 32, 2
+    g = torch.Generator().manual_seed(32)
+    w = torch.randn(n, K, N, generator=g) * 0.02
+    mx = make(block)
+    codes, scales = moe.alloc_mx_codes(mx, n, K, N)
+    moe.moe_mx_quantize(mx, n, K, N, w.cuda(), None, codes, scales)
+    want, ws = ref.quantize_rows(w.transpose(1, 2).reshape(n * N, K).numpy(),
+                                 block, 1.0)
+    assert np.array_equal(np8(codes).reshape(n * N, -1), want)
+    assert np.array_equal(np8(scales).reshape(n * N, -1), ws)
+    packed = moe.alloc_mx(mx, n, K, N)
+    moe.moe_mx_pack(mx, n, K, N, codes, scales, packed)
+    v = torch.empty((n, K, N), device="cuda")
+    moe.moe_mx_dequantize(mx, n, K, N, packed, None, v)
+    values = ref.dequantize_rows(want, ws, block, 1.0).reshape(n, N, K)
+    assert torch.equal(v.cpu(), torch.from_numpy(
+        values.transpose(0, 2, 1).astype(np.float32)))
+
+
 def test_weights_of_a_checkpoint():
     """Scales whose padding is not zero are packed as if it were."""
     mx, n, K, N = make(32), 1, 160, 8
