@@ -738,14 +738,7 @@ struct Gmm {
     uint32_t phase = 0;
     launch::wait_for_previous();
     passes(a, chunks, n_items, tiles, [&](const Item& it) {
-      const float w0 = a.s0 ? a.s0[it.expert] : 1.0f;
-      const float w1 = DUAL && a.s1 ? a.s1[it.expert] : 1.0f;
-      float t0 = a.x_scale * w0, t1 = a.x_scale * w1;
-      bool far = BLOCK == 16 && !(in_range(t0) && in_range(t1));
-      if (DUAL && BLOCK == 16) {
-        t1 *= a.inv_out;
-        far |= !in_range(t1);
-      }
+      const Scales t = scales_of(a, it.expert);
       if (!wait_all(b.acc_full + 8 * buf, phase, abort_flag, a.status))
         return false;
       tc::tc_fence_after();
@@ -754,11 +747,6 @@ struct Gmm {
       const uint32_t at =
           tmem + buf * kAcc + (static_cast<uint32_t>(quarter * 32) << 16);
       if (col0 < a.l.N) {  // N is a multiple of 32
-        if (BLOCK == 16 && far) {
-          t0 = t1 = 1.0f;
-          scale_sums(a, at, warp / 4 * (NT / kRowParts),
-                     min(it.rows, (warp / 4 + 1) * (NT / kRowParts)), w0, w1);
-        }
         if constexpr (DUAL && PAIR) {
           // h of this warp's rows, then the sums are free, then the codes
           constexpr int kRows = NT / kRowParts;
@@ -775,8 +763,8 @@ struct Gmm {
               tmem_ld_wait(u);
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                h[r + i] = swiglu(__uint_as_float(g[i]), __uint_as_float(u[i]), t0,
-                                  t1);
+                h[r + i] =
+                    swiglu(__uint_as_float(g[i]), __uint_as_float(u[i]), t);
             }
           tc::tc_fence_before();
           __syncwarp();
@@ -786,6 +774,8 @@ struct Gmm {
             if (r0 + r < it.rows) write_h(a, it, col0, r0 + r, lane, h + r);
         } else {
           const int r1 = min(it.rows, (warp / 4 + 1) * (NT / kRowParts));
+          if (!DUAL && BLOCK == 16 && t.first != 1.0f)
+            multiply_sums(at, warp / 4 * (NT / kRowParts), r1, t.first);
 #pragma unroll 1
           for (int r = warp / 4 * (NT / kRowParts); r < r1; r += 16) {
             uint32_t g[16], u[16];
@@ -801,7 +791,7 @@ struct Gmm {
 #pragma unroll
                   for (int j = 0; j < 8; ++j)
                     h[j] = swiglu(__uint_as_float(g[i + j]),
-                                  __uint_as_float(u[i + j]), t0, t1);
+                                  __uint_as_float(u[i + j]), t);
                   write_h(a, it, col0, r + i, lane, h);
                 }
             } else {
@@ -811,7 +801,7 @@ struct Gmm {
                 const long long o =
                     static_cast<long long>(it.row + r + i) * a.l.N + col0 +
                     lane;
-                const float v = t0 * __uint_as_float(g[i]);
+                const float v = t.last * __uint_as_float(g[i]);
                 if (a.f32)
                   put(static_cast<float*>(a.y) + o, v);
                 else
@@ -834,59 +824,75 @@ struct Gmm {
     });
   }
 
-  // Tensor scales whose product, and a sum under it, are normal numbers: a sum of
-  // 2^20 products of two codes and two scales of 448 at most is below 8e12, and
-  // none but 0 is below 2^-20.
+  // What sums are multiplied by: the tensor scales of the rows and the matrices,
+  // up's sums by the reciprocal of h's scale too (one rounding of h less).  Down:
+  // by `first`, if it is not 1, then by `last`.  Gate and up: gate's by `first`
+  // and up's by `last`, whose product alone counts, and gate's by `exponent`,
+  // -log2 e in it, for the exponential.
+  struct Scales {
+    float first, last, exponent;
+  };
+  static constexpr float kMinusLog2e = -1.44269504f;
+  __device__ static __forceinline__ Scales scales_of(const GmmArgs& a,
+                                                     int expert) {
+    if (BLOCK == 32) return {1.0f, 1.0f, kMinusLog2e};
+    const float x = a.x_scale, w0 = a.s0 ? a.s0[expert] : 1.0f;
+    const float p0 = x * w0;
+    if (!DUAL) {
+      if (in_range(p0)) return {1.0f, p0, 0.0f};
+      // first the scale that leads away from the end of float32's range
+      const bool w_first = (p0 >= 1.0f) == (x > w0);
+      return {w_first ? w0 : x, w_first ? x : w0, 0.0f};
+    }
+    const float w1 = a.s1 ? a.s1[expert] : 1.0f;
+    const float p1 = x * w1, q1 = p1 * a.inv_out;
+    if (in_range(p0) && in_range(p1) && in_range(q1))
+      return {p0, q1, p0 * kMinusLog2e};
+    return far_scales(x, w0, w1, a.inv_out);
+  }
+  // Whether a product of scales, and any sum under it, is a normal number: a sum
+  // of 2^20 products of two codes and two scales of 448 at most is below 8e12,
+  // and none but 0 is below 2^-20.
   __device__ static __forceinline__ bool in_range(float t) {
     return t >= 1e-25f && t <= 1e25f;
   }
-  // v x w, without x w, which may be out of float32's range: first the scale
-  // that leads away from the end of the range.
-  __device__ static __forceinline__ float scaled(float v, float x, float w) {
-    const bool up = x * w >= 1.0f, w_first = up == (x > w);
-    return v * (w_first ? w : x) * (w_first ? x : w);
-  }
-  // Puts rows r0 .. r1 of the sums, in tensor memory, under other scales: what
-  // follows takes them as they are.  For gate and up, 128 and a number whose
-  // product with silu(128) = 128 is h under its scale.  (Apart from the reading
-  // of sums: two factors for every sum there took a 4096-token prompt 907 us,
-  // a branch beside it 909, this 896 to 901, none of it 890 to 896.)
-  __device__ static __noinline__ void scale_sums(const GmmArgs& a, uint32_t at,
-                                                 int r0, int r1, float w0,
-                                                 float w1) {
+  // Down's sums of rows r0 .. r1, in tensor memory, times f, before they are read
+  // (a second factor where they are read took 32768 rows 348 us, not 338).
+  __device__ static __noinline__ void multiply_sums(uint32_t at, int r0,
+                                                    int r1, float f) {
 #pragma unroll 1
     for (int r = r0; r < r1; r += 16) {
-      uint32_t g[16], u[16];
-      tmem_ld16(at + r, g);
-      tmem_ld_wait(g);
-      if (DUAL) {
-        tmem_ld16(at + NT + r, u);
-        tmem_ld_wait(u);
-      }
+      uint32_t v[16];
+      tmem_ld16(at + r, v);
+      tmem_ld_wait(v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float v = scaled(__uint_as_float(g[i]), a.x_scale, w0);
-        g[i] = __float_as_uint(v);
-        if (DUAL) {
-          const float h = swiglu(
-              v, scaled(__uint_as_float(u[i]), a.x_scale, w1), 1.0f, 1.0f);
-          u[i] = __float_as_uint(h * a.inv_out * (1.0f / 128.0f));
-          g[i] = __float_as_uint(128.0f);
-        }
-      }
-      tmem_st(at + r, g);
-      if (DUAL) tmem_st(at + NT + r, u);
+      for (int i = 0; i < 16; ++i)
+        v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+      tmem_st(at + r, v);
     }
     tmem_st_wait();
   }
-  // silu(t0 g) t1 u, silu(z) = z / (1 + exp(-z)); exp(-z) may be infinite.
-  // (t1 includes the reciprocal of h's scale: one rounding of h less.)
-  __device__ static __forceinline__ float swiglu(float g, float u, float t0,
-                                                 float t1) {
+  // Gate's and up's where one is not: the product of all in two parts of like
+  // size, so that neither leaves the range before h does.  (A gate's scale over
+  // 1e30 puts any sum but 0 so far out that the exponential is 0 or infinite.)
+  __device__ static __noinline__ Scales far_scales(float x, float w0, float w1,
+                                                   float inv_out) {
+    int ex, e0, e1, eo;
+    const float fx = frexpf(x, &ex);
+    const float f = fx * fx * frexpf(w0, &e0) * frexpf(w1, &e1) *
+                    frexpf(inv_out, &eo);
+    const int e = max(-250, min(250, 2 * ex + e0 + e1 + eo)), half = e / 2;
+    return {ldexpf(f, half), ldexpf(1.0f, e - half),
+            fminf(x * w0, 1e30f) * kMinusLog2e};
+  }
+  // silu(g) u under their scales, silu(z) = z / (1 + exp(-z)); exp(-z) may be
+  // infinite.
+  __device__ static __forceinline__ float swiglu(float g, float u,
+                                                 const Scales& t) {
     float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * (t0 * -1.44269504f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * t.exponent));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-    return t0 * g * s * (t1 * u);
+    return t.first * g * s * (t.last * u);
   }
 
   // Eight rows of 32 columns of h: each lane has one column of all rows, a
