@@ -642,14 +642,20 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
     int e = 0;
     float l = 0.0f;
     if (!__any_sync(kAll, again)) {
-      // Keys that reach the k-th, equal ones and those that their lane did not
-      // bring among them: as many as were chosen.
+      // what is left out below this is surely behind the k-th
+      const float bar = fmaxf(
+          reached - 2.0f * (err + kKeyErr<EPL> * fabsf(reached) + FLT_MIN),
+          -FLT_MAX);
+      // Keys that reach the k-th, equal ones among them: as many as were chosen.
+      // A lane that brought three may have others, which must not come near.
       int n = (top.a >= reached) + (top.b >= reached) + (top.c >= reached);
       if (EPL > 3 && __any_sync(kAll, n == 3)) {
-        n = 0;
+        if (n == 3) {
+          n = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          n += kept && Top<EPL>::key(c[i], i) >= reached;
+          for (int i = 0; i < EPL; ++i)
+            n += kept && Top<EPL>::key(c[i], i) >= bar;
+        }
       }
       __syncwarp();
       const float2 own = chosen[warp][lane];
@@ -664,10 +670,6 @@ __global__ void __launch_bounds__(kThreads, EPL <= 8 ? 8 : 4)
           !(own.x - next > 2.0f * err + FLT_MIN +
                                kKeyErr<EPL> * (fabsf(own.x) + fabsf(next)));
       if (__any_sync(kAll, near) || __reduce_add_sync(kAll, n) != a.k) {
-        // what is left out is surely behind
-        const float bar = fmaxf(
-            reached - 2.0f * (err + kKeyErr<EPL> * fabsf(reached) + FLT_MIN),
-            -FLT_MAX);
         uint32_t hits = 0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)

@@ -102,6 +102,34 @@ def test_near_ties_rank_as_in_64_bits(sigmoid):
     check(x[:1], bias, 12, sigmoid, 4, 2, 2, False, 1.0)
 
 
+@pytest.mark.parametrize("E", [100, 128, 200, 256, 500, 1000, 1024])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("with_bias", [True, False])
+@pytest.mark.parametrize("ulps", [0, 1])
+@pytest.mark.parametrize("shift", [0.0, -8.0])
+def test_neighbours_that_are_equal_at_the_last_place(E, sigmoid, with_bias,
+                                                     ulps, shift):
+    """Of the experts that one lane has, two are far ahead and two or more, equal
+    or an ulp apart, share the third place, which is the last one chosen."""
+    g = torch.Generator().manual_seed(19)
+    per = 2 ** (-(-E // 32) - 1).bit_length()            # experts of a lane
+    bias = torch.full((E,), 0.125) if with_bias else None
+    for more in (0, 1, 4):           # chosen in other lanes
+        x = torch.randn(64, E, generator=g) * 0.5 + shift
+        for t in range(64):
+            at = torch.randint(0, E // per, (1,), generator=g).item() * per
+            mine = at + torch.randperm(per, generator=g)[:4 + t % 3]
+            top = torch.tensor(shift + 3 + torch.rand(1, generator=g).item())
+            x[t, mine] = top
+            x[t, mine[0]], x[t, mine[1]] = top + 2, top + 1
+            if ulps:
+                x[t, mine[2]] = torch.nextafter(top, torch.tensor(9.0))
+            far = torch.randperm(E, generator=g)
+            far = far[(far < at) | (far >= at + per)][:more]
+            x[t, far] = top + 0.5 + torch.arange(more) * 0.1
+        check(x, bias, 3 + more, sigmoid, 1, 1, 1, True, 1.0)
+
+
 @pytest.mark.parametrize("sigmoid", [True, False])
 def test_far_logits(sigmoid):
     """All scores tiny or all saturated, and rows that span float32."""
