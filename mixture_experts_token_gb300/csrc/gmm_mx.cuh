@@ -33,12 +33,12 @@
 // Measured, quantising the rows and both products: one token, 8 experts of 7168
 // x 2048, blocks of 16, 198 MB, 42 us (4.7 TB/s; 128 items leave 24 of 152 SMs
 // idle in the first product); 64 tokens over 146 such experts, blocks of 32, 546
-// to 581 us (5.7 to 6.1 TB/s, with where the buffers lie); 16 experts of 5120 x
-// 8192, a row each, 160 to 174.  32768 rows over 32 experts of 7168 x 2048, blocks
-// of 16, 896 us: quantising the rows 125, gate and up 438 (4.4 PFLOP/s), down 338
-// (2.8 PFLOP/s).  Of 444 and 338, 385 and 297 are left if nothing reads the sums,
-// 369 and 266 without matrix instructions, 235 and 217 if scales are not loaded
-// either.
+// to 589 us (5.6 to 6.1 TB/s, with where the buffers lie); 16 experts of 5120 x
+// 8192, a row each, 149 to 173.  32768 rows over 32 experts of 7168 x 2048, blocks
+// of 16, 884 to 890 us: quantising the rows 128, gate and up 438 to 441 (4.4
+// PFLOP/s), down 338 (2.8 PFLOP/s).  At a step before, of 444 and 338, 385 and 297
+// were left if nothing read the sums, 369 and 266 without matrix instructions,
+// 235 and 217 if scales were not loaded either.
 #pragma once
 
 #include <atomic>
@@ -90,7 +90,10 @@ cudaError_t launch_gmm_mx_down(const GmmArgs& a, const void* codes,
 // quantised and both products, singles against pairs: 32 rows a group 169 and 171
 // us, 48 rows 173 and 177, 64 rows 194 and 181, 128 rows 300 and 198, 1024 rows
 // 1872 and 890.  (Passes of 16 rows gained nothing: 113 us for one row a group, 114
-// in passes of 64.)
+// in passes of 64.)  Those groups are alike.  The mean counts empty groups and does
+// not see a popular one: 256 experts, blocks of 32, 1024 tokens x 8 (a mean of 32)
+// take 1015 us if drawn alike and 1154 by Zipf's law, where one expert has 810
+// rows in passes of 64; 4096 tokens 1175 and 1435.
 inline bool many_rows(const GmmArgs& a) {
   return a.tokens > 64 &&
          a.rows > 48ll * std::min(a.n_groups, a.rows);
@@ -270,7 +273,8 @@ struct Gmm {
   // are short, two such teams do so in turn, each every other stage (down, 32768
   // rows: 391 us with one, 360 with two, 338 with the rows' scales written before
   // the stage is there, 346 with four).  Gate and up have no registers for two:
-  // 455 us against 438.
+  // 455 us against 438 (with one, 80 registers and 44 bytes spilled in blocks of
+  // 16, 20 in blocks of 32).
   static constexpr int kTeams = PAIR && !DUAL ? 2 : 1;
   static constexpr int kWarps = kScaleWarp + kScaleWarps * kTeams;
   static constexpr int kThreads = kWarps * 32;

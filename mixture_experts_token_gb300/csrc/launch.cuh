@@ -1,5 +1,5 @@
-// Host-side launch helpers shared by the block norms and the 4-bit products:
-// device properties and kernel occupancy, asked for once and kept (they
+// Host-side launch helpers shared by the block norms, the 4-bit products and
+// routing by scores: device properties and kernel occupancy, asked for once and kept (they
 // belong to the device and the kernel, not to a call's data), and a launch
 // that may begin while the kernel before it drains.
 #pragma once

@@ -3,9 +3,9 @@
 // kernel reads its input once and writes its output once.  Measured: 8192 x
 // 7168 bf16 rows, blocks of 32, quantised 28 to 31 us, expanded 23 to 24 (148 MB
 // each, 22 us at 6.8 TB/s); eight bf16 matrices of 7168 x 2048, blocks of 16,
-// quantised 71 us (301 MB, 44 us), packed 22 (132 MB, 19), expanded 49 (301 MB,
-// 44).  Rows both ways and quantising matrices are bound by issue (slots 72 to 81%
-// busy, with one number an instruction), the others by bytes.
+// quantised 67 us (301 MB, 44 us), packed 22 (132 MB, 19), expanded 48 (301 MB,
+// 44).  Rows both ways and quantising matrices are bound by issue (slots 64 to 77%
+// busy), the others by bytes.
 #include "launch.cuh"
 #include "mx.cuh"
 
@@ -196,7 +196,9 @@ __global__ void __launch_bounds__(kThreads)
 
 // A weight matrix w [K, N] becomes N rows of codes: 64 columns and 256 of K at
 // a time through shared memory, read a row of w and written a row of codes at
-// a time.  A warp has 32 of K, a lane two neighbouring columns of them.
+// a time.  A warp has 32 of K, a lane two neighbouring columns of them.  (What a
+// thread loads at once passes its registers: blocks of 16 and 32 spill 16 and 52
+// bytes in bf16, under 64 registers, 144 and 248 in float32, under 80.)
 constexpr int kTurnN = 64;
 template <typename T>
 struct Two;
