@@ -1,7 +1,7 @@
 // Host-side launch helpers shared by the block norms, the 4-bit products and
-// routing by scores: device properties and kernel occupancy, asked for once and kept (they
-// belong to the device and the kernel, not to a call's data), and a launch
-// that may begin while the kernel before it drains.
+// routing by scores: device properties and kernel occupancy, asked for once and
+// kept (they belong to the device and the kernel, not to a call's data), and a
+// launch that may begin while the kernel before it drains.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -859,16 +859,21 @@ __global__ void __launch_bounds__(kThreads) scores_backward_kernel(
       w = sum > 0.0f ? w / sum : 0.0f;
     }
     float g = finite ? a.scale * d : 0.0f;
-    const bool far = __any_sync(
-        kAll, finite && (w < 1e-30f || fabsf(g) > 1e30f ||
-                         (SIGMOID && fabsf(l) > -kFar)));
-    g *= w;
-    if (a.renorm) g -= w * token_sum(g);
-    if (far) g = far_gradient<SIGMOID, LANES>(a, finite, l, d, m, z);
-    const float all = SIGMOID ? 0.0f : token_sum(g);
-    // an index that stands twice has the sum of both
     const uint32_t mine = (LANES == 32 ? kAll : (1u << LANES) - 1)
                           << (tok * LANES);
+    const uint32_t far_lanes = __ballot_sync(
+        kAll, finite && (w < 1e-30f || fabsf(g) > 1e30f ||
+                         (SIGMOID && fabsf(l) > -kFar)));
+    // (by the token: what others in the warp have changes no bit of it)
+    const bool far = far_lanes & mine;
+    g *= w;
+    if (a.renorm) g -= w * token_sum(g);
+    if (far_lanes != 0) {
+      const float f = far_gradient<SIGMOID, LANES>(a, finite, l, d, m, z);
+      if (far) g = f;
+    }
+    const float all = SIGMOID ? 0.0f : token_sum(g);
+    // an index that stands twice has the sum of both
     const uint32_t same =
         __match_any_sync(kAll, e) & mine & ~(1u << lane);
     if (__any_sync(kAll, e >= 0 && same != 0)) {

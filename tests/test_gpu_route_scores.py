@@ -413,6 +413,32 @@ def test_backward_of_scores_below_float32_beside_others(sigmoid, renorm,
 
 @pytest.mark.parametrize("sigmoid", [True, False])
 @pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("k", [2, 6, 13, 20])
+def test_a_token_is_routed_alike_beside_any_others(sigmoid, renorm, k):
+    """Rows with far scores, NaN or ties between them change no bit of others:
+    neither of the weights nor of the gradient."""
+    g = torch.Generator().manual_seed(20)
+    T, E = 61, 96
+    x = torch.randn(T, E, generator=g) * 2
+    dw = torch.randn(T, k, generator=g)
+    opt = (k, sigmoid, 6, 4, 2, renorm, 2.5)
+    idx, w, _ = call(x, None, *opt)
+    dl = back(x, torch.from_numpy(idx), dw, sigmoid, renorm, 2.5)
+    other = x.clone()
+    other[1::4] = x[1::4] * 60 - 200
+    other[2::8, 5] = float("nan")
+    other[6::8] = 1.0
+    keep = np.ones(T, dtype=bool)
+    keep[1::4] = keep[2::8] = keep[6::8] = False
+    i2, w2, _ = call(other, None, *opt)
+    d2 = back(other, torch.from_numpy(i2), dw, sigmoid, renorm, 2.5)
+    assert np.array_equal(idx[keep], i2[keep])
+    assert np.array_equal(w[keep], w2[keep])
+    assert np.array_equal(dl[keep], d2[keep])
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
 def test_backward_beside_a_bias_that_is_not_finite(sigmoid, renorm):
     """Experts chosen for want of others, whose weight is 0: with their indexes
     taken out the gradient is that of the weights."""
