@@ -35,7 +35,7 @@
 // idle in the first product); 64 tokens over 146 such experts, blocks of 32, 546
 // to 589 us (5.6 to 6.1 TB/s, with where the buffers lie); 16 experts of 5120 x
 // 8192, a row each, 149 to 173.  32768 rows over 32 experts of 7168 x 2048, blocks
-// of 16, 884 to 890 us: quantising the rows 128, gate and up 438 to 441 (4.4
+// of 16, 884 to 891 us: quantising the rows 128, gate and up 438 to 441 (4.4
 // PFLOP/s), down 338 (2.8 PFLOP/s).  At a step before, of 444 and 338, 385 and 297
 // were left if nothing read the sums, 369 and 266 without matrix instructions,
 // 235 and 217 if scales were not loaded either.

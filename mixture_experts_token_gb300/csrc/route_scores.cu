@@ -20,14 +20,14 @@
 // of scores is compared, the logits rank, and the bits are the only error.
 //
 // Measured, 256 experts in 8 groups, 4 kept, 8 chosen, sigmoid with a bias:
-// 65536 tokens 43.4 to 44.1 us (the bytes need 10.5; 505 instructions a token,
+// 65536 tokens 43.1 to 44.2 us (the bytes need 10.5; 505 instructions a token,
 // issue slots 69% busy; of 490 at a step before, 80 were for the scores, 56 for
 // the lanes' largest, 121 for the groups, 81 for the rounds, 82 to see that the
 // order is sure, 68 for weights and stores; more CTAs an SM, or the bias read for
 // each row, took 1 to 2 us longer), one token 3.6 us.  A row that float64 ranks
 // adds 1.3 us where candidates are near, 2 to 3.6 where group sums are, 17 to 20
 // in rank64().  Logits that are all equal send every row there: 65536 tokens then
-// take 1.0 ms, without groups and a bias 0.30.  The gradient, 65536 tokens: 20.8
+// take 1.0 ms, without groups and a bias 0.30.  The gradient, 65536 tokens: 20.6
 // us (73 MB must move, 10.8 us; 105 MB, 15.5 us, if HBM reads 64 bytes for a
 // chosen logit).
 #include <float.h>
